@@ -1,6 +1,7 @@
 """GB300-native FP32 SGEMM: C = alpha * A @ B + beta * C on row-major FP32
 matrices, computed by hand-written sm_103a CUDA kernels behind a C ABI
-(include/sgemm_gb300.h).  This package holds that library's sources
+(include/sgemm_gb300.h), with the matrix products of language models beside
+them (include/sgemm_gb300_lm.h).  This package holds that library's sources
 (csrc/), its in-tree build step and a thin ctypes binding; the seeded input
 generator lives in ``inputs``.
 
@@ -14,6 +15,10 @@ _BINDING_NAMES = {
     "SIGNATURES",
 }
 
+_LM_NAMES = {
+    "grouped_gemm", "grouped_gemm_weight_grad",
+}
+
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile the CUDA library for sm_103a (in tree); returns the .so path."""
@@ -25,4 +30,7 @@ def __getattr__(name):
     if name in _BINDING_NAMES:
         from . import _binding
         return getattr(_binding, name)
+    if name in _LM_NAMES:
+        from . import _lm
+        return getattr(_lm, name)
     raise AttributeError(name)

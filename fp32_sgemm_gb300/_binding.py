@@ -51,7 +51,7 @@ class Plan(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
-# name -> (restype, argtypes); must list every function of include/sgemm_gb300.h
+# name -> (restype, argtypes); must list every function of include/*.h
 SIGNATURES = {
     "sgemmGetStatusString": (ctypes.c_char_p, [_st]),
     "sgemmGetVersion": (_st, [ctypes.POINTER(ctypes.c_int)]),
@@ -85,6 +85,15 @@ SIGNATURES = {
     "sgemmNoAllocSetWaitTimeout": (_st, [ctypes.c_uint64]),
     "sgemmNoAllocSetTestWithheldSignal": (_st, [ctypes.c_int]),
     "sgemmSetTestWithheldSignal": (_st, [_vp, ctypes.c_int]),
+    # include/sgemm_gb300_lm.h
+    "sgemmGrouped": (_st, [_vp, ctypes.c_int, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64,
+                           _i64, _vp, _vp, _i64, _vp]),
+    "sgemmGroupedWorkspaceSize": (_st, [_vp, ctypes.c_int, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, _i64,
+                                        _vp, _i64, _i64, ctypes.POINTER(ctypes.c_size_t)]),
+    "sgemmGroupedWeightGrad": (_st, [_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp,
+                                     _vp, _i64, _i64, _vp]),
+    "sgemmGroupedWeightGradWorkspaceSize": (_st, [_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, _i64,
+                                                  _vp, _i64, ctypes.POINTER(ctypes.c_size_t)]),
 }
 
 _lock = threading.Lock()

@@ -1,0 +1,239 @@
+// Small kernels around the tensor-core products of the language-model
+// operators: operand copies TMA can address, FP32 split into bf16 planes,
+// the joins of partial results.  All are bound by memory; each thread moves
+// 8 neighbouring elements, so that writes are whole 16-byte words.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "lm_kernels.h"
+#include "ptx.cuh"
+
+namespace sg {
+namespace {
+
+// A launch that may begin while the kernel before it in the stream ends
+// (griddepcontrol.wait orders its memory accesses).
+template <class... P, class... A>
+cudaError_t launch(void (*fn)(P...), int64_t blocks, int threads, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(std::max<int64_t>(1, blocks)));
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, P(args)...);
+}
+
+constexpr int kThreads = 256;
+constexpr int64_t kMaxBlocks = 152 * 16;
+
+__global__ void __launch_bounds__(kThreads)
+lm_pack16_kernel(const uint16_t *src, int64_t ld, int64_t stride, uint16_t *dst, int64_t ld_dst, int64_t rows,
+                 int64_t cols, int64_t batch) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int64_t per_row = ld_dst / 8, total = per_row * rows * batch;
+    for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < total; i += gridDim.x * (int64_t)kThreads) {
+        const int64_t r = i / per_row, c = (i - r * per_row) * 8, b = r / rows;
+        const uint16_t *s = src + b * stride + (r - b * rows) * ld + c;
+        alignas(16) uint16_t v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? s[e] : (uint16_t)0;
+        *reinterpret_cast<uint4 *>(dst + r * ld_dst + c) = *reinterpret_cast<const uint4 *>(v);
+    }
+}
+
+// x = p0 + p1 + p2 exactly: the leading 8, the next 8 and the last 8 bits of
+// its significand (each plane truncated, so that the rest keeps x's sign and
+// p0 never rounds up to infinity).  Values that are not finite stay in p0.
+__device__ __forceinline__ void split3(float x, uint16_t &a, uint16_t &b, uint16_t &c) {
+    const uint32_t u = __float_as_uint(x);
+    // A NaN whose payload lies in the low bits must stay a NaN.
+    const bool odd = (u & 0x7F800000u) == 0x7F800000u;
+    const uint32_t h = odd && (u & 0x7FFFFFu) ? 0x7FC00000u : u & 0xFFFF0000u;
+    const float r1 = odd ? 0.f : x - __uint_as_float(h);
+    const uint32_t m = __float_as_uint(r1) & 0xFFFF0000u;
+    const float r2 = r1 - __uint_as_float(m);
+    a = (uint16_t)(h >> 16);
+    b = (uint16_t)(m >> 16);
+    c = (uint16_t)(__float_as_uint(r2) >> 16);
+}
+
+template <bool VEC>
+__global__ void __launch_bounds__(kThreads)
+lm_split3_kernel(const float *src, int64_t ld, int64_t stride, uint16_t *dst, int64_t ld_dst, int64_t plane,
+                 int64_t rows, int64_t cols, int64_t batch) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int64_t per_row = ld_dst / 8, total = per_row * rows * batch;
+    for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < total; i += gridDim.x * (int64_t)kThreads) {
+        const int64_t r = i / per_row, c = (i - r * per_row) * 8, b = r / rows;
+        const float *s = src + b * stride + (r - b * rows) * ld + c;
+        float x[8];
+        if (VEC && c + 8 <= cols) {
+            *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(s);
+            *reinterpret_cast<float4 *>(x + 4) = *reinterpret_cast<const float4 *>(s + 4);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = c + e < cols ? s[e] : 0.f;
+        }
+        alignas(16) uint16_t v[3][8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) split3(x[e], v[0][e], v[1][e], v[2][e]);
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+            *reinterpret_cast<uint4 *>(dst + q * plane + r * ld_dst + c) = *reinterpret_cast<const uint4 *>(v[q]);
+    }
+}
+
+// One warp per row joins the slabs' {maximum, sum of exp(l - maximum)} in a
+// fixed order.
+__global__ void __launch_bounds__(kThreads)
+lm_lse_join_kernel(const float2 *part, int slabs, int rows, const float *picked, const int64_t *target,
+                   int64_t vocab, float *loss, float *lse) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int row = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (row >= rows) return;
+    float m = -INFINITY;
+    for (int i = lane; i < slabs; i += 32) m = fmaxf(m, part[(int64_t)i * rows + row].x);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+    const float ref = m == -INFINITY ? 0.f : m;
+    float s = 0.f;
+    for (int i = lane; i < slabs; i += 32) {
+        const float2 p = part[(int64_t)i * rows + row];
+        s += p.y * expf(p.x - ref);
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
+    if (lane == 0) {
+        const float l = ref + logf(s);
+        lse[row] = l;
+        const int64_t t = target[row];
+        loss[row] = t >= 0 && t < vocab ? l - picked[row] : 0.f;
+    }
+}
+
+// scale2[0] = 2^e with max |grad| * 2^e in [2^12, 2^13), scale2[1] = 2^-e.
+__global__ void __launch_bounds__(1024)
+lm_grad_scale_kernel(const float *grad, const int64_t *target, int64_t vocab, int rows, float *scale2) {
+    griddep_launch_dependents();
+    griddep_wait();
+    __shared__ float top[32];
+    float m = 0.f;
+    for (int i = threadIdx.x; i < rows; i += 1024) {
+        const int64_t t = target[i];
+        if (t >= 0 && t < vocab) m = fmaxf(m, fabsf(grad[i]));
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+    if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = m;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        m = top[threadIdx.x];
+#pragma unroll
+        for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+        if (threadIdx.x == 0) {
+            int e = 0;
+            if (m > 0.f && m <= 3.0e38f) {
+                frexpf(m, &e);                      // m in [2^(e-1), 2^e)
+                e = min(max(13 - e, -100), 100);
+            }
+            scale2[0] = ldexpf(1.f, e);
+            scale2[1] = ldexpf(1.f, -e);
+        }
+    }
+}
+
+template <class Out> __device__ __forceinline__ Out to_out(float x);
+template <> __device__ __forceinline__ float to_out<float>(float x) { return x; }
+template <> __device__ __forceinline__ __half to_out<__half>(float x) { return __float2half_rn(x); }
+template <> __device__ __forceinline__ __nv_bfloat16 to_out<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+template <class Out>
+__global__ void __launch_bounds__(kThreads)
+lm_join_splits_kernel(const float *part, int64_t ld, int64_t plane, int splits, const float *alpha, int rows,
+                      int cols, Out *out, int64_t ldo) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const float a = alpha != nullptr ? *alpha : 1.f;
+    const int64_t total = (int64_t)rows * cols;
+    for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < total; i += gridDim.x * (int64_t)kThreads) {
+        const int64_t r = i / cols, c = i - r * cols;
+        float s = 0.f;
+        for (int z = 0; z < splits; ++z) s += part[z * plane + r * ld + c];
+        out[r * ldo + c] = to_out<Out>(a * s);
+    }
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads)
+lm_zero_kernel(T *p, int64_t ld, int64_t stride, int64_t rows, int64_t cols, int64_t batch) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int64_t total = rows * cols * batch;
+    for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < total; i += gridDim.x * (int64_t)kThreads) {
+        const int64_t r = i / cols, b = r / rows;
+        p[b * stride + (r - b * rows) * ld + (i - r * cols)] = T(0);
+    }
+}
+
+int64_t blocks_for(int64_t threads) { return std::min<int64_t>((threads + kThreads - 1) / kThreads, kMaxBlocks); }
+
+}  // namespace
+
+cudaError_t lm_launch_pack16(const void *src, int64_t ld, int64_t stride, void *dst, int64_t ld_dst, int64_t rows,
+                             int64_t cols, int64_t batch, cudaStream_t s) {
+    return launch(lm_pack16_kernel, blocks_for(ld_dst / 8 * rows * batch), kThreads, s,
+                  static_cast<const uint16_t *>(src), ld, stride, static_cast<uint16_t *>(dst), ld_dst, rows, cols,
+                  batch);
+}
+
+cudaError_t lm_launch_split3(const float *src, int64_t ld, int64_t stride, void *dst, int64_t ld_dst,
+                             int64_t plane, int64_t rows, int64_t cols, int64_t batch, cudaStream_t s) {
+    const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && ld % 4 == 0 && stride % 4 == 0;
+    return launch(vec ? lm_split3_kernel<true> : lm_split3_kernel<false>, blocks_for(ld_dst / 8 * rows * batch),
+                  kThreads, s, src, ld, stride, static_cast<uint16_t *>(dst), ld_dst, plane, rows, cols, batch);
+}
+
+cudaError_t lm_launch_lse_join(const float2 *part, int slabs, int rows, const float *picked, const int64_t *target,
+                               int64_t vocab, float *loss, float *lse, cudaStream_t s) {
+    return launch(lm_lse_join_kernel, (rows + kThreads / 32 - 1) / (kThreads / 32), kThreads, s, part, slabs, rows,
+                  picked, target, vocab, loss, lse);
+}
+
+cudaError_t lm_launch_grad_scale(const float *grad, const int64_t *target, int64_t vocab, int rows, float *scale2,
+                                 cudaStream_t s) {
+    return launch(lm_grad_scale_kernel, 1, 1024, s, grad, target, vocab, rows, scale2);
+}
+
+cudaError_t lm_launch_join_splits(const float *part, int64_t ld_part, int64_t plane, int splits, const float *alpha,
+                                  int rows, int cols, void *out, int64_t ldo, int out_type, cudaStream_t s) {
+    const int64_t blocks = blocks_for((int64_t)rows * cols);
+    if (out_type == kOutF32)
+        return launch(lm_join_splits_kernel<float>, blocks, kThreads, s, part, ld_part, plane, splits, alpha, rows,
+                      cols, static_cast<float *>(out), ldo);
+    if (out_type == kOutF16)
+        return launch(lm_join_splits_kernel<__half>, blocks, kThreads, s, part, ld_part, plane, splits, alpha, rows,
+                      cols, static_cast<__half *>(out), ldo);
+    return launch(lm_join_splits_kernel<__nv_bfloat16>, blocks, kThreads, s, part, ld_part, plane, splits, alpha,
+                  rows, cols, static_cast<__nv_bfloat16 *>(out), ldo);
+}
+
+cudaError_t lm_launch_zero(void *p, int64_t ld, int64_t stride, int elem, int64_t rows, int64_t cols, int64_t batch,
+                           cudaStream_t s) {
+    const int64_t blocks = blocks_for(rows * cols * batch);
+    if (elem == 4)
+        return launch(lm_zero_kernel<uint32_t>, blocks, kThreads, s, static_cast<uint32_t *>(p), ld, stride, rows,
+                      cols, batch);
+    return launch(lm_zero_kernel<uint16_t>, blocks, kThreads, s, static_cast<uint16_t *>(p), ld, stride, rows, cols,
+                  batch);
+}
+
+}  // namespace sg

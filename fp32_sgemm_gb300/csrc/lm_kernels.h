@@ -1,0 +1,86 @@
+// What the host side of the language-model operators and their kernels share.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace sg {
+
+constexpr int kLmMaxGroups = 1024;
+constexpr float kLog2E = 1.4426950408889634f;
+
+// Wait / check site of the error word (bits 24..31) beside those of the
+// main kernels: group ends that run backwards or past the last row.
+constexpr uint32_t kSiteGroupEnds = 6;
+
+enum LmRag { kRagNone = 0, kRagN = 1, kRagK = 2 };
+enum LmEpi {
+    kEpiCols = 0,      // D^T into a row-major matrix (columns of D are its rows)
+    kEpiRows = 1,      // alpha * (D + acc_in) into a row-major matrix
+    kEpiLse = 2,       // running maximum and sum of exponentials of each row of D
+    kEpiDLogits = 3    // gradient of the loss by each element of D
+};
+enum LmOut { kOutF32 = 0, kOutF16 = 1, kOutBF16 = 2 };
+
+struct LmArgs {
+    int M, N;             // rows and columns of D (kRagN: columns by groups)
+    int T;                // token rows (ragged extent)
+    int kb;               // blocks of 64 of the contraction (not kRagK)
+    int G;
+    const int32_t *ends;  // [G] end row of each group
+    int tiles_m, tiles_n, tile_n, num_tiles, splits, group_m;
+    int pairs;            // 1, or 6 for FP32 operands in three bf16 planes
+    uint32_t bf16;        // operands bf16 (else f16)
+    void *C;
+    int64_t ldc, stride_c;   // stride_c: per group (kRagK) or per K split
+    int out, vec;            // LmOut; vec: rows take aligned vector stores
+    const float *acc_in;     // added to D before alpha, or NULL
+    int64_t ld_acc;
+    const float *alpha;      // device scalar, or NULL for 1
+    // Loss epilogues; D's columns are vocabulary entries v0 .. v0 + N - 1.
+    const int64_t *target;
+    int64_t vocab, v0;
+    float2 *part;            // [column slab][row] {maximum, sum}
+    float *picked;           // logit of the row's target
+    const float *lse, *grad, *gscale;
+    uint32_t *err;
+    uint64_t timeout_ns;
+    int withhold;
+};
+
+struct LmKernel {
+    const void *fn = nullptr;
+    int threads = 0, smem = 0, tile_m = 0, bn = 0, gran = 0, pair = 0, box_a = 0, box_b = 0, slabs = 0;
+    int a_mn = 0, b_mn = 0;
+};
+
+// Kernel tables.  size: 0 thin, 1 middle, 2 big (SM pair).
+LmKernel lm_grouped_kernel(int size, bool w_mn, bool f32);      // lm_grouped*.cu
+LmKernel lm_weight_grad_kernel(int size, bool f32);             // size 1 or 2
+LmKernel lm_lse_kernel(bool big);                               // lm_loss.cu
+LmKernel lm_dlogits_kernel(bool big);
+LmKernel lm_rows_kernel(bool big, bool a_mn);                   // B MN-major
+
+// lm_aux.cu.  Operand copies TMA can address: rows x cols (x batch) with
+// pitch ld -> pitch ld_dst (a multiple of 8), 16-bit copied as they are,
+// FP32 as three bf16 planes (plane stride in elements).
+cudaError_t lm_launch_pack16(const void *src, int64_t ld, int64_t stride, void *dst, int64_t ld_dst, int64_t rows,
+                             int64_t cols, int64_t batch, cudaStream_t s);
+cudaError_t lm_launch_split3(const float *src, int64_t ld, int64_t stride, void *dst, int64_t ld_dst,
+                             int64_t plane, int64_t rows, int64_t cols, int64_t batch, cudaStream_t s);
+// Joins the slabs' maxima and sums: lse and loss of each row.
+cudaError_t lm_launch_lse_join(const float2 *part, int slabs, int rows, const float *picked, const int64_t *target,
+                               int64_t vocab, float *loss, float *lse, cudaStream_t s);
+// Power of two that brings the largest |grad| of a counted row to 2^13.
+cudaError_t lm_launch_grad_scale(const float *grad, const int64_t *target, int64_t vocab, int rows, float *scale2,
+                                 cudaStream_t s);
+// out = alpha * (sum of `splits` FP32 planes), rounded to `out_type`.
+cudaError_t lm_launch_join_splits(const float *part, int64_t ld_part, int64_t plane, int splits, const float *alpha,
+                                  int rows, int cols, void *out, int64_t ldo, int out_type, cudaStream_t s);
+// rows x cols (x batch) elements of 2 or 4 bytes set to zero.
+cudaError_t lm_launch_zero(void *p, int64_t ld, int64_t stride, int elem, int64_t rows, int64_t cols, int64_t batch,
+                           cudaStream_t s);
+
+}  // namespace sg

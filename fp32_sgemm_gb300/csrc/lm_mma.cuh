@@ -1,0 +1,761 @@
+// Tensor-core products behind the language-model operators (grouped
+// products, vocabulary cross entropy): 16-bit operands, FP32 accumulation,
+// tcgen05.mma kind::f16 with operands staged by TMA.
+//
+//   D[m, n] = sum_k A[m, k] B[k, n]
+//
+// One kernel template serves every form; what changes is
+//   * how each operand is stored: K contiguous ("K-major") or M / N
+//     contiguous ("MN-major").  Both are read as they are (the MMA's
+//     descriptors name the layout), so no operand is ever transposed in
+//     memory;
+//   * which extent is ragged (kRagNone, kRagN: columns of D are rows of a
+//     token matrix that belong to groups, kRagK: the contraction runs over
+//     the rows of a group);
+//   * what the epilogue does with D (Epi).
+//
+// For kRagN the tokens are put on the MMA's N side and the group's matrix
+// on its M side, because N may be any multiple of 16 (32 on an SM pair) per
+// instruction: a group of r rows costs ceil(r / 16) * 16 columns of MMA
+// time instead of a multiple of 128 or 256 rows.
+//
+// Structure: persistent CTAs (or SM pairs, cta_group::2: each SM holds half
+// of the 256 rows of A and half of B's columns, so that shared memory feeds
+// the tensor core 2/3 of the bytes per MMA that one SM alone would).  Warp 0
+// is the TMA producer, warp 1 issues the MMAs, the others run the epilogue
+// out of TMEM while the next tile is multiplied into the other accumulator.
+// Every wait is bounded and reports its site in the handle's error word.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "lm_kernels.h"
+#include "ptx.cuh"
+
+namespace sg {
+
+// ------------------------------------------------------------ PTX wrappers
+
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// MN-major operand stored with the 128-byte swizzle: chunks of 64 elements
+// of M (N) by 64 of K, each K row 128 bytes, as a TMA box {64, 64} writes
+// them.  Leading offset: from one chunk of 64 to the next (8 KB); stride
+// offset: from 8 rows of K to the next 8 (1 KB).  K = 16 advances 2 KB.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)(8192u >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+
+// Instruction descriptor, kind::f16: D f32, A and B both f16 (0) or bf16 (1).
+__device__ __forceinline__ uint32_t idesc_f16(uint32_t bf16, bool a_mn, bool b_mn, int M, int N) {
+    return (1u << 4) | (bf16 << 7) | (bf16 << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void fence_proxy_async_smem() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_32cols_nowait(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+// 32 bytes to a 32-byte aligned address in one store: a whole sector.
+__device__ __forceinline__ void st_global_32B(void *p, const uint32_t *v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 :: "l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
+                    "r"(v[7]) : "memory");
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <class T> __device__ __forceinline__ T lm_cvt(float x);
+template <> __device__ __forceinline__ float lm_cvt<float>(float x) { return x; }
+template <> __device__ __forceinline__ __half lm_cvt<__half>(float x) { return __float2half_rn(x); }
+template <> __device__ __forceinline__ __nv_bfloat16 lm_cvt<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+template <class T> __device__ __forceinline__ uint32_t lm_pack2(float a, float b);
+template <> __device__ __forceinline__ uint32_t lm_pack2<__half>(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <> __device__ __forceinline__ uint32_t lm_pack2<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// ----------------------------------------------------------------- tiles
+
+// One output tile: 128 rows of A per SM (256 on a pair) by up to BN columns.
+template <int BN_, int STAGES_, bool PAIR_>
+struct LmTile {
+    static constexpr bool PAIR = PAIR_;
+    static constexpr int BM = 128, BN = BN_, BK = 64, STAGES = STAGES_;
+    static constexpr int TILE_M = PAIR ? 256 : 128;
+    static constexpr int B_ROWS = PAIR ? BN / 2 : BN;       // columns of B this SM stages
+    static constexpr int GRAN = PAIR ? 32 : 16;             // granule of the MMA's N
+    static constexpr int A_BYTES = BM * BK * 2, B_BYTES = B_ROWS * BK * 2;
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int EPI_WARPS = BN >= 64 ? 8 : 4;
+    static constexpr int SLAB = BN / (EPI_WARPS / 4);       // columns per epilogue warp
+    static constexpr int TMEM_COLS = 2 * BN <= 64 ? 64 : 2 * BN <= 128 ? 128 : 2 * BN <= 256 ? 256 : 512;
+    static constexpr int THREADS = (2 + EPI_WARPS) * 32;
+    static constexpr int BARS = 2 * STAGES + 6;
+    static constexpr int STAGING = EPI_WARPS * 32 * 33 * 4;
+    // Ring, barriers (8 bytes each), TMEM address (16), epilogue staging;
+    // the group tables of kRagN / kRagK follow.
+    static constexpr int FIXED = STAGES * STAGE_BYTES + ((BARS * 8 + 16 + 15) / 16) * 16 + STAGING + 1024;
+    static_assert(BN % 32 == 0 && SLAB % 32 == 0 && B_BYTES % 1024 == 0, "tile");
+    static_assert(FIXED <= 227 * 1024, "shared memory per CTA");
+};
+
+struct LmWork {
+    int m0, n0;          // first row, first column of D
+    int nmma, nvalid;    // columns multiplied, columns that exist
+    int kb0, nkb;        // blocks of 64 of the contraction
+    int krow0, klast;    // kRagK: first token row, rows in the last block
+    int g, s;            // group, K split
+};
+
+// Ends of the groups -> start rows and (kRagN) the running number of tiles,
+// by one warp.  Ends that run backwards or past T are pulled into range
+// (every access stays inside the operands) and reported (kSiteGroupEnds).
+// Entry G is a group of its own, the rows behind the last end, which get zeros.
+template <class Tile, int RAG>
+__device__ __forceinline__ void lm_group_tables(const LmArgs &p, int *start, uint32_t *prefix, int lane) {
+    int row = 0;
+    uint32_t tiles = 0;
+    bool bad = false;
+    for (int g0 = 0; g0 <= p.G; g0 += 32) {
+        const int g = g0 + lane;
+        int e = g < p.G ? p.ends[g] : p.T;
+        bad |= e < 0 || e > p.T;
+        e = min(max(e, 0), p.T);
+        int top = e;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(~0u, top, d);
+            if (lane >= d) top = max(top, o);
+        }
+        top = max(top, row);
+        bad |= top != e;
+        int first = __shfl_up_sync(~0u, top, 1);
+        if (lane == 0) first = row;
+        if (g <= p.G) start[g] = first;
+        if (g == p.G) start[p.G + 1] = p.T;
+        row = __shfl_sync(~0u, top, 31);
+        if constexpr (RAG == kRagN) {
+            uint32_t n = g <= p.G ? (uint32_t)((top - first + p.tile_n - 1) / p.tile_n) * (uint32_t)p.tiles_m : 0u;
+            uint32_t sum = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const uint32_t o = __shfl_up_sync(~0u, sum, d);
+                if (lane >= d) sum += o;
+            }
+            if (g <= p.G) prefix[g] = tiles + sum - n;
+            tiles += __shfl_sync(~0u, sum, 31);
+            if (g == p.G) prefix[p.G + 1] = tiles;
+        }
+    }
+    if (__any_sync(~0u, bad) && lane == 0 && blockIdx.x == 0) record_error(p.err, kSiteGroupEnds);
+}
+
+template <class Tile, int RAG>
+__device__ __forceinline__ LmWork lm_work(const LmArgs &p, const int *start, const uint32_t *prefix, int t) {
+    LmWork w;
+    w.s = 0;
+    w.kb0 = 0;
+    w.krow0 = 0;
+    w.klast = 64;
+    if constexpr (RAG == kRagN) {
+        int lo = 0, hi = p.G;                   // last g with prefix[g] <= t
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (prefix[mid] <= (uint32_t)t) lo = mid;
+            else hi = mid - 1;
+        }
+        w.g = lo;
+        const int local = t - (int)prefix[lo];
+        const int r0 = start[lo], rows = start[lo + 1] - r0;
+        const int nt = (rows + p.tile_n - 1) / p.tile_n;
+        // Columns spread evenly over the group's tiles.
+        const int per = ((rows + nt - 1) / nt + Tile::GRAN - 1) / Tile::GRAN * Tile::GRAN;
+        const int band = local / (p.group_m * nt), in = local - band * p.group_m * nt;
+        const int bw = min(p.group_m, p.tiles_m - band * p.group_m);
+        const int tn = in / bw, tm = band * p.group_m + in - tn * bw;
+        w.m0 = tm * Tile::TILE_M;
+        w.n0 = r0 + tn * per;
+        w.nvalid = min(per, rows - tn * per);
+        w.nmma = (w.nvalid + Tile::GRAN - 1) / Tile::GRAN * Tile::GRAN;
+        w.nkb = lo == p.G ? 0 : p.kb;
+    } else if constexpr (RAG == kRagK) {
+        const int per_g = p.tiles_m * p.tiles_n;
+        w.g = t / per_g;
+        const int in = t - w.g * per_g;
+        const int tn = in / p.tiles_m, tm = in - tn * p.tiles_m;
+        const int rows = start[w.g + 1] - start[w.g];
+        w.m0 = tm * Tile::TILE_M;
+        w.n0 = tn * p.tile_n;
+        w.nvalid = min(p.tile_n, p.N - w.n0);
+        w.nmma = p.tile_n;
+        w.krow0 = start[w.g];
+        w.nkb = (rows + 63) >> 6;
+        w.klast = rows - ((w.nkb - 1) << 6);
+    } else {
+        w.g = 0;
+        const int tile = t / p.splits;
+        w.s = t - tile * p.splits;
+        const int per_band = p.group_m * p.tiles_n;
+        const int band = tile / per_band, in = tile - band * per_band;
+        const int bw = min(p.group_m, p.tiles_m - band * p.group_m);
+        const int tn = in / bw, tm = band * p.group_m + in - tn * bw;
+        w.m0 = tm * Tile::TILE_M;
+        w.n0 = tn * p.tile_n;
+        w.nvalid = min(p.tile_n, p.N - w.n0);
+        w.nmma = p.tile_n;
+        w.kb0 = (int)((int64_t)p.kb * w.s / p.splits);
+        w.nkb = (int)((int64_t)p.kb * (w.s + 1) / p.splits) - w.kb0;
+    }
+    return w;
+}
+
+// Planes multiplied in one step of a product of FP32 operands (each held as
+// three bf16 planes, x = p0 + p1 + p2 exactly): p_i q_j with i + j <= 2,
+// smallest first.  With one pair: plane 0 only.
+__device__ __forceinline__ void lm_planes(int pairs, int pr, int &ia, int &ib) {
+    if (pairs == 1) { ia = ib = 0; return; }
+    // (2,0) (1,1) (0,2) (1,0) (0,1) (0,0), two bits each
+    ia = (0x046 >> (2 * pr)) & 3;      // 2,1,0,1,0,0
+    ib = (0x124 >> (2 * pr)) & 3;      // 0,1,2,0,1,0
+}
+
+// -------------------------------------------------------------- epilogues
+
+// 32 columns of this lane's row of D, as a piece of a row-major matrix.
+template <class Out>
+__device__ __forceinline__ void lm_store_rows(const LmArgs &p, Out *base, int row, int row0, int col, int cnt,
+                                              const float (&v)[32], float *stg, int lane) {
+    if (p.vec) {
+        if (row >= p.M) return;
+        Out *c = base + (int64_t)row * p.ldc + col;
+        if (cnt == 32) {
+            if constexpr (sizeof(Out) == 2) {
+                uint32_t u[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) u[i] = lm_pack2<Out>(v[2 * i], v[2 * i + 1]);
+                st_global_32B(c, u);
+                st_global_32B(c + 16, u + 8);
+            } else {
+                uint32_t u[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) st_global_32B(c + 8 * i, u + 8 * i);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (i < cnt) c[i] = lm_cvt<Out>(v[i]);
+        }
+    } else {
+        // Rows that vector stores cannot reach: turned in shared memory, so
+        // that a warp writes 32 neighbours of one row at a time.
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) stg[lane * 33 + i] = v[i];
+        __syncwarp();
+        if (lane < cnt)
+#pragma unroll 8
+            for (int r = 0; r < 32; ++r)
+                if (row0 + r < p.M) base[(int64_t)(row0 + r) * p.ldc + col + lane] = lm_cvt<Out>(stg[r * 33 + lane]);
+    }
+}
+
+// 32 columns of D are 32 token rows of the output; this lane holds output
+// column f of each.
+template <class Out>
+__device__ __forceinline__ void lm_store_cols(const LmArgs &p, Out *base, int f0, int tok, int cnt,
+                                              const float (&v)[32], float *stg, int lane) {
+    if (sizeof(Out) == 4 || !p.vec) {
+        const int f = f0 + lane;
+        if (f >= p.M) return;
+        Out *c = base + (int64_t)tok * p.ldc + f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < cnt) c[(int64_t)j * p.ldc] = lm_cvt<Out>(v[j]);
+        return;
+    }
+    if constexpr (sizeof(Out) == 2) {
+        // Through shared memory: 16 bytes of one token row per lane.
+        Out *s = reinterpret_cast<Out *>(stg);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) s[j * 32 + lane] = lm_cvt<Out>(v[j]);
+        __syncwarp();
+        const int f = f0 + (lane & 3) * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = i * 8 + (lane >> 2);
+            if (j >= cnt) continue;
+            Out *c = base + (int64_t)(tok + j) * p.ldc + f;
+            const Out *src = s + j * 32 + (lane & 3) * 8;
+            if (f + 8 <= p.M) {
+                *reinterpret_cast<uint4 *>(c) = *reinterpret_cast<const uint4 *>(src);
+            } else {
+                for (int e = 0; e < 8; ++e)
+                    if (f + e < p.M) c[e] = src[e];
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- kernel
+
+template <class Tile, bool A_MN, bool B_MN, int RAG, int EPI, bool CHUNKED>
+__global__ void __launch_bounds__(Tile::THREADS, 1)
+lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const LmArgs p) {
+    constexpr bool PAIR = Tile::PAIR;
+    constexpr int BN = Tile::BN, STAGES = Tile::STAGES, SLAB = Tile::SLAB;
+    static_assert(!B_MN || Tile::B_ROWS % 64 == 0, "MN-major B is staged in chunks of 64 columns");
+
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+    unsigned char *smem = smem_raw + pad;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * Tile::STAGE_BYTES);
+    uint64_t *full = bars;                  // TMA -> MMA
+    uint64_t *empty = bars + STAGES;        // MMA -> TMA
+    uint64_t *tfull = bars + 2 * STAGES;    // MMA -> epilogue, per accumulator
+    uint64_t *tempty = tfull + 2;           // epilogue -> MMA, per accumulator
+    uint64_t *drain = tempty + 2;           // MMA completion before teardown
+    uint64_t *tailbar = drain + 1;          // kRagK: copies of a group's last block
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Tile::BARS);
+    unsigned char *after = reinterpret_cast<unsigned char *>(bars) + ((Tile::BARS * 8 + 16 + 15) / 16) * 16;
+    float *staging = reinterpret_cast<float *>(after);
+    int *g_start = reinterpret_cast<int *>(after + Tile::STAGING);
+    uint32_t *g_prefix = reinterpret_cast<uint32_t *>(g_start + p.G + 2);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = PAIR ? cluster_rank() : 0u;
+
+    if (warp == 0) {
+        if constexpr (PAIR) tmem_alloc_pair(tmem_slot, Tile::TMEM_COLS);
+        else tmem_alloc(tmem_slot, Tile::TMEM_COLS);
+    }
+    if (threadIdx.x == 32) {
+        for (int s = 0; s < STAGES; ++s) {
+            // kRagK on a pair: the other SM's producer arrives as well (it
+            // may have to clear rows of a group's last block first).
+            mbar_init(&full[s], PAIR && RAG == kRagK ? 2 : 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull[b], 1);
+            mbar_init(&tempty[b], (PAIR ? 2 : 1) * Tile::EPI_WARPS);
+        }
+        mbar_init(drain, 1);
+        mbar_init(tailbar, 1);
+        fence_barrier_init();
+        prefetch_tensormap(&tmA);
+        prefetch_tensormap(&tmB);
+    }
+    griddep_launch_dependents();
+    griddep_wait();
+    if constexpr (RAG != kRagNone)
+        if (warp == 2) lm_group_tables<Tile, RAG>(p, g_start, g_prefix, lane);
+    tc_fence_before();
+    if constexpr (PAIR) cluster_sync();
+    else __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
+    const int slot = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+    const int slots = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+    const int num_tiles = RAG == kRagN ? (int)g_prefix[p.G + 1] : p.num_tiles;
+
+    if (warp == 0) {
+        // ---------------- TMA producer (lane 0; the warp clears tails) ----------------
+        int stage = 0, issued = 0;
+        uint32_t phase = 0, tail_phase = 0;
+        bool ok = true;
+        for (int t = slot; ok && t < num_tiles; t += slots) {
+            const LmWork w = lm_work<Tile, RAG>(p, g_start, g_prefix, t);
+            const int ma = w.m0 + (int)rank * Tile::BM;
+            const int nb = w.n0 + (int)rank * (w.nmma >> 1);
+            for (int kb = 0; ok && kb < w.nkb; ++kb) {
+                const int kc = RAG == kRagK ? w.krow0 + kb * 64 : (w.kb0 + kb) * 64;
+                const bool tail = RAG == kRagK && kb == w.nkb - 1 && (w.klast & 15) != 0;
+                for (int pr = 0; pr < p.pairs; ++pr) {
+                    if (p.withhold == kWithholdRefill && issued >= STAGES) { ok = false; break; }
+                    if (lane == 0 && !mbar_wait_bounded<PAIR>(&empty[stage], phase ^ 1u, p.timeout_ns)) {
+                        record_error(p.err, kSiteProducerEmpty);
+                        ok = false;
+                    }
+                    ok = __shfl_sync(~0u, ok, 0);
+                    if (!ok) break;
+                    unsigned char *sa = smem + stage * Tile::STAGE_BYTES, *sb = sa + Tile::A_BYTES;
+                    int ia, ib;
+                    lm_planes(p.pairs, pr, ia, ib);
+                    const int za = RAG == kRagN ? ia * p.G + w.g : ia;
+                    if (lane == 0) {
+                        uint32_t fb = 0;
+                        if constexpr (PAIR) {
+                            fb = cluster_addr(&full[stage], 0);
+                            if (!tail) {
+                                // Both SMs' copies complete on rank 0's barrier.
+                                if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * Tile::STAGE_BYTES);
+                                else if (RAG == kRagK) mbar_arrive_cluster(fb);
+                            }
+                        } else if (!tail) {
+                            mbar_arrive_expect_tx(&full[stage], Tile::STAGE_BYTES);
+                        }
+                        if (tail) mbar_arrive_expect_tx(tailbar, Tile::STAGE_BYTES);
+                        auto load = [&](void *dst, const CUtensorMap *m, int c0, int c1, int c2) {
+                            if (tail) tma_load_3d(dst, m, tailbar, c0, c1, c2);
+                            else if constexpr (PAIR) tma_load_3d_pair(dst, m, fb, c0, c1, c2);
+                            else tma_load_3d(dst, m, &full[stage], c0, c1, c2);
+                        };
+                        if constexpr (A_MN) {
+                            load(sa, &tmA, ma, kc, za);
+                            load(sa + 8192, &tmA, ma + 64, kc, za);
+                        } else {
+                            load(sa, &tmA, kc, ma, za);
+                        }
+                        if constexpr (B_MN) {
+#pragma unroll
+                            for (int c = 0; c < Tile::B_ROWS / 64; ++c)
+                                load(sb + c * 8192, &tmB, nb + c * 64, kc, ib);
+                        } else {
+                            load(sb, &tmB, kc, nb, ib);
+                        }
+                    }
+                    if constexpr (RAG == kRagK) {
+                        if (tail) {
+                            // The block's rows behind the group belong to
+                            // others: cleared up to the next multiple of 16,
+                            // where the MMAs stop (both operands, so that an
+                            // infinity there does not meet a zero).
+                            __syncwarp();
+                            if (!mbar_wait_bounded(tailbar, tail_phase, downstream_limit(p.timeout_ns))) {
+                                if (lane == 0) record_error(p.err, kSiteConsumerFull);
+                                ok = false;
+                            }
+                            ok = __all_sync(~0u, ok);
+                            tail_phase ^= 1u;
+                            const int r0 = w.klast, r1 = (w.klast + 15) & ~15;
+                            constexpr int CHUNKS = (Tile::A_BYTES + Tile::B_BYTES) / 8192;
+                            for (int i = lane; i < CHUNKS * (r1 - r0) * 8; i += 32) {
+                                const int c = i / ((r1 - r0) * 8), in = i - c * (r1 - r0) * 8;
+                                *reinterpret_cast<uint4 *>(sa + c * 8192 + r0 * 128 + in * 16) = make_uint4(0, 0, 0, 0);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                if (PAIR && rank != 0) mbar_arrive_cluster(cluster_addr(&full[stage], 0));
+                                else mbar_arrive(&full[stage]);
+                            }
+                        }
+                    }
+                    ++issued;
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                }
+            }
+        }
+        if (!ok && lane == 0) {
+            // Let this CTA's own copies land before it can exit (rank 1 of
+            // a pair sees them as the release of its stages).
+            const int pending = issued < STAGES ? issued : STAGES;
+            for (int back = 1; back <= pending; ++back) {
+                int s = stage - back;
+                uint32_t ph = phase;
+                if (s < 0) { s += STAGES; ph ^= 1u; }
+                mbar_wait_bounded<PAIR>(rank == 0 ? &full[s] : &empty[s], ph, p.timeout_ns);
+            }
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        // ---------------- MMA issuer (rank 0 of a pair) ----------------
+        int stage = 0, gc = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int t = slot; ok && t < num_tiles; t += slots) {
+            const LmWork w = lm_work<Tile, RAG>(p, g_start, g_prefix, t);
+            const uint32_t idesc = idesc_f16(p.bf16, A_MN, B_MN, Tile::TILE_M, w.nmma);
+            uint32_t d_tmem = 0;
+            for (int kb = 0; ok && kb < w.nkb; ++kb) {
+                const bool first = CHUNKED || kb == 0, last = CHUNKED || kb == w.nkb - 1;
+                if (first) {
+                    const int ab = gc & 1;
+                    if (!mbar_wait_bounded<PAIR>(&tempty[ab], ((uint32_t)(gc >> 1) & 1u) ^ 1u, p.timeout_ns)) {
+                        record_error(p.err, kSiteConsumerFull);
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    d_tmem = tmem_base + (uint32_t)(ab * BN);
+                }
+                const int steps = RAG == kRagK && kb == w.nkb - 1 ? (w.klast + 15) >> 4 : 4;
+                for (int pr = 0; pr < p.pairs; ++pr) {
+                    if (!mbar_wait_bounded<PAIR>(&full[stage], phase, downstream_limit(p.timeout_ns))) {
+                        record_error(p.err, kSiteConsumerFull);
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(smem + stage * Tile::STAGE_BYTES), sb = sa + Tile::A_BYTES;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        if (RAG == kRagK && kk >= steps) break;
+                        const uint64_t a = A_MN ? smem_desc_mn_sw128(sa + kk * 2048) : smem_desc_k_sw128(sa + kk * 32);
+                        const uint64_t b = B_MN ? smem_desc_mn_sw128(sb + kk * 2048) : smem_desc_k_sw128(sb + kk * 32);
+                        const uint32_t acc = first && pr == 0 && kk == 0 ? 0u : 1u;
+                        if constexpr (PAIR) mma_f16_pair(d_tmem, a, b, idesc, acc);
+                        else mma_f16(d_tmem, a, b, idesc, acc);
+                    }
+                    if (p.withhold != kWithholdRelease) {
+                        if constexpr (PAIR) mma_commit_pair_mc(&empty[stage], 0x3);
+                        else mma_commit(&empty[stage]);
+                    }
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                }
+                if (ok && last) {
+                    if constexpr (PAIR) mma_commit_pair_mc(&tfull[gc & 1], 0x3);
+                    else mma_commit(&tfull[gc & 1]);
+                    ++gc;
+                }
+            }
+        }
+        if constexpr (PAIR) mma_commit_pair(drain);
+        else mma_commit(drain);
+        mbar_wait_bounded(drain, 0u, p.timeout_ns);
+    } else if (warp >= 2) {
+        // ---------------- epilogue ----------------
+        const int quarter = warp & 3, ew = warp - 2;
+        const int slab0 = (ew >> 2) * SLAB;
+        float *stg = staging + ew * (32 * 33);
+        const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
+        int gc = 0;
+        bool ok = true;
+        float alpha = 1.f;
+        if (EPI == kEpiRows && p.alpha != nullptr) alpha = *p.alpha;
+        for (int t = slot; ok && t < num_tiles; t += slots) {
+            const LmWork w = lm_work<Tile, RAG>(p, g_start, g_prefix, t);
+            float sum[CHUNKED ? SLAB : 1];
+            uint32_t taddr = 0;
+            auto wait_acc = [&]() {
+                if (!mbar_wait_bounded<PAIR>(&tfull[gc & 1], (uint32_t)(gc >> 1) & 1u, downstream_limit(p.timeout_ns))) {
+                    record_error(p.err, kSiteConsumerFull);
+                    ok = false;
+                }
+                ok = __all_sync(~0u, ok);
+                tc_fence_after();
+                taddr = lane_base + (uint32_t)((gc & 1) * BN + slab0);
+            };
+            auto release_acc = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (PAIR) mbar_arrive_cluster(cluster_addr(&tempty[gc & 1], 0));
+                    else mbar_arrive(&tempty[gc & 1]);
+                }
+                ++gc;
+            };
+            if constexpr (CHUNKED) {
+                // Each block of 64 of the contraction is summed in its own
+                // accumulator and added here in FP32 with rounding to nearest
+                // (the tensor core's own running sum truncates).
+#pragma unroll
+                for (int c = 0; c < SLAB; ++c) sum[c] = 0.f;
+                for (int kb = 0; ok && kb < w.nkb; ++kb) {
+                    wait_acc();
+                    if (!ok) break;
+#pragma unroll
+                    for (int c0 = 0; c0 < SLAB; c0 += 32) {
+                        if (slab0 + c0 < w.nvalid) {
+                            uint32_t r[32];
+                            tmem_ld_32cols_nowait(taddr + (uint32_t)c0, r);
+                            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) sum[c0 + i] += __uint_as_float(r[i]);
+                        }
+                    }
+                    release_acc();
+                }
+            } else if (w.nkb > 0) {
+                wait_acc();
+            }
+            if (!ok) break;
+
+            const int row0 = w.m0 + (int)rank * Tile::BM + quarter * 32;   // first row of this warp
+            const int row = row0 + lane;
+            // Per-row state of the loss epilogues.
+            float run_max = -INFINITY, run_sum = 0.f, row_lse = 0.f, row_g = 0.f;
+            int tgt = -1;
+            if constexpr (EPI == kEpiLse || EPI == kEpiDLogits) {
+                if (row < p.M) {
+                    const int64_t tv = p.target[row];
+                    if (tv >= 0 && tv < p.vocab) {
+                        const int64_t rel = tv - p.v0;
+                        tgt = rel >= 0 && rel < p.N ? (int)rel : -1;
+                        if constexpr (EPI == kEpiDLogits) {
+                            row_lse = p.lse[row];
+                            row_g = p.grad[row] * (p.gscale != nullptr ? *p.gscale : 1.f);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int c0 = 0; c0 < SLAB; c0 += 32) {
+                const int col = slab0 + c0;                 // column in the tile
+                if (col < w.nvalid) {
+                    float v[32];
+                    if constexpr (CHUNKED) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = sum[c0 + i];
+                    } else if (w.nkb > 0) {
+                        uint32_t r[32];
+                        tmem_ld_32cols_nowait(taddr + (uint32_t)c0, r);
+                        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                    }
+                    const int cnt = min(32, w.nvalid - col);
+                    const int n = w.n0 + col;               // column of D
+                    if constexpr (EPI == kEpiCols) {
+                        if (p.out == kOutF32)
+                            lm_store_cols(p, static_cast<float *>(p.C), row0, n, cnt, v, stg, lane);
+                        else if (p.out == kOutF16)
+                            lm_store_cols(p, static_cast<__half *>(p.C), row0, n, cnt, v, stg, lane);
+                        else
+                            lm_store_cols(p, static_cast<__nv_bfloat16 *>(p.C), row0, n, cnt, v, stg, lane);
+                    } else if constexpr (EPI == kEpiLse) {
+                        if (cnt < 32)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (i >= cnt) v[i] = -INFINITY;
+                        float bm = v[0];
+#pragma unroll
+                        for (int i = 1; i < 32; ++i) bm = fmaxf(bm, v[i]);
+                        const float nm = fmaxf(run_max, bm);
+                        const float ref = (nm == -INFINITY ? 0.f : nm) * kLog2E;
+                        float s = run_sum * exp2_approx(fmaf(run_max, kLog2E, -ref));
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) s += exp2_approx(fmaf(v[i], kLog2E, -ref));
+                        run_sum = s;
+                        run_max = nm;
+                        const int rel = tgt - n;
+                        if (rel >= 0 && rel < cnt) {
+                            float pick = v[0];
+#pragma unroll
+                            for (int i = 1; i < 32; ++i)
+                                if (i == rel) pick = v[i];
+                            p.picked[row] = pick;
+                        }
+                    } else {
+                        if constexpr (EPI == kEpiDLogits) {
+                            const int rel = tgt - n;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                float e = exp2_approx((v[i] - row_lse) * kLog2E);
+                                if (i == rel) e -= 1.f;
+                                v[i] = row_g == 0.f ? 0.f : e * row_g;
+                            }
+                        } else {
+                            if (p.acc_in != nullptr && row < p.M) {
+                                const float *a = p.acc_in + (int64_t)row * p.ld_acc + n;
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (i < cnt) v[i] += a[i];
+                            }
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] *= alpha;
+                        }
+                        const int64_t z = (int64_t)(RAG == kRagK ? w.g : w.s) * p.stride_c;
+                        if (p.out == kOutF32)
+                            lm_store_rows(p, static_cast<float *>(p.C) + z, row, row0, n, cnt, v, stg, lane);
+                        else if (p.out == kOutF16)
+                            lm_store_rows(p, static_cast<__half *>(p.C) + z, row, row0, n, cnt, v, stg, lane);
+                        else
+                            lm_store_rows(p, static_cast<__nv_bfloat16 *>(p.C) + z, row, row0, n, cnt, v, stg, lane);
+                    }
+                }
+            }
+            if constexpr (EPI == kEpiLse) {
+                if (row < p.M)
+                    p.part[(int64_t)((w.n0 / p.tile_n) * (BN / SLAB) + (ew >> 2)) * p.M + row] =
+                        make_float2(run_max, run_sum);
+            }
+            if (!CHUNKED && w.nkb > 0) release_acc();
+        }
+    }
+
+    // ---------------- teardown ----------------
+    tc_fence_before();
+    if constexpr (PAIR) cluster_sync();
+    else __syncthreads();
+    tc_fence_after();
+    if (warp == 0) {
+        if constexpr (PAIR) tmem_dealloc_pair(tmem_base, Tile::TMEM_COLS);
+        else tmem_dealloc(tmem_base, Tile::TMEM_COLS);
+    }
+}
+
+template <class Tile, bool A_MN, bool B_MN, int RAG, int EPI, bool CHUNKED>
+LmKernel lm_kernel_info() {
+    static_assert(RAG == kRagNone || Tile::FIXED + 8 * (kLmMaxGroups + 2) <= 227 * 1024, "room for the group tables");
+    LmKernel k;
+    k.fn = reinterpret_cast<const void *>(&lm_mma_kernel<Tile, A_MN, B_MN, RAG, EPI, CHUNKED>);
+    k.threads = Tile::THREADS;
+    k.smem = Tile::FIXED;
+    k.tile_m = Tile::TILE_M;
+    k.bn = Tile::BN;
+    k.gran = Tile::GRAN;
+    k.pair = Tile::PAIR ? 1 : 0;
+    k.box_a = Tile::BM;
+    k.box_b = Tile::B_ROWS;
+    k.slabs = Tile::BN / Tile::SLAB;
+    k.a_mn = A_MN ? 1 : 0;
+    k.b_mn = B_MN ? 1 : 0;
+    return k;
+}
+
+using LmBig = LmTile<256, 5, true>;      // 256 x 256 on an SM pair
+using LmMid = LmTile<128, 5, false>;     // 128 x 128
+using LmWide = LmTile<256, 4, false>;    // 128 x 256, for few rows against a long matrix
+using LmThin = LmTile<32, 8, false>;     // 128 x 32, for few tokens
+
+}  // namespace sg

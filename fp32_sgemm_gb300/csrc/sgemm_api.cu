@@ -19,12 +19,13 @@
 #include <mutex>
 
 #include "../../include/sgemm_gb300.h"
+#include "context.h"
 #include "kernel_table.h"
 
 namespace {
 
 constexpr int kVersion = 1 * 10000 + 0 * 100 + 0;
-constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
+using sg::kDefaultTimeoutNs;
 constexpr uint64_t kMinTimeoutNs = 1000000ull;
 // Device control block: error word and stream-K sequence in the first 256
 // bytes, then one flag word per CTA and warp of a stream-K launch (up to
@@ -74,32 +75,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 }  // namespace
 
-struct sgemmContext {
-    int device = -1;
-    int sm_count = 0;
-    // Device control block (allocated with the handle): word 0 the error
-    // word, words 1-2 the stream-K launch sequence {tag, CTAs finished},
-    // from word kCtlFlagsOffset the stream-K flags (kCtlFlagWords words: one
-    // per CTA and warp of a launch).
-    uint32_t *d_err = nullptr;
-    uint32_t *d_flags = nullptr;
-    uint32_t *d_sk_seq = nullptr;
-    int flag_words = 0;
-    void *ws = nullptr;
-    size_t ws_bytes = 0;
-    uint64_t timeout_ns = kDefaultTimeoutNs;
-    int algo = 0;
-    int schedule = 0;   // 0 automatic, 1 whole tiles only, 2 stream-K whenever it applies
-    int math = 0;       // 0 FP32 FFMA, 1 error-compensated 3xTF32 on the tensor cores
-    int withhold = 0;   // test hook: signal the kernels leave out (sg::Withhold)
-    cudaEvent_t ev_start = nullptr, ev_stop = nullptr;   // around the main kernel, if set
-    // sgemmHostEx pipeline: copy-in and copy-out streams and their events,
-    // created with the handle.
-    static constexpr int kHostChunks = 8;     // pieces of one sgemmHostEx call (at most 7)
-    cudaStream_t s_in = nullptr, s_out = nullptr;
-    cudaEvent_t ev_begin = nullptr, ev_end = nullptr;
-    cudaEvent_t ev_in[kHostChunks] = {}, ev_done[kHostChunks] = {};
-};
+PFN_cuTensorMapEncodeTiled_v12000 sg::tensor_map_encoder() { return encode_fn(); }
+
 
 namespace {
 
