@@ -16,7 +16,8 @@ _BINDING_NAMES = {
 }
 
 _LM_NAMES = {
-    "grouped_gemm", "grouped_gemm_weight_grad",
+    "grouped_gemm", "grouped_gemm_weight_grad", "linear_cross_entropy", "linear_cross_entropy_grad",
+    "w4_gemm",
 }
 
 

@@ -94,6 +94,18 @@ SIGNATURES = {
                                      _vp, _i64, _i64, _vp]),
     "sgemmGroupedWeightGradWorkspaceSize": (_st, [_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, _i64,
                                                   _vp, _i64, ctypes.POINTER(ctypes.c_size_t)]),
+    "sgemmCrossEntropy": (_st, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                                _vp]),
+    "sgemmCrossEntropyWorkspaceSize": (_st, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64,
+                                             ctypes.POINTER(ctypes.c_size_t)]),
+    "sgemmCrossEntropyGrad": (_st, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp,
+                                    _vp, _vp, _i64, _vp, _i64, _vp]),
+    "sgemmCrossEntropyGradWorkspaceSize": (_st, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64,
+                                                 ctypes.POINTER(ctypes.c_size_t)]),
+    "sgemmW4": (_st, [_vp, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _vp, _i64, _vp, _i64, _vp, _i64,
+                      _vp, _i64, _vp, _i64, _vp]),
+    "sgemmW4WorkspaceSize": (_st, [_vp, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int,
+                                   ctypes.POINTER(ctypes.c_size_t)]),
 }
 
 _lock = threading.Lock()

@@ -155,3 +155,107 @@ def grouped_gemm_weight_grad(x, dy, group_ends, *, trans_w: bool = False, out=No
     _check(h._lib.sgemmGroupedWeightGrad(h.ptr, ty, T, M, N, G, ap, lda, bp, ldb, ends, cp, ldc, sc,
                                          _stream_ptr(stream, dev.index)), "sgemmGroupedWeightGrad")
     return out
+
+
+def _vector(t, name, dtype, device, n):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
+        raise TypeError(f"{name} must be a {dtype} tensor")
+    if not t.is_cuda or t.device != device or tuple(t.shape) != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {n} on {device}")
+    return t.data_ptr()
+
+
+def _loss_operands(x, w, target):
+    torch = _torch()
+    ty = _type_of(x, "x")
+    dev = _device(x, "x")
+    xp, ldx = _mat(x, "x", x.dtype, dev)
+    wp, ldw = _mat(w, "w", x.dtype, dev)
+    T, D = x.shape
+    V = w.shape[0]
+    if w.shape[1] != D:
+        raise ValueError(f"x has {D} columns, w {w.shape[1]}")
+    return ty, dev, T, V, D, xp, ldx, wp, ldw, _vector(target, "target", torch.int64, dev, T)
+
+
+def linear_cross_entropy(x, w, target, *, handle=None, stream=None):
+    """Cross entropy of the logits x @ w.T, which are never kept.
+
+    x [T, D], w [V, D], target [T] int64 (outside [0, V): not counted, loss
+    0); returns (loss, lse), float32 [T]: lse[t] = log sum_v exp(x_t . w_v),
+    loss[t] = lse[t] - x_t . w_target.
+    """
+    torch = _torch()
+    ty, dev, T, V, D, xp, ldx, wp, ldw, tp = _loss_operands(x, w, target)
+    loss, lse = (torch.empty(T, dtype=torch.float32, device=dev) for _ in range(2))
+    h = handle or default_handle(dev)
+    if T:
+        key = ("xent", ty, T, V, D, xp & 15, ldx, wp & 15, ldw)
+        _workspace(h, key, lambda n: _check(h._lib.sgemmCrossEntropyWorkspaceSize(
+            h.ptr, ty, T, V, D, xp, ldx, wp, ldw, n), "sgemmCrossEntropyWorkspaceSize"))
+    _check(h._lib.sgemmCrossEntropy(h.ptr, ty, T, V, D, xp, ldx, wp, ldw, tp, loss.data_ptr(), lse.data_ptr(),
+                                    _stream_ptr(stream, dev.index)), "sgemmCrossEntropy")
+    return loss, lse
+
+
+def linear_cross_entropy_grad(x, w, target, lse, dloss, *, handle=None, stream=None):
+    """Gradients (dx, dw) of linear_cross_entropy() for the gradient dloss
+    [T] (float32) by each token's loss; lse from the forward call."""
+    torch = _torch()
+    ty, dev, T, V, D, xp, ldx, wp, ldw, tp = _loss_operands(x, w, target)
+    lp = _vector(lse, "lse", torch.float32, dev, T)
+    gp = _vector(dloss, "dloss", torch.float32, dev, T)
+    dx = torch.empty((T, D), dtype=x.dtype, device=dev)
+    dw = torch.empty((V, D), dtype=x.dtype, device=dev)
+    h = handle or default_handle(dev)
+    if T:
+        key = ("xent_grad", ty, T, V, D, xp & 15, ldx, wp & 15, ldw)
+        _workspace(h, key, lambda n: _check(h._lib.sgemmCrossEntropyGradWorkspaceSize(
+            h.ptr, ty, T, V, D, xp, ldx, wp, ldw, n), "sgemmCrossEntropyGradWorkspaceSize"))
+    _check(h._lib.sgemmCrossEntropyGrad(h.ptr, ty, T, V, D, xp, ldx, wp, ldw, tp, lp, gp, dx.data_ptr(),
+                                        max(D, 1), dw.data_ptr(), max(D, 1),
+                                        _stream_ptr(stream, dev.index)), "sgemmCrossEntropyGrad")
+    return dx, dw
+
+
+def w4_gemm(x, q, scales, zeros=None, *, out=None, handle=None, stream=None):
+    """y = x @ W.T for 4-bit weights with group scales; returns y [M, N].
+
+    x [M, K] (a few rows); q [N, K // 2] uint8, column 2 i of W in the low
+    four bits of byte i, column 2 i + 1 in the high four; scales [N, groups]
+    of x's type and zeros [N, groups] uint8 or None (8 everywhere), groups of
+    K // groups = 32, 64 or 128 columns:
+    W[n, k] = scales[n, k // group] * (q[n, k] - zeros[n, k // group]).
+    """
+    torch = _torch()
+    ty = _type_of(x, "x")
+    dev = _device(x, "x")
+    xp, ldx = _mat(x, "x", x.dtype, dev)
+    M, K = x.shape
+    if not isinstance(q, torch.Tensor) or q.dim() != 2:
+        raise ValueError("q must be a 2-D tensor")
+    N = q.shape[0]
+    qp, ldq = _mat(q, "q", torch.uint8, dev, (N, K // 2))
+    sp, lds = _mat(scales, "scales", x.dtype, dev)
+    groups = scales.shape[1]
+    if scales.shape[0] != N:
+        raise ValueError(f"scales has {scales.shape[0]} rows, q {N}")
+    if K == 0 or groups == 0 or K % groups:
+        if K or groups:
+            raise ValueError(f"{groups} groups do not divide {K} columns")
+        group = 32
+    else:
+        group = K // groups
+    zp, ldz = (None, 0) if zeros is None else _mat(zeros, "zeros", torch.uint8, dev, (N, groups))
+    if out is None:
+        out = torch.empty((M, N), dtype=x.dtype, device=dev)
+    yp, ldy = _mat(out, "out", x.dtype, dev, (M, N))
+    h = handle or default_handle(dev)
+    if M and N and K:
+        key = ("w4", ty, M, N, K, group)
+        _workspace(h, key, lambda n: _check(h._lib.sgemmW4WorkspaceSize(h.ptr, ty, M, N, K, group, n),
+                                            "sgemmW4WorkspaceSize"))
+    _check(h._lib.sgemmW4(h.ptr, ty, M, N, K, group, xp, ldx, qp, ldq, sp, lds, zp, ldz, yp, ldy,
+                          _stream_ptr(stream, dev.index)), "sgemmW4")
+    return out

@@ -9,6 +9,7 @@
 #include "../../include/sgemm_gb300_lm.h"
 #include "context.h"
 #include "lm_kernels.h"
+#include "lm_w4.h"
 
 namespace {
 
@@ -17,6 +18,7 @@ using sg::LmKernel;
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxBytes = int64_t(1) << 40;
+constexpr int kMaxSmem = 227 * 1024;    // dynamic shared memory per CTA
 
 inline int64_t ceil_div(int64_t x, int64_t a) { return (x + a - 1) / a; }
 inline int64_t round_up(int64_t x, int64_t a) { return ceil_div(x, a) * a; }
@@ -103,16 +105,18 @@ sgemmStatus_t check_device(const sgemmContext *h) {
 }
 
 // CTAs (or SM pairs) of a kernel that are resident at once on the device,
-// asked for once per kernel and device after its shared-memory opt-in.
+// asked for once per kernel, device and size after its shared-memory opt-in.
 int resident_slots(const sgemmContext *h, const LmKernel &k, int smem) {
-    struct Known { const void *fn; int device, slots; };
-    static Known known[64];
+    struct Known { const void *fn; int device, smem, slots; };
+    static Known known[256];
     static int count = 0;
     static std::mutex mutex;
     std::lock_guard<std::mutex> lock(mutex);
     for (int i = 0; i < count; ++i)
-        if (known[i].fn == k.fn && known[i].device == h->device) return known[i].slots;
-    if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return -1;
+        if (known[i].fn == k.fn && known[i].device == h->device && known[i].smem == smem) return known[i].slots;
+    // The opt-in is for the most any launch may ask for, so that one launch
+    // never lowers it under another.
+    if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess) return -1;
     int n = 0;
     if (k.pair) {
         cudaLaunchConfig_t cfg{};
@@ -132,7 +136,7 @@ int resident_slots(const sgemmContext *h, const LmKernel &k, int smem) {
         n *= h->sm_count;
     }
     if (n < 1) return -1;
-    if (count < 64) known[count++] = Known{k.fn, h->device, n};
+    if (count < 256) known[count++] = Known{k.fn, h->device, smem, n};
     return n;
 }
 
@@ -235,6 +239,156 @@ sgemmStatus_t plan_weight_grad(int type, int64_t T, int64_t M, int64_t N, int64_
         q.a.plan();
         q.b.plan();
     }
+    return SGEMM_STATUS_SUCCESS;
+}
+
+// ---------------------------------------------------- vocabulary loss
+
+// Bytes of one piece of the logits' gradient: the piece is as many
+// vocabulary columns as fit, so that the gradient products are long.
+constexpr int64_t kPieceBytes = int64_t(512) << 20;
+constexpr int64_t kMinPieceCols = 2048;
+
+struct Loss {
+    int type = 0;
+    int64_t T = 0, V = 0, D = 0;
+    Operand x, w;
+    bool big = false;
+    // Forward.
+    int tile_n = 0, tiles_n = 0, slabs = 0;
+    size_t ws_part = 0, ws_picked = 0;
+    // Gradient.
+    int64_t piece = 0, pieces = 0, ld_d = 0, ld_acc = 0;
+    int splits = 1;
+    size_t ws_d = 0, ws_planes = 0, ws_acc = 0;
+    size_t forward_bytes() const { return x.ws + w.ws + ws_part + ws_picked; }
+    size_t grad_bytes() const { return x.ws + w.ws + ws_d + ws_planes + ws_acc + 256; }
+};
+
+// Columns per tile of a rows x cols product on `slots` CTAs or pairs: the
+// width with the least waves x (width + what a tile costs beside its MMAs).
+int balanced_tile_n(int64_t tiles_m, int64_t cols, int64_t slots, int gran, int most) {
+    int best = most;
+    double best_cost = 0.0;
+    for (int n = most; n >= most / 2; n -= gran) {
+        const double cost = double(ceil_div(tiles_m * ceil_div(cols, n), slots)) * (n + 8.0);
+        if (n == most || cost < best_cost) { best_cost = cost; best = n; }
+    }
+    return best;
+}
+
+sgemmStatus_t plan_loss(int type, int64_t T, int64_t V, int64_t D, const void *X, int64_t ldx, const void *W,
+                        int64_t ldw, const sgemmContext *h, Loss &q) {
+    if (!type_ok(type) || T < 0 || V < 1 || D < 1) return SGEMM_STATUS_INVALID_VALUE;
+    if (T > kMaxDim - 512 || V > kMaxDim - 512 || D > kMaxDim - 512) return SGEMM_STATUS_NOT_SUPPORTED;
+    sgemmStatus_t st = check_matrix(X, T, D, ldx, type, T > 0);
+    if (st != SGEMM_STATUS_SUCCESS) return st;
+    st = check_matrix(W, V, D, ldw, type, T > 0);
+    if (st != SGEMM_STATUS_SUCCESS) return st;
+    // Tiles of the largest product, with the narrowest tiles.
+    if (ceil_div(T, 128) > kMaxDim / ceil_div(V, 128) || ceil_div(V, 128) > kMaxDim / ceil_div(D, 128) ||
+        ceil_div(T, 128) > kMaxDim / ceil_div(D, 128))
+        return SGEMM_STATUS_NOT_SUPPORTED;
+    q.type = type;
+    q.T = T; q.V = V; q.D = D;
+    q.x.ptr = X; q.x.rows = T; q.x.cols = D; q.x.ld = ldx; q.x.type = type;
+    q.w.ptr = W; q.w.rows = V; q.w.cols = D; q.w.ld = ldw; q.w.type = type;
+    if (T == 0 || h == nullptr) return SGEMM_STATUS_SUCCESS;
+    q.x.plan();
+    q.w.plan();
+    const bool f32 = type == SGEMM_TYPE_F32;
+    q.big = T > 128;
+    const int64_t slots = q.big ? h->sm_count / 2 : h->sm_count;
+    const int64_t tiles_m = ceil_div(T, q.big ? 256 : 128);
+    q.tile_n = balanced_tile_n(tiles_m, V, slots, q.big ? 32 : 16, 256);
+    q.tiles_n = int(ceil_div(V, q.tile_n));
+    q.slabs = q.tiles_n * 2;
+    q.ws_part = align256(int64_t(q.slabs) * T * 8);
+    q.ws_picked = align256(T * 4);
+    // Gradient: pieces of the vocabulary, each a multiple of 256 columns.
+    const int64_t elem = f32 ? 10 : 2;      // FP32: the piece itself and its three planes
+    q.piece = V;
+    if (T * V * elem > kPieceBytes) {
+        q.piece = std::max<int64_t>(kMinPieceCols, kPieceBytes / (elem * T) / 256 * 256);
+        q.piece = std::min(q.piece, V);
+    }
+    q.pieces = ceil_div(V, q.piece);
+    q.piece = std::min(V, round_up(ceil_div(V, q.pieces), 256));
+    q.pieces = ceil_div(V, q.piece);
+    q.ld_d = round_up(q.piece, 16);
+    q.ws_d = align256(T * q.ld_d * (f32 ? 4 : 2));
+    q.ws_planes = f32 ? align256(T * q.ld_d * 6) : 0;
+    // The rows' gradient: one piece, K split when its tiles are few; more
+    // pieces, summed in FP32 from one to the next.
+    q.ld_acc = round_up(D, 8);
+    const int64_t dx_tiles = tiles_m * ceil_div(D, 256);
+    if (q.pieces == 1) {
+        q.splits = int(std::max<int64_t>(1, std::min(slots / dx_tiles, ceil_div(V, 64) / 8)));
+        q.ws_acc = q.splits > 1 ? align256(q.splits * T * q.ld_acc * 4) : 0;
+    } else {
+        q.ws_acc = align256(T * q.ld_acc * 4);
+    }
+    return SGEMM_STATUS_SUCCESS;
+}
+
+sgemmStatus_t check_vector(const void *p, int align) {
+    if (p == nullptr) return SGEMM_STATUS_INVALID_VALUE;
+    return aligned(p, align) ? SGEMM_STATUS_SUCCESS : SGEMM_STATUS_MISALIGNED;
+}
+
+LmArgs loss_args(const Loss &q, const LmKernel &k, int64_t M, int64_t N, int64_t K, int tile_n) {
+    LmArgs p{};
+    p.M = int(M);
+    p.N = int(N);
+    p.T = int(M);
+    p.kb = int(ceil_div(K, 64));
+    p.tile_n = tile_n;
+    p.tiles_m = int(ceil_div(M, k.tile_m));
+    p.tiles_n = int(ceil_div(N, tile_n));
+    p.num_tiles = p.tiles_m * p.tiles_n;
+    p.splits = 1;
+    p.group_m = 8;
+    p.pairs = q.type == SGEMM_TYPE_F32 ? 6 : 1;
+    p.bf16 = q.type == SGEMM_TYPE_F16 ? 0 : 1;
+    return p;
+}
+
+// ------------------------------------------------------ 4-bit weights
+
+struct W4 {
+    int type = 0, planes = 1, group = 0;
+    int64_t M = 0, N = 0, K = 0;
+    int most = 0;                // rows of x per launch
+    int slices = 1, k_slice = 0;
+    size_t ws = 0;
+};
+
+// Shared memory for the staged x.
+constexpr int64_t kW4XBytes = 128 * 1024;
+
+int64_t w4_pitch(int64_t k) {
+    // 64 modulo 128 bytes: eight lanes of neighbouring tokens meet no bank twice.
+    return round_up(k * 2, 128) + 64;
+}
+
+sgemmStatus_t plan_w4(int type, int64_t M, int64_t N, int64_t K, int group, W4 &q) {
+    if (!type_ok(type) || M < 0 || N < 0 || K < 0) return SGEMM_STATUS_INVALID_VALUE;
+    if (group != 32 && group != 64 && group != 128) return SGEMM_STATUS_INVALID_VALUE;
+    if (K % group != 0) return SGEMM_STATUS_INVALID_VALUE;
+    if (M > kMaxDim - 512 || N > kMaxDim - 512 || K > kMaxDim - 512) return SGEMM_STATUS_NOT_SUPPORTED;
+    q.type = type;
+    q.planes = type == SGEMM_TYPE_F32 ? 3 : 1;
+    q.group = group;
+    q.M = M; q.N = N; q.K = K;
+    q.most = int(std::min<int64_t>(M, type == SGEMM_TYPE_F32 ? 10 : 32));
+    if (M == 0 || N == 0 || K == 0) return SGEMM_STATUS_SUCCESS;
+    // K is cut when x does not fit beside the ring.
+    const int64_t cols = int64_t(q.most) * q.planes;
+    int64_t slices = 1;
+    while (cols * w4_pitch(round_up(ceil_div(K, slices), 128)) > kW4XBytes && ceil_div(K, slices) > 128) ++slices;
+    q.k_slice = int(round_up(ceil_div(K, slices), 128));
+    q.slices = int(ceil_div(K, q.k_slice));
+    q.ws = q.slices > 1 ? align256(int64_t(q.slices) * q.most * round_up(N, 8) * 4) : 0;
     return SGEMM_STATUS_SUCCESS;
 }
 
@@ -378,6 +532,271 @@ sgemmStatus_t sgemmGroupedWeightGrad(sgemmHandle_t h, sgemmDataType_t type, int6
     CUtensorMap tm_a, tm_b;
     if (!q.a.map(&tm_a, 64) || !q.b.map(&tm_b, 64)) return SGEMM_STATUS_LAUNCH_FAILED;
     return launch_lm(h, k, true, tm_a, tm_b, p, tiles, stream);
+}
+
+sgemmStatus_t sgemmCrossEntropyWorkspaceSize(sgemmHandle_t h, sgemmDataType_t type, int64_t T, int64_t V, int64_t D,
+                                             const void *X, int64_t ldx, const void *W, int64_t ldw,
+                                             size_t *bytes) {
+    if (bytes == nullptr) return SGEMM_STATUS_INVALID_VALUE;
+    *bytes = 0;
+    Loss q;
+    sgemmStatus_t st = plan_loss(type, T, V, D, X, ldx, W, ldw, h, q);
+    if (st != SGEMM_STATUS_SUCCESS) return st;
+    if (h == nullptr) return SGEMM_STATUS_INVALID_VALUE;
+    *bytes = T > 0 ? q.forward_bytes() : 0;
+    return SGEMM_STATUS_SUCCESS;
+}
+
+sgemmStatus_t sgemmCrossEntropy(sgemmHandle_t h, sgemmDataType_t type, int64_t T, int64_t V, int64_t D,
+                                const void *X, int64_t ldx, const void *W, int64_t ldw, const int64_t *target,
+                                float *loss, float *lse, cudaStream_t stream) {
+    Loss q;
+    sgemmStatus_t st = plan_loss(type, T, V, D, X, ldx, W, ldw, h, q);
+    if (st != SGEMM_STATUS_SUCCESS) return st;
+    if (T == 0) return SGEMM_STATUS_SUCCESS;
+    if ((st = check_vector(target, 8)) != SGEMM_STATUS_SUCCESS || (st = check_vector(loss, 4)) != SGEMM_STATUS_SUCCESS ||
+        (st = check_vector(lse, 4)) != SGEMM_STATUS_SUCCESS)
+        return st;
+    if (h == nullptr) return SGEMM_STATUS_INVALID_VALUE;
+    st = check_device(h);
+    if (st != SGEMM_STATUS_SUCCESS) return st;
+    if (h->ws == nullptr || h->ws_bytes < q.forward_bytes()) return SGEMM_STATUS_WORKSPACE_REQUIRED;
+
+    const bool f32 = type == SGEMM_TYPE_F32;
+    const LmKernel k = sg::lm_lse_kernel(q.big, f32);
+    LmArgs p = loss_args(q, k, T, V, D, q.tile_n);
+    char *ws = static_cast<char *>(h->ws);
+    p.target = target;
+    p.vocab = V;
+    p.part = reinterpret_cast<float2 *>(ws);
+    p.picked = reinterpret_cast<float *>(ws + q.ws_part);
+    ws += q.ws_part + q.ws_picked;
+    if (!q.x.prepare(ws, stream) || !q.w.prepare(ws + q.x.ws, stream)) return SGEMM_STATUS_LAUNCH_FAILED;
+    CUtensorMap tm_x, tm_w;
+    if (!q.x.map(&tm_x, k.box_a) || !q.w.map(&tm_w, k.box_b)) return SGEMM_STATUS_LAUNCH_FAILED;
+    st = launch_lm(h, k, false, tm_x, tm_w, p, p.num_tiles, stream);
+    if (st != SGEMM_STATUS_SUCCESS) return st;
+    return sg::lm_launch_lse_join(p.part, q.slabs, int(T), p.picked, target, V, loss, lse, stream) == cudaSuccess
+               ? SGEMM_STATUS_SUCCESS : SGEMM_STATUS_LAUNCH_FAILED;
+}
+
+sgemmStatus_t sgemmCrossEntropyGradWorkspaceSize(sgemmHandle_t h, sgemmDataType_t type, int64_t T, int64_t V,
+                                                 int64_t D, const void *X, int64_t ldx, const void *W, int64_t ldw,
+                                                 size_t *bytes) {
+    if (bytes == nullptr) return SGEMM_STATUS_INVALID_VALUE;
+    *bytes = 0;
+    Loss q;
+    sgemmStatus_t st = plan_loss(type, T, V, D, X, ldx, W, ldw, h, q);
+    if (st != SGEMM_STATUS_SUCCESS) return st;
+    if (h == nullptr) return SGEMM_STATUS_INVALID_VALUE;
+    *bytes = T > 0 ? q.grad_bytes() : 0;
+    return SGEMM_STATUS_SUCCESS;
+}
+
+sgemmStatus_t sgemmCrossEntropyGrad(sgemmHandle_t h, sgemmDataType_t type, int64_t T, int64_t V, int64_t D,
+                                    const void *X, int64_t ldx, const void *W, int64_t ldw, const int64_t *target,
+                                    const float *lse, const float *dloss, void *dX, int64_t lddx, void *dW,
+                                    int64_t lddw, cudaStream_t stream) {
+    Loss q;
+    sgemmStatus_t st = plan_loss(type, T, V, D, X, ldx, W, ldw, h, q);
+    if (st != SGEMM_STATUS_SUCCESS) return st;
+    st = check_matrix(dX, T, D, lddx, type, T > 0);
+    if (st != SGEMM_STATUS_SUCCESS) return st;
+    st = check_matrix(dW, V, D, lddw, type, true);
+    if (st != SGEMM_STATUS_SUCCESS) return st;
+    const int elem = type_size(type);
+    if (T > 0 && ((st = check_vector(target, 8)) != SGEMM_STATUS_SUCCESS ||
+                  (st = check_vector(lse, 4)) != SGEMM_STATUS_SUCCESS ||
+                  (st = check_vector(dloss, 4)) != SGEMM_STATUS_SUCCESS))
+        return st;
+    if (h == nullptr) return SGEMM_STATUS_INVALID_VALUE;
+    st = check_device(h);
+    if (st != SGEMM_STATUS_SUCCESS) return st;
+    if (T == 0)
+        return sg::lm_launch_zero(dW, lddw, 0, elem, V, D, 1, stream) == cudaSuccess ? SGEMM_STATUS_SUCCESS
+                                                                                     : SGEMM_STATUS_LAUNCH_FAILED;
+    if (h->ws == nullptr || h->ws_bytes < q.grad_bytes()) return SGEMM_STATUS_WORKSPACE_REQUIRED;
+
+    const bool f32 = type == SGEMM_TYPE_F32, f16 = type == SGEMM_TYPE_F16;
+    char *ws = static_cast<char *>(h->ws);
+    float *scale2 = reinterpret_cast<float *>(ws);
+    void *d = ws + 256;
+    void *planes = ws + 256 + q.ws_d;
+    float *acc = reinterpret_cast<float *>(ws + 256 + q.ws_d + q.ws_planes);
+    ws += 256 + q.ws_d + q.ws_planes + q.ws_acc;
+    if (!q.x.prepare(ws, stream) || !q.w.prepare(ws + q.x.ws, stream)) return SGEMM_STATUS_LAUNCH_FAILED;
+    // F16 holds the logits' gradient times a power of two, taken out again
+    // by the gradient products: its smallest normal number, 2^-14, is above
+    // most softmax values over a long vocabulary times a mean's 1 / T.
+    if (f16 && sg::lm_launch_grad_scale(dloss, target, V, int(T), scale2, stream) != cudaSuccess)
+        return SGEMM_STATUS_LAUNCH_FAILED;
+
+    const LmKernel kd = sg::lm_dlogits_kernel(q.big, f32);
+    const LmKernel kx = sg::lm_rows_kernel(q.big, false, f32);
+    CUtensorMap tm_x, tm_w, tm_d, tm_x_mn, tm_w_mn, tm_d_mn;
+    if (!q.x.map(&tm_x, kd.box_a) || !q.x.map(&tm_x_mn, 64)) return SGEMM_STATUS_LAUNCH_FAILED;
+    for (int64_t i = 0; i < q.pieces; ++i) {
+        const int64_t v0 = i * q.piece, width = std::min(q.piece, q.V - v0);
+        const bool first = i == 0, last = i == q.pieces - 1;
+        // d = (softmax - one at the target) * dloss for this piece.
+        const int64_t slots = q.big ? h->sm_count / 2 : h->sm_count;
+        const int tn = balanced_tile_n(ceil_div(T, kd.tile_m), width, slots, kd.gran, 256);
+        LmArgs p = loss_args(q, kd, T, width, D, tn);
+        p.C = d;
+        p.ldc = q.ld_d;
+        p.out = out_type(type);
+        p.vec = 1;
+        p.target = target;
+        p.vocab = V;
+        p.v0 = v0;
+        p.lse = lse;
+        p.grad = dloss;
+        p.gscale = f16 ? scale2 : nullptr;
+        if (!q.w.map_rows(&tm_w, kd.box_b, v0, width)) return SGEMM_STATUS_LAUNCH_FAILED;
+        st = launch_lm(h, kd, false, tm_x, tm_w, p, p.num_tiles, stream);
+        if (st != SGEMM_STATUS_SUCCESS) return st;
+
+        Operand dd;
+        dd.ptr = d;
+        dd.rows = T;
+        dd.cols = width;
+        dd.ld = q.ld_d;
+        dd.type = type;
+        dd.plan();
+        if (!dd.prepare(planes, stream)) return SGEMM_STATUS_LAUNCH_FAILED;
+        if (!dd.map(&tm_d, kx.box_a) || !dd.map(&tm_d_mn, 64) || !q.w.map_rows(&tm_w_mn, 64, v0, width))
+            return SGEMM_STATUS_LAUNCH_FAILED;
+
+        // Rows' gradient: d . W over this piece of the vocabulary.
+        p = loss_args(q, kx, T, D, width, 256);
+        p.splits = q.splits;
+        p.num_tiles *= q.splits;
+        if (q.splits > 1 || !last) {
+            p.C = acc;
+            p.ldc = q.ld_acc;
+            p.stride_c = q.splits > 1 ? T * q.ld_acc : 0;
+            p.out = sg::kOutF32;
+            p.vec = 1;
+        } else {
+            p.C = dX;
+            p.ldc = lddx;
+            p.out = out_type(type);
+            p.vec = vec_ok(dX, lddx, 0, elem, 32);
+            p.alpha = f16 ? scale2 + 1 : nullptr;
+        }
+        p.acc_in = first ? nullptr : acc;
+        p.ld_acc = q.ld_acc;
+        st = launch_lm(h, kx, false, tm_d, tm_w_mn, p, p.num_tiles, stream);
+        if (st != SGEMM_STATUS_SUCCESS) return st;
+        if (q.splits > 1 &&
+            sg::lm_launch_join_splits(acc, q.ld_acc, T * q.ld_acc, q.splits, f16 ? scale2 + 1 : nullptr, int(T),
+                                      int(D), dX, lddx, out_type(type), stream) != cudaSuccess)
+            return SGEMM_STATUS_LAUNCH_FAILED;
+
+        // Vocabulary rows' gradient: d^T . X, complete for this piece.
+        const LmKernel kw = sg::lm_rows_kernel(width > 128, true, f32);
+        p = loss_args(q, kw, width, D, T, 256);
+        p.C = static_cast<char *>(dW) + v0 * lddw * elem;
+        p.ldc = lddw;
+        p.out = out_type(type);
+        p.vec = vec_ok(p.C, lddw, 0, elem, 32);
+        p.alpha = f16 ? scale2 + 1 : nullptr;
+        st = launch_lm(h, kw, false, tm_d_mn, tm_x_mn, p, p.num_tiles, stream);
+        if (st != SGEMM_STATUS_SUCCESS) return st;
+    }
+    return SGEMM_STATUS_SUCCESS;
+}
+
+sgemmStatus_t sgemmW4WorkspaceSize(sgemmHandle_t h, sgemmDataType_t type, int64_t M, int64_t N, int64_t K, int group,
+                                   size_t *bytes) {
+    if (bytes == nullptr) return SGEMM_STATUS_INVALID_VALUE;
+    *bytes = 0;
+    W4 q;
+    sgemmStatus_t st = plan_w4(type, M, N, K, group, q);
+    if (st != SGEMM_STATUS_SUCCESS) return st;
+    if (h == nullptr) return SGEMM_STATUS_INVALID_VALUE;
+    *bytes = q.ws;
+    return SGEMM_STATUS_SUCCESS;
+}
+
+sgemmStatus_t sgemmW4(sgemmHandle_t h, sgemmDataType_t type, int64_t M, int64_t N, int64_t K, int group,
+                      const void *X, int64_t ldx, const uint8_t *Q, int64_t ldq, const void *scales, int64_t lds,
+                      const uint8_t *zeros, int64_t ldz, void *Y, int64_t ldy, cudaStream_t stream) {
+    W4 q;
+    sgemmStatus_t st = plan_w4(type, M, N, K, group, q);
+    if (st != SGEMM_STATUS_SUCCESS) return st;
+    const bool any = M > 0 && N > 0, used = any && K > 0;
+    const int64_t groups = K / group;
+    if ((st = check_matrix(X, M, K, ldx, type, used)) != SGEMM_STATUS_SUCCESS ||
+        (st = check_matrix(scales, N, groups, lds, type, used)) != SGEMM_STATUS_SUCCESS ||
+        (st = check_matrix(Y, M, N, ldy, type, any)) != SGEMM_STATUS_SUCCESS)
+        return st;
+    if (ldq < std::max<int64_t>(1, K / 2) || (zeros != nullptr && ldz < std::max<int64_t>(1, groups)))
+        return SGEMM_STATUS_INVALID_VALUE;
+    if (used) {
+        if (Q == nullptr) return SGEMM_STATUS_INVALID_VALUE;
+        if (!aligned(Q, 16) || (N > 1 && ldq % 16 != 0)) return SGEMM_STATUS_MISALIGNED;
+        if (ldq > kMaxBytes / N || (zeros != nullptr && ldz > kMaxBytes / N)) return SGEMM_STATUS_NOT_SUPPORTED;
+    }
+    if (!any) return SGEMM_STATUS_SUCCESS;
+    if (h == nullptr) return SGEMM_STATUS_INVALID_VALUE;
+    st = check_device(h);
+    if (st != SGEMM_STATUS_SUCCESS) return st;
+    const int elem = type_size(type);
+    if (K == 0)
+        return sg::lm_launch_zero(Y, ldy, 0, elem, M, N, 1, stream) == cudaSuccess ? SGEMM_STATUS_SUCCESS
+                                                                                   : SGEMM_STATUS_LAUNCH_FAILED;
+    if (q.ws > 0 && (h->ws == nullptr || h->ws_bytes < q.ws)) return SGEMM_STATUS_WORKSPACE_REQUIRED;
+
+    for (int64_t t0 = 0; t0 < M; t0 += q.most) {
+        const int tokens = int(std::min<int64_t>(q.most, M - t0));
+        const int cols = tokens * q.planes, nb = cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
+        sg::W4Args p{};
+        p.N = int(N);
+        p.K = int(K);
+        p.tokens = tokens;
+        p.k_slice = q.k_slice;
+        p.X = static_cast<const char *>(X) + t0 * ldx * elem;
+        p.ldx = ldx;
+        p.x_vec = vec_ok(p.X, ldx, 0, elem, 16);
+        p.x_pitch = int(w4_pitch(q.k_slice));
+        p.Q = Q;
+        p.ldq = ldq;
+        p.scales = scales;
+        p.lds = lds;
+        p.zeros = zeros;
+        p.ldz = ldz;
+        p.Y = static_cast<char *>(Y) + t0 * ldy * elem;
+        p.ldy = ldy;
+        p.part = q.slices > 1 ? static_cast<float *>(h->ws) : nullptr;
+        p.ld_part = round_up(N, 8);
+        LmKernel k;
+        k.fn = type == SGEMM_TYPE_F32 ? sg::w4_kernel_f32(group, nb)
+               : type == SGEMM_TYPE_F16 ? sg::w4_kernel_f16(group, nb) : sg::w4_kernel_bf16(group, nb);
+        k.threads = sg::kW4Threads;
+        const int smem = int(sg::w4_fixed_smem(nb)) + cols * p.x_pitch;
+        const int slots = resident_slots(h, k, smem);
+        if (slots < 1) return SGEMM_STATUS_LAUNCH_FAILED;
+        const int64_t blocks = ceil_div(N, 16);
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(unsigned(std::max<int64_t>(1, std::min<int64_t>(blocks, slots / q.slices))),
+                           unsigned(q.slices));
+        cfg.blockDim = dim3(sg::kW4Threads);
+        cfg.dynamicSmemBytes = size_t(smem);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        void *kargs[] = {&p};
+        if (cudaLaunchKernelExC(&cfg, k.fn, kargs) != cudaSuccess) return SGEMM_STATUS_LAUNCH_FAILED;
+        if (q.slices > 1 &&
+            sg::lm_launch_join_splits(p.part, p.ld_part, int64_t(tokens) * p.ld_part, q.slices, nullptr, tokens, int(N),
+                                      p.Y, ldy, out_type(type), stream) != cudaSuccess)
+            return SGEMM_STATUS_LAUNCH_FAILED;
+    }
+    return SGEMM_STATUS_SUCCESS;
 }
 
 }  // extern "C"

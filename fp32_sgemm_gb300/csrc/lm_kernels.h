@@ -59,9 +59,9 @@ struct LmKernel {
 // Kernel tables.  size: 0 thin, 1 middle, 2 big (SM pair).
 LmKernel lm_grouped_kernel(int size, bool w_mn, bool f32);      // lm_grouped*.cu
 LmKernel lm_weight_grad_kernel(int size, bool f32);             // size 1 or 2
-LmKernel lm_lse_kernel(bool big);                               // lm_loss.cu
-LmKernel lm_dlogits_kernel(bool big);
-LmKernel lm_rows_kernel(bool big, bool a_mn);                   // B MN-major
+LmKernel lm_lse_kernel(bool big, bool f32);                     // lm_loss*.cu
+LmKernel lm_dlogits_kernel(bool big, bool f32);
+LmKernel lm_rows_kernel(bool big, bool a_mn, bool f32);         // B MN-major
 
 // lm_aux.cu.  Operand copies TMA can address: rows x cols (x batch) with
 // pitch ld -> pitch ld_dst (a multiple of 8), 16-bit copied as they are,

@@ -1,17 +1,24 @@
-// Products of the vocabulary cross entropy (see lm_mma.cuh): the logits of a
-// tile live in tensor memory only.
+// Products of the vocabulary cross entropy for 16-bit operands (see
+// lm_mma.cuh): the logits of a tile live in tensor memory only.
 #include "lm_mma.cuh"
 
 namespace sg {
-LmKernel lm_lse_kernel(bool big) {
+LmKernel lm_lse_kernel32(bool big);
+LmKernel lm_dlogits_kernel32(bool big);
+LmKernel lm_rows_kernel32(bool big, bool a_mn);
+
+LmKernel lm_lse_kernel(bool big, bool f32) {
+    if (f32) return lm_lse_kernel32(big);
     if (big) return lm_kernel_info<LmBig, false, false, kRagNone, kEpiLse, false>();
     return lm_kernel_info<LmWide, false, false, kRagNone, kEpiLse, false>();
 }
-LmKernel lm_dlogits_kernel(bool big) {
+LmKernel lm_dlogits_kernel(bool big, bool f32) {
+    if (f32) return lm_dlogits_kernel32(big);
     if (big) return lm_kernel_info<LmBig, false, false, kRagNone, kEpiDLogits, false>();
     return lm_kernel_info<LmWide, false, false, kRagNone, kEpiDLogits, false>();
 }
-LmKernel lm_rows_kernel(bool big, bool a_mn) {
+LmKernel lm_rows_kernel(bool big, bool a_mn, bool f32) {
+    if (f32) return lm_rows_kernel32(big, a_mn);
     if (a_mn) {
         if (big) return lm_kernel_info<LmBig, true, true, kRagNone, kEpiRows, false>();
         return lm_kernel_info<LmWide, true, true, kRagNone, kEpiRows, false>();

@@ -103,6 +103,13 @@ __device__ __forceinline__ float exp2_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// The same without flushing results below 2^-126 (gradients of improbable
+// entries).
+__device__ __forceinline__ float exp2_approx_subnormal(float x) {
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 template <class T> __device__ __forceinline__ T lm_cvt(float x);
 template <> __device__ __forceinline__ float lm_cvt<float>(float x) { return x; }
@@ -690,7 +697,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                             const int rel = tgt - n;
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
-                                float e = exp2_approx((v[i] - row_lse) * kLog2E);
+                                float e = exp2_approx_subnormal((v[i] - row_lse) * kLog2E);
                                 if (i == rel) e -= 1.f;
                                 v[i] = row_g == 0.f ? 0.f : e * row_g;
                             }

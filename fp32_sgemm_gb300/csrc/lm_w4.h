@@ -1,0 +1,35 @@
+// What the host side of the 4-bit products and their kernel share.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+namespace sg {
+
+struct W4Args {
+    int N, K, tokens;          // rows of W, columns, rows of x in this launch
+    int k_slice;               // columns per blockIdx.y (a multiple of 128)
+    const void *X;
+    int64_t ldx;
+    int x_vec;                 // rows of x take 16-byte loads
+    int x_pitch;               // bytes of a staged row of x
+    const uint8_t *Q;
+    int64_t ldq;
+    const void *scales;
+    int64_t lds;
+    const uint8_t *zeros;
+    int64_t ldz;
+    void *Y;
+    int64_t ldy;
+    float *part;               // [slice][token][ld_part] FP32, or NULL for Y itself
+    int64_t ld_part;
+};
+
+const void *w4_kernel_f32(int group, int nb);
+const void *w4_kernel_f16(int group, int nb);
+const void *w4_kernel_bf16(int group, int nb);
+constexpr int kW4Threads = 256;
+// Shared memory beside the staged x.
+size_t w4_fixed_smem(int nb);
+
+}  // namespace sg

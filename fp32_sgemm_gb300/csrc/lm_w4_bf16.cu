@@ -1,0 +1,7 @@
+// 4-bit products, x of type bf16 (see lm_w4.cuh).
+#include "lm_w4.cuh"
+
+namespace sg {
+const void *w4_kernel_bf16(int group, int nb) { return w4_kernel_of<2>(group, nb); }
+
+}  // namespace sg

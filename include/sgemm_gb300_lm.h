@@ -100,6 +100,80 @@ sgemmStatus_t sgemmGroupedWeightGradWorkspaceSize(sgemmHandle_t handle, sgemmDat
                                                   int64_t N, int64_t G, const void *A, int64_t lda, const void *B,
                                                   int64_t ldb, size_t *bytes);
 
+/*
+ * Softmax cross entropy over a vocabulary.  X is T x D (one row per token),
+ * W is V x D (one row per vocabulary entry), target[t] a vocabulary index:
+ *
+ *   lse[t]  = log sum_v exp(X[t, :] . W[v, :])
+ *   loss[t] = lse[t] - X[t, :] . W[target[t], :]
+ *
+ * The T x V logits are never written to memory: each tile of them is
+ * reduced to a maximum and a sum of exponentials per row where it was
+ * computed, and the partial results are joined in a fixed order.  A target
+ * outside [0, V) marks a token that is not counted: its loss is 0 (its lse
+ * is computed).  loss and lse are FP32 in every type.  Arithmetic of the
+ * products as for sgemmGrouped().  INVALID_VALUE also for V < 1 or D < 1;
+ * T == 0 is a no-op.  A workspace is always required (the partial results).
+ */
+sgemmStatus_t sgemmCrossEntropy(sgemmHandle_t handle, sgemmDataType_t type, int64_t T, int64_t V, int64_t D,
+                                const void *X, int64_t ldx, const void *W, int64_t ldw, const int64_t *target,
+                                float *loss, float *lse, cudaStream_t stream);
+
+sgemmStatus_t sgemmCrossEntropyWorkspaceSize(sgemmHandle_t handle, sgemmDataType_t type, int64_t T, int64_t V,
+                                             int64_t D, const void *X, int64_t ldx, const void *W, int64_t ldw,
+                                             size_t *bytes);
+
+/*
+ * Its gradients, from the lse of sgemmCrossEntropy() and the gradient
+ * dloss[t] (FP32) by each token's loss:
+ *
+ *   d[t, v] = dloss[t] * (exp(X[t, :] . W[v, :] - lse[t]) - [v == target[t]])
+ *   dX = d . W        dW = d^T . X
+ *
+ * in pieces of the vocabulary: d is computed for one piece at a time (512 MB
+ * at most, or 2048 columns), in the type of the matrices (F16: times a power
+ * of two that keeps it in range; F32: FP32, then three bf16 planes), and
+ * both products over the piece follow; dX is summed over the pieces in FP32.
+ * Tokens that are not counted, and those with dloss 0, have no part in
+ * either gradient.  T == 0 sets dW to zero.
+ */
+sgemmStatus_t sgemmCrossEntropyGrad(sgemmHandle_t handle, sgemmDataType_t type, int64_t T, int64_t V, int64_t D,
+                                    const void *X, int64_t ldx, const void *W, int64_t ldw, const int64_t *target,
+                                    const float *lse, const float *dloss, void *dX, int64_t lddx, void *dW,
+                                    int64_t lddw, cudaStream_t stream);
+
+sgemmStatus_t sgemmCrossEntropyGradWorkspaceSize(sgemmHandle_t handle, sgemmDataType_t type, int64_t T, int64_t V,
+                                                 int64_t D, const void *X, int64_t ldx, const void *W, int64_t ldw,
+                                                 size_t *bytes);
+
+/*
+ * Products of a few rows with 4-bit weights and group scales.  X is M x K,
+ * the weights are N x K (one row per output column), two to a byte along K:
+ * Q is N rows of K / 2 bytes (pitch ldq BYTES), column 2 i in the low four
+ * bits of byte i, column 2 i + 1 in the high four.  Each row has a scale (of
+ * the call's type; pitch lds) and, if `zeros` is not NULL, a zero point (a
+ * byte, its low four bits; pitch ldz; otherwise 8) for every `group` columns:
+ *
+ *   Y[t, n] = sum_k scales[n, k / group] * (q[n, k] - zeros[n, k / group]) * X[t, k]
+ *
+ * group is 32, 64 or 128 and divides K.  q - zero meets X unrounded and
+ * unscaled, the scale is applied to each group's FP32 sum; F32 X is split
+ * into three bf16 planes (exactly).  One pass over the weights serves up to
+ * 32 rows (F32: 10); more rows take further passes.
+ *
+ * INVALID_VALUE, NOT_SUPPORTED as above, also for another group or a K it
+ * does not divide.  MISALIGNED also when Q is not 16-byte aligned or ldq not
+ * a multiple of 16 bytes.  WORKSPACE_REQUIRED when X is too long for shared
+ * memory and K is cut (the size query says).  M == 0 or N == 0 is a no-op;
+ * K == 0 sets Y to zero.
+ */
+sgemmStatus_t sgemmW4(sgemmHandle_t handle, sgemmDataType_t type, int64_t M, int64_t N, int64_t K, int group,
+                      const void *X, int64_t ldx, const uint8_t *Q, int64_t ldq, const void *scales, int64_t lds,
+                      const uint8_t *zeros, int64_t ldz, void *Y, int64_t ldy, cudaStream_t stream);
+
+sgemmStatus_t sgemmW4WorkspaceSize(sgemmHandle_t handle, sgemmDataType_t type, int64_t M, int64_t N, int64_t K,
+                                   int group, size_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif
