@@ -9,7 +9,7 @@ LmKernel lm_rows_kernel32(bool big, bool a_mn);
 
 LmKernel lm_lse_kernel(bool big, bool f32) {
     if (f32) return lm_lse_kernel32(big);
-    if (big) return lm_kernel_info<LmBig, false, false, kRagNone, kEpiLse, false>();
+    if (big) return lm_kernel_info<LmBigLse, false, false, kRagNone, kEpiLse, false>();
     return lm_kernel_info<LmWide, false, false, kRagNone, kEpiLse, false>();
 }
 LmKernel lm_dlogits_kernel(bool big, bool f32) {

@@ -4,7 +4,7 @@
 
 namespace sg {
 LmKernel lm_lse_kernel32(bool big) {
-    if (big) return lm_kernel_info<LmBig, false, false, kRagNone, kEpiLse, true>();
+    if (big) return lm_kernel_info<LmBigLse, false, false, kRagNone, kEpiLse, true>();
     return lm_kernel_info<LmWide, false, false, kRagNone, kEpiLse, true>();
 }
 LmKernel lm_dlogits_kernel32(bool big) {

@@ -74,6 +74,20 @@ __device__ __forceinline__ uint32_t idesc_f16(uint32_t bf16, bool a_mn, bool b_m
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// Arrive on an mbarrier of a CTA of the cluster, with nothing to publish.
+// (With release semantics the arrival waits for the thread's earlier writes:
+// once per stage, that halved the rate of the weight gradients.)
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_bar) : "memory");
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t is;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
+    return is != 0;
+}
+
 __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -128,7 +142,8 @@ template <> __device__ __forceinline__ uint32_t lm_pack2<__nv_bfloat16>(float a,
 // ----------------------------------------------------------------- tiles
 
 // One output tile: 128 rows of A per SM (256 on a pair) by up to BN columns.
-template <int BN_, int STAGES_, bool PAIR_>
+// STG: floats of epilogue staging per warp (0 where the epilogue needs none).
+template <int BN_, int STAGES_, bool PAIR_, int STG_ = 32 * 17>
 struct LmTile {
     static constexpr bool PAIR = PAIR_;
     static constexpr int BM = 128, BN = BN_, BK = 64, STAGES = STAGES_;
@@ -142,7 +157,7 @@ struct LmTile {
     static constexpr int TMEM_COLS = 2 * BN <= 64 ? 64 : 2 * BN <= 128 ? 128 : 2 * BN <= 256 ? 256 : 512;
     static constexpr int THREADS = (2 + EPI_WARPS) * 32;
     static constexpr int BARS = 2 * STAGES + 6;
-    static constexpr int STAGING = EPI_WARPS * 32 * 33 * 4;
+    static constexpr int STG = STG_, STAGING = EPI_WARPS * STG * 4;
     // Ring, barriers (8 bytes each), TMEM address (16), epilogue staging;
     // the group tables of kRagN / kRagK follow.
     static constexpr int FIXED = STAGES * STAGE_BYTES + ((BARS * 8 + 16 + 15) / 16) * 16 + STAGING + 1024;
@@ -300,15 +315,19 @@ __device__ __forceinline__ void lm_store_rows(const LmArgs &p, Out *base, int ro
         }
     } else {
         // Rows that vector stores cannot reach: turned in shared memory, so
-        // that a warp writes 32 neighbours of one row at a time.
-        __syncwarp();
+        // that half a warp writes 16 neighbours of one row at a time.
+        const int c = lane & 15, rr = lane >> 4;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) stg[lane * 33 + i] = v[i];
-        __syncwarp();
-        if (lane < cnt)
+        for (int h = 0; h < 32; h += 16) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) stg[lane * 17 + i] = v[h + i];
+            __syncwarp();
+            if (h + c < cnt)
 #pragma unroll 8
-            for (int r = 0; r < 32; ++r)
-                if (row0 + r < p.M) base[(int64_t)(row0 + r) * p.ldc + col + lane] = lm_cvt<Out>(stg[r * 33 + lane]);
+                for (int r = rr; r < 32; r += 2)
+                    if (row0 + r < p.M) base[(int64_t)(row0 + r) * p.ldc + col + h + c] = lm_cvt<Out>(stg[r * 17 + c]);
+        }
     }
 }
 
@@ -413,10 +432,11 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     const int num_tiles = RAG == kRagN ? (int)g_prefix[p.G + 1] : p.num_tiles;
 
     if (warp == 0) {
-        // ---------------- TMA producer (lane 0; the warp clears tails) ----------------
+        // ---------------- TMA producer (one elected lane issues) ----------------
         int stage = 0, issued = 0;
         uint32_t phase = 0, tail_phase = 0;
         bool ok = true;
+        const uint32_t full_pair = PAIR ? cluster_addr(&full[0], 0) : 0u;   // rank 0's barriers
         for (int t = slot; ok && t < num_tiles; t += slots) {
             const LmWork w = lm_work<Tile, RAG>(p, g_start, g_prefix, t);
             const int ma = w.m0 + (int)rank * Tile::BM;
@@ -426,34 +446,20 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 const bool tail = RAG == kRagK && kb == w.nkb - 1 && (w.klast & 15) != 0;
                 for (int pr = 0; pr < p.pairs; ++pr) {
                     if (p.withhold == kWithholdRefill && issued >= STAGES) { ok = false; break; }
-                    if (lane == 0 && !mbar_wait_bounded<PAIR>(&empty[stage], phase ^ 1u, p.timeout_ns)) {
-                        record_error(p.err, kSiteProducerEmpty);
+                    if (!mbar_wait_bounded<PAIR>(&empty[stage], phase ^ 1u, p.timeout_ns)) {
+                        if (lane == 0) record_error(p.err, kSiteProducerEmpty);
                         ok = false;
                     }
-                    ok = __shfl_sync(~0u, ok, 0);
+                    ok = __all_sync(~0u, ok);
                     if (!ok) break;
                     unsigned char *sa = smem + stage * Tile::STAGE_BYTES, *sb = sa + Tile::A_BYTES;
                     int ia, ib;
                     lm_planes(p.pairs, pr, ia, ib);
                     const int za = RAG == kRagN ? ia * p.G + w.g : ia;
-                    if (lane == 0) {
-                        uint32_t fb = 0;
-                        if constexpr (PAIR) {
-                            fb = cluster_addr(&full[stage], 0);
-                            if (!tail) {
-                                // Both SMs' copies complete on rank 0's barrier.
-                                if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * Tile::STAGE_BYTES);
-                                else if (RAG == kRagK) mbar_arrive_cluster(fb);
-                            }
-                        } else if (!tail) {
-                            mbar_arrive_expect_tx(&full[stage], Tile::STAGE_BYTES);
-                        }
-                        if (tail) mbar_arrive_expect_tx(tailbar, Tile::STAGE_BYTES);
-                        auto load = [&](void *dst, const CUtensorMap *m, int c0, int c1, int c2) {
-                            if (tail) tma_load_3d(dst, m, tailbar, c0, c1, c2);
-                            else if constexpr (PAIR) tma_load_3d_pair(dst, m, fb, c0, c1, c2);
-                            else tma_load_3d(dst, m, &full[stage], c0, c1, c2);
-                        };
+                    const uint32_t fb = full_pair + (uint32_t)stage * 8u;
+                    // Copies of this stage, completing on the ring's barrier
+                    // (rank 0's for a pair) or, for a tail, on a local one.
+                    auto load_all = [&](auto &&load) {
                         if constexpr (A_MN) {
                             load(sa, &tmA, ma, kc, za);
                             load(sa + 8192, &tmA, ma + 64, kc, za);
@@ -467,32 +473,52 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                         } else {
                             load(sb, &tmB, kc, nb, ib);
                         }
-                    }
-                    if constexpr (RAG == kRagK) {
-                        if (tail) {
-                            // The block's rows behind the group belong to
-                            // others: cleared up to the next multiple of 16,
-                            // where the MMAs stop (both operands, so that an
-                            // infinity there does not meet a zero).
-                            __syncwarp();
-                            if (!mbar_wait_bounded(tailbar, tail_phase, downstream_limit(p.timeout_ns))) {
-                                if (lane == 0) record_error(p.err, kSiteConsumerFull);
-                                ok = false;
+                    };
+                    if (!tail) {
+                        if (elect_one()) {
+                            if constexpr (PAIR) {
+                                if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * Tile::STAGE_BYTES);
+                                else if (RAG == kRagK) mbar_arrive_cluster_relaxed(fb);
+                                load_all([&](void *dst, const CUtensorMap *m, int c0, int c1, int c2) {
+                                    tma_load_3d_pair(dst, m, fb, c0, c1, c2);
+                                });
+                            } else {
+                                mbar_arrive_expect_tx(&full[stage], Tile::STAGE_BYTES);
+                                load_all([&](void *dst, const CUtensorMap *m, int c0, int c1, int c2) {
+                                    tma_load_3d(dst, m, &full[stage], c0, c1, c2);
+                                });
                             }
-                            ok = __all_sync(~0u, ok);
-                            tail_phase ^= 1u;
-                            const int r0 = w.klast, r1 = (w.klast + 15) & ~15;
-                            constexpr int CHUNKS = (Tile::A_BYTES + Tile::B_BYTES) / 8192;
-                            for (int i = lane; i < CHUNKS * (r1 - r0) * 8; i += 32) {
-                                const int c = i / ((r1 - r0) * 8), in = i - c * (r1 - r0) * 8;
-                                *reinterpret_cast<uint4 *>(sa + c * 8192 + r0 * 128 + in * 16) = make_uint4(0, 0, 0, 0);
-                            }
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0) {
-                                if (PAIR && rank != 0) mbar_arrive_cluster(cluster_addr(&full[stage], 0));
-                                else mbar_arrive(&full[stage]);
-                            }
+                        }
+                        __syncwarp();
+                    } else {
+                        // The block's rows behind the group belong to others:
+                        // cleared up to the next multiple of 16, where the
+                        // MMAs stop (both operands, so that an infinity there
+                        // does not meet a zero).
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(tailbar, Tile::STAGE_BYTES);
+                            load_all([&](void *dst, const CUtensorMap *m, int c0, int c1, int c2) {
+                                tma_load_3d(dst, m, tailbar, c0, c1, c2);
+                            });
+                        }
+                        __syncwarp();
+                        if (!mbar_wait_bounded(tailbar, tail_phase, downstream_limit(p.timeout_ns))) {
+                            if (lane == 0) record_error(p.err, kSiteConsumerFull);
+                            ok = false;
+                        }
+                        ok = __all_sync(~0u, ok);
+                        tail_phase ^= 1u;
+                        const int r0 = w.klast, r1 = (w.klast + 15) & ~15;
+                        constexpr int CHUNKS = (Tile::A_BYTES + Tile::B_BYTES) / 8192;
+                        for (int i = lane; i < CHUNKS * (r1 - r0) * 8; i += 32) {
+                            const int c = i / ((r1 - r0) * 8), in = i - c * (r1 - r0) * 8;
+                            *reinterpret_cast<uint4 *>(sa + c * 8192 + r0 * 128 + in * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (PAIR && rank != 0) mbar_arrive_cluster(fb);
+                            else mbar_arrive(&full[stage]);
                         }
                     }
                     ++issued;
@@ -500,7 +526,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 }
             }
         }
-        if (!ok && lane == 0) {
+        if (!ok) {
             // Let this CTA's own copies land before it can exit (rank 1 of
             // a pair sees them as the release of its stages).
             const int pending = issued < STAGES ? issued : STAGES;
@@ -511,8 +537,16 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 mbar_wait_bounded<PAIR>(rank == 0 ? &full[s] : &empty[s], ph, p.timeout_ns);
             }
         }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
         // ---------------- MMA issuer (rank 0 of a pair) ----------------
+        // The whole warp walks the loop and one elected lane issues: with
+        // the control flow uniform, descriptors stay in uniform registers,
+        // where the MMA takes them.  (Under a branch on the lane number the
+        // issue of a stage's four MMAs took longer than their execution.)
+        const uint64_t da0 = A_MN ? smem_desc_mn_sw128(smem_u32(smem)) : smem_desc_k_sw128(smem_u32(smem));
+        const uint64_t db0 = B_MN ? smem_desc_mn_sw128(smem_u32(smem) + Tile::A_BYTES)
+                                  : smem_desc_k_sw128(smem_u32(smem) + Tile::A_BYTES);
+        constexpr uint64_t KA = A_MN ? 2048 >> 4 : 32 >> 4, KB = B_MN ? 2048 >> 4 : 32 >> 4;   // per 16 of K
         int stage = 0, gc = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -525,52 +559,59 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 if (first) {
                     const int ab = gc & 1;
                     if (!mbar_wait_bounded<PAIR>(&tempty[ab], ((uint32_t)(gc >> 1) & 1u) ^ 1u, p.timeout_ns)) {
-                        record_error(p.err, kSiteConsumerFull);
+                        if (lane == 0) record_error(p.err, kSiteConsumerFull);
                         ok = false;
-                        break;
                     }
+                    ok = __all_sync(~0u, ok);
+                    if (!ok) break;
                     tc_fence_after();
                     d_tmem = tmem_base + (uint32_t)(ab * BN);
                 }
                 const int steps = RAG == kRagK && kb == w.nkb - 1 ? (w.klast + 15) >> 4 : 4;
                 for (int pr = 0; pr < p.pairs; ++pr) {
                     if (!mbar_wait_bounded<PAIR>(&full[stage], phase, downstream_limit(p.timeout_ns))) {
-                        record_error(p.err, kSiteConsumerFull);
+                        if (lane == 0) record_error(p.err, kSiteConsumerFull);
                         ok = false;
-                        break;
                     }
+                    ok = __all_sync(~0u, ok);
+                    if (!ok) break;
                     tc_fence_after();
-                    const uint32_t sa = smem_u32(smem + stage * Tile::STAGE_BYTES), sb = sa + Tile::A_BYTES;
+                    const uint64_t da = da0 + (uint64_t)(stage * (Tile::STAGE_BYTES >> 4));
+                    const uint64_t db = db0 + (uint64_t)(stage * (Tile::STAGE_BYTES >> 4));
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        if (RAG == kRagK && kk >= steps) break;
-                        const uint64_t a = A_MN ? smem_desc_mn_sw128(sa + kk * 2048) : smem_desc_k_sw128(sa + kk * 32);
-                        const uint64_t b = B_MN ? smem_desc_mn_sw128(sb + kk * 2048) : smem_desc_k_sw128(sb + kk * 32);
-                        const uint32_t acc = first && pr == 0 && kk == 0 ? 0u : 1u;
-                        if constexpr (PAIR) mma_f16_pair(d_tmem, a, b, idesc, acc);
-                        else mma_f16(d_tmem, a, b, idesc, acc);
+                        for (int kk = 0; kk < 4; ++kk) {
+                            if (RAG == kRagK && kk >= steps) break;
+                            const uint32_t acc = first && pr == 0 && kk == 0 ? 0u : 1u;
+                            if constexpr (PAIR) mma_f16_pair(d_tmem, da + kk * KA, db + kk * KB, idesc, acc);
+                            else mma_f16(d_tmem, da + kk * KA, db + kk * KB, idesc, acc);
+                        }
+                        if (p.withhold != kWithholdRelease) {
+                            if constexpr (PAIR) mma_commit_pair_mc(&empty[stage], 0x3);
+                            else mma_commit(&empty[stage]);
+                        }
+                        if (last && pr == p.pairs - 1) {
+                            if constexpr (PAIR) mma_commit_pair_mc(&tfull[gc & 1], 0x3);
+                            else mma_commit(&tfull[gc & 1]);
+                        }
                     }
-                    if (p.withhold != kWithholdRelease) {
-                        if constexpr (PAIR) mma_commit_pair_mc(&empty[stage], 0x3);
-                        else mma_commit(&empty[stage]);
-                    }
+                    __syncwarp();
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
-                if (ok && last) {
-                    if constexpr (PAIR) mma_commit_pair_mc(&tfull[gc & 1], 0x3);
-                    else mma_commit(&tfull[gc & 1]);
-                    ++gc;
-                }
+                if (last) ++gc;
             }
         }
-        if constexpr (PAIR) mma_commit_pair(drain);
-        else mma_commit(drain);
+        if (elect_one()) {
+            if constexpr (PAIR) mma_commit_pair(drain);
+            else mma_commit(drain);
+        }
+        __syncwarp();
         mbar_wait_bounded(drain, 0u, p.timeout_ns);
     } else if (warp >= 2) {
         // ---------------- epilogue ----------------
         const int quarter = warp & 3, ew = warp - 2;
         const int slab0 = (ew >> 2) * SLAB;
-        float *stg = staging + ew * (32 * 33);
+        float *stg = staging + ew * Tile::STG;
         const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
         int gc = 0;
         bool ok = true;
@@ -760,9 +801,10 @@ LmKernel lm_kernel_info() {
     return k;
 }
 
-using LmBig = LmTile<256, 5, true>;      // 256 x 256 on an SM pair
-using LmMid = LmTile<128, 5, false>;     // 128 x 128
+using LmBig = LmTile<256, 6, true>;      // 256 x 256 on an SM pair
+using LmBigLse = LmTile<256, 7, true, 0>;
+using LmMid = LmTile<128, 6, false>;     // 128 x 128
 using LmWide = LmTile<256, 4, false>;    // 128 x 256, for few rows against a long matrix
-using LmThin = LmTile<32, 8, false>;     // 128 x 32, for few tokens
+using LmThin = LmTile<32, 10, false>;    // 128 x 32, for few tokens
 
 }  // namespace sg
