@@ -107,13 +107,15 @@ sgemmStatus_t check_device(const sgemmContext *h) {
 // CTAs (or SM pairs) of a kernel that are resident at once on the device,
 // asked for once per kernel, device and size after its shared-memory opt-in.
 int resident_slots(const sgemmContext *h, const LmKernel &k, int smem) {
-    struct Known { const void *fn; int device, smem, slots; };
+    struct Known { const void *fn; int device, smem, threads, slots; };
     static Known known[256];
     static int count = 0;
     static std::mutex mutex;
     std::lock_guard<std::mutex> lock(mutex);
     for (int i = 0; i < count; ++i)
-        if (known[i].fn == k.fn && known[i].device == h->device && known[i].smem == smem) return known[i].slots;
+        if (known[i].fn == k.fn && known[i].device == h->device && known[i].smem == smem &&
+            known[i].threads == k.threads)
+            return known[i].slots;
     // The opt-in is for the most any launch may ask for, so that one launch
     // never lowers it under another.
     if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess) return -1;
@@ -136,7 +138,7 @@ int resident_slots(const sgemmContext *h, const LmKernel &k, int smem) {
         n *= h->sm_count;
     }
     if (n < 1) return -1;
-    if (count < 256) known[count++] = Known{k.fn, h->device, smem, n};
+    if (count < 256) known[count++] = Known{k.fn, h->device, smem, k.threads, n};
     return n;
 }
 
@@ -363,13 +365,14 @@ struct W4 {
     size_t ws = 0;
 };
 
-// Shared memory for the staged x.
-constexpr int64_t kW4XBytes = 128 * 1024;
-
 int64_t w4_pitch(int64_t k) {
     // 64 modulo 128 bytes: eight lanes of neighbouring tokens meet no bank twice.
     return round_up(k * 2, 128) + 64;
 }
+
+int w4_blocks(int64_t cols) { return cols <= 8 ? 1 : cols <= 16 ? 2 : 4; }
+// Warps of a CTA when it has an SM for itself.
+int w4_warps(int64_t cols) { return cols <= 16 ? 16 : 8; }
 
 sgemmStatus_t plan_w4(int type, int64_t M, int64_t N, int64_t K, int group, W4 &q) {
     if (!type_ok(type) || M < 0 || N < 0 || K < 0) return SGEMM_STATUS_INVALID_VALUE;
@@ -384,9 +387,10 @@ sgemmStatus_t plan_w4(int type, int64_t M, int64_t N, int64_t K, int group, W4 &
     if (M == 0 || N == 0 || K == 0) return SGEMM_STATUS_SUCCESS;
     // K is cut when x does not fit beside the ring.
     const int64_t cols = int64_t(q.most) * q.planes;
+    const int64_t room = kMaxSmem - int64_t(sg::w4_fixed_smem(w4_blocks(cols), w4_warps(cols)));
     int64_t slices = 1;
-    while (cols * w4_pitch(round_up(ceil_div(K, slices), 128)) > kW4XBytes && ceil_div(K, slices) > 128) ++slices;
-    q.k_slice = int(round_up(ceil_div(K, slices), 128));
+    while (cols * w4_pitch(round_up(ceil_div(K, slices), 256)) > room && ceil_div(K, slices) > 256) ++slices;
+    q.k_slice = int(round_up(ceil_div(K, slices), 256));
     q.slices = int(ceil_div(K, q.k_slice));
     q.ws = q.slices > 1 ? align256(int64_t(q.slices) * q.most * round_up(N, 8) * 4) : 0;
     return SGEMM_STATUS_SUCCESS;
@@ -750,7 +754,7 @@ sgemmStatus_t sgemmW4(sgemmHandle_t h, sgemmDataType_t type, int64_t M, int64_t 
 
     for (int64_t t0 = 0; t0 < M; t0 += q.most) {
         const int tokens = int(std::min<int64_t>(q.most, M - t0));
-        const int cols = tokens * q.planes, nb = cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
+        const int cols = tokens * q.planes, nb = w4_blocks(cols);
         sg::W4Args p{};
         p.N = int(N);
         p.K = int(K);
@@ -766,6 +770,8 @@ sgemmStatus_t sgemmW4(sgemmHandle_t h, sgemmDataType_t type, int64_t M, int64_t 
         p.lds = lds;
         p.zeros = zeros;
         p.ldz = ldz;
+        p.s_vec = vec_ok(scales, lds, 0, elem, 16);
+        p.z_vec = zeros == nullptr || vec_ok(zeros, ldz, 0, 1, 8);
         p.Y = static_cast<char *>(Y) + t0 * ldy * elem;
         p.ldy = ldy;
         p.part = q.slices > 1 ? static_cast<float *>(h->ws) : nullptr;
@@ -773,15 +779,21 @@ sgemmStatus_t sgemmW4(sgemmHandle_t h, sgemmDataType_t type, int64_t M, int64_t 
         LmKernel k;
         k.fn = type == SGEMM_TYPE_F32 ? sg::w4_kernel_f32(group, nb)
                : type == SGEMM_TYPE_F16 ? sg::w4_kernel_f16(group, nb) : sg::w4_kernel_bf16(group, nb);
-        k.threads = sg::kW4Threads;
-        const int smem = int(sg::w4_fixed_smem(nb)) + cols * p.x_pitch;
+        // Two CTAs of 8 warps on an SM where both fit, else one (of 16).
+        int warps = 8;
+        int smem = int(sg::w4_fixed_smem(nb, warps)) + cols * p.x_pitch;
+        if (smem > 113 * 1024) {
+            warps = w4_warps(cols);
+            smem = int(sg::w4_fixed_smem(nb, warps)) + cols * p.x_pitch;
+        }
+        k.threads = warps * 32;
         const int slots = resident_slots(h, k, smem);
         if (slots < 1) return SGEMM_STATUS_LAUNCH_FAILED;
         const int64_t blocks = ceil_div(N, 16);
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(unsigned(std::max<int64_t>(1, std::min<int64_t>(blocks, slots / q.slices))),
                            unsigned(q.slices));
-        cfg.blockDim = dim3(sg::kW4Threads);
+        cfg.blockDim = dim3(unsigned(k.threads));
         cfg.dynamicSmemBytes = size_t(smem);
         cfg.stream = stream;
         cudaLaunchAttribute attr[1];

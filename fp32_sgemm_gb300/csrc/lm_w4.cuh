@@ -4,7 +4,7 @@
 //
 // The weights are read once (half a byte each) and that read bounds the
 // product, so everything else is kept off its way:
-//   * each warp streams 16 weight rows, 128 columns (1 KB) at a time, through
+//   * each warp streams 16 weight rows, 256 columns (2 KB) at a time, through
 //     its own ring of asynchronous copies;
 //   * q - z is an integer of at most 5 bits, exact in f16 and bf16, so the
 //     weights meet x in the tensor core unscaled (mma.sync m16n8k16, the rows
@@ -12,13 +12,15 @@
 //     the FP32 sum of its group: no weight is ever rounded.  A nibble becomes
 //     a float by one logic operation (its bits under those of 128 or 1024)
 //     and one subtraction, for two weights at a time;
-//   * the order of k inside a group is free as long as both operands agree:
-//     the lane that unpacks a 32-bit word (8 weights) multiplies it with the
-//     8 x values of the same columns, kept in shared memory in the order in
-//     which the nibbles come out;
+//   * the order of k inside a group is free as long as both operands agree.
+//     A lane multiplies the 8 weights of a 32-bit word with the 8 x values
+//     of the same columns, kept in shared memory in the order in which the
+//     nibbles come out; which word a lane takes is chosen so that it reads
+//     as many neighbouring words at once as the group allows (16, 8 or 4
+//     bytes for groups of 128, 64, 32);
 //   * FP32 x is held as three bf16 planes (exactly), as three tokens.
-// The eight warps of a CTA share 16 rows and split K; their sums are joined
-// in a fixed order through shared memory.
+// The warps of a CTA share 16 rows and split K; their sums are joined in a
+// fixed order through shared memory.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -29,120 +31,243 @@
 
 namespace sg {
 
-constexpr int kW4Warps = 8, kW4Stages = 5;
-constexpr int kW4RowBytes = 80;                          // 64 bytes of a row, padded off bank conflicts
-constexpr int kW4StageBytes = 16 * kW4RowBytes;
-constexpr int kW4RingBytes = kW4Warps * kW4Stages * kW4StageBytes;
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src, bool valid) {
     const uint32_t n = valid ? 16u : 0u;
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
 
 template <bool BF16>
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
     if constexpr (BF16)
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-                     "{%8, %9}, {%0, %1, %2, %3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                     "{%8, %9}, {%10, %11, %12, %13};"
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
     else
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-                     "{%8, %9}, {%0, %1, %2, %3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                     "{%8, %9}, {%10, %11, %12, %13};"
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
-// Two nibbles (bits 0-3 and 16-19 of w) -> two 16-bit floats q - z; `zero`
-// holds 128 + z (bf16) or 1024 + z (f16) twice.
-template <bool BF16>
-__device__ __forceinline__ uint32_t unpack2(uint32_t w, uint32_t zero) {
-    const uint32_t magic = BF16 ? 0x43004300u : 0x64006400u;
-    const uint32_t v = (w & 0x000F000Fu) | magic;
+// (w & mask) | magic in one operation, with both constants in registers.
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
     uint32_t r;
-    if constexpr (BF16) {
-        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v),
-                                         *reinterpret_cast<const __nv_bfloat162 *>(&zero));
-        r = *reinterpret_cast<const uint32_t *>(&d);
-    } else {
-        const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&v), *reinterpret_cast<const __half2 *>(&zero));
-        r = *reinterpret_cast<const uint32_t *>(&d);
-    }
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));
+    return r;
+}
+__device__ __forceinline__ uint32_t in_register(uint32_t v) {
+    uint32_t r;
+    asm volatile("mov.b32 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
 
-template <int TYPE>
-__device__ __forceinline__ float w4_scale(const void *scales, int64_t i) {
-    if constexpr (TYPE == 0) return static_cast<const float *>(scales)[i];
-    else if constexpr (TYPE == 1) return __half2float(static_cast<const __half *>(scales)[i]);
-    else return __bfloat162float(static_cast<const __nv_bfloat16 *>(scales)[i]);
-}
+// The constants of the unpacking, kept in registers.
+template <bool BF16>
+struct W4Unpack {
+    uint32_t mask, magic, mask4, sixteenth;
+    __device__ __forceinline__ W4Unpack() {
+        mask = in_register(0x000F000Fu);
+        magic = in_register(BF16 ? 0x43004300u : 0x64006400u);
+        mask4 = in_register(0x00F000F0u);
+        sixteenth = 0x2C002C00u;     // 1 / 16 twice, f16
+    }
+    // The 8 nibbles of w as four pairs (0,4) (1,5) (2,6) (3,7) of q - z.
+    // `zero`: 128 + z (bf16) or 1024 + z (f16), twice.  f16 has room for the
+    // nibble four bits higher, as 1024 + 16 q, which one fused operation
+    // brings to q - z (`zero4` = 64 + z): two shifts fewer.
+    __device__ __forceinline__ void operator()(uint32_t w, uint32_t zero, uint32_t zero4, uint32_t (&o)[4]) const {
+        if constexpr (BF16) {
+            const __nv_bfloat162 z = *reinterpret_cast<const __nv_bfloat162 *>(&zero);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t v = and_or(w >> (4 * i), mask, magic);
+                const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), z);
+                o[i] = *reinterpret_cast<const uint32_t *>(&d);
+            }
+        } else {
+            const __half2 z = *reinterpret_cast<const __half2 *>(&zero);
+            const __half2 z4 = *reinterpret_cast<const __half2 *>(&zero4);
+            const __half2 s = *reinterpret_cast<const __half2 *>(&sixteenth);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t u = i ? w >> 8 : w;
+                const uint32_t v = and_or(u, mask, magic), v4 = and_or(u, mask4, magic);
+                const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&v), z);
+                const __half2 d4 = __hfma2(*reinterpret_cast<const __half2 *>(&v4), s, __hneg2(z4));
+                o[2 * i] = *reinterpret_cast<const uint32_t *>(&d);
+                o[2 * i + 1] = *reinterpret_cast<const uint32_t *>(&d4);
+            }
+        }
+    }
+};
 
-// TYPE: 0 FP32, 1 f16, 2 bf16.  COLS = 8 * NB columns on the N side.
+// N scales of one row (raw bits; 16-bit ones two to a register) and N zero
+// points (bytes), by vector loads where the rows are aligned for them.
+template <int TYPE, int N>
+struct W4Meta {
+    static constexpr int REGS = TYPE == 0 ? N : N / 2;
+    uint32_t s[REGS];
+    uint32_t z[(N + 3) / 4];
+
+    // n of them exist (N but for the last step of a row).
+    __device__ __forceinline__ void load(const W4Args &p, const unsigned char *scales, const uint8_t *zeros, int n) {
+        if (p.s_vec && n == N) {
+            const uint32_t *src = reinterpret_cast<const uint32_t *>(scales);
+            if constexpr (REGS == 1) {
+                s[0] = *src;
+            } else if constexpr (REGS == 2) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(src);
+                s[0] = v.x; s[1] = v.y;
+            } else {
+#pragma unroll
+                for (int i = 0; i < REGS; i += 4) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(src + i);
+                    s[i] = v.x; s[i + 1] = v.y; s[i + 2] = v.z; s[i + 3] = v.w;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < REGS; ++i) s[i] = 0u;
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (j < n) {
+                    if constexpr (TYPE == 0) s[j] = reinterpret_cast<const uint32_t *>(scales)[j];
+                    else s[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(scales)[j] << (16 * (j & 1));
+                }
+        }
+        if (p.zeros != nullptr) {
+            if (p.z_vec && n == N) {
+                if constexpr (N == 2) z[0] = *reinterpret_cast<const uint16_t *>(zeros);
+                else if constexpr (N == 4) z[0] = *reinterpret_cast<const uint32_t *>(zeros);
+                else {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(zeros);
+                    z[0] = v.x; z[1] = v.y;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < (N + 3) / 4; ++i) z[i] = 0u;
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (j < n) z[j / 4] |= (uint32_t)zeros[j] << (8 * (j & 3));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < (N + 3) / 4; ++i) z[i] = 0x08080808u;
+        }
+    }
+    __device__ __forceinline__ float scale(int j) const {
+        if constexpr (TYPE == 0) return __uint_as_float(s[j]);
+        else if constexpr (TYPE == 2) return __uint_as_float((j & 1) ? s[j / 2] & 0xFFFF0000u : s[j / 2] << 16);
+        else {
+            const __half2 h = *reinterpret_cast<const __half2 *>(&s[j / 2]);
+            return (j & 1) ? __high2float(h) : __low2float(h);
+        }
+    }
+    // z twice in the low bits of two halves.
+    __device__ __forceinline__ uint32_t zero(int j) const {
+        return ((z[j / 4] >> (8 * (j & 3))) & 15u) * 0x10001u;
+    }
+};
+
+// TYPE: 0 FP32, 1 f16, 2 bf16.  8 * NB columns on the N side.
 template <int TYPE, int GROUP, int NB>
-__global__ void __launch_bounds__(kW4Warps * 32)
+__global__ void __launch_bounds__(kW4MaxWarps * 32)
 lm_w4_kernel(const W4Args p) {
     constexpr bool BF16 = TYPE != 1;
     constexpr int PLANES = TYPE == 0 ? 3 : 1;
-    constexpr int SLOTS = GROUP / 32;                     // 32-column slots per group
-    constexpr int NG = 4 / SLOTS;                         // groups per step of 128
+    constexpr int SLOTS = GROUP / 32;                     // words a lane takes of a group and row
+    constexpr int NG = 256 / GROUP;                       // groups per step
     extern __shared__ __align__(128) unsigned char smem_raw[];
+    const int warps = blockDim.x >> 5;
     unsigned char *ring = smem_raw;
-    float *red = reinterpret_cast<float *>(smem_raw + kW4RingBytes);          // [2][warp][NB * 4][32]
-    unsigned char *xs = smem_raw + kW4RingBytes + 2 * kW4Warps * NB * 512;    // [column][x_pitch bytes]
+    float *red = reinterpret_cast<float *>(smem_raw + warps * kW4RingBytes);   // [2][warp][NB * 4][32]
+    unsigned char *xs = reinterpret_cast<unsigned char *>(red) + 2 * warps * NB * 512;   // [column][x_pitch]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, q = lane & 3;
     // This CTA's slice of K and this warp's steps in it.
     const int k_begin = blockIdx.y * p.k_slice, k_end = min(p.K, k_begin + p.k_slice);
-    const int steps = (k_end - k_begin + 127) >> 7;
-    const int s0 = steps * warp / kW4Warps, s1 = steps * (warp + 1) / kW4Warps;
-    const int per = s1 - s0;
+    const int steps = (k_end - k_begin + 255) >> 8;
+    const int s0 = steps * warp / warps, per = steps * (warp + 1) / warps - s0;
+    const int k_warp = k_begin + s0 * 256;
     const int blocks = (p.N + 15) >> 4;
     const int mine = blocks > (int)blockIdx.x ? (blocks - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
 
     griddep_launch_dependents();
     griddep_wait();
 
-    const uint32_t ring_w = smem_u32(ring) + warp * (kW4Stages * kW4StageBytes);
-    // Copies of step i (of this warp's sequence) into stage i % kW4Stages.
-    int ld_b = 0, ld_s = 0, ld_stage = 0;
+    // Rows of 128 bytes; 16-byte piece c of row r sits at c ^ swizzle(r), so
+    // that the rows a warp reads together meet different banks.
+    auto swizzle = [](int r) { return GROUP == 32 ? r & 7 : GROUP == 64 ? (r & 3) * 2 : (r & 1) * 4; };
+    unsigned char *ring_w = ring + warp * kW4RingBytes;
+    // Copies: lane takes piece lane % 8 of rows lane / 8 + 4 i.
+    const int lr = lane >> 3, lp = lane & 7;
+    uint32_t dst[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dst[i] = smem_u32(ring_w) + (lr + 4 * i) * 128 + ((lp ^ swizzle(lr + 4 * i)) << 4);
+    const uint8_t *src[4];
+    int ld_b = 0, ld_s = 0, ld_k = k_warp;
+    uint32_t ld_off = 0;
+    auto point = [&]() {
+        const int row0 = ((int)blockIdx.x + ld_b * (int)gridDim.x) << 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            src[i] = p.Q + (int64_t)min(row0 + lr + 4 * i, p.N - 1) * p.ldq + (k_warp >> 1) + lp * 16;
+    };
     auto issue = [&]() {
         if (ld_b < mine) {
-            const int row0 = ((int)blockIdx.x + ld_b * (int)gridDim.x) << 4;
-            const int k0 = k_begin + (s0 + ld_s) * 128;
+            if (ld_k + 256 <= k_end) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int id = lane + 32 * i, r = id >> 2, piece = id & 3;
-                const int row = min(row0 + r, p.N - 1);
-                const bool valid = k0 + piece * 32 < k_end;
-                const uint8_t *src = p.Q + (int64_t)row * p.ldq + ((valid ? k0 + piece * 32 : k_begin) >> 1);
-                cp_async16(ring_w + ld_stage * kW4StageBytes + r * kW4RowBytes + piece * 16, src, valid);
+                for (int i = 0; i < 4; ++i) cp_async16(dst[i] + ld_off, src[i]);
+            } else {
+                const bool valid = ld_k + lp * 32 < k_end;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) cp_async16_or_zero(dst[i] + ld_off, valid ? src[i] : p.Q, valid);
             }
-            if (++ld_s == per) { ld_s = 0; ++ld_b; }
-            if (++ld_stage == kW4Stages) ld_stage = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) src[i] += 128;
+            ld_k += 256;
+            ld_off = ld_off == (kW4Stages - 1) * 2048 ? 0 : ld_off + 2048;
+            if (++ld_s == per) {
+                ld_s = 0;
+                ld_k = k_warp;
+                ++ld_b;
+                point();
+            }
         }
         cp_async_commit();
     };
-    if (per > 0)
+    if (per > 0) {
+        point();
 #pragma unroll
         for (int i = 0; i < kW4Stages - 1; ++i) issue();
+    }
 
-    // x in nibble order: within 8 columns, 0 4 1 5 2 6 3 7.
+    // x in nibble order (within 8 columns 0 4 1 5 2 6 3 7), the 16 chunks of
+    // 128 columns in the order in which the lanes q = 0..3 take them.
     {
-        const int chunks = steps * 16;                    // of 8 columns
-        for (int i = threadIdx.x; i < chunks * p.tokens; i += kW4Warps * 32) {
+        const int chunks = steps * 32;                    // of 8 columns
+        for (int i = threadIdx.x; i < chunks * p.tokens; i += blockDim.x) {
             const int t = i / chunks, c = i - t * chunks, k = k_begin + c * 8;
+            // Chunk c is word `slot` of lane `lq`; see the loop below.
+            const int in = c & 15;
+            const int lq = GROUP == 128 ? in >> 2 : GROUP == 64 ? (in >> 1) & 3 : in & 3;
+            const int slot = GROUP == 128 ? in & 3 : GROUP == 64 ? (in >> 3) * 2 + (in & 1) : in >> 2;
+            unsigned char *at = xs + ((c & ~15) + slot * 4 + lq) * 16;
             if constexpr (TYPE == 0) {
-                const float *src = static_cast<const float *>(p.X) + (int64_t)t * p.ldx + k;
+                const float *sx = static_cast<const float *>(p.X) + (int64_t)t * p.ldx + k;
                 uint16_t v[3][8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float f = k + e < k_end ? src[e] : 0.f;
+                    const float f = k + e < k_end ? sx[e] : 0.f;
                     const uint32_t u = __float_as_uint(f);
                     const bool odd = (u & 0x7F800000u) == 0x7F800000u;
                     const uint32_t h = odd && (u & 0x7FFFFFu) ? 0x7FC00000u : u & 0xFFFF0000u;
@@ -159,117 +284,153 @@ lm_w4_kernel(const W4Args p) {
                     o.y = v[pl][1] | (uint32_t)v[pl][5] << 16;
                     o.z = v[pl][2] | (uint32_t)v[pl][6] << 16;
                     o.w = v[pl][3] | (uint32_t)v[pl][7] << 16;
-                    *reinterpret_cast<uint4 *>(xs + (int64_t)(t * 3 + pl) * p.x_pitch + c * 16) = o;
+                    *reinterpret_cast<uint4 *>(at + (t * 3 + pl) * p.x_pitch) = o;
                 }
             } else {
-                const uint16_t *src = static_cast<const uint16_t *>(p.X) + (int64_t)t * p.ldx + k;
+                const uint16_t *sx = static_cast<const uint16_t *>(p.X) + (int64_t)t * p.ldx + k;
                 uint16_t v[8];
                 if (p.x_vec && k + 8 <= k_end) {
-                    *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(src);
+                    *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(sx);
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = k + e < k_end ? src[e] : (uint16_t)0;
+                    for (int e = 0; e < 8; ++e) v[e] = k + e < k_end ? sx[e] : (uint16_t)0;
                 }
                 uint4 o;
                 o.x = v[0] | (uint32_t)v[4] << 16;
                 o.y = v[1] | (uint32_t)v[5] << 16;
                 o.z = v[2] | (uint32_t)v[6] << 16;
                 o.w = v[3] | (uint32_t)v[7] << 16;
-                *reinterpret_cast<uint4 *>(xs + (int64_t)t * p.x_pitch + c * 16) = o;
+                *reinterpret_cast<uint4 *>(at + t * p.x_pitch) = o;
             }
         }
     }
+
+    // Scales and zero points come one step ahead of their use.
+    W4Meta<TYPE, NG> ma, mb, na, nb;
+    constexpr int SB = TYPE == 0 ? 4 : 2;                 // bytes of a scale
+    const unsigned char *sa = nullptr, *sb = nullptr;
+    const uint8_t *za = nullptr, *zb = nullptr;
+    int m_b = 0, m_s = 0;
+    auto point_meta = [&]() {
+        const int row0 = ((int)blockIdx.x + m_b * (int)gridDim.x) << 4;
+        const int64_t ra = min(row0 + g, p.N - 1), rb = min(row0 + g + 8, p.N - 1);
+        const unsigned char *base = static_cast<const unsigned char *>(p.scales) + (k_warp / GROUP) * SB;
+        sa = base + ra * p.lds * SB;
+        sb = base + rb * p.lds * SB;
+        za = p.zeros + ra * p.ldz + k_warp / GROUP;
+        zb = p.zeros + rb * p.ldz + k_warp / GROUP;
+    };
+    auto meta = [&]() {
+        if (m_b < mine) {
+            const int n = min(NG, (k_end - k_warp - m_s * 256) / GROUP);
+            na.load(p, sa, za, n);
+            nb.load(p, sb, zb, n);
+            sa += NG * SB;
+            sb += NG * SB;
+            za += NG;
+            zb += NG;
+            if (++m_s == per) {
+                m_s = 0;
+                ++m_b;
+                point_meta();
+            }
+        }
+    };
+    if (per > 0) {
+        point_meta();
+        meta();
+    }
     __syncthreads();
 
+    const W4Unpack<BF16> unpack;
+    // Columns beyond the last take its x: their products go nowhere.
     const int cols = p.tokens * PLANES;
-    const uint32_t zsym = BF16 ? 0x43084308u : 0x64086408u;
-    int stage = 0;
+    const unsigned char *x_lane[NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) x_lane[n] = xs + (s0 * 32 + q) * 16 + min(n * 8 + g, cols - 1) * p.x_pitch;
+    // Words of a lane: row g (g + 8), of each 128 columns.
+    const int sw = swizzle(g);                 // swizzle(g + 8) is the same
+    int off = 0;
     for (int b = 0; b < mine; ++b) {
-        const int row0 = ((int)blockIdx.x + b * (int)gridDim.x) << 4;
-        const int ra = min(row0 + g, p.N - 1), rb = min(row0 + g + 8, p.N - 1);
         float sum[NB][4];
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) sum[n][i] = 0.f;
         for (int s = 0; s < per; ++s) {
-            const int k0 = k_begin + (s0 + s) * 128;
-            const int live = min(4, (k_end - k0 + 31) >> 5);      // slots that exist
-            // Scales and zero points of this step's groups.
-            float sc[NG][2];
-            uint32_t zc[NG][2];
-#pragma unroll
-            for (int j = 0; j < NG; ++j) {
-                const int64_t gi = (k0 / GROUP) + j;
-                const bool in = j * SLOTS < live;
-                sc[j][0] = in ? w4_scale<TYPE>(p.scales, ra * p.lds + gi) : 0.f;
-                sc[j][1] = in ? w4_scale<TYPE>(p.scales, rb * p.lds + gi) : 0.f;
-                zc[j][0] = zc[j][1] = zsym;
-                if (p.zeros != nullptr && in) {
-                    const uint32_t base = BF16 ? 0x4300u : 0x6400u;
-                    zc[j][0] = (base | (p.zeros[ra * p.ldz + gi] & 15u)) * 0x10001u;
-                    zc[j][1] = (base | (p.zeros[rb * p.ldz + gi] & 15u)) * 0x10001u;
-                }
-            }
+            ma = na;
+            mb = nb;
+            meta();
             cp_async_wait<kW4Stages - 2>();
             __syncwarp();
-            const unsigned char *st = ring + warp * (kW4Stages * kW4StageBytes) + stage * kW4StageBytes;
-            uint32_t wa[4], wb[4];
+            const unsigned char *st = ring_w + off + g * 128;
+            uint32_t wa[8], wb[8];
+            if constexpr (GROUP == 128) {
 #pragma unroll
-            for (int slot = 0; slot < 4; ++slot) {
-                wa[slot] = *reinterpret_cast<const uint32_t *>(st + g * kW4RowBytes + slot * 16 + q * 4);
-                wb[slot] = *reinterpret_cast<const uint32_t *>(st + (g + 8) * kW4RowBytes + slot * 16 + q * 4);
+                for (int h = 0; h < 2; ++h) {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(st + (((h * 4 + q) ^ sw) << 4));
+                    const uint4 v = *reinterpret_cast<const uint4 *>(st + 1024 + (((h * 4 + q) ^ sw) << 4));
+                    wa[4 * h] = u.x; wa[4 * h + 1] = u.y; wa[4 * h + 2] = u.z; wa[4 * h + 3] = u.w;
+                    wb[4 * h] = v.x; wb[4 * h + 1] = v.y; wb[4 * h + 2] = v.z; wb[4 * h + 3] = v.w;
+                }
+            } else if constexpr (GROUP == 64) {
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const int at = (((h * 2 + (q >> 1)) ^ sw) << 4) + (q & 1) * 8;
+                    const uint2 u = *reinterpret_cast<const uint2 *>(st + at);
+                    const uint2 v = *reinterpret_cast<const uint2 *>(st + 1024 + at);
+                    wa[2 * h] = u.x; wa[2 * h + 1] = u.y;
+                    wb[2 * h] = v.x; wb[2 * h + 1] = v.y;
+                }
+            } else {
+#pragma unroll
+                for (int h = 0; h < 8; ++h) {
+                    const int at = ((h ^ sw) << 4) + q * 4;
+                    wa[h] = *reinterpret_cast<const uint32_t *>(st + at);
+                    wb[h] = *reinterpret_cast<const uint32_t *>(st + 1024 + at);
+                }
             }
             __syncwarp();
             issue();
-            if (++stage == kW4Stages) stage = 0;
+            off = off == (kW4Stages - 1) * 2048 ? 0 : off + 2048;
+            // Past the end of K the words are 0 and x is 0: they add nothing.
             float c[NB][4];
 #pragma unroll
-            for (int slot = 0; slot < 4; ++slot) {
-                const int j = slot / SLOTS;
-                if (slot % SLOTS == 0) {
+            for (int w = 0; w < 8; ++w) {
+                const int j = w / SLOTS;
+                const bool first = w % SLOTS == 0;
+                const uint32_t z0 = ma.zero(j), z1 = mb.zero(j);
+                uint32_t a[4], d[4];
+                unpack(wa[w], z0 | (BF16 ? 0x43004300u : 0x64006400u), (z0 << 4) | 0x54005400u, a);
+                unpack(wb[w], z1 | (BF16 ? 0x43004300u : 0x64006400u), (z1 << 4) | 0x54005400u, d);
 #pragma unroll
-                    for (int n = 0; n < NB; ++n)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) c[n][i] = 0.f;
+                for (int n = 0; n < NB; ++n) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(x_lane[n] + s * 512 + w * 64);
+                    if (first) mma16816<BF16>(c[n], a[0], d[0], a[1], d[1], x.x, x.y, 0.f, 0.f, 0.f, 0.f);
+                    else mma16816<BF16>(c[n], a[0], d[0], a[1], d[1], x.x, x.y, c[n][0], c[n][1], c[n][2], c[n][3]);
+                    mma16816<BF16>(c[n], a[2], d[2], a[3], d[3], x.z, x.w, c[n][0], c[n][1], c[n][2], c[n][3]);
                 }
-                if (GROUP == 128 || slot < live) {
-                    uint32_t a[4], d[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        a[i] = unpack2<BF16>(wa[slot] >> (4 * i), zc[j][0]);
-                        d[i] = unpack2<BF16>(wb[slot] >> (4 * i), zc[j][1]);
-                    }
+                if (w % SLOTS == SLOTS - 1) {
+                    const float f0 = ma.scale(j), f1 = mb.scale(j);
 #pragma unroll
                     for (int n = 0; n < NB; ++n) {
-                        const int col = n * 8 + g;
-                        uint4 x = make_uint4(0, 0, 0, 0);
-                        if (col < cols)
-                            x = *reinterpret_cast<const uint4 *>(xs + (int64_t)col * p.x_pitch +
-                                                                 ((s0 + s) * 16 + slot * 4 + q) * 16);
-                        mma16816<BF16>(c[n], a[0], d[0], a[1], d[1], x.x, x.y);
-                        mma16816<BF16>(c[n], a[2], d[2], a[3], d[3], x.z, x.w);
-                    }
-                }
-                if (slot % SLOTS == SLOTS - 1) {
-#pragma unroll
-                    for (int n = 0; n < NB; ++n) {
-                        sum[n][0] = fmaf(sc[j][0], c[n][0], sum[n][0]);
-                        sum[n][1] = fmaf(sc[j][0], c[n][1], sum[n][1]);
-                        sum[n][2] = fmaf(sc[j][1], c[n][2], sum[n][2]);
-                        sum[n][3] = fmaf(sc[j][1], c[n][3], sum[n][3]);
+                        sum[n][0] = fmaf(f0, c[n][0], sum[n][0]);
+                        sum[n][1] = fmaf(f0, c[n][1], sum[n][1]);
+                        sum[n][2] = fmaf(f1, c[n][2], sum[n][2]);
+                        sum[n][3] = fmaf(f1, c[n][3], sum[n][3]);
                     }
                 }
             }
         }
         // Join the warps' sums (two buffers: a warp may be one block ahead).
-        float *buf = red + (b & 1) * (kW4Warps * NB * 128);
+        float *buf = red + (b & 1) * (warps * NB * 128);
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) buf[(warp * NB * 4 + n * 4 + i) * 32 + lane] = sum[n][i];
         __syncthreads();
-        for (int o = threadIdx.x; o < 16 * p.tokens; o += kW4Warps * 32) {
+        const int row0 = ((int)blockIdx.x + b * (int)gridDim.x) << 4;
+        for (int o = threadIdx.x; o < 16 * p.tokens; o += blockDim.x) {
             const int t = o >> 4, r = o & 15;
             float y = 0.f;
 #pragma unroll
@@ -279,8 +440,7 @@ lm_w4_kernel(const W4Args p) {
                 const int col = t * PLANES + pl;
                 const int at = ((col >> 3) * 4 + (r >> 3) * 2 + (col & 1)) * 32 + (r & 7) * 4 + ((col & 7) >> 1);
                 float v = 0.f;
-#pragma unroll
-                for (int w = 0; w < kW4Warps; ++w) v += buf[w * NB * 128 + at];
+                for (int w = 0; w < warps; ++w) v += buf[w * NB * 128 + at];
                 y += v;
             }
             const int n = row0 + r;

@@ -8,7 +8,7 @@ namespace sg {
 
 struct W4Args {
     int N, K, tokens;          // rows of W, columns, rows of x in this launch
-    int k_slice;               // columns per blockIdx.y (a multiple of 128)
+    int k_slice;               // columns per blockIdx.y (a multiple of 256)
     const void *X;
     int64_t ldx;
     int x_vec;                 // rows of x take 16-byte loads
@@ -19,6 +19,7 @@ struct W4Args {
     int64_t lds;
     const uint8_t *zeros;
     int64_t ldz;
+    int s_vec, z_vec;          // a step's scales / zero points of a row in one vector load
     void *Y;
     int64_t ldy;
     float *part;               // [slice][token][ld_part] FP32, or NULL for Y itself
@@ -28,8 +29,9 @@ struct W4Args {
 const void *w4_kernel_f32(int group, int nb);
 const void *w4_kernel_f16(int group, int nb);
 const void *w4_kernel_bf16(int group, int nb);
-constexpr int kW4Threads = 256;
+constexpr int kW4MaxWarps = 16, kW4Stages = 4;
+constexpr int kW4RingBytes = kW4Stages * 2048;            // per warp
 // Shared memory beside the staged x.
-size_t w4_fixed_smem(int nb);
+inline size_t w4_fixed_smem(int nb, int warps) { return size_t(warps) * (kW4RingBytes + 2 * nb * 512); }
 
 }  // namespace sg
