@@ -29,9 +29,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 def __getattr__(name):
     if name in _BINDING_NAMES:
-        from . import _binding
-        return getattr(_binding, name)
-    if name in _LM_NAMES:
-        from . import _lm
-        return getattr(_lm, name)
-    raise AttributeError(name)
+        from . import _binding as module
+    elif name in _LM_NAMES:
+        from . import _lm as module
+    else:
+        raise AttributeError(name)
+    value = globals()[name] = getattr(module, name)
+    return value

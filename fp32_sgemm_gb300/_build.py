@@ -1,5 +1,6 @@
 """Build the CUDA library in tree: nvcc for sm_103a, one object per
-translation unit compiled in parallel, linked into lib/libsgemm_gb300.so."""
+translation unit compiled in parallel, linked into lib/libsgemm_gb300.so, and
+the Python module of the language-model operators beside it."""
 
 from __future__ import annotations
 
@@ -15,7 +16,10 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_DIR = os.path.join(HERE, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libsgemm_gb300.so")
-HEADER = os.path.join(ROOT, "include", "sgemm_gb300.h")
+HEADERS = [os.path.join(ROOT, "include", name) for name in ("sgemm_gb300.h", "sgemm_gb300_lm.h")]
+# Python module of the language-model operators (csrc/lm_binding.cpp).
+LM_BINDING_SRC = os.path.join(CSRC, "lm_binding.cpp")
+LM_BINDING_PATH = os.path.join(LIB_DIR, "_lm_binding.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
@@ -35,13 +39,13 @@ def sources() -> list[str]:
 
 def _deps() -> list[str]:
     return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        glob.glob(os.path.join(CSRC, "*.h")) + [HEADER, os.path.abspath(__file__)]
+        glob.glob(os.path.join(CSRC, "*.h")) + HEADERS + [LM_BINDING_SRC, os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(LM_BINDING_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(LM_BINDING_PATH))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -54,6 +58,37 @@ def _compile(src: str, extra: list[str]) -> tuple[str, str]:
     return obj, r.stdout + r.stderr
 
 
+def _compile_binding() -> str:
+    """Object file of the Python module, against torch's headers."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    obj = os.path.join(BUILD_DIR, "lm_binding.o")
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
+           "-c", LM_BINDING_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {LM_BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str):
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = LM_BINDING_PATH + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", obj, "-o", tmp, f"-L{LIB_DIR}", f"-L{libs}", "-lsgemm_gb300", "-ltorch_python",
+           "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, LM_BINDING_PATH)
+
+
 def build(force: bool = False, jobs: int | None = None, extra_flags: list[str] | None = None,
           verbose: bool = False) -> str:
     """Compile every .cu under csrc/ and link the shared library; returns its path."""
@@ -64,8 +99,10 @@ def build(force: bool = False, jobs: int | None = None, extra_flags: list[str] |
     srcs = sources()
     jobs = jobs or min(len(srcs), os.cpu_count() or 4)
     logs = []
-    with concurrent.futures.ThreadPoolExecutor(max_workers=jobs) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=jobs + 1) as ex:
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(lambda s: _compile(s, extra_flags or []), srcs))
+        binding = binding.result()
     objs = [o for o, _ in results]
     for (o, log) in results:
         logs.append(f"== {os.path.basename(o)}\n{log}")
@@ -77,6 +114,7 @@ def build(force: bool = False, jobs: int | None = None, extra_flags: list[str] |
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    _link_binding(binding)
     if verbose:
         print("\n".join(logs))
     return LIB_PATH

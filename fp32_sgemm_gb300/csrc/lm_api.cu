@@ -371,8 +371,6 @@ int64_t w4_pitch(int64_t k) {
 }
 
 int w4_blocks(int64_t cols) { return cols <= 8 ? 1 : cols <= 16 ? 2 : 4; }
-// Warps of a CTA when it has an SM for itself.
-int w4_warps(int64_t cols) { return cols <= 16 ? 16 : 8; }
 
 sgemmStatus_t plan_w4(int type, int64_t M, int64_t N, int64_t K, int group, W4 &q) {
     if (!type_ok(type) || M < 0 || N < 0 || K < 0) return SGEMM_STATUS_INVALID_VALUE;
@@ -387,7 +385,7 @@ sgemmStatus_t plan_w4(int type, int64_t M, int64_t N, int64_t K, int group, W4 &
     if (M == 0 || N == 0 || K == 0) return SGEMM_STATUS_SUCCESS;
     // K is cut when x does not fit beside the ring.
     const int64_t cols = int64_t(q.most) * q.planes;
-    const int64_t room = kMaxSmem - int64_t(sg::w4_fixed_smem(w4_blocks(cols), w4_warps(cols)));
+    const int64_t room = kMaxSmem - int64_t(sg::w4_fixed_smem(w4_blocks(cols), true));
     int64_t slices = 1;
     while (cols * w4_pitch(round_up(ceil_div(K, slices), 256)) > room && ceil_div(K, slices) > 256) ++slices;
     q.k_slice = int(round_up(ceil_div(K, slices), 256));
@@ -777,16 +775,13 @@ sgemmStatus_t sgemmW4(sgemmHandle_t h, sgemmDataType_t type, int64_t M, int64_t 
         p.part = q.slices > 1 ? static_cast<float *>(h->ws) : nullptr;
         p.ld_part = round_up(N, 8);
         LmKernel k;
-        k.fn = type == SGEMM_TYPE_F32 ? sg::w4_kernel_f32(group, nb)
-               : type == SGEMM_TYPE_F16 ? sg::w4_kernel_f16(group, nb) : sg::w4_kernel_bf16(group, nb);
-        // Two CTAs of 8 warps on an SM where both fit, else one (of 16).
-        int warps = 8;
-        int smem = int(sg::w4_fixed_smem(nb, warps)) + cols * p.x_pitch;
-        if (smem > 113 * 1024) {
-            warps = w4_warps(cols);
-            smem = int(sg::w4_fixed_smem(nb, warps)) + cols * p.x_pitch;
-        }
-        k.threads = warps * 32;
+        // Three CTAs on an SM where they fit, else one with more warps.
+        const int64_t xs = int64_t(cols) * p.x_pitch;
+        const bool alone = nb == 4 || int64_t(sg::w4_fixed_smem(nb, false)) + xs > 75 * 1024;
+        const int smem = int(int64_t(sg::w4_fixed_smem(nb, alone)) + xs);
+        k.fn = type == SGEMM_TYPE_F32 ? sg::w4_kernel_f32(group, nb, alone)
+               : type == SGEMM_TYPE_F16 ? sg::w4_kernel_f16(group, nb, alone) : sg::w4_kernel_bf16(group, nb, alone);
+        k.threads = sg::w4_warps(nb, alone) * 32;
         const int slots = resident_slots(h, k, smem);
         if (slots < 1) return SGEMM_STATUS_LAUNCH_FAILED;
         const int64_t blocks = ceil_div(N, 16);

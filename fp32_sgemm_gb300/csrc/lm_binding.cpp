@@ -1,0 +1,368 @@
+// Python side of the language-model operators: reads torch tensors, checks
+// them, asks the C ABI (include/sgemm_gb300_lm.h) for the workspace and makes
+// the call.  Argument marshalling only.  In C++ because the same checks in
+// Python take 13 to 20 us a call, three times what the smallest products take
+// on the device.
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include <ATen/core/Tensor.h>
+#include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <algorithm>
+#include <exception>
+
+#include "../../include/sgemm_gb300_lm.h"
+
+namespace {
+
+PyObject *g_check = nullptr;        // _binding._check(status, where)
+PyObject *g_stream_ptr = nullptr;   // _binding._stream_ptr(stream, device index)
+PyObject *g_name_ptr = nullptr, *g_name_bytes = nullptr, *g_name_grow = nullptr;
+
+struct Failed {};                   // a Python error is set
+
+[[noreturn]] void fail(PyObject *type, const char *format, ...) {
+    va_list args;
+    va_start(args, format);
+    PyErr_FormatV(type, format, args);
+    va_end(args);
+    throw Failed{};
+}
+
+const at::Tensor &tensor(PyObject *o, const char *name) {
+    if (!THPVariable_Check(o)) fail(PyExc_TypeError, "%s must be a torch.Tensor", name);
+    return THPVariable_Unpack(o);
+}
+
+const char *type_name(at::ScalarType t) { return c10::toString(t); }
+
+sgemmDataType_t type_of(const at::Tensor &t, const char *name) {
+    switch (t.scalar_type()) {
+        case at::kFloat: return SGEMM_TYPE_F32;
+        case at::kHalf: return SGEMM_TYPE_F16;
+        case at::kBFloat16: return SGEMM_TYPE_BF16;
+        default: fail(PyExc_TypeError, "%s must be float32, float16 or bfloat16, got %s", name,
+                      type_name(t.scalar_type()));
+    }
+}
+
+c10::Device device_of(const at::Tensor &t, const char *name) {
+    if (!t.is_cuda()) fail(PyExc_ValueError, "%s must be a CUDA tensor", name);
+    return t.device();
+}
+
+struct Matrix {
+    void *ptr = nullptr;
+    int64_t rows = 0, cols = 0, ld = 1, stride = 0;
+};
+
+void check_kind(const at::Tensor &t, const char *name, at::ScalarType type, c10::Device dev) {
+    if (t.scalar_type() != type)
+        fail(PyExc_TypeError, "%s must be %s, got %s", name, type_name(type), type_name(t.scalar_type()));
+    if (t.device() != dev) fail(PyExc_ValueError, "%s must be on %s", name, dev.str().c_str());
+}
+
+// Row-major matrix of the call's type and device; rows, cols < 0: any.
+Matrix matrix(const at::Tensor &t, const char *name, at::ScalarType type, c10::Device dev, int64_t rows = -1,
+              int64_t cols = -1) {
+    check_kind(t, name, type, dev);
+    if (t.dim() != 2) fail(PyExc_ValueError, "%s must be 2-D", name);
+    Matrix m;
+    m.rows = t.size(0);
+    m.cols = t.size(1);
+    if ((rows >= 0 && m.rows != rows) || (cols >= 0 && m.cols != cols))
+        fail(PyExc_ValueError, "%s has shape (%lld, %lld), expected (%lld, %lld)", name, (long long)m.rows,
+             (long long)m.cols, (long long)(rows < 0 ? m.rows : rows), (long long)(cols < 0 ? m.cols : cols));
+    if (m.rows > 0 && m.cols > 1 && t.stride(1) != 1)
+        fail(PyExc_ValueError, "%s must be row major (stride(1) == 1)", name);
+    m.ld = std::max<int64_t>(1, m.rows > 1 ? t.stride(0) : m.cols);
+    if (m.rows > 1 && m.ld < m.cols) fail(PyExc_ValueError, "%s has overlapping rows", name);
+    m.ptr = const_cast<void *>(t.const_data_ptr());
+    return m;
+}
+
+// Stack of `n` row-major rows x cols matrices.
+Matrix stack(const at::Tensor &t, const char *name, at::ScalarType type, c10::Device dev, int64_t n, int64_t rows,
+             int64_t cols) {
+    check_kind(t, name, type, dev);
+    if (t.dim() != 3) fail(PyExc_ValueError, "%s must be 3-D", name);
+    if (t.size(0) != n || t.size(1) != rows || t.size(2) != cols)
+        fail(PyExc_ValueError, "%s has shape (%lld, %lld, %lld), expected (%lld, %lld, %lld)", name,
+             (long long)t.size(0), (long long)t.size(1), (long long)t.size(2), (long long)n, (long long)rows,
+             (long long)cols);
+    Matrix m;
+    m.rows = rows;
+    m.cols = cols;
+    if (rows > 0 && cols > 1 && t.stride(2) != 1)
+        fail(PyExc_ValueError, "%s must be row major (stride(2) == 1)", name);
+    m.ld = std::max<int64_t>(1, rows > 1 ? t.stride(1) : cols);
+    if (rows > 1 && m.ld < cols) fail(PyExc_ValueError, "%s has overlapping rows", name);
+    m.stride = n > 1 ? t.stride(0) : 0;
+    if (n > 1 && rows > 0 && cols > 0 && m.stride < (rows - 1) * m.ld + cols)
+        fail(PyExc_ValueError, "%s must hold one matrix per group (no broadcast)", name);
+    m.ptr = const_cast<void *>(t.const_data_ptr());
+    return m;
+}
+
+template <class T>
+T *vector(PyObject *o, const char *name, at::ScalarType type, c10::Device dev, int64_t n) {
+    const at::Tensor &t = tensor(o, name);
+    if (t.scalar_type() != type) fail(PyExc_TypeError, "%s must be a %s tensor", name, type_name(type));
+    if (t.device() != dev || t.dim() != 1 || (n >= 0 && t.size(0) != n) || !t.is_contiguous())
+        fail(PyExc_ValueError, "%s must be a contiguous vector%s on %s", name, n >= 0 ? " of the call's length" : "",
+             dev.str().c_str());
+    return static_cast<T *>(const_cast<void *>(t.const_data_ptr()));
+}
+
+at::Tensor make(at::IntArrayRef sizes, at::ScalarType type, c10::Device dev) {
+    return at::empty(sizes, at::TensorOptions().dtype(type).device(dev));
+}
+
+// `out` or a new matrix.
+at::Tensor output(PyObject *out, at::IntArrayRef sizes, at::ScalarType type, c10::Device dev) {
+    return out == Py_None ? make(sizes, type, dev) : tensor(out, "out");
+}
+
+void check(sgemmStatus_t st, const char *where) {
+    if (st == SGEMM_STATUS_SUCCESS) return;
+    PyObject *r = PyObject_CallFunction(g_check, "is", int(st), where);
+    Py_XDECREF(r);
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, where);
+    throw Failed{};
+}
+
+// A Handle of this package: its C handle, and a workspace of `need` bytes
+// attached to it.
+struct Call {
+    sgemmHandle_t handle = nullptr;
+    cudaStream_t stream = nullptr;
+    PyObject *owner;
+
+    Call(PyObject *h, PyObject *s, c10::Device dev) : owner(h) {
+        PyObject *p = PyObject_GetAttr(h, g_name_ptr);
+        if (p == nullptr) throw Failed{};
+        handle = static_cast<sgemmHandle_t>(PyLong_AsVoidPtr(p));
+        Py_DECREF(p);
+        if (PyErr_Occurred()) throw Failed{};
+        if (s == Py_None) {
+            stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+        } else {
+            PyObject *v = PyObject_CallFunction(g_stream_ptr, "Oi", s, int(dev.index()));
+            if (v == nullptr) throw Failed{};
+            stream = v == Py_None ? nullptr : static_cast<cudaStream_t>(PyLong_AsVoidPtr(v));
+            Py_DECREF(v);
+            if (PyErr_Occurred()) throw Failed{};
+        }
+    }
+    void workspace(size_t need) const {
+        if (need == 0) return;
+        PyObject *b = PyObject_GetAttr(owner, g_name_bytes);
+        if (b == nullptr) throw Failed{};
+        const size_t have = PyLong_AsSize_t(b);
+        Py_DECREF(b);
+        if (PyErr_Occurred()) throw Failed{};
+        if (have >= need) return;
+        PyObject *n = PyLong_FromSize_t(need);
+        PyObject *r = PyObject_CallMethodObjArgs(owner, g_name_grow, n, nullptr);
+        Py_XDECREF(n);
+        Py_XDECREF(r);
+        if (r == nullptr) throw Failed{};
+    }
+};
+
+void expect(Py_ssize_t given, Py_ssize_t want) {
+    if (given != want) fail(PyExc_TypeError, "expected %zd arguments, got %zd", want, given);
+}
+
+template <class F>
+PyObject *guarded(F &&f) {
+    try {
+        return f();
+    } catch (const Failed &) {
+        return nullptr;
+    } catch (const std::exception &e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
+PyObject *wrap(const at::Tensor &t) { return THPVariable_Wrap(t); }
+
+// (x, w, group_ends, trans_w, out, handle, stream)
+PyObject *py_grouped_gemm(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&] {
+        expect(n, 7);
+        const at::Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "w");
+        const sgemmDataType_t ty = type_of(x, "x");
+        const c10::Device dev = device_of(x, "x");
+        const at::ScalarType st = x.scalar_type();
+        const Matrix mx = matrix(x, "x", st, dev);
+        if (w.dim() != 3) fail(PyExc_ValueError, "w must be a 3-D tensor [groups, rows, cols]");
+        const bool trans = PyObject_IsTrue(a[3]);
+        const int64_t T = mx.rows, K = mx.cols, G = w.size(0), N = w.size(trans ? 1 : 2);
+        const Matrix mw = stack(w, "w", st, dev, G, trans ? N : K, trans ? K : N);
+        const int32_t *ends = vector<int32_t>(a[2], "group_ends", at::kInt, dev, G);
+        const at::Tensor out = output(a[4], {T, N}, st, dev);
+        const Matrix my = matrix(out, "out", st, dev, T, N);
+        const Call c(a[5], a[6], dev);
+        const sgemmOperation_t op = trans ? SGEMM_OP_T : SGEMM_OP_N;
+        size_t need = 0;
+        check(sgemmGroupedWorkspaceSize(c.handle, ty, op, T, N, K, G, mx.ptr, mx.ld, mw.ptr, mw.ld, mw.stride, &need),
+              "sgemmGroupedWorkspaceSize");
+        c.workspace(need);
+        check(sgemmGrouped(c.handle, ty, op, T, N, K, G, mx.ptr, mx.ld, mw.ptr, mw.ld, mw.stride, ends, my.ptr, my.ld,
+                           c.stream), "sgemmGrouped");
+        return wrap(out);
+    });
+}
+
+// (x, dy, group_ends, trans_w, out, handle, stream)
+PyObject *py_grouped_gemm_weight_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&] {
+        expect(n, 7);
+        const at::Tensor &x = tensor(a[0], "x"), &dy = tensor(a[1], "dy");
+        const sgemmDataType_t ty = type_of(x, "x");
+        const c10::Device dev = device_of(x, "x");
+        const at::ScalarType st = x.scalar_type();
+        Matrix l = matrix(x, "x", st, dev), r = matrix(dy, "dy", st, dev);
+        if (l.rows != r.rows)
+            fail(PyExc_ValueError, "x has %lld rows, dy has %lld", (long long)l.rows, (long long)r.rows);
+        if (PyObject_IsTrue(a[3])) std::swap(l, r);
+        const int64_t T = l.rows, M = l.cols, N = r.cols;
+        const int32_t *ends = vector<int32_t>(a[2], "group_ends", at::kInt, dev, -1);
+        const int64_t G = THPVariable_Unpack(a[2]).size(0);
+        const at::Tensor out = output(a[4], {G, M, N}, st, dev);
+        const Matrix mc = stack(out, "out", st, dev, G, M, N);
+        const Call c(a[5], a[6], dev);
+        size_t need = 0;
+        check(sgemmGroupedWeightGradWorkspaceSize(c.handle, ty, T, M, N, G, l.ptr, l.ld, r.ptr, r.ld, &need),
+              "sgemmGroupedWeightGradWorkspaceSize");
+        c.workspace(need);
+        check(sgemmGroupedWeightGrad(c.handle, ty, T, M, N, G, l.ptr, l.ld, r.ptr, r.ld, ends, mc.ptr, mc.ld,
+                                     mc.stride, c.stream), "sgemmGroupedWeightGrad");
+        return wrap(out);
+    });
+}
+
+struct LossOperands {
+    sgemmDataType_t ty;
+    c10::Device dev;
+    at::ScalarType st;
+    Matrix x, w;
+    const int64_t *target;
+    LossOperands(PyObject *px, PyObject *pw, PyObject *pt) : dev(c10::kCPU) {
+        const at::Tensor &tx = tensor(px, "x"), &tw = tensor(pw, "w");
+        ty = type_of(tx, "x");
+        dev = device_of(tx, "x");
+        st = tx.scalar_type();
+        x = matrix(tx, "x", st, dev);
+        w = matrix(tw, "w", st, dev);
+        if (x.cols != w.cols)
+            fail(PyExc_ValueError, "x has %lld columns, w %lld", (long long)x.cols, (long long)w.cols);
+        target = vector<int64_t>(pt, "target", at::kLong, dev, x.rows);
+    }
+};
+
+// (x, w, target, handle, stream) -> (loss, lse)
+PyObject *py_linear_cross_entropy(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&] {
+        expect(n, 5);
+        const LossOperands o(a[0], a[1], a[2]);
+        const int64_t T = o.x.rows, V = o.w.rows, D = o.x.cols;
+        const at::Tensor loss = make({T}, at::kFloat, o.dev), lse = make({T}, at::kFloat, o.dev);
+        const Call c(a[3], a[4], o.dev);
+        size_t need = 0;
+        check(sgemmCrossEntropyWorkspaceSize(c.handle, o.ty, T, V, D, o.x.ptr, o.x.ld, o.w.ptr, o.w.ld, &need),
+              "sgemmCrossEntropyWorkspaceSize");
+        c.workspace(need);
+        check(sgemmCrossEntropy(c.handle, o.ty, T, V, D, o.x.ptr, o.x.ld, o.w.ptr, o.w.ld, o.target,
+                                static_cast<float *>(loss.mutable_data_ptr()),
+                                static_cast<float *>(lse.mutable_data_ptr()), c.stream), "sgemmCrossEntropy");
+        return Py_BuildValue("NN", wrap(loss), wrap(lse));
+    });
+}
+
+// (x, w, target, lse, dloss, handle, stream) -> (dx, dw)
+PyObject *py_linear_cross_entropy_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&] {
+        expect(n, 7);
+        const LossOperands o(a[0], a[1], a[2]);
+        const int64_t T = o.x.rows, V = o.w.rows, D = o.x.cols;
+        const float *lse = vector<float>(a[3], "lse", at::kFloat, o.dev, T);
+        const float *dloss = vector<float>(a[4], "dloss", at::kFloat, o.dev, T);
+        const at::Tensor dx = make({T, D}, o.st, o.dev), dw = make({V, D}, o.st, o.dev);
+        const Call c(a[5], a[6], o.dev);
+        size_t need = 0;
+        check(sgemmCrossEntropyGradWorkspaceSize(c.handle, o.ty, T, V, D, o.x.ptr, o.x.ld, o.w.ptr, o.w.ld, &need),
+              "sgemmCrossEntropyGradWorkspaceSize");
+        c.workspace(need);
+        check(sgemmCrossEntropyGrad(c.handle, o.ty, T, V, D, o.x.ptr, o.x.ld, o.w.ptr, o.w.ld, o.target, lse, dloss,
+                                    dx.mutable_data_ptr(), std::max<int64_t>(D, 1), dw.mutable_data_ptr(),
+                                    std::max<int64_t>(D, 1), c.stream), "sgemmCrossEntropyGrad");
+        return Py_BuildValue("NN", wrap(dx), wrap(dw));
+    });
+}
+
+// (x, q, scales, zeros, out, handle, stream)
+PyObject *py_w4_gemm(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&] {
+        expect(n, 7);
+        const at::Tensor &x = tensor(a[0], "x"), &q = tensor(a[1], "q"), &s = tensor(a[2], "scales");
+        const sgemmDataType_t ty = type_of(x, "x");
+        const c10::Device dev = device_of(x, "x");
+        const at::ScalarType st = x.scalar_type();
+        const Matrix mx = matrix(x, "x", st, dev);
+        const int64_t M = mx.rows, K = mx.cols;
+        const Matrix mq = matrix(q, "q", at::kByte, dev, -1, K / 2);
+        const int64_t N = mq.rows;
+        const Matrix ms = matrix(s, "scales", st, dev, N, -1);
+        const int64_t groups = ms.cols;
+        if (groups == 0 ? K != 0 : K % groups != 0 || K == 0)
+            fail(PyExc_ValueError, "%lld groups do not divide %lld columns", (long long)groups, (long long)K);
+        const int64_t group = groups == 0 ? 32 : K / groups;
+        Matrix mz;
+        mz.ld = 0;
+        if (a[3] != Py_None) mz = matrix(tensor(a[3], "zeros"), "zeros", at::kByte, dev, N, groups);
+        const at::Tensor out = output(a[4], {M, N}, st, dev);
+        const Matrix my = matrix(out, "out", st, dev, M, N);
+        const Call c(a[5], a[6], dev);
+        const int gr = group > 1024 ? 1024 : int(group);       // beyond any that is taken
+        size_t need = 0;
+        check(sgemmW4WorkspaceSize(c.handle, ty, M, N, K, gr, &need), "sgemmW4WorkspaceSize");
+        c.workspace(need);
+        check(sgemmW4(c.handle, ty, M, N, K, gr, mx.ptr, mx.ld, static_cast<const uint8_t *>(mq.ptr), mq.ld, ms.ptr,
+                      ms.ld, static_cast<const uint8_t *>(mz.ptr), mz.ld, my.ptr, my.ld, c.stream), "sgemmW4");
+        return wrap(out);
+    });
+}
+
+PyMethodDef methods[] = {
+    {"grouped_gemm", reinterpret_cast<PyCFunction>(py_grouped_gemm), METH_FASTCALL, nullptr},
+    {"grouped_gemm_weight_grad", reinterpret_cast<PyCFunction>(py_grouped_gemm_weight_grad), METH_FASTCALL, nullptr},
+    {"linear_cross_entropy", reinterpret_cast<PyCFunction>(py_linear_cross_entropy), METH_FASTCALL, nullptr},
+    {"linear_cross_entropy_grad", reinterpret_cast<PyCFunction>(py_linear_cross_entropy_grad), METH_FASTCALL,
+     nullptr},
+    {"w4_gemm", reinterpret_cast<PyCFunction>(py_w4_gemm), METH_FASTCALL, nullptr},
+    {nullptr, nullptr, 0, nullptr}};
+
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_lm_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__lm_binding(void) {
+    PyObject *b = PyImport_ImportModule("fp32_sgemm_gb300._binding");
+    if (b == nullptr) return nullptr;
+    g_check = PyObject_GetAttrString(b, "_check");
+    g_stream_ptr = PyObject_GetAttrString(b, "_stream_ptr");
+    Py_DECREF(b);
+    g_name_ptr = PyUnicode_InternFromString("address");
+    g_name_bytes = PyUnicode_InternFromString("workspace_bytes");
+    g_name_grow = PyUnicode_InternFromString("_ensure_workspace");
+    if (g_check == nullptr || g_stream_ptr == nullptr || g_name_ptr == nullptr || g_name_bytes == nullptr ||
+        g_name_grow == nullptr)
+        return nullptr;
+    return PyModule_Create(&module);
+}

@@ -178,15 +178,18 @@ struct W4Meta {
 };
 
 // TYPE: 0 FP32, 1 f16, 2 bf16.  8 * NB columns on the N side.
-template <int TYPE, int GROUP, int NB>
-__global__ void __launch_bounds__(kW4MaxWarps * 32)
+// WARPS: 8, three CTAs on an SM (kept to the registers for that), or one CTA of 16 where
+// x takes most of shared memory (8 for 32 columns).
+template <int TYPE, int GROUP, int NB, int WARPS, int MIN_CTAS>
+__global__ void __launch_bounds__(WARPS * 32, MIN_CTAS)
 lm_w4_kernel(const W4Args p) {
+    constexpr int kW4Stages = w4_stages(MIN_CTAS), kW4RingBytes = kW4Stages * 2048;
+    constexpr int warps = WARPS;
     constexpr bool BF16 = TYPE != 1;
     constexpr int PLANES = TYPE == 0 ? 3 : 1;
     constexpr int SLOTS = GROUP / 32;                     // words a lane takes of a group and row
     constexpr int NG = 256 / GROUP;                       // groups per step
     extern __shared__ __align__(128) unsigned char smem_raw[];
-    const int warps = blockDim.x >> 5;
     unsigned char *ring = smem_raw;
     float *red = reinterpret_cast<float *>(smem_raw + warps * kW4RingBytes);   // [2][warp][NB * 4][32]
     unsigned char *xs = reinterpret_cast<unsigned char *>(red) + 2 * warps * NB * 512;   // [column][x_pitch]
@@ -255,7 +258,7 @@ lm_w4_kernel(const W4Args p) {
     // 128 columns in the order in which the lanes q = 0..3 take them.
     {
         const int chunks = steps * 32;                    // of 8 columns
-        for (int i = threadIdx.x; i < chunks * p.tokens; i += blockDim.x) {
+        for (int i = threadIdx.x; i < chunks * p.tokens; i += WARPS * 32) {
             const int t = i / chunks, c = i - t * chunks, k = k_begin + c * 8;
             // Chunk c is word `slot` of lane `lq`; see the loop below.
             const int in = c & 15;
@@ -430,7 +433,7 @@ lm_w4_kernel(const W4Args p) {
             for (int i = 0; i < 4; ++i) buf[(warp * NB * 4 + n * 4 + i) * 32 + lane] = sum[n][i];
         __syncthreads();
         const int row0 = ((int)blockIdx.x + b * (int)gridDim.x) << 4;
-        for (int o = threadIdx.x; o < 16 * p.tokens; o += blockDim.x) {
+        for (int o = threadIdx.x; o < 16 * p.tokens; o += WARPS * 32) {
             const int t = o >> 4, r = o & 15;
             float y = 0.f;
 #pragma unroll
@@ -440,6 +443,7 @@ lm_w4_kernel(const W4Args p) {
                 const int col = t * PLANES + pl;
                 const int at = ((col >> 3) * 4 + (r >> 3) * 2 + (col & 1)) * 32 + (r & 7) * 4 + ((col & 7) >> 1);
                 float v = 0.f;
+#pragma unroll
                 for (int w = 0; w < warps; ++w) v += buf[w * NB * 128 + at];
                 y += v;
             }
@@ -459,21 +463,20 @@ lm_w4_kernel(const W4Args p) {
     }
 }
 
+template <int TYPE, int GROUP>
+const void *w4_kernel_by_size(int nb, bool alone) {
+    if (nb == 1)
+        return alone ? reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, GROUP, 1, 16, 1>)
+                     : reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, GROUP, 1, 8, 3>);
+    if (nb == 2)
+        return alone ? reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, GROUP, 2, 16, 1>)
+                     : reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, GROUP, 2, 8, 3>);
+    return reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, GROUP, 4, 8, 1>);
+}
 template <int TYPE>
-const void *w4_kernel_of(int group, int nb) {
-    if (group == 32) {
-        if (nb == 1) return reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, 32, 1>);
-        if (nb == 2) return reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, 32, 2>);
-        return reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, 32, 4>);
-    }
-    if (group == 64) {
-        if (nb == 1) return reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, 64, 1>);
-        if (nb == 2) return reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, 64, 2>);
-        return reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, 64, 4>);
-    }
-    if (nb == 1) return reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, 128, 1>);
-    if (nb == 2) return reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, 128, 2>);
-    return reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, 128, 4>);
+const void *w4_kernel_of(int group, int nb, bool alone) {
+    return group == 32 ? w4_kernel_by_size<TYPE, 32>(nb, alone)
+         : group == 64 ? w4_kernel_by_size<TYPE, 64>(nb, alone) : w4_kernel_by_size<TYPE, 128>(nb, alone);
 }
 
 }  // namespace sg

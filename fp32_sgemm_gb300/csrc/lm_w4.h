@@ -26,12 +26,17 @@ struct W4Args {
     int64_t ld_part;
 };
 
-const void *w4_kernel_f32(int group, int nb);
-const void *w4_kernel_f16(int group, int nb);
-const void *w4_kernel_bf16(int group, int nb);
-constexpr int kW4MaxWarps = 16, kW4Stages = 4;
-constexpr int kW4RingBytes = kW4Stages * 2048;            // per warp
+// nb: blocks of 8 columns (1, 2 or 4); alone: one CTA has an SM for itself.
+const void *w4_kernel_f32(int group, int nb, bool alone);
+const void *w4_kernel_f16(int group, int nb, bool alone);
+const void *w4_kernel_bf16(int group, int nb, bool alone);
+constexpr int w4_warps(int nb, bool alone) { return alone && nb < 4 ? 16 : 8; }
+// Steps of 2 KB per warp in the ring: two in flight with three CTAs on an
+// SM, three with one.
+constexpr int w4_stages(int ctas) { return ctas > 1 ? 3 : 4; }
 // Shared memory beside the staged x.
-inline size_t w4_fixed_smem(int nb, int warps) { return size_t(warps) * (kW4RingBytes + 2 * nb * 512); }
+inline size_t w4_fixed_smem(int nb, bool alone) {
+    return size_t(w4_warps(nb, alone)) * (w4_stages(alone ? 1 : 3) * 2048 + 2 * nb * 512);
+}
 
 }  // namespace sg

@@ -2,6 +2,6 @@
 #include "lm_w4.cuh"
 
 namespace sg {
-const void *w4_kernel_bf16(int group, int nb) { return w4_kernel_of<2>(group, nb); }
+const void *w4_kernel_bf16(int group, int nb, bool alone) { return w4_kernel_of<2>(group, nb, alone); }
 
 }  // namespace sg

@@ -2,5 +2,5 @@
 #include "lm_w4.cuh"
 
 namespace sg {
-const void *w4_kernel_f32(int group, int nb) { return w4_kernel_of<0>(group, nb); }
+const void *w4_kernel_f32(int group, int nb, bool alone) { return w4_kernel_of<0>(group, nb, alone); }
 }  // namespace sg
