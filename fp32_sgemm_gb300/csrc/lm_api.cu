@@ -750,6 +750,19 @@ sgemmStatus_t sgemmW4(sgemmHandle_t h, sgemmDataType_t type, int64_t M, int64_t 
                                                                                    : SGEMM_STATUS_LAUNCH_FAILED;
     if (q.ws > 0 && (h->ws == nullptr || h->ws_bytes < q.ws)) return SGEMM_STATUS_WORKSPACE_REQUIRED;
 
+    // Q as bytes: boxes of 16 rows by 128 bytes (256 columns).
+    CUtensorMap tm_q;
+    {
+        auto enc = sg::tensor_map_encoder();
+        if (enc == nullptr) return SGEMM_STATUS_LAUNCH_FAILED;
+        cuuint64_t dims[2] = {cuuint64_t(K / 2), cuuint64_t(N)};
+        cuuint64_t strides[1] = {cuuint64_t(N > 1 ? ldq : round_up(K / 2, 16))};
+        cuuint32_t box[2] = {128, 16}, one[2] = {1, 1};
+        if (enc(&tm_q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(Q), dims, strides, box, one,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return SGEMM_STATUS_LAUNCH_FAILED;
+    }
     for (int64_t t0 = 0; t0 < M; t0 += q.most) {
         const int tokens = int(std::min<int64_t>(q.most, M - t0));
         const int cols = tokens * q.planes, nb = w4_blocks(cols);
@@ -775,12 +788,14 @@ sgemmStatus_t sgemmW4(sgemmHandle_t h, sgemmDataType_t type, int64_t M, int64_t 
         p.part = q.slices > 1 ? static_cast<float *>(h->ws) : nullptr;
         p.ld_part = round_up(N, 8);
         LmKernel k;
-        // Three CTAs on an SM where they fit, else one with more warps.
+        // Two CTAs on an SM where they fit, else one with more warps.
         const int64_t xs = int64_t(cols) * p.x_pitch;
-        const bool alone = nb == 4 || int64_t(sg::w4_fixed_smem(nb, false)) + xs > 75 * 1024;
+        const bool alone = nb == 4 || int64_t(sg::w4_fixed_smem(nb, false)) + xs > 113 * 1024;
         const int smem = int(int64_t(sg::w4_fixed_smem(nb, alone)) + xs);
-        k.fn = type == SGEMM_TYPE_F32 ? sg::w4_kernel_f32(group, nb, alone)
-               : type == SGEMM_TYPE_F16 ? sg::w4_kernel_f16(group, nb, alone) : sg::w4_kernel_bf16(group, nb, alone);
+        const bool z = zeros != nullptr;
+        k.fn = type == SGEMM_TYPE_F32 ? sg::w4_kernel_f32(group, nb, z, alone)
+               : type == SGEMM_TYPE_F16 ? sg::w4_kernel_f16(group, nb, z, alone)
+                                        : sg::w4_kernel_bf16(group, nb, z, alone);
         k.threads = sg::w4_warps(nb, alone) * 32;
         const int slots = resident_slots(h, k, smem);
         if (slots < 1) return SGEMM_STATUS_LAUNCH_FAILED;
@@ -796,7 +811,9 @@ sgemmStatus_t sgemmW4(sgemmHandle_t h, sgemmDataType_t type, int64_t M, int64_t 
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        void *kargs[] = {&p};
+        p.err = h->d_err;
+        p.timeout_ns = h->timeout_ns;
+        void *kargs[] = {&tm_q, &p};
         if (cudaLaunchKernelExC(&cfg, k.fn, kargs) != cudaSuccess) return SGEMM_STATUS_LAUNCH_FAILED;
         if (q.slices > 1 &&
             sg::lm_launch_join_splits(p.part, p.ld_part, int64_t(tokens) * p.ld_part, q.slices, nullptr, tokens, int(N),

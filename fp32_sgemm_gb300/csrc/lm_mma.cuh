@@ -31,7 +31,7 @@
 #include <cuda_fp16.h>
 
 #include "lm_kernels.h"
-#include "ptx.cuh"
+#include "lm_ptx.cuh"
 
 namespace sg {
 
@@ -79,13 +79,6 @@ __device__ __forceinline__ uint32_t idesc_f16(uint32_t bf16, bool a_mn, bool b_m
 // once per stage, that halved the rate of the weight gradients.)
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_bar) : "memory");
-}
-
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t is;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
-    return is != 0;
 }
 
 __device__ __forceinline__ void fence_proxy_async_smem() {

@@ -5,7 +5,7 @@
 // The weights are read once (half a byte each) and that read bounds the
 // product, so everything else is kept off its way:
 //   * each warp streams 16 weight rows, 256 columns (2 KB) at a time, through
-//     its own ring of asynchronous copies;
+//     its own ring of TMA copies;
 //   * q - z is an integer of at most 5 bits, exact in f16 and bf16, so the
 //     weights meet x in the tensor core unscaled (mma.sync m16n8k16, the rows
 //     of W on the M side, 8 tokens on the N side) and the scale is applied to
@@ -26,21 +26,10 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "lm_ptx.cuh"
 #include "lm_w4.h"
-#include "ptx.cuh"
 
 namespace sg {
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src, bool valid) {
-    const uint32_t n = valid ? 16u : 0u;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
 
 template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -111,7 +100,7 @@ struct W4Unpack {
 
 // N scales of one row (raw bits; 16-bit ones two to a register) and N zero
 // points (bytes), by vector loads where the rows are aligned for them.
-template <int TYPE, int N>
+template <int TYPE, int N, bool ZEROS>
 struct W4Meta {
     static constexpr int REGS = TYPE == 0 ? N : N / 2;
     uint32_t s[REGS];
@@ -143,7 +132,7 @@ struct W4Meta {
                     else s[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(scales)[j] << (16 * (j & 1));
                 }
         }
-        if (p.zeros != nullptr) {
+        if constexpr (ZEROS) {
             if (p.z_vec && n == N) {
                 if constexpr (N == 2) z[0] = *reinterpret_cast<const uint16_t *>(zeros);
                 else if constexpr (N == 4) z[0] = *reinterpret_cast<const uint32_t *>(zeros);
@@ -158,9 +147,6 @@ struct W4Meta {
                 for (int j = 0; j < N; ++j)
                     if (j < n) z[j / 4] |= (uint32_t)zeros[j] << (8 * (j & 3));
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < (N + 3) / 4; ++i) z[i] = 0x08080808u;
         }
     }
     __device__ __forceinline__ float scale(int j) const {
@@ -173,86 +159,69 @@ struct W4Meta {
     }
     // z twice in the low bits of two halves.
     __device__ __forceinline__ uint32_t zero(int j) const {
-        return ((z[j / 4] >> (8 * (j & 3))) & 15u) * 0x10001u;
+        if constexpr (!ZEROS) return 0x00080008u;
+        else return ((z[j / 4] >> (8 * (j & 3))) & 15u) * 0x10001u;
     }
 };
 
 // TYPE: 0 FP32, 1 f16, 2 bf16.  8 * NB columns on the N side.
-// WARPS: 8, three CTAs on an SM (kept to the registers for that), or one CTA of 16 where
-// x takes most of shared memory (8 for 32 columns).
-template <int TYPE, int GROUP, int NB, int WARPS, int MIN_CTAS>
+// WARPS: 8 with two CTAs on an SM, or one CTA of 16 where x takes most of
+// shared memory (8 for 32 columns: more registers).
+template <int TYPE, int GROUP, int NB, bool ZEROS, int WARPS, int MIN_CTAS>
 __global__ void __launch_bounds__(WARPS * 32, MIN_CTAS)
-lm_w4_kernel(const W4Args p) {
-    constexpr int kW4Stages = w4_stages(MIN_CTAS), kW4RingBytes = kW4Stages * 2048;
-    constexpr int warps = WARPS;
+lm_w4_kernel(const __grid_constant__ CUtensorMap tmQ, const W4Args p) {
     constexpr bool BF16 = TYPE != 1;
     constexpr int PLANES = TYPE == 0 ? 3 : 1;
     constexpr int SLOTS = GROUP / 32;                     // words a lane takes of a group and row
     constexpr int NG = 256 / GROUP;                       // groups per step
-    extern __shared__ __align__(128) unsigned char smem_raw[];
-    unsigned char *ring = smem_raw;
-    float *red = reinterpret_cast<float *>(smem_raw + warps * kW4RingBytes);   // [2][warp][NB * 4][32]
-    unsigned char *xs = reinterpret_cast<unsigned char *>(red) + 2 * warps * NB * 512;   // [column][x_pitch]
+    constexpr int STAGES = kW4Stages;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    unsigned char *ring = smem;
+    float *red = reinterpret_cast<float *>(smem + WARPS * STAGES * 2048);      // [2][warp][NB * 4][32]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(red + 2 * WARPS * NB * 128);
+    unsigned char *xs = reinterpret_cast<unsigned char *>(bars + WARPS * STAGES);   // [column][x_pitch]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, q = lane & 3;
     // This CTA's slice of K and this warp's steps in it.
     const int k_begin = blockIdx.y * p.k_slice, k_end = min(p.K, k_begin + p.k_slice);
     const int steps = (k_end - k_begin + 255) >> 8;
-    const int s0 = steps * warp / warps, per = steps * (warp + 1) / warps - s0;
+    const int s0 = steps * warp / WARPS, per = steps * (warp + 1) / WARPS - s0;
     const int k_warp = k_begin + s0 * 256;
     const int blocks = (p.N + 15) >> 4;
     const int mine = blocks > (int)blockIdx.x ? (blocks - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
 
+    // Per warp: a ring of 2 KB stages filled by TMA (16 rows of 128 bytes,
+    // 128-byte swizzle: 16-byte piece c of row r sits at c ^ (r % 8); rows
+    // past N and columns past K arrive as zeros).
+    unsigned char *ring_w = ring + warp * (STAGES * 2048);
+    uint64_t *full = bars + warp * STAGES;
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], 1);
+        fence_barrier_init();
+    }
+    __syncwarp();
     griddep_launch_dependents();
     griddep_wait();
-
-    // Rows of 128 bytes; 16-byte piece c of row r sits at c ^ swizzle(r), so
-    // that the rows a warp reads together meet different banks.
-    auto swizzle = [](int r) { return GROUP == 32 ? r & 7 : GROUP == 64 ? (r & 3) * 2 : (r & 1) * 4; };
-    unsigned char *ring_w = ring + warp * kW4RingBytes;
-    // Copies: lane takes piece lane % 8 of rows lane / 8 + 4 i.
-    const int lr = lane >> 3, lp = lane & 7;
-    uint32_t dst[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) dst[i] = smem_u32(ring_w) + (lr + 4 * i) * 128 + ((lp ^ swizzle(lr + 4 * i)) << 4);
-    const uint8_t *src[4];
-    int ld_b = 0, ld_s = 0, ld_k = k_warp;
-    uint32_t ld_off = 0;
-    auto point = [&]() {
-        const int row0 = ((int)blockIdx.x + ld_b * (int)gridDim.x) << 4;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            src[i] = p.Q + (int64_t)min(row0 + lr + 4 * i, p.N - 1) * p.ldq + (k_warp >> 1) + lp * 16;
-    };
+    int ld_row = (int)blockIdx.x << 4, ld_s = 0, ld_stage = 0;
     auto issue = [&]() {
-        if (ld_b < mine) {
-            if (ld_k + 256 <= k_end) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) cp_async16(dst[i] + ld_off, src[i]);
-            } else {
-                const bool valid = ld_k + lp * 32 < k_end;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) cp_async16_or_zero(dst[i] + ld_off, valid ? src[i] : p.Q, valid);
+        if (ld_row < p.N && per > 0) {
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&full[ld_stage], 2048);
+                tma_load_2d(ring_w + ld_stage * 2048, &tmQ, &full[ld_stage], (k_warp >> 1) + ld_s * 128, ld_row);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) src[i] += 128;
-            ld_k += 256;
-            ld_off = ld_off == (kW4Stages - 1) * 2048 ? 0 : ld_off + 2048;
+            __syncwarp();
+            ld_stage = ld_stage == STAGES - 1 ? 0 : ld_stage + 1;
             if (++ld_s == per) {
                 ld_s = 0;
-                ld_k = k_warp;
-                ++ld_b;
-                point();
+                ld_row += (int)gridDim.x << 4;
             }
         }
-        cp_async_commit();
     };
-    if (per > 0) {
-        point();
 #pragma unroll
-        for (int i = 0; i < kW4Stages - 1; ++i) issue();
-    }
+    for (int i = 0; i < STAGES - 1; ++i) issue();
 
     // x in nibble order (within 8 columns 0 4 1 5 2 6 3 7), the 16 chunks of
     // 128 columns in the order in which the lanes q = 0..3 take them.
@@ -291,7 +260,7 @@ lm_w4_kernel(const W4Args p) {
                 }
             } else {
                 const uint16_t *sx = static_cast<const uint16_t *>(p.X) + (int64_t)t * p.ldx + k;
-                uint16_t v[8];
+                alignas(16) uint16_t v[8];
                 if (p.x_vec && k + 8 <= k_end) {
                     *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(sx);
                 } else {
@@ -309,39 +278,35 @@ lm_w4_kernel(const W4Args p) {
     }
 
     // Scales and zero points come one step ahead of their use.
-    W4Meta<TYPE, NG> ma, mb, na, nb;
+    W4Meta<TYPE, NG, ZEROS> ma, mb, na, nb;
     constexpr int SB = TYPE == 0 ? 4 : 2;                 // bytes of a scale
     const unsigned char *sa = nullptr, *sb = nullptr;
     const uint8_t *za = nullptr, *zb = nullptr;
-    int m_b = 0, m_s = 0;
-    auto point_meta = [&]() {
-        const int row0 = ((int)blockIdx.x + m_b * (int)gridDim.x) << 4;
+    auto point_meta = [&](int row0) {
         const int64_t ra = min(row0 + g, p.N - 1), rb = min(row0 + g + 8, p.N - 1);
         const unsigned char *base = static_cast<const unsigned char *>(p.scales) + (k_warp / GROUP) * SB;
         sa = base + ra * p.lds * SB;
         sb = base + rb * p.lds * SB;
-        za = p.zeros + ra * p.ldz + k_warp / GROUP;
-        zb = p.zeros + rb * p.ldz + k_warp / GROUP;
-    };
-    auto meta = [&]() {
-        if (m_b < mine) {
-            const int n = min(NG, (k_end - k_warp - m_s * 256) / GROUP);
-            na.load(p, sa, za, n);
-            nb.load(p, sb, zb, n);
-            sa += NG * SB;
-            sb += NG * SB;
-            za += NG;
-            zb += NG;
-            if (++m_s == per) {
-                m_s = 0;
-                ++m_b;
-                point_meta();
-            }
+        if constexpr (ZEROS) {
+            za = p.zeros + ra * p.ldz + k_warp / GROUP;
+            zb = p.zeros + rb * p.ldz + k_warp / GROUP;
         }
     };
-    if (per > 0) {
-        point_meta();
-        meta();
+    const int n_last = (k_end - k_warp - (per - 1) * 256) / GROUP;     // groups in this warp's last step
+    auto load_meta = [&](int s) {
+        const int n = s == per - 1 ? min(NG, n_last) : NG;
+        na.load(p, sa, za, n);
+        nb.load(p, sb, zb, n);
+        sa += NG * SB;
+        sb += NG * SB;
+        if constexpr (ZEROS) {
+            za += NG;
+            zb += NG;
+        }
+    };
+    if (per > 0 && mine > 0) {
+        point_meta((int)blockIdx.x << 4);
+        load_meta(0);
     }
     __syncthreads();
 
@@ -351,10 +316,11 @@ lm_w4_kernel(const W4Args p) {
     const unsigned char *x_lane[NB];
 #pragma unroll
     for (int n = 0; n < NB; ++n) x_lane[n] = xs + (s0 * 32 + q) * 16 + min(n * 8 + g, cols - 1) * p.x_pitch;
-    // Words of a lane: row g (g + 8), of each 128 columns.
-    const int sw = swizzle(g);                 // swizzle(g + 8) is the same
-    int off = 0;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
     for (int b = 0; b < mine; ++b) {
+        const int row0 = ((int)blockIdx.x + b * (int)gridDim.x) << 4;
         float sum[NB][4];
 #pragma unroll
         for (int n = 0; n < NB; ++n)
@@ -363,23 +329,30 @@ lm_w4_kernel(const W4Args p) {
         for (int s = 0; s < per; ++s) {
             ma = na;
             mb = nb;
-            meta();
-            cp_async_wait<kW4Stages - 2>();
-            __syncwarp();
-            const unsigned char *st = ring_w + off + g * 128;
+            if (s + 1 < per) {
+                load_meta(s + 1);
+            } else if (b + 1 < mine) {
+                point_meta(row0 + ((int)gridDim.x << 4));
+                load_meta(0);
+            }
+            if (ok && !mbar_wait_bounded(&full[stage], phase, p.timeout_ns)) {
+                record_error(p.err, kSiteConsumerFull);
+                ok = false;
+            }
+            const unsigned char *st = ring_w + stage * 2048 + g * 128;
             uint32_t wa[8], wb[8];
             if constexpr (GROUP == 128) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint4 u = *reinterpret_cast<const uint4 *>(st + (((h * 4 + q) ^ sw) << 4));
-                    const uint4 v = *reinterpret_cast<const uint4 *>(st + 1024 + (((h * 4 + q) ^ sw) << 4));
+                    const uint4 u = *reinterpret_cast<const uint4 *>(st + (((h * 4 + q) ^ g) << 4));
+                    const uint4 v = *reinterpret_cast<const uint4 *>(st + 1024 + (((h * 4 + q) ^ g) << 4));
                     wa[4 * h] = u.x; wa[4 * h + 1] = u.y; wa[4 * h + 2] = u.z; wa[4 * h + 3] = u.w;
                     wb[4 * h] = v.x; wb[4 * h + 1] = v.y; wb[4 * h + 2] = v.z; wb[4 * h + 3] = v.w;
                 }
             } else if constexpr (GROUP == 64) {
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
-                    const int at = (((h * 2 + (q >> 1)) ^ sw) << 4) + (q & 1) * 8;
+                    const int at = (((h * 2 + (q >> 1)) ^ g) << 4) + (q & 1) * 8;
                     const uint2 u = *reinterpret_cast<const uint2 *>(st + at);
                     const uint2 v = *reinterpret_cast<const uint2 *>(st + 1024 + at);
                     wa[2 * h] = u.x; wa[2 * h + 1] = u.y;
@@ -388,14 +361,14 @@ lm_w4_kernel(const W4Args p) {
             } else {
 #pragma unroll
                 for (int h = 0; h < 8; ++h) {
-                    const int at = ((h ^ sw) << 4) + q * 4;
+                    const int at = ((h ^ g) << 4) + q * 4;
                     wa[h] = *reinterpret_cast<const uint32_t *>(st + at);
                     wb[h] = *reinterpret_cast<const uint32_t *>(st + 1024 + at);
                 }
             }
+            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
             __syncwarp();
             issue();
-            off = off == (kW4Stages - 1) * 2048 ? 0 : off + 2048;
             // Past the end of K the words are 0 and x is 0: they add nothing.
             float c[NB][4];
 #pragma unroll
@@ -426,13 +399,12 @@ lm_w4_kernel(const W4Args p) {
             }
         }
         // Join the warps' sums (two buffers: a warp may be one block ahead).
-        float *buf = red + (b & 1) * (warps * NB * 128);
+        float *buf = red + (b & 1) * (WARPS * NB * 128);
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) buf[(warp * NB * 4 + n * 4 + i) * 32 + lane] = sum[n][i];
         __syncthreads();
-        const int row0 = ((int)blockIdx.x + b * (int)gridDim.x) << 4;
         for (int o = threadIdx.x; o < 16 * p.tokens; o += WARPS * 32) {
             const int t = o >> 4, r = o & 15;
             float y = 0.f;
@@ -444,7 +416,7 @@ lm_w4_kernel(const W4Args p) {
                 const int at = ((col >> 3) * 4 + (r >> 3) * 2 + (col & 1)) * 32 + (r & 7) * 4 + ((col & 7) >> 1);
                 float v = 0.f;
 #pragma unroll
-                for (int w = 0; w < warps; ++w) v += buf[w * NB * 128 + at];
+                for (int w = 0; w < WARPS; ++w) v += buf[w * NB * 128 + at];
                 y += v;
             }
             const int n = row0 + r;
@@ -463,20 +435,21 @@ lm_w4_kernel(const W4Args p) {
     }
 }
 
-template <int TYPE, int GROUP>
+template <int TYPE, int GROUP, bool ZEROS>
 const void *w4_kernel_by_size(int nb, bool alone) {
     if (nb == 1)
-        return alone ? reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, GROUP, 1, 16, 1>)
-                     : reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, GROUP, 1, 8, 3>);
+        return alone ? reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, GROUP, 1, ZEROS, 16, 1>)
+                     : reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, GROUP, 1, ZEROS, 8, 2>);
     if (nb == 2)
-        return alone ? reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, GROUP, 2, 16, 1>)
-                     : reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, GROUP, 2, 8, 3>);
-    return reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, GROUP, 4, 8, 1>);
+        return alone ? reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, GROUP, 2, ZEROS, 16, 1>)
+                     : reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, GROUP, 2, ZEROS, 8, 2>);
+    return reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, GROUP, 4, ZEROS, 8, 1>);
 }
-template <int TYPE>
-const void *w4_kernel_of(int group, int nb, bool alone) {
-    return group == 32 ? w4_kernel_by_size<TYPE, 32>(nb, alone)
-         : group == 64 ? w4_kernel_by_size<TYPE, 64>(nb, alone) : w4_kernel_by_size<TYPE, 128>(nb, alone);
+template <int TYPE, bool ZEROS>
+const void *w4_kernel_by_group(int group, int nb, bool alone) {
+    return group == 32 ? w4_kernel_by_size<TYPE, 32, ZEROS>(nb, alone)
+         : group == 64 ? w4_kernel_by_size<TYPE, 64, ZEROS>(nb, alone)
+                       : w4_kernel_by_size<TYPE, 128, ZEROS>(nb, alone);
 }
 
 }  // namespace sg

@@ -24,19 +24,19 @@ struct W4Args {
     int64_t ldy;
     float *part;               // [slice][token][ld_part] FP32, or NULL for Y itself
     int64_t ld_part;
+    uint32_t *err;
+    uint64_t timeout_ns;
 };
 
 // nb: blocks of 8 columns (1, 2 or 4); alone: one CTA has an SM for itself.
-const void *w4_kernel_f32(int group, int nb, bool alone);
-const void *w4_kernel_f16(int group, int nb, bool alone);
-const void *w4_kernel_bf16(int group, int nb, bool alone);
+const void *w4_kernel_f32(int group, int nb, bool zeros, bool alone);
+const void *w4_kernel_f16(int group, int nb, bool zeros, bool alone);
+const void *w4_kernel_bf16(int group, int nb, bool zeros, bool alone);
+constexpr int kW4Stages = 4;                              // of 2 KB, per warp
 constexpr int w4_warps(int nb, bool alone) { return alone && nb < 4 ? 16 : 8; }
-// Steps of 2 KB per warp in the ring: two in flight with three CTAs on an
-// SM, three with one.
-constexpr int w4_stages(int ctas) { return ctas > 1 ? 3 : 4; }
-// Shared memory beside the staged x.
+// Shared memory beside the staged x: rings, the warps' sums twice, barriers.
 inline size_t w4_fixed_smem(int nb, bool alone) {
-    return size_t(w4_warps(nb, alone)) * (w4_stages(alone ? 1 : 3) * 2048 + 2 * nb * 512);
+    return 1024 + size_t(w4_warps(nb, alone)) * (kW4Stages * (2048 + 8) + 2 * nb * 512);
 }
 
 }  // namespace sg
