@@ -91,28 +91,47 @@ lm_split3_kernel(const float *src, int64_t ld, int64_t stride, uint16_t *dst, in
     }
 }
 
-// One warp per row joins the slabs' {maximum, sum of exp(l - maximum)} in a
-// fixed order.
-__global__ void __launch_bounds__(kThreads)
+// Joins the slabs' {maximum, sum of exp(l - maximum)} of each row in a fixed
+// order: 32 rows per CTA, one per lane (neighbouring rows are neighbours in
+// memory), the slabs dealt to 32 warps; first the maximum, then the sum, so
+// that the exponentials do not wait for one another.
+constexpr int kJoinWarps = 32;
+__global__ void __launch_bounds__(kJoinWarps * 32)
 lm_lse_join_kernel(const float2 *part, int slabs, int rows, const float *picked, const int64_t *target,
                    int64_t vocab, float *loss, float *lse) {
     griddep_launch_dependents();
     griddep_wait();
-    const int row = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (row >= rows) return;
-    float m = -INFINITY;
-    for (int i = lane; i < slabs; i += 32) m = fmaxf(m, part[(int64_t)i * rows + row].x);
+    __shared__ float met[kJoinWarps][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = min(blockIdx.x * 32 + lane, rows - 1);
+    constexpr int U = 8;                            // loads in flight
+    auto each = [&](auto &&f) {
+        for (int i = warp; i < slabs; i += U * kJoinWarps) {
+            float2 v[U];
 #pragma unroll
-    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+            for (int u = 0; u < U; ++u)
+                v[u] = part[(int64_t)min(i + u * kJoinWarps, slabs - 1) * rows + row];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i + u * kJoinWarps < slabs) f(v[u]);
+        }
+    };
+    float m = -INFINITY;
+    each([&](float2 v) { m = fmaxf(m, v.x); });
+    met[warp][lane] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, met[w][lane]);
     const float ref = m == -INFINITY ? 0.f : m;
     float s = 0.f;
-    for (int i = lane; i < slabs; i += 32) {
-        const float2 p = part[(int64_t)i * rows + row];
-        s += p.y * expf(p.x - ref);
-    }
+    each([&](float2 v) { s += v.y * expf(v.x - ref); });
+    __syncthreads();
+    met[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && (int)blockIdx.x * 32 + lane < rows) {
+        s = 0.f;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-    if (lane == 0) {
+        for (int w = 0; w < kJoinWarps; ++w) s += met[w][lane];
         const float l = ref + logf(s);
         lse[row] = l;
         const int64_t t = target[row];
@@ -204,8 +223,8 @@ cudaError_t lm_launch_split3(const float *src, int64_t ld, int64_t stride, void 
 
 cudaError_t lm_launch_lse_join(const float2 *part, int slabs, int rows, const float *picked, const int64_t *target,
                                int64_t vocab, float *loss, float *lse, cudaStream_t s) {
-    return launch(lm_lse_join_kernel, (rows + kThreads / 32 - 1) / (kThreads / 32), kThreads, s, part, slabs, rows,
-                  picked, target, vocab, loss, lse);
+    return launch(lm_lse_join_kernel, (rows + 31) / 32, kJoinWarps * 32, s, part, slabs, rows, picked, target,
+                  vocab, loss, lse);
 }
 
 cudaError_t lm_launch_grad_scale(const float *grad, const int64_t *target, int64_t vocab, int rows, float *scale2,

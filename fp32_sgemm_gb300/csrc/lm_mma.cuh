@@ -149,7 +149,7 @@ struct LmTile {
     static constexpr int SLAB = BN / (EPI_WARPS / 4);       // columns per epilogue warp
     static constexpr int TMEM_COLS = 2 * BN <= 64 ? 64 : 2 * BN <= 128 ? 128 : 2 * BN <= 256 ? 256 : 512;
     static constexpr int THREADS = (2 + EPI_WARPS) * 32;
-    static constexpr int BARS = 2 * STAGES + 6;
+    static constexpr int BARS = 3 * STAGES + 5;
     static constexpr int STG = STG_, STAGING = EPI_WARPS * STG * 4;
     // Ring, barriers (8 bytes each), TMEM address (16), epilogue staging;
     // the group tables of kRagN / kRagK follow.
@@ -362,6 +362,30 @@ __device__ __forceinline__ void lm_store_cols(const LmArgs &p, Out *base, int f0
     }
 }
 
+// kRagK, a group's last block of rows: once this SM's copies have landed,
+// the warp clears the rows behind the group (they belong to others) up to the
+// next multiple of 16, where the MMAs stop; both operands, so that an
+// infinity there does not meet a zero.  False if the copies did not land.
+template <class Tile>
+__device__ __forceinline__ bool lm_clear_tail(unsigned char *stage, uint64_t *landed, uint32_t parity, int rows,
+                                              const LmArgs &p, int lane) {
+    // The copies wait for a free stage, that for earlier products: the limit
+    // of a wait behind two others.
+    bool ok = mbar_wait_bounded(landed, parity, 2 * downstream_limit(p.timeout_ns));
+    if (!ok && lane == 0) record_error(p.err, kSiteConsumerFull);
+    ok = __all_sync(~0u, ok);
+    const int r1 = (rows + 15) & ~15, per = (r1 - rows) * 8;      // 16-byte words per chunk of 64 columns
+    constexpr int CHUNKS = Tile::STAGE_BYTES / 8192;
+    if (ok)
+        for (int i = lane; i < CHUNKS * per; i += 32) {
+            const int c = i / per;
+            *reinterpret_cast<uint4 *>(stage + c * 8192 + rows * 128 + (i - c * per) * 16) = make_uint4(0, 0, 0, 0);
+        }
+    fence_proxy_async_smem();
+    __syncwarp();
+    return ok;
+}
+
 // ---------------------------------------------------------------- kernel
 
 template <class Tile, bool A_MN, bool B_MN, int RAG, int EPI, bool CHUNKED>
@@ -380,7 +404,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     uint64_t *tfull = bars + 2 * STAGES;    // MMA -> epilogue, per accumulator
     uint64_t *tempty = tfull + 2;           // epilogue -> MMA, per accumulator
     uint64_t *drain = tempty + 2;           // MMA completion before teardown
-    uint64_t *tailbar = drain + 1;          // kRagK: copies of a group's last block
+    uint64_t *tailbar = drain + 1;          // kRagK, per stage: this SM's copies of a group's last block
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Tile::BARS);
     unsigned char *after = reinterpret_cast<unsigned char *>(bars) + ((Tile::BARS * 8 + 16 + 15) / 16) * 16;
     float *staging = reinterpret_cast<float *>(after);
@@ -396,17 +420,17 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     }
     if (threadIdx.x == 32) {
         for (int s = 0; s < STAGES; ++s) {
-            // kRagK on a pair: the other SM's producer arrives as well (it
-            // may have to clear rows of a group's last block first).
+            // kRagK on a pair: the other SM arrives as well (it may have to
+            // clear rows of a group's last block first).
             mbar_init(&full[s], PAIR && RAG == kRagK ? 2 : 1);
             mbar_init(&empty[s], 1);
+            mbar_init(&tailbar[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
             mbar_init(&tempty[b], (PAIR ? 2 : 1) * Tile::EPI_WARPS);
         }
         mbar_init(drain, 1);
-        mbar_init(tailbar, 1);
         fence_barrier_init();
         prefetch_tensormap(&tmA);
         prefetch_tensormap(&tmB);
@@ -427,7 +451,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     if (warp == 0) {
         // ---------------- TMA producer (one elected lane issues) ----------------
         int stage = 0, issued = 0;
-        uint32_t phase = 0, tail_phase = 0;
+        uint32_t phase = 0;
         bool ok = true;
         const uint32_t full_pair = PAIR ? cluster_addr(&full[0], 0) : 0u;   // rank 0's barriers
         for (int t = slot; ok && t < num_tiles; t += slots) {
@@ -484,35 +508,18 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                         }
                         __syncwarp();
                     } else {
-                        // The block's rows behind the group belong to others:
-                        // cleared up to the next multiple of 16, where the
-                        // MMAs stop (both operands, so that an infinity there
-                        // does not meet a zero).
+                        // Rows behind the group have to be cleared first
+                        // (lm_clear_tail): the copies report to this SM's
+                        // own barrier, rank 0's arrival stands for itself,
+                        // rank 1 arrives once it has cleared its part.
                         if (elect_one()) {
-                            mbar_arrive_expect_tx(tailbar, Tile::STAGE_BYTES);
+                            mbar_arrive_expect_tx(&tailbar[stage], Tile::STAGE_BYTES);
                             load_all([&](void *dst, const CUtensorMap *m, int c0, int c1, int c2) {
-                                tma_load_3d(dst, m, tailbar, c0, c1, c2);
+                                tma_load_3d(dst, m, &tailbar[stage], c0, c1, c2);
                             });
+                            if (rank == 0) mbar_arrive(&full[stage]);
                         }
                         __syncwarp();
-                        if (!mbar_wait_bounded(tailbar, tail_phase, downstream_limit(p.timeout_ns))) {
-                            if (lane == 0) record_error(p.err, kSiteConsumerFull);
-                            ok = false;
-                        }
-                        ok = __all_sync(~0u, ok);
-                        tail_phase ^= 1u;
-                        const int r0 = w.klast, r1 = (w.klast + 15) & ~15;
-                        constexpr int CHUNKS = (Tile::A_BYTES + Tile::B_BYTES) / 8192;
-                        for (int i = lane; i < CHUNKS * (r1 - r0) * 8; i += 32) {
-                            const int c = i / ((r1 - r0) * 8), in = i - c * (r1 - r0) * 8;
-                            *reinterpret_cast<uint4 *>(sa + c * 8192 + r0 * 128 + in * 16) = make_uint4(0, 0, 0, 0);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if (PAIR && rank != 0) mbar_arrive_cluster(fb);
-                            else mbar_arrive(&full[stage]);
-                        }
                     }
                     ++issued;
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
@@ -541,13 +548,16 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                                   : smem_desc_k_sw128(smem_u32(smem) + Tile::A_BYTES);
         constexpr uint64_t KA = A_MN ? 2048 >> 4 : 32 >> 4, KB = B_MN ? 2048 >> 4 : 32 >> 4;   // per 16 of K
         int stage = 0, gc = 0;
-        uint32_t phase = 0;
+        uint32_t phase = 0, tail_phases = 0;
         bool ok = true;
         for (int t = slot; ok && t < num_tiles; t += slots) {
             const LmWork w = lm_work<Tile, RAG>(p, g_start, g_prefix, t);
             const uint32_t idesc = idesc_f16(p.bf16, A_MN, B_MN, Tile::TILE_M, w.nmma);
             uint32_t d_tmem = 0;
-            for (int kb = 0; ok && kb < w.nkb; ++kb) {
+            // The last block of a group's rows may be short: kept out of the
+            // loop, whose instructions have to stay ahead of the tensor core.
+            const int whole = RAG == kRagK && w.nkb > 0 && w.klast < 64 ? w.nkb - 1 : w.nkb;
+            for (int kb = 0; kb < whole; ++kb) {
                 const bool first = CHUNKED || kb == 0, last = CHUNKED || kb == w.nkb - 1;
                 if (first) {
                     const int ab = gc & 1;
@@ -560,7 +570,6 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                     tc_fence_after();
                     d_tmem = tmem_base + (uint32_t)(ab * BN);
                 }
-                const int steps = RAG == kRagK && kb == w.nkb - 1 ? (w.klast + 15) >> 4 : 4;
                 for (int pr = 0; pr < p.pairs; ++pr) {
                     if (!mbar_wait_bounded<PAIR>(&full[stage], phase, downstream_limit(p.timeout_ns))) {
                         if (lane == 0) record_error(p.err, kSiteConsumerFull);
@@ -574,7 +583,6 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
-                            if (RAG == kRagK && kk >= steps) break;
                             const uint32_t acc = first && pr == 0 && kk == 0 ? 0u : 1u;
                             if constexpr (PAIR) mma_f16_pair(d_tmem, da + kk * KA, db + kk * KB, idesc, acc);
                             else mma_f16(d_tmem, da + kk * KA, db + kk * KB, idesc, acc);
@@ -591,7 +599,53 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                     __syncwarp();
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
+                if (!ok) break;
                 if (last) ++gc;
+            }
+            if constexpr (RAG == kRagK) {
+                if (ok && whole < w.nkb) {
+                    const bool first = CHUNKED || whole == 0, clear = (w.klast & 15) != 0;
+                    const int steps = (w.klast + 15) >> 4, ab = gc & 1;
+                    if (first) {
+                        ok = mbar_wait_bounded<PAIR>(&tempty[ab], ((uint32_t)(gc >> 1) & 1u) ^ 1u, p.timeout_ns);
+                        if (!ok && lane == 0) record_error(p.err, kSiteConsumerFull);
+                        tc_fence_after();
+                        d_tmem = tmem_base + (uint32_t)(ab * BN);
+                    }
+                    for (int pr = 0; pr < p.pairs; ++pr) {
+                        ok = ok && mbar_wait_bounded<PAIR>(&full[stage], phase, downstream_limit(p.timeout_ns));
+                        if (!ok && lane == 0) record_error(p.err, kSiteConsumerFull);
+                        ok = __all_sync(~0u, ok);
+                        if (!ok) break;
+                        if (clear) {
+                            ok = lm_clear_tail<Tile>(smem + stage * Tile::STAGE_BYTES, &tailbar[stage],
+                                                     (tail_phases >> stage) & 1u, w.klast, p, lane);
+                            tail_phases ^= 1u << stage;
+                            if (!ok) break;
+                        }
+                        tc_fence_after();
+                        const uint64_t da = da0 + (uint64_t)(stage * (Tile::STAGE_BYTES >> 4));
+                        const uint64_t db = db0 + (uint64_t)(stage * (Tile::STAGE_BYTES >> 4));
+                        if (elect_one()) {
+                            for (int kk = 0; kk < steps; ++kk) {
+                                const uint32_t acc = first && pr == 0 && kk == 0 ? 0u : 1u;
+                                if constexpr (PAIR) mma_f16_pair(d_tmem, da + kk * KA, db + kk * KB, idesc, acc);
+                                else mma_f16(d_tmem, da + kk * KA, db + kk * KB, idesc, acc);
+                            }
+                            if (p.withhold != kWithholdRelease) {
+                                if constexpr (PAIR) mma_commit_pair_mc(&empty[stage], 0x3);
+                                else mma_commit(&empty[stage]);
+                            }
+                            if (pr == p.pairs - 1) {
+                                if constexpr (PAIR) mma_commit_pair_mc(&tfull[ab], 0x3);
+                                else mma_commit(&tfull[ab]);
+                            }
+                        }
+                        __syncwarp();
+                        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                    }
+                    ++gc;
+                }
             }
         }
         if (elect_one()) {
@@ -600,6 +654,23 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         }
         __syncwarp();
         mbar_wait_bounded(drain, 0u, p.timeout_ns);
+    } else if (PAIR && RAG == kRagK && warp == 1) {
+        // ---------------- rank 1 of a pair: clears its part of the tails ----------------
+        int stage = 0;
+        uint32_t tail_phases = 0;
+        bool ok = true;
+        for (int t = slot; ok && t < num_tiles; t += slots) {
+            const LmWork w = lm_work<Tile, RAG>(p, g_start, g_prefix, t);
+            const bool tail = w.nkb > 0 && (w.klast & 15) != 0;
+            stage = (stage + (w.nkb - (tail ? 1 : 0)) * p.pairs) % STAGES;
+            for (int pr = 0; tail && ok && pr < p.pairs; ++pr) {
+                ok = lm_clear_tail<Tile>(smem + stage * Tile::STAGE_BYTES, &tailbar[stage],
+                                         (tail_phases >> stage) & 1u, w.klast, p, lane);
+                tail_phases ^= 1u << stage;
+                if (ok && lane == 0) mbar_arrive_cluster(cluster_addr(&full[stage], 0));
+                stage = stage + 1 == STAGES ? 0 : stage + 1;
+            }
+        }
     } else if (warp >= 2) {
         // ---------------- epilogue ----------------
         const int quarter = warp & 3, ew = warp - 2;
@@ -632,6 +703,24 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 }
                 ++gc;
             };
+            const int row0 = w.m0 + (int)rank * Tile::BM + quarter * 32;   // first row of this warp
+            const int row = row0 + lane;
+            // Per-row state of the loss epilogues.
+            float run_max = -INFINITY, run_sum = 0.f, row_lse = 0.f, row_g = 0.f;
+            int tgt = -1;
+            if constexpr (EPI == kEpiLse || EPI == kEpiDLogits) {
+                if (row < p.M) {
+                    const int64_t tv = p.target[row];
+                    if (tv >= 0 && tv < p.vocab) {
+                        const int64_t rel = tv - p.v0;
+                        tgt = rel >= 0 && rel < p.N ? (int)rel : -1;
+                        if constexpr (EPI == kEpiDLogits) {
+                            row_lse = p.lse[row];
+                            row_g = p.grad[row] * (p.gscale != nullptr ? *p.gscale : 1.f);
+                        }
+                    }
+                }
+            }
             if constexpr (CHUNKED) {
                 // Each block of 64 of the contraction is summed in its own
                 // accumulator and added here in FP32 with rounding to nearest
@@ -658,24 +747,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             }
             if (!ok) break;
 
-            const int row0 = w.m0 + (int)rank * Tile::BM + quarter * 32;   // first row of this warp
-            const int row = row0 + lane;
-            // Per-row state of the loss epilogues.
-            float run_max = -INFINITY, run_sum = 0.f, row_lse = 0.f, row_g = 0.f;
-            int tgt = -1;
-            if constexpr (EPI == kEpiLse || EPI == kEpiDLogits) {
-                if (row < p.M) {
-                    const int64_t tv = p.target[row];
-                    if (tv >= 0 && tv < p.vocab) {
-                        const int64_t rel = tv - p.v0;
-                        tgt = rel >= 0 && rel < p.N ? (int)rel : -1;
-                        if constexpr (EPI == kEpiDLogits) {
-                            row_lse = p.lse[row];
-                            row_g = p.grad[row] * (p.gscale != nullptr ? *p.gscale : 1.f);
-                        }
-                    }
-                }
-            }
+            uint32_t next[32];
 #pragma unroll
             for (int c0 = 0; c0 < SLAB; c0 += 32) {
                 const int col = slab0 + c0;                 // column in the tile
@@ -685,11 +757,14 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = sum[c0 + i];
                     } else if (w.nkb > 0) {
-                        uint32_t r[32];
-                        tmem_ld_32cols_nowait(taddr + (uint32_t)c0, r);
+                        // The next 32 columns are on their way while these
+                        // are worked on.
+                        if (c0 == 0) tmem_ld_32cols_nowait(taddr, next);
                         asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+                        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(next[i]);
+                        if (c0 + 32 < SLAB && col + 32 < w.nvalid)
+                            tmem_ld_32cols_nowait(taddr + (uint32_t)(c0 + 32), next);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = 0.f;
