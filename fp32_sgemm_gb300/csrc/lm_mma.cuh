@@ -175,9 +175,11 @@ __device__ __forceinline__ void lm_group_tables(const LmArgs &p, int *start, uin
     int row = 0;
     uint32_t tiles = 0;
     bool bad = false;
+    int following = lane < p.G ? p.ends[lane] : p.T;
     for (int g0 = 0; g0 <= p.G; g0 += 32) {
         const int g = g0 + lane;
-        int e = g < p.G ? p.ends[g] : p.T;
+        int e = following;
+        following = g + 32 < p.G ? p.ends[g + 32] : p.T;
         bad |= e < 0 || e > p.T;
         e = min(max(e, 0), p.T);
         int top = e;

@@ -183,7 +183,11 @@ lm_w4_kernel(const __grid_constant__ CUtensorMap tmQ, const W4Args p) {
     unsigned char *xs = reinterpret_cast<unsigned char *>(bars + WARPS * STAGES);   // [column][x_pitch]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = lane >> 2, q = lane & 3;
+    // The MMA's row lane / 4 (and + 8) is weight row g (and g + 8), in an
+    // order in which the rows a shared-memory phase reads meet different
+    // banks: rows 0 4 | 1 5 | .. for 16-byte reads, 0 2 4 6 | .. for 8-byte ones.
+    const int m = lane >> 2, q = lane & 3;
+    const int g = GROUP == 128 ? (m >> 1) | (m & 1) << 2 : GROUP == 64 ? (m >> 2) | (m & 3) << 1 : m;
     // This CTA's slice of K and this warp's steps in it.
     const int k_begin = blockIdx.y * p.k_slice, k_end = min(p.K, k_begin + p.k_slice);
     const int steps = (k_end - k_begin + 255) >> 8;
@@ -315,7 +319,7 @@ lm_w4_kernel(const __grid_constant__ CUtensorMap tmQ, const W4Args p) {
     const int cols = p.tokens * PLANES;
     const unsigned char *x_lane[NB];
 #pragma unroll
-    for (int n = 0; n < NB; ++n) x_lane[n] = xs + (s0 * 32 + q) * 16 + min(n * 8 + g, cols - 1) * p.x_pitch;
+    for (int n = 0; n < NB; ++n) x_lane[n] = xs + (s0 * 32 + q) * 16 + min(n * 8 + m, cols - 1) * p.x_pitch;
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -410,10 +414,12 @@ lm_w4_kernel(const __grid_constant__ CUtensorMap tmQ, const W4Args p) {
             float y = 0.f;
 #pragma unroll
             for (int pl = PLANES - 1; pl >= 0; --pl) {
-                // Column col of row r sits in lane (r % 8) * 4 + (col % 8) / 2,
+                // Column col of the MMA's row r sits in lane (r % 8) * 4 + (col % 8) / 2,
                 // register (r / 8) * 2 + col % 2 of block col / 8.
                 const int col = t * PLANES + pl;
-                const int at = ((col >> 3) * 4 + (r >> 3) * 2 + (col & 1)) * 32 + (r & 7) * 4 + ((col & 7) >> 1);
+                const int r7 = r & 7;                     // row -> the MMA's row
+                const int mr = GROUP == 128 ? (r7 & 3) << 1 | r7 >> 2 : GROUP == 64 ? (r7 & 1) << 2 | r7 >> 1 : r7;
+                const int at = ((col >> 3) * 4 + (r >> 3) * 2 + (col & 1)) * 32 + mr * 4 + ((col & 7) >> 1);
                 float v = 0.f;
 #pragma unroll
                 for (int w = 0; w < WARPS; ++w) v += buf[w * NB * 128 + at];
