@@ -165,10 +165,11 @@ struct W4Meta {
 };
 
 // TYPE: 0 FP32, 1 f16, 2 bf16.  8 * NB columns on the N side.
-// WARPS: 8 with two CTAs on an SM, or one CTA of 16 where x takes most of
-// shared memory (8 for 32 columns: more registers).
-template <int TYPE, int GROUP, int NB, bool ZEROS, int WARPS, int MIN_CTAS>
-__global__ void __launch_bounds__(WARPS * 32, MIN_CTAS)
+// Eight warps share 16 rows and split K.  TEAMS: two such teams in one CTA
+// where x takes most of shared memory (one for 32 columns: more registers);
+// otherwise one, and two CTAs on an SM.
+template <int TYPE, int GROUP, int NB, bool ZEROS, int TEAMS, int MIN_CTAS>
+__global__ void __launch_bounds__(TEAMS * 256, MIN_CTAS)
 lm_w4_kernel(const __grid_constant__ CUtensorMap tmQ, const W4Args p) {
     constexpr bool BF16 = TYPE != 1;
     constexpr int PLANES = TYPE == 0 ? 3 : 1;
@@ -178,11 +179,15 @@ lm_w4_kernel(const __grid_constant__ CUtensorMap tmQ, const W4Args p) {
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     unsigned char *ring = smem;
-    float *red = reinterpret_cast<float *>(smem + WARPS * STAGES * 2048);      // [2][warp][NB * 4][32]
-    uint64_t *bars = reinterpret_cast<uint64_t *>(red + 2 * WARPS * NB * 128);
-    unsigned char *xs = reinterpret_cast<unsigned char *>(bars + WARPS * STAGES);   // [column][x_pitch]
+    constexpr int WARPS = 8, THREADS = TEAMS * 256;
+    float *red = reinterpret_cast<float *>(smem + TEAMS * WARPS * STAGES * 2048);   // [team][2][warp][NB * 4][32]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(red + TEAMS * 2 * WARPS * NB * 128);
+    unsigned char *xs = reinterpret_cast<unsigned char *>(bars + TEAMS * WARPS * STAGES);   // [column][x_pitch]
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, team = TEAMS == 1 ? 0 : (int)(threadIdx.x >> 8);
+    const int warp = (int)(threadIdx.x >> 5) & 7, thread = (int)threadIdx.x & 255;     // of the team
+    const int slot = (int)blockIdx.x * TEAMS + team, slots = (int)gridDim.x * TEAMS;
+    red += team * (2 * WARPS * NB * 128);
     // The MMA's row lane / 4 (and + 8) is weight row g (and g + 8), in an
     // order in which the rows a shared-memory phase reads meet different
     // banks: rows 0 4 | 1 5 | .. for 16-byte reads, 0 2 4 6 | .. for 8-byte ones.
@@ -194,13 +199,13 @@ lm_w4_kernel(const __grid_constant__ CUtensorMap tmQ, const W4Args p) {
     const int s0 = steps * warp / WARPS, per = steps * (warp + 1) / WARPS - s0;
     const int k_warp = k_begin + s0 * 256;
     const int blocks = (p.N + 15) >> 4;
-    const int mine = blocks > (int)blockIdx.x ? (blocks - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+    const int mine = blocks > slot ? (blocks - 1 - slot) / slots + 1 : 0;
 
     // Per warp: a ring of 2 KB stages filled by TMA (16 rows of 128 bytes,
     // 128-byte swizzle: 16-byte piece c of row r sits at c ^ (r % 8); rows
     // past N and columns past K arrive as zeros).
-    unsigned char *ring_w = ring + warp * (STAGES * 2048);
-    uint64_t *full = bars + warp * STAGES;
+    unsigned char *ring_w = ring + (team * WARPS + warp) * (STAGES * 2048);
+    uint64_t *full = bars + (team * WARPS + warp) * STAGES;
     if (lane == 0) {
 #pragma unroll
         for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], 1);
@@ -209,7 +214,7 @@ lm_w4_kernel(const __grid_constant__ CUtensorMap tmQ, const W4Args p) {
     __syncwarp();
     griddep_launch_dependents();
     griddep_wait();
-    int ld_row = (int)blockIdx.x << 4, ld_s = 0, ld_stage = 0;
+    int ld_row = slot << 4, ld_s = 0, ld_stage = 0;
     auto issue = [&]() {
         if (ld_row < p.N && per > 0) {
             if (elect_one()) {
@@ -220,7 +225,7 @@ lm_w4_kernel(const __grid_constant__ CUtensorMap tmQ, const W4Args p) {
             ld_stage = ld_stage == STAGES - 1 ? 0 : ld_stage + 1;
             if (++ld_s == per) {
                 ld_s = 0;
-                ld_row += (int)gridDim.x << 4;
+                ld_row += slots << 4;
             }
         }
     };
@@ -230,53 +235,67 @@ lm_w4_kernel(const __grid_constant__ CUtensorMap tmQ, const W4Args p) {
     // x in nibble order (within 8 columns 0 4 1 5 2 6 3 7), the 16 chunks of
     // 128 columns in the order in which the lanes q = 0..3 take them.
     {
-        const int chunks = steps * 32;                    // of 8 columns
-        for (int i = threadIdx.x; i < chunks * p.tokens; i += WARPS * 32) {
-            const int t = i / chunks, c = i - t * chunks, k = k_begin + c * 8;
-            // Chunk c is word `slot` of lane `lq`; see the loop below.
+        const int chunks = steps * 32, total = chunks * p.tokens;      // chunks of 8 columns
+        // Chunk c is word `slot` of lane `lq`; see the loop below.
+        auto place = [&](int c) {
             const int in = c & 15;
             const int lq = GROUP == 128 ? in >> 2 : GROUP == 64 ? (in >> 1) & 3 : in & 3;
             const int slot = GROUP == 128 ? in & 3 : GROUP == 64 ? (in >> 3) * 2 + (in & 1) : in >> 2;
-            unsigned char *at = xs + ((c & ~15) + slot * 4 + lq) * 16;
-            if constexpr (TYPE == 0) {
-                const float *sx = static_cast<const float *>(p.X) + (int64_t)t * p.ldx + k;
-                uint16_t v[3][8];
+            return xs + ((c & ~15) + slot * 4 + lq) * 16;
+        };
+        auto ordered = [](const uint16_t *v) {
+            return make_uint4(v[0] | (uint32_t)v[4] << 16, v[1] | (uint32_t)v[5] << 16,
+                              v[2] | (uint32_t)v[6] << 16, v[3] | (uint32_t)v[7] << 16);
+        };
+        if (TYPE != 0 && p.x_vec && k_end - k_begin == steps * 256) {
+            // Whole chunks: several loads on their way at a time.
+            constexpr int U = 8;
+            for (int i0 = threadIdx.x; i0 < total; i0 += U * THREADS) {
+                uint4 v[U];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float f = k + e < k_end ? sx[e] : 0.f;
-                    const uint32_t u = __float_as_uint(f);
-                    const bool odd = (u & 0x7F800000u) == 0x7F800000u;
-                    const uint32_t h = odd && (u & 0x7FFFFFu) ? 0x7FC00000u : u & 0xFFFF0000u;
-                    const float r1 = odd ? 0.f : f - __uint_as_float(h);
-                    const uint32_t m = __float_as_uint(r1) & 0xFFFF0000u;
-                    v[0][e] = (uint16_t)(h >> 16);
-                    v[1][e] = (uint16_t)(m >> 16);
-                    v[2][e] = (uint16_t)(__float_as_uint(r1 - __uint_as_float(m)) >> 16);
+                for (int j = 0; j < U; ++j) {
+                    const int i = min(i0 + j * THREADS, total - 1), t = i / chunks, c = i - t * chunks;
+                    v[j] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.X) +
+                                                            (int64_t)t * p.ldx + k_begin + c * 8);
                 }
 #pragma unroll
-                for (int pl = 0; pl < 3; ++pl) {
-                    uint4 o;
-                    o.x = v[pl][0] | (uint32_t)v[pl][4] << 16;
-                    o.y = v[pl][1] | (uint32_t)v[pl][5] << 16;
-                    o.z = v[pl][2] | (uint32_t)v[pl][6] << 16;
-                    o.w = v[pl][3] | (uint32_t)v[pl][7] << 16;
-                    *reinterpret_cast<uint4 *>(at + (t * 3 + pl) * p.x_pitch) = o;
+                for (int j = 0; j < U; ++j) {
+                    const int i = i0 + j * THREADS, t = i / chunks, c = i - t * chunks;
+                    if (i < total)
+                        *reinterpret_cast<uint4 *>(place(c) + t * p.x_pitch) =
+                            make_uint4(__byte_perm(v[j].x, v[j].z, 0x5410), __byte_perm(v[j].x, v[j].z, 0x7632),
+                                       __byte_perm(v[j].y, v[j].w, 0x5410), __byte_perm(v[j].y, v[j].w, 0x7632));
                 }
-            } else {
-                const uint16_t *sx = static_cast<const uint16_t *>(p.X) + (int64_t)t * p.ldx + k;
-                alignas(16) uint16_t v[8];
-                if (p.x_vec && k + 8 <= k_end) {
-                    *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(sx);
+            }
+        } else {
+            for (int i = threadIdx.x; i < total; i += THREADS) {
+                const int t = i / chunks, c = i - t * chunks, k = k_begin + c * 8;
+                unsigned char *at = place(c);
+                if constexpr (TYPE == 0) {
+                    const float *sx = static_cast<const float *>(p.X) + (int64_t)t * p.ldx + k;
+                    uint16_t v[3][8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float f = k + e < k_end ? sx[e] : 0.f;
+                        const uint32_t u = __float_as_uint(f);
+                        const bool odd = (u & 0x7F800000u) == 0x7F800000u;
+                        const uint32_t h = odd && (u & 0x7FFFFFu) ? 0x7FC00000u : u & 0xFFFF0000u;
+                        const float r1 = odd ? 0.f : f - __uint_as_float(h);
+                        const uint32_t m = __float_as_uint(r1) & 0xFFFF0000u;
+                        v[0][e] = (uint16_t)(h >> 16);
+                        v[1][e] = (uint16_t)(m >> 16);
+                        v[2][e] = (uint16_t)(__float_as_uint(r1 - __uint_as_float(m)) >> 16);
+                    }
+#pragma unroll
+                    for (int pl = 0; pl < 3; ++pl)
+                        *reinterpret_cast<uint4 *>(at + (t * 3 + pl) * p.x_pitch) = ordered(v[pl]);
                 } else {
+                    const uint16_t *sx = static_cast<const uint16_t *>(p.X) + (int64_t)t * p.ldx + k;
+                    uint16_t v[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) v[e] = k + e < k_end ? sx[e] : (uint16_t)0;
+                    *reinterpret_cast<uint4 *>(at + t * p.x_pitch) = ordered(v);
                 }
-                uint4 o;
-                o.x = v[0] | (uint32_t)v[4] << 16;
-                o.y = v[1] | (uint32_t)v[5] << 16;
-                o.z = v[2] | (uint32_t)v[6] << 16;
-                o.w = v[3] | (uint32_t)v[7] << 16;
-                *reinterpret_cast<uint4 *>(at + t * p.x_pitch) = o;
             }
         }
     }
@@ -309,7 +328,7 @@ lm_w4_kernel(const __grid_constant__ CUtensorMap tmQ, const W4Args p) {
         }
     };
     if (per > 0 && mine > 0) {
-        point_meta((int)blockIdx.x << 4);
+        point_meta(slot << 4);
         load_meta(0);
     }
     __syncthreads();
@@ -324,7 +343,7 @@ lm_w4_kernel(const __grid_constant__ CUtensorMap tmQ, const W4Args p) {
     uint32_t phase = 0;
     bool ok = true;
     for (int b = 0; b < mine; ++b) {
-        const int row0 = ((int)blockIdx.x + b * (int)gridDim.x) << 4;
+        const int row0 = (slot + b * slots) << 4;
         float sum[NB][4];
 #pragma unroll
         for (int n = 0; n < NB; ++n)
@@ -336,7 +355,7 @@ lm_w4_kernel(const __grid_constant__ CUtensorMap tmQ, const W4Args p) {
             if (s + 1 < per) {
                 load_meta(s + 1);
             } else if (b + 1 < mine) {
-                point_meta(row0 + ((int)gridDim.x << 4));
+                point_meta(row0 + (slots << 4));
                 load_meta(0);
             }
             if (ok && !mbar_wait_bounded(&full[stage], phase, p.timeout_ns)) {
@@ -408,8 +427,9 @@ lm_w4_kernel(const __grid_constant__ CUtensorMap tmQ, const W4Args p) {
         for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) buf[(warp * NB * 4 + n * 4 + i) * 32 + lane] = sum[n][i];
-        __syncthreads();
-        for (int o = threadIdx.x; o < 16 * p.tokens; o += WARPS * 32) {
+        if constexpr (TEAMS == 1) __syncthreads();
+        else asm volatile("bar.sync %0, 256;" :: "r"(1 + team) : "memory");
+        for (int o = thread; o < 16 * p.tokens; o += 256) {
             const int t = o >> 4, r = o & 15;
             float y = 0.f;
 #pragma unroll
@@ -444,12 +464,12 @@ lm_w4_kernel(const __grid_constant__ CUtensorMap tmQ, const W4Args p) {
 template <int TYPE, int GROUP, bool ZEROS>
 const void *w4_kernel_by_size(int nb, bool alone) {
     if (nb == 1)
-        return alone ? reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, GROUP, 1, ZEROS, 16, 1>)
-                     : reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, GROUP, 1, ZEROS, 8, 2>);
+        return alone ? reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, GROUP, 1, ZEROS, 2, 1>)
+                     : reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, GROUP, 1, ZEROS, 1, 2>);
     if (nb == 2)
-        return alone ? reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, GROUP, 2, ZEROS, 16, 1>)
-                     : reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, GROUP, 2, ZEROS, 8, 2>);
-    return reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, GROUP, 4, ZEROS, 8, 1>);
+        return alone ? reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, GROUP, 2, ZEROS, 2, 1>)
+                     : reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, GROUP, 2, ZEROS, 1, 2>);
+    return reinterpret_cast<const void *>(&lm_w4_kernel<TYPE, GROUP, 4, ZEROS, 1, 1>);
 }
 template <int TYPE, bool ZEROS>
 const void *w4_kernel_by_group(int group, int nb, bool alone) {
