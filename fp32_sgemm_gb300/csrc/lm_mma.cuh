@@ -379,10 +379,10 @@ __device__ __forceinline__ bool lm_clear_tail(unsigned char *stage, uint64_t *la
     const int r1 = (rows + 15) & ~15, per = (r1 - rows) * 8;      // 16-byte words per chunk of 64 columns
     constexpr int CHUNKS = Tile::STAGE_BYTES / 8192;
     if (ok)
-        for (int i = lane; i < CHUNKS * per; i += 32) {
-            const int c = i / per;
-            *reinterpret_cast<uint4 *>(stage + c * 8192 + rows * 128 + (i - c * per) * 16) = make_uint4(0, 0, 0, 0);
-        }
+        for (int i = lane; i < per; i += 32)
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c)
+                *reinterpret_cast<uint4 *>(stage + c * 8192 + rows * 128 + i * 16) = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     __syncwarp();
     return ok;
@@ -390,8 +390,12 @@ __device__ __forceinline__ bool lm_clear_tail(unsigned char *stage, uint64_t *la
 
 // ---------------------------------------------------------------- kernel
 
+// Threads of a kernel: kRagK has one more warp, which clears tails.
+template <class Tile, int RAG>
+constexpr int lm_threads() { return Tile::THREADS + (RAG == kRagK ? 32 : 0); }
+
 template <class Tile, bool A_MN, bool B_MN, int RAG, int EPI, bool CHUNKED>
-__global__ void __launch_bounds__(Tile::THREADS, 1)
+__global__ void __launch_bounds__(lm_threads<Tile, RAG>(), 1)
 lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const LmArgs p) {
     constexpr bool PAIR = Tile::PAIR;
     constexpr int BN = Tile::BN, STAGES = Tile::STAGES, SLAB = Tile::SLAB;
@@ -510,16 +514,15 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                         }
                         __syncwarp();
                     } else {
-                        // Rows behind the group have to be cleared first
-                        // (lm_clear_tail): the copies report to this SM's
-                        // own barrier, rank 0's arrival stands for itself,
-                        // rank 1 arrives once it has cleared its part.
+                        // Rows behind the group have to be cleared first: the
+                        // copies report to this SM's own barrier, and the
+                        // warp that clears (lm_clear_tail) arrives in this
+                        // one's place.
                         if (elect_one()) {
                             mbar_arrive_expect_tx(&tailbar[stage], Tile::STAGE_BYTES);
                             load_all([&](void *dst, const CUtensorMap *m, int c0, int c1, int c2) {
                                 tma_load_3d(dst, m, &tailbar[stage], c0, c1, c2);
                             });
-                            if (rank == 0) mbar_arrive(&full[stage]);
                         }
                         __syncwarp();
                     }
@@ -550,7 +553,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                                   : smem_desc_k_sw128(smem_u32(smem) + Tile::A_BYTES);
         constexpr uint64_t KA = A_MN ? 2048 >> 4 : 32 >> 4, KB = B_MN ? 2048 >> 4 : 32 >> 4;   // per 16 of K
         int stage = 0, gc = 0;
-        uint32_t phase = 0, tail_phases = 0;
+        uint32_t phase = 0;
         bool ok = true;
         for (int t = slot; ok && t < num_tiles; t += slots) {
             const LmWork w = lm_work<Tile, RAG>(p, g_start, g_prefix, t);
@@ -606,7 +609,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             }
             if constexpr (RAG == kRagK) {
                 if (ok && whole < w.nkb) {
-                    const bool first = CHUNKED || whole == 0, clear = (w.klast & 15) != 0;
+                    const bool first = CHUNKED || whole == 0;
                     const int steps = (w.klast + 15) >> 4, ab = gc & 1;
                     if (first) {
                         ok = mbar_wait_bounded<PAIR>(&tempty[ab], ((uint32_t)(gc >> 1) & 1u) ^ 1u, p.timeout_ns);
@@ -615,16 +618,10 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                         d_tmem = tmem_base + (uint32_t)(ab * BN);
                     }
                     for (int pr = 0; pr < p.pairs; ++pr) {
-                        ok = ok && mbar_wait_bounded<PAIR>(&full[stage], phase, downstream_limit(p.timeout_ns));
+                        ok = ok && mbar_wait_bounded<PAIR>(&full[stage], phase, 2 * downstream_limit(p.timeout_ns));
                         if (!ok && lane == 0) record_error(p.err, kSiteConsumerFull);
                         ok = __all_sync(~0u, ok);
                         if (!ok) break;
-                        if (clear) {
-                            ok = lm_clear_tail<Tile>(smem + stage * Tile::STAGE_BYTES, &tailbar[stage],
-                                                     (tail_phases >> stage) & 1u, w.klast, p, lane);
-                            tail_phases ^= 1u << stage;
-                            if (!ok) break;
-                        }
                         tc_fence_after();
                         const uint64_t da = da0 + (uint64_t)(stage * (Tile::STAGE_BYTES >> 4));
                         const uint64_t db = db0 + (uint64_t)(stage * (Tile::STAGE_BYTES >> 4));
@@ -656,24 +653,27 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         }
         __syncwarp();
         mbar_wait_bounded(drain, 0u, p.timeout_ns);
-    } else if (PAIR && RAG == kRagK && warp == 1) {
-        // ---------------- rank 1 of a pair: clears its part of the tails ----------------
+    } else if (RAG == kRagK && warp == 2 + Tile::EPI_WARPS) {
+        // ---------------- clears the tails, ahead of the MMAs ----------------
         int stage = 0;
-        uint32_t tail_phases = 0;
+        uint32_t phases = 0;                    // of the tail barriers, a bit each
         bool ok = true;
         for (int t = slot; ok && t < num_tiles; t += slots) {
             const LmWork w = lm_work<Tile, RAG>(p, g_start, g_prefix, t);
             const bool tail = w.nkb > 0 && (w.klast & 15) != 0;
             stage = (stage + (w.nkb - (tail ? 1 : 0)) * p.pairs) % STAGES;
             for (int pr = 0; tail && ok && pr < p.pairs; ++pr) {
-                ok = lm_clear_tail<Tile>(smem + stage * Tile::STAGE_BYTES, &tailbar[stage],
-                                         (tail_phases >> stage) & 1u, w.klast, p, lane);
-                tail_phases ^= 1u << stage;
-                if (ok && lane == 0) mbar_arrive_cluster(cluster_addr(&full[stage], 0));
+                ok = lm_clear_tail<Tile>(smem + stage * Tile::STAGE_BYTES, &tailbar[stage], (phases >> stage) & 1u,
+                                         w.klast, p, lane);
+                phases ^= 1u << stage;
+                if (ok && lane == 0) {
+                    if (rank == 0) mbar_arrive(&full[stage]);
+                    else mbar_arrive_cluster(cluster_addr(&full[stage], 0));
+                }
                 stage = stage + 1 == STAGES ? 0 : stage + 1;
             }
         }
-    } else if (warp >= 2) {
+    } else if (warp >= 2 && warp < 2 + Tile::EPI_WARPS) {
         // ---------------- epilogue ----------------
         const int quarter = warp & 3, ew = warp - 2;
         const int slab0 = (ew >> 2) * SLAB;
@@ -726,7 +726,9 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             if constexpr (CHUNKED) {
                 // Each block of 64 of the contraction is summed in its own
                 // accumulator and added here in FP32 with rounding to nearest
-                // (the tensor core's own running sum truncates).
+                // (the tensor core's own running sum truncates; two blocks per
+                // accumulator doubled the error, at 40003 terms to 2^-20 of
+                // their magnitudes).
 #pragma unroll
                 for (int c = 0; c < SLAB; ++c) sum[c] = 0.f;
                 for (int kb = 0; ok && kb < w.nkb; ++kb) {
@@ -857,7 +859,7 @@ LmKernel lm_kernel_info() {
     static_assert(RAG == kRagNone || Tile::FIXED + 8 * (kLmMaxGroups + 2) <= 227 * 1024, "room for the group tables");
     LmKernel k;
     k.fn = reinterpret_cast<const void *>(&lm_mma_kernel<Tile, A_MN, B_MN, RAG, EPI, CHUNKED>);
-    k.threads = Tile::THREADS;
+    k.threads = lm_threads<Tile, RAG>();
     k.smem = Tile::FIXED;
     k.tile_m = Tile::TILE_M;
     k.bn = Tile::BN;
