@@ -31,7 +31,6 @@ struct LmArgs {
     int G;
     const int32_t *ends;  // [G] end row of each group
     int tiles_m, tiles_n, tile_n, num_tiles, splits, group_m;
-    int pairs;            // 1, or 6 for FP32 operands in three bf16 planes
     uint32_t bf16;        // operands bf16 (else f16)
     void *C;
     int64_t ldc, stride_c;   // stride_c: per group (kRagK) or per K split

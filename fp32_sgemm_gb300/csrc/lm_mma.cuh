@@ -270,15 +270,11 @@ __device__ __forceinline__ LmWork lm_work(const LmArgs &p, const int *start, con
     return w;
 }
 
-// Planes multiplied in one step of a product of FP32 operands (each held as
-// three bf16 planes, x = p0 + p1 + p2 exactly): p_i q_j with i + j <= 2,
-// smallest first.  With one pair: plane 0 only.
-__device__ __forceinline__ void lm_planes(int pairs, int pr, int &ia, int &ib) {
-    if (pairs == 1) { ia = ib = 0; return; }
-    // (2,0) (1,1) (0,2) (1,0) (0,1) (0,0), two bits each
-    ia = (0x046 >> (2 * pr)) & 3;      // 2,1,0,1,0,0
-    ib = (0x124 >> (2 * pr)) & 3;      // 0,1,2,0,1,0
-}
+// A product of FP32 operands, each held as three bf16 planes (x = p0 + p1 +
+// p2 exactly): stage i of a block of 64 holds plane i of both, and p_i q_j
+// with i + j <= 2 are multiplied, smallest first.
+__device__ constexpr int plane_a(int pr) { return (0x046 >> (2 * pr)) & 3; }     // 2 1 0 1 0 0
+__device__ constexpr int plane_b(int pr) { return (0x124 >> (2 * pr)) & 3; }     // 0 1 2 0 1 0
 
 // -------------------------------------------------------------- epilogues
 
@@ -399,6 +395,7 @@ __global__ void __launch_bounds__(lm_threads<Tile, RAG>(), 1)
 lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const LmArgs p) {
     constexpr bool PAIR = Tile::PAIR;
     constexpr int BN = Tile::BN, STAGES = Tile::STAGES, SLAB = Tile::SLAB;
+    constexpr int PLANES = CHUNKED ? 3 : 1;                 // CHUNKED: FP32 operands
     static_assert(!B_MN || Tile::B_ROWS % 64 == 0, "MN-major B is staged in chunks of 64 columns");
 
     extern __shared__ unsigned char smem_raw[];
@@ -459,6 +456,9 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         int stage = 0, issued = 0;
         uint32_t phase = 0;
         bool ok = true;
+        // kRagN: the copies of B have as many rows as a tile may have.
+        const uint32_t stage_bytes =
+            RAG == kRagN ? (uint32_t)(Tile::A_BYTES + p.tile_n / (PAIR ? 2 : 1) * 128) : (uint32_t)Tile::STAGE_BYTES;
         const uint32_t full_pair = PAIR ? cluster_addr(&full[0], 0) : 0u;   // rank 0's barriers
         for (int t = slot; ok && t < num_tiles; t += slots) {
             const LmWork w = lm_work<Tile, RAG>(p, g_start, g_prefix, t);
@@ -467,7 +467,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             for (int kb = 0; ok && kb < w.nkb; ++kb) {
                 const int kc = RAG == kRagK ? w.krow0 + kb * 64 : (w.kb0 + kb) * 64;
                 const bool tail = RAG == kRagK && kb == w.nkb - 1 && (w.klast & 15) != 0;
-                for (int pr = 0; pr < p.pairs; ++pr) {
+                for (int pl = 0; pl < PLANES; ++pl) {
                     if (p.withhold == kWithholdRefill && issued >= STAGES) { ok = false; break; }
                     if (!mbar_wait_bounded<PAIR>(&empty[stage], phase ^ 1u, p.timeout_ns)) {
                         if (lane == 0) record_error(p.err, kSiteProducerEmpty);
@@ -476,9 +476,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                     ok = __all_sync(~0u, ok);
                     if (!ok) break;
                     unsigned char *sa = smem + stage * Tile::STAGE_BYTES, *sb = sa + Tile::A_BYTES;
-                    int ia, ib;
-                    lm_planes(p.pairs, pr, ia, ib);
-                    const int za = RAG == kRagN ? ia * p.G + w.g : ia;
+                    const int za = RAG == kRagN ? pl * p.G + w.g : pl;
                     const uint32_t fb = full_pair + (uint32_t)stage * 8u;
                     // Copies of this stage, completing on the ring's barrier
                     // (rank 0's for a pair) or, for a tail, on a local one.
@@ -492,21 +490,21 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                         if constexpr (B_MN) {
 #pragma unroll
                             for (int c = 0; c < Tile::B_ROWS / 64; ++c)
-                                load(sb + c * 8192, &tmB, nb + c * 64, kc, ib);
+                                load(sb + c * 8192, &tmB, nb + c * 64, kc, pl);
                         } else {
-                            load(sb, &tmB, kc, nb, ib);
+                            load(sb, &tmB, kc, nb, pl);
                         }
                     };
                     if (!tail) {
                         if (elect_one()) {
                             if constexpr (PAIR) {
-                                if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * Tile::STAGE_BYTES);
+                                if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * stage_bytes);
                                 else if (RAG == kRagK) mbar_arrive_cluster_relaxed(fb);
                                 load_all([&](void *dst, const CUtensorMap *m, int c0, int c1, int c2) {
                                     tma_load_3d_pair(dst, m, fb, c0, c1, c2);
                                 });
                             } else {
-                                mbar_arrive_expect_tx(&full[stage], Tile::STAGE_BYTES);
+                                mbar_arrive_expect_tx(&full[stage], stage_bytes);
                                 load_all([&](void *dst, const CUtensorMap *m, int c0, int c1, int c2) {
                                     tma_load_3d(dst, m, &full[stage], c0, c1, c2);
                                 });
@@ -575,35 +573,46 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                     tc_fence_after();
                     d_tmem = tmem_base + (uint32_t)(ab * BN);
                 }
-                for (int pr = 0; pr < p.pairs; ++pr) {
-                    if (!mbar_wait_bounded<PAIR>(&full[stage], phase, downstream_limit(p.timeout_ns))) {
+                uint64_t da[PLANES], db[PLANES];
+                int st[PLANES];
+#pragma unroll
+                for (int pl = 0; pl < PLANES; ++pl) {
+                    if (ok && !mbar_wait_bounded<PAIR>(&full[stage], phase, downstream_limit(p.timeout_ns))) {
                         if (lane == 0) record_error(p.err, kSiteConsumerFull);
                         ok = false;
                     }
                     ok = __all_sync(~0u, ok);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t da = da0 + (uint64_t)(stage * (Tile::STAGE_BYTES >> 4));
-                    const uint64_t db = db0 + (uint64_t)(stage * (Tile::STAGE_BYTES >> 4));
-                    if (elect_one()) {
+                    da[pl] = da0 + (uint64_t)(stage * (Tile::STAGE_BYTES >> 4));
+                    db[pl] = db0 + (uint64_t)(stage * (Tile::STAGE_BYTES >> 4));
+                    st[pl] = stage;
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                }
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int pr = 0; pr < (CHUNKED ? 6 : 1); ++pr) {
+                        const uint64_t a = da[CHUNKED ? plane_a(pr) : 0], b = db[CHUNKED ? plane_b(pr) : 0];
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
                             const uint32_t acc = first && pr == 0 && kk == 0 ? 0u : 1u;
-                            if constexpr (PAIR) mma_f16_pair(d_tmem, da + kk * KA, db + kk * KB, idesc, acc);
-                            else mma_f16(d_tmem, da + kk * KA, db + kk * KB, idesc, acc);
-                        }
-                        if (p.withhold != kWithholdRelease) {
-                            if constexpr (PAIR) mma_commit_pair_mc(&empty[stage], 0x3);
-                            else mma_commit(&empty[stage]);
-                        }
-                        if (last && pr == p.pairs - 1) {
-                            if constexpr (PAIR) mma_commit_pair_mc(&tfull[gc & 1], 0x3);
-                            else mma_commit(&tfull[gc & 1]);
+                            if constexpr (PAIR) mma_f16_pair(d_tmem, a + kk * KA, b + kk * KB, idesc, acc);
+                            else mma_f16(d_tmem, a + kk * KA, b + kk * KB, idesc, acc);
                         }
                     }
-                    __syncwarp();
-                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                    if (p.withhold != kWithholdRelease) {
+#pragma unroll
+                        for (int pl = 0; pl < PLANES; ++pl) {
+                            if constexpr (PAIR) mma_commit_pair_mc(&empty[st[pl]], 0x3);
+                            else mma_commit(&empty[st[pl]]);
+                        }
+                    }
+                    if (last) {
+                        if constexpr (PAIR) mma_commit_pair_mc(&tfull[gc & 1], 0x3);
+                        else mma_commit(&tfull[gc & 1]);
+                    }
                 }
+                __syncwarp();
                 if (!ok) break;
                 if (last) ++gc;
             }
@@ -617,32 +626,41 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                         tc_fence_after();
                         d_tmem = tmem_base + (uint32_t)(ab * BN);
                     }
-                    for (int pr = 0; pr < p.pairs; ++pr) {
+                    uint64_t da[PLANES], db[PLANES];
+                    int st[PLANES];
+#pragma unroll
+                    for (int pl = 0; pl < PLANES; ++pl) {
                         ok = ok && mbar_wait_bounded<PAIR>(&full[stage], phase, 2 * downstream_limit(p.timeout_ns));
                         if (!ok && lane == 0) record_error(p.err, kSiteConsumerFull);
                         ok = __all_sync(~0u, ok);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t da = da0 + (uint64_t)(stage * (Tile::STAGE_BYTES >> 4));
-                        const uint64_t db = db0 + (uint64_t)(stage * (Tile::STAGE_BYTES >> 4));
-                        if (elect_one()) {
-                            for (int kk = 0; kk < steps; ++kk) {
-                                const uint32_t acc = first && pr == 0 && kk == 0 ? 0u : 1u;
-                                if constexpr (PAIR) mma_f16_pair(d_tmem, da + kk * KA, db + kk * KB, idesc, acc);
-                                else mma_f16(d_tmem, da + kk * KA, db + kk * KB, idesc, acc);
-                            }
-                            if (p.withhold != kWithholdRelease) {
-                                if constexpr (PAIR) mma_commit_pair_mc(&empty[stage], 0x3);
-                                else mma_commit(&empty[stage]);
-                            }
-                            if (pr == p.pairs - 1) {
-                                if constexpr (PAIR) mma_commit_pair_mc(&tfull[ab], 0x3);
-                                else mma_commit(&tfull[ab]);
-                            }
-                        }
-                        __syncwarp();
+                        da[pl] = da0 + (uint64_t)(stage * (Tile::STAGE_BYTES >> 4));
+                        db[pl] = db0 + (uint64_t)(stage * (Tile::STAGE_BYTES >> 4));
+                        st[pl] = stage;
                         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                     }
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int pr = 0; pr < (CHUNKED ? 6 : 1); ++pr) {
+                            const uint64_t a = da[CHUNKED ? plane_a(pr) : 0], b = db[CHUNKED ? plane_b(pr) : 0];
+                            for (int kk = 0; kk < steps; ++kk) {
+                                const uint32_t acc = first && pr == 0 && kk == 0 ? 0u : 1u;
+                                if constexpr (PAIR) mma_f16_pair(d_tmem, a + kk * KA, b + kk * KB, idesc, acc);
+                                else mma_f16(d_tmem, a + kk * KA, b + kk * KB, idesc, acc);
+                            }
+                        }
+                        if (p.withhold != kWithholdRelease) {
+#pragma unroll
+                            for (int pl = 0; pl < PLANES; ++pl) {
+                                if constexpr (PAIR) mma_commit_pair_mc(&empty[st[pl]], 0x3);
+                                else mma_commit(&empty[st[pl]]);
+                            }
+                        }
+                        if constexpr (PAIR) mma_commit_pair_mc(&tfull[ab], 0x3);
+                        else mma_commit(&tfull[ab]);
+                    }
+                    __syncwarp();
                     ++gc;
                 }
             }
@@ -661,8 +679,8 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         for (int t = slot; ok && t < num_tiles; t += slots) {
             const LmWork w = lm_work<Tile, RAG>(p, g_start, g_prefix, t);
             const bool tail = w.nkb > 0 && (w.klast & 15) != 0;
-            stage = (stage + (w.nkb - (tail ? 1 : 0)) * p.pairs) % STAGES;
-            for (int pr = 0; tail && ok && pr < p.pairs; ++pr) {
+            stage = (stage + (w.nkb - (tail ? 1 : 0)) * PLANES) % STAGES;
+            for (int pl = 0; tail && ok && pl < PLANES; ++pl) {
                 ok = lm_clear_tail<Tile>(smem + stage * Tile::STAGE_BYTES, &tailbar[stage], (phases >> stage) & 1u,
                                          w.klast, p, lane);
                 phases ^= 1u << stage;
@@ -856,6 +874,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
 
 template <class Tile, bool A_MN, bool B_MN, int RAG, int EPI, bool CHUNKED>
 LmKernel lm_kernel_info() {
+    static_assert(!CHUNKED || Tile::STAGES >= 6, "two blocks of three planes in flight");
     static_assert(RAG == kRagNone || Tile::FIXED + 8 * (kLmMaxGroups + 2) <= 227 * 1024, "room for the group tables");
     LmKernel k;
     k.fn = reinterpret_cast<const void *>(&lm_mma_kernel<Tile, A_MN, B_MN, RAG, EPI, CHUNKED>);
