@@ -262,6 +262,7 @@ struct Loss {
     size_t ws_part = 0, ws_picked = 0;
     // Gradient.
     int64_t piece = 0, pieces = 0, ld_d = 0, ld_acc = 0;
+    int d_planes = 1;
     int splits = 1;
     size_t ws_d = 0, ws_planes = 0, ws_acc = 0;
     size_t forward_bytes() const { return x.ws + w.ws + ws_part + ws_picked; }
@@ -310,7 +311,12 @@ sgemmStatus_t plan_loss(int type, int64_t T, int64_t V, int64_t D, const void *X
     q.ws_part = align256(int64_t(q.slabs) * T * 8);
     q.ws_picked = align256(T * 4);
     // Gradient: pieces of the vocabulary, each a multiple of 256 columns.
-    const int64_t elem = f32 ? 10 : 2;      // FP32: the piece itself and its three planes
+    // 16 bits hold d with up to half a unit in the last place lost, and a few
+    // rows do not average that out (of one row, the target's entry is most of
+    // both gradients): up to 128 rows, whose products are bound by reading W
+    // and writing its gradient, d is held in two planes, itself and the rest.
+    q.d_planes = !f32 && !q.big ? 2 : 1;
+    const int64_t elem = f32 ? 10 : 2 * q.d_planes;      // FP32: the piece itself and its three planes
     q.piece = V;
     if (T * V * elem > kPieceBytes) {
         q.piece = std::max<int64_t>(kMinPieceCols, kPieceBytes / (elem * T) / 256 * 256);
@@ -320,7 +326,7 @@ sgemmStatus_t plan_loss(int type, int64_t T, int64_t V, int64_t D, const void *X
     q.piece = std::min(V, round_up(ceil_div(V, q.pieces), 256));
     q.pieces = ceil_div(V, q.piece);
     q.ld_d = round_up(q.piece, 16);
-    q.ws_d = align256(T * q.ld_d * (f32 ? 4 : 2));
+    q.ws_d = align256(T * q.ld_d * (f32 ? 4 : 2 * q.d_planes));
     q.ws_planes = f32 ? align256(T * q.ld_d * 6) : 0;
     // The rows' gradient: one piece, K split when its tiles are few; more
     // pieces, summed in FP32 from one to the next.
@@ -345,7 +351,7 @@ LmArgs loss_args(const Loss &q, const LmKernel &k, int64_t M, int64_t N, int64_t
     p.M = int(M);
     p.N = int(N);
     p.T = int(M);
-    p.kb = int(ceil_div(K, 64));
+    p.kb = p.kb_plane = int(ceil_div(K, 64));
     p.tile_n = tile_n;
     p.tiles_m = int(ceil_div(M, k.tile_m));
     p.tiles_n = int(ceil_div(N, tile_n));
@@ -633,10 +639,14 @@ sgemmStatus_t sgemmCrossEntropyGrad(sgemmHandle_t h, sgemmDataType_t type, int64
     float *acc = reinterpret_cast<float *>(ws + 256 + q.ws_d + q.ws_planes);
     ws += 256 + q.ws_d + q.ws_planes + q.ws_acc;
     if (!q.x.prepare(ws, stream) || !q.w.prepare(ws + q.x.ws, stream)) return SGEMM_STATUS_LAUNCH_FAILED;
-    // F16 holds the logits' gradient times a power of two, taken out again
-    // by the gradient products: its smallest normal number, 2^-14, is above
-    // most softmax values over a long vocabulary times a mean's 1 / T.
-    if (f16 && sg::lm_launch_grad_scale(dloss, target, V, int(T), scale2, stream) != cudaSuccess)
+    // d is held over the largest |dloss|, taken in again by the gradient
+    // products: then the entries of the targets lie at 1 - p, where all of
+    // them are not rounded the same way, as they are when dloss is one over
+    // the number of tokens (bf16, 853 tokens: gradients off by 0.28%, all in
+    // one direction).  F16 besides times 2^13: its smallest normal number,
+    // 2^-14, is above most softmax values over a long vocabulary.
+    const bool scaled = f16 || (!f32 && q.d_planes == 1);
+    if (scaled && sg::lm_launch_grad_scale(dloss, target, V, int(T), f16 ? 8192.f : 1.f, scale2, stream) != cudaSuccess)
         return SGEMM_STATUS_LAUNCH_FAILED;
 
     const LmKernel kd = sg::lm_dlogits_kernel(q.big, f32);
@@ -659,7 +669,8 @@ sgemmStatus_t sgemmCrossEntropyGrad(sgemmHandle_t h, sgemmDataType_t type, int64
         p.v0 = v0;
         p.lse = lse;
         p.grad = dloss;
-        p.gscale = f16 ? scale2 : nullptr;
+        p.gscale = scaled ? scale2 : nullptr;
+        if (q.d_planes == 2) p.lo = static_cast<char *>(d) + T * q.ld_d * 2;
         if (!q.w.map_rows(&tm_w, kd.box_b, v0, width)) return SGEMM_STATUS_LAUNCH_FAILED;
         st = launch_lm(h, kd, false, tm_x, tm_w, p, p.num_tiles, stream);
         if (st != SGEMM_STATUS_SUCCESS) return st;
@@ -670,6 +681,8 @@ sgemmStatus_t sgemmCrossEntropyGrad(sgemmHandle_t h, sgemmDataType_t type, int64
         dd.cols = width;
         dd.ld = q.ld_d;
         dd.type = type;
+        dd.batch = q.d_planes;
+        dd.stride = T * q.ld_d;
         dd.plan();
         if (!dd.prepare(planes, stream)) return SGEMM_STATUS_LAUNCH_FAILED;
         if (!dd.map(&tm_d, kx.box_a) || !dd.map(&tm_d_mn, 64) || !q.w.map_rows(&tm_w_mn, 64, v0, width))
@@ -677,6 +690,7 @@ sgemmStatus_t sgemmCrossEntropyGrad(sgemmHandle_t h, sgemmDataType_t type, int64
 
         // Rows' gradient: d . W over this piece of the vocabulary.
         p = loss_args(q, kx, T, D, width, kx.bn);
+        p.kb *= q.d_planes;
         p.splits = q.splits;
         p.num_tiles *= q.splits;
         if (q.splits > 1 || !last) {
@@ -690,25 +704,26 @@ sgemmStatus_t sgemmCrossEntropyGrad(sgemmHandle_t h, sgemmDataType_t type, int64
             p.ldc = lddx;
             p.out = out_type(type);
             p.vec = vec_ok(dX, lddx, 0, elem, 32);
-            p.alpha = f16 ? scale2 + 1 : nullptr;
+            p.alpha = scaled ? scale2 + 1 : nullptr;
         }
         p.acc_in = first ? nullptr : acc;
         p.ld_acc = q.ld_acc;
         st = launch_lm(h, kx, false, tm_d, tm_w_mn, p, p.num_tiles, stream);
         if (st != SGEMM_STATUS_SUCCESS) return st;
         if (q.splits > 1 &&
-            sg::lm_launch_join_splits(acc, q.ld_acc, T * q.ld_acc, q.splits, f16 ? scale2 + 1 : nullptr, int(T),
+            sg::lm_launch_join_splits(acc, q.ld_acc, T * q.ld_acc, q.splits, scaled ? scale2 + 1 : nullptr, int(T),
                                       int(D), dX, lddx, out_type(type), stream) != cudaSuccess)
             return SGEMM_STATUS_LAUNCH_FAILED;
 
         // Vocabulary rows' gradient: d^T . X, complete for this piece.
         const LmKernel kw = sg::lm_rows_kernel(width > 128, true, f32);
         p = loss_args(q, kw, width, D, T, kw.bn);
+        p.kb *= q.d_planes;
         p.C = static_cast<char *>(dW) + v0 * lddw * elem;
         p.ldc = lddw;
         p.out = out_type(type);
         p.vec = vec_ok(p.C, lddw, 0, elem, 32);
-        p.alpha = f16 ? scale2 + 1 : nullptr;
+        p.alpha = scaled ? scale2 + 1 : nullptr;
         st = launch_lm(h, kw, false, tm_d_mn, tm_x_mn, p, p.num_tiles, stream);
         if (st != SGEMM_STATUS_SUCCESS) return st;
     }

@@ -139,12 +139,12 @@ lm_lse_join_kernel(const float2 *part, int slabs, int rows, const float *picked,
     }
 }
 
-// scale2[0] = 2^e with max |grad| * 2^e in [2^12, 2^13), scale2[1] = 2^-e.
+// scale2 = {top / m, m / top}, m the largest |grad| of a counted row.
 __global__ void __launch_bounds__(1024)
-lm_grad_scale_kernel(const float *grad, const int64_t *target, int64_t vocab, int rows, float *scale2) {
+lm_grad_scale_kernel(const float *grad, const int64_t *target, int64_t vocab, int rows, float top, float *scale2) {
     griddep_launch_dependents();
     griddep_wait();
-    __shared__ float top[32];
+    __shared__ float most[32];
     float m = 0.f;
     for (int i = threadIdx.x; i < rows; i += 1024) {
         const int64_t t = target[i];
@@ -152,20 +152,16 @@ lm_grad_scale_kernel(const float *grad, const int64_t *target, int64_t vocab, in
     }
 #pragma unroll
     for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-    if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = m;
+    if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = m;
     __syncthreads();
     if (threadIdx.x < 32) {
-        m = top[threadIdx.x];
+        m = most[threadIdx.x];
 #pragma unroll
         for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
         if (threadIdx.x == 0) {
-            int e = 0;
-            if (m > 0.f && m <= 3.0e38f) {
-                frexpf(m, &e);                      // m in [2^(e-1), 2^e)
-                e = min(max(13 - e, -100), 100);
-            }
-            scale2[0] = ldexpf(1.f, e);
-            scale2[1] = ldexpf(1.f, -e);
+            const bool usable = m > 1.0e-30f && m < 1.0e30f;
+            scale2[0] = usable ? top / m : 1.f;
+            scale2[1] = usable ? m / top : 1.f;
         }
     }
 }
@@ -227,9 +223,9 @@ cudaError_t lm_launch_lse_join(const float2 *part, int slabs, int rows, const fl
                   vocab, loss, lse);
 }
 
-cudaError_t lm_launch_grad_scale(const float *grad, const int64_t *target, int64_t vocab, int rows, float *scale2,
-                                 cudaStream_t s) {
-    return launch(lm_grad_scale_kernel, 1, 1024, s, grad, target, vocab, rows, scale2);
+cudaError_t lm_launch_grad_scale(const float *grad, const int64_t *target, int64_t vocab, int rows, float top,
+                                 float *scale2, cudaStream_t s) {
+    return launch(lm_grad_scale_kernel, 1, 1024, s, grad, target, vocab, rows, top, scale2);
 }
 
 cudaError_t lm_launch_join_splits(const float *part, int64_t ld_part, int64_t plane, int splits, const float *alpha,

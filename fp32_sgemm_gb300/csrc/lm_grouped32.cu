@@ -8,12 +8,12 @@ LmKernel lm_grouped_kernel16(int size, bool w_mn);
 LmKernel lm_grouped_kernel(int size, bool w_mn, bool f32) {
     if (!f32) return lm_grouped_kernel16(size, w_mn);
     if (w_mn) {
-        if (size == 0) return lm_kernel_info<LmThin, true, false, kRagN, kEpiCols, true>();
-        if (size == 1) return lm_kernel_info<LmMid, true, false, kRagN, kEpiCols, true>();
-        return lm_kernel_info<LmBig, true, false, kRagN, kEpiCols, true>();
+        if (size == 0) return lm_kernel_info<LmThin, true, false, kRagN, kEpiCols, kPlanes>();
+        if (size == 1) return lm_kernel_info<LmMid, true, false, kRagN, kEpiCols, kPlanes>();
+        return lm_kernel_info<LmBig, true, false, kRagN, kEpiCols, kPlanes>();
     }
-    if (size == 0) return lm_kernel_info<LmThin, false, false, kRagN, kEpiCols, true>();
-    if (size == 1) return lm_kernel_info<LmMid, false, false, kRagN, kEpiCols, true>();
-    return lm_kernel_info<LmBig, false, false, kRagN, kEpiCols, true>();
+    if (size == 0) return lm_kernel_info<LmThin, false, false, kRagN, kEpiCols, kPlanes>();
+    if (size == 1) return lm_kernel_info<LmMid, false, false, kRagN, kEpiCols, kPlanes>();
+    return lm_kernel_info<LmBig, false, false, kRagN, kEpiCols, kPlanes>();
 }
 }  // namespace sg

@@ -28,6 +28,7 @@ struct LmArgs {
     int M, N;             // rows and columns of D (kRagN: columns by groups)
     int T;                // token rows (ragged extent)
     int kb;               // blocks of 64 of the contraction (not kRagK)
+    int kb_plane;         // kRagNone: of one plane of A (kb, or half of it)
     int G;
     const int32_t *ends;  // [G] end row of each group
     int tiles_m, tiles_n, tile_n, num_tiles, splits, group_m;
@@ -44,6 +45,7 @@ struct LmArgs {
     float2 *part;            // [column slab][row] {maximum, sum}
     float *picked;           // logit of the row's target
     const float *lse, *grad, *gscale;
+    void *lo;                // rest of the rounding to 16 bits, laid out as C, or NULL
     uint32_t *err;
     uint64_t timeout_ns;
     int withhold;
@@ -72,9 +74,9 @@ cudaError_t lm_launch_split3(const float *src, int64_t ld, int64_t stride, void 
 // Joins the slabs' maxima and sums: lse and loss of each row.
 cudaError_t lm_launch_lse_join(const float2 *part, int slabs, int rows, const float *picked, const int64_t *target,
                                int64_t vocab, float *loss, float *lse, cudaStream_t s);
-// Power of two that brings the largest |grad| of a counted row to 2^13.
-cudaError_t lm_launch_grad_scale(const float *grad, const int64_t *target, int64_t vocab, int rows, float *scale2,
-                                 cudaStream_t s);
+// scale2 = {top / m, m / top} for the largest |grad| m of a counted row.
+cudaError_t lm_launch_grad_scale(const float *grad, const int64_t *target, int64_t vocab, int rows, float top,
+                                 float *scale2, cudaStream_t s);
 // out = alpha * (sum of `splits` FP32 planes), rounded to `out_type`.
 cudaError_t lm_launch_join_splits(const float *part, int64_t ld_part, int64_t plane, int splits, const float *alpha,
                                   int rows, int cols, void *out, int64_t ldo, int out_type, cudaStream_t s);

@@ -9,21 +9,21 @@ LmKernel lm_rows_kernel32(bool big, bool a_mn);
 
 LmKernel lm_lse_kernel(bool big, bool f32) {
     if (f32) return lm_lse_kernel32(big);
-    if (big) return lm_kernel_info<LmBigLse, false, false, kRagNone, kEpiLse, false>();
-    return lm_kernel_info<LmWide, false, false, kRagNone, kEpiLse, false>();
+    if (big) return lm_kernel_info<LmBigLse, false, false, kRagNone, kEpiLse, kRuns>();
+    return lm_kernel_info<LmWide, false, false, kRagNone, kEpiLse, kRuns>();
 }
 LmKernel lm_dlogits_kernel(bool big, bool f32) {
     if (f32) return lm_dlogits_kernel32(big);
-    if (big) return lm_kernel_info<LmBig, false, false, kRagNone, kEpiDLogits, false>();
-    return lm_kernel_info<LmWide, false, false, kRagNone, kEpiDLogits, false>();
+    if (big) return lm_kernel_info<LmBig, false, false, kRagNone, kEpiDLogits, kPlain>();
+    return lm_kernel_info<LmWide, false, false, kRagNone, kEpiDLogits, kPlain>();
 }
 LmKernel lm_rows_kernel(bool big, bool a_mn, bool f32) {
     if (f32) return lm_rows_kernel32(big, a_mn);
     if (a_mn) {
-        if (big) return lm_kernel_info<LmBig, true, true, kRagNone, kEpiRows, false>();
-        return lm_kernel_info<LmWide, true, true, kRagNone, kEpiRows, false>();
+        if (big) return lm_kernel_info<LmBig, true, true, kRagNone, kEpiRows, kPlain>();
+        return lm_kernel_info<LmWide, true, true, kRagNone, kEpiRows, kPlain>();
     }
-    if (big) return lm_kernel_info<LmBig, false, true, kRagNone, kEpiRows, false>();
-    return lm_kernel_info<LmWide, false, true, kRagNone, kEpiRows, false>();
+    if (big) return lm_kernel_info<LmBig, false, true, kRagNone, kEpiRows, kPlain>();
+    return lm_kernel_info<LmWide, false, true, kRagNone, kEpiRows, kPlain>();
 }
 }  // namespace sg

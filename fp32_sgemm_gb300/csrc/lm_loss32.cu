@@ -4,19 +4,19 @@
 
 namespace sg {
 LmKernel lm_lse_kernel32(bool big) {
-    if (big) return lm_kernel_info<LmBig, false, false, kRagNone, kEpiLse, true>();
-    return lm_kernel_info<LmMid, false, false, kRagNone, kEpiLse, true>();
+    if (big) return lm_kernel_info<LmBig, false, false, kRagNone, kEpiLse, kPlanes>();
+    return lm_kernel_info<LmMid, false, false, kRagNone, kEpiLse, kPlanes>();
 }
 LmKernel lm_dlogits_kernel32(bool big) {
-    if (big) return lm_kernel_info<LmBig, false, false, kRagNone, kEpiDLogits, true>();
-    return lm_kernel_info<LmMid, false, false, kRagNone, kEpiDLogits, true>();
+    if (big) return lm_kernel_info<LmBig, false, false, kRagNone, kEpiDLogits, kPlanes>();
+    return lm_kernel_info<LmMid, false, false, kRagNone, kEpiDLogits, kPlanes>();
 }
 LmKernel lm_rows_kernel32(bool big, bool a_mn) {
     if (a_mn) {
-        if (big) return lm_kernel_info<LmBig, true, true, kRagNone, kEpiRows, true>();
-        return lm_kernel_info<LmMid, true, true, kRagNone, kEpiRows, true>();
+        if (big) return lm_kernel_info<LmBig, true, true, kRagNone, kEpiRows, kPlanes>();
+        return lm_kernel_info<LmMid, true, true, kRagNone, kEpiRows, kPlanes>();
     }
-    if (big) return lm_kernel_info<LmBig, false, true, kRagNone, kEpiRows, true>();
-    return lm_kernel_info<LmMid, false, true, kRagNone, kEpiRows, true>();
+    if (big) return lm_kernel_info<LmBig, false, true, kRagNone, kEpiRows, kPlanes>();
+    return lm_kernel_info<LmMid, false, true, kRagNone, kEpiRows, kPlanes>();
 }
 }  // namespace sg

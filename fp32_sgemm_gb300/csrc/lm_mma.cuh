@@ -384,18 +384,24 @@ __device__ __forceinline__ bool lm_clear_tail(unsigned char *stage, uint64_t *la
     return ok;
 }
 
+// MODE of a kernel: 16-bit operands in one running sum; the same in runs of
+// eight blocks; FP32 operands in three planes, summed block by block.
+constexpr int kPlain = 0, kRuns = 1, kPlanes = 3;
+
 // ---------------------------------------------------------------- kernel
 
 // Threads of a kernel: kRagK has one more warp, which clears tails.
 template <class Tile, int RAG>
 constexpr int lm_threads() { return Tile::THREADS + (RAG == kRagK ? 32 : 0); }
 
-template <class Tile, bool A_MN, bool B_MN, int RAG, int EPI, bool CHUNKED>
+template <class Tile, bool A_MN, bool B_MN, int RAG, int EPI, int MODE>
 __global__ void __launch_bounds__(lm_threads<Tile, RAG>(), 1)
 lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const LmArgs p) {
     constexpr bool PAIR = Tile::PAIR;
     constexpr int BN = Tile::BN, STAGES = Tile::STAGES, SLAB = Tile::SLAB;
-    constexpr int PLANES = CHUNKED ? 3 : 1;                 // CHUNKED: FP32 operands
+    constexpr bool CHUNKED = MODE != kPlain;
+    constexpr int PLANES = MODE == kPlanes ? 3 : 1, CH = MODE == kRuns ? 8 : 1;
+    static_assert((CH & (CH - 1)) == 0, "");
     static_assert(!B_MN || Tile::B_ROWS % 64 == 0, "MN-major B is staged in chunks of 64 columns");
 
     extern __shared__ unsigned char smem_raw[];
@@ -465,7 +471,9 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             const int ma = w.m0 + (int)rank * Tile::BM;
             const int nb = w.n0 + (int)rank * (w.nmma >> 1);
             for (int kb = 0; ok && kb < w.nkb; ++kb) {
-                const int kc = RAG == kRagK ? w.krow0 + kb * 64 : (w.kb0 + kb) * 64;
+                // kRagNone: A may have a second plane, which goes over the same B.
+                const int again = RAG == kRagNone && w.kb0 + kb >= p.kb_plane ? 1 : 0;
+                const int kc = RAG == kRagK ? w.krow0 + kb * 64 : (w.kb0 + kb - again * p.kb_plane) * 64;
                 const bool tail = RAG == kRagK && kb == w.nkb - 1 && (w.klast & 15) != 0;
                 for (int pl = 0; pl < PLANES; ++pl) {
                     if (p.withhold == kWithholdRefill && issued >= STAGES) { ok = false; break; }
@@ -476,7 +484,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                     ok = __all_sync(~0u, ok);
                     if (!ok) break;
                     unsigned char *sa = smem + stage * Tile::STAGE_BYTES, *sb = sa + Tile::A_BYTES;
-                    const int za = RAG == kRagN ? pl * p.G + w.g : pl;
+                    const int za = RAG == kRagN ? pl * p.G + w.g : pl + again;
                     const uint32_t fb = full_pair + (uint32_t)stage * 8u;
                     // Copies of this stage, completing on the ring's barrier
                     // (rank 0's for a pair) or, for a tail, on a local one.
@@ -561,7 +569,8 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             // loop, whose instructions have to stay ahead of the tensor core.
             const int whole = RAG == kRagK && w.nkb > 0 && w.klast < 64 ? w.nkb - 1 : w.nkb;
             for (int kb = 0; kb < whole; ++kb) {
-                const bool first = CHUNKED || kb == 0, last = CHUNKED || kb == w.nkb - 1;
+                const bool first = CHUNKED ? (kb & (CH - 1)) == 0 : kb == 0;
+                const bool last = kb == w.nkb - 1 || (CHUNKED && (kb & (CH - 1)) == CH - 1);
                 if (first) {
                     const int ab = gc & 1;
                     if (!mbar_wait_bounded<PAIR>(&tempty[ab], ((uint32_t)(gc >> 1) & 1u) ^ 1u, p.timeout_ns)) {
@@ -591,8 +600,8 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
-                    for (int pr = 0; pr < (CHUNKED ? 6 : 1); ++pr) {
-                        const uint64_t a = da[CHUNKED ? plane_a(pr) : 0], b = db[CHUNKED ? plane_b(pr) : 0];
+                    for (int pr = 0; pr < (PLANES == 3 ? 6 : 1); ++pr) {
+                        const uint64_t a = da[PLANES == 3 ? plane_a(pr) : 0], b = db[PLANES == 3 ? plane_b(pr) : 0];
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
                             const uint32_t acc = first && pr == 0 && kk == 0 ? 0u : 1u;
@@ -618,7 +627,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             }
             if constexpr (RAG == kRagK) {
                 if (ok && whole < w.nkb) {
-                    const bool first = CHUNKED || whole == 0;
+                    const bool first = CHUNKED ? (whole & (CH - 1)) == 0 : whole == 0;
                     const int steps = (w.klast + 15) >> 4, ab = gc & 1;
                     if (first) {
                         ok = mbar_wait_bounded<PAIR>(&tempty[ab], ((uint32_t)(gc >> 1) & 1u) ^ 1u, p.timeout_ns);
@@ -642,8 +651,8 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
-                        for (int pr = 0; pr < (CHUNKED ? 6 : 1); ++pr) {
-                            const uint64_t a = da[CHUNKED ? plane_a(pr) : 0], b = db[CHUNKED ? plane_b(pr) : 0];
+                        for (int pr = 0; pr < (PLANES == 3 ? 6 : 1); ++pr) {
+                            const uint64_t a = da[PLANES == 3 ? plane_a(pr) : 0], b = db[PLANES == 3 ? plane_b(pr) : 0];
                             for (int kk = 0; kk < steps; ++kk) {
                                 const uint32_t acc = first && pr == 0 && kk == 0 ? 0u : 1u;
                                 if constexpr (PAIR) mma_f16_pair(d_tmem, a + kk * KA, b + kk * KB, idesc, acc);
@@ -742,14 +751,16 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 }
             }
             if constexpr (CHUNKED) {
-                // Each block of 64 of the contraction is summed in its own
-                // accumulator and added here in FP32 with rounding to nearest
-                // (the tensor core's own running sum truncates; two blocks per
-                // accumulator doubled the error, at 40003 terms to 2^-20 of
-                // their magnitudes).
+                // Runs of CH blocks of the contraction are summed in an
+                // accumulator of their own and added here in FP32 with rounding
+                // to nearest (the tensor core's own running sum truncates).
+                // FP32 operands: one block (two doubled the error, at 40003
+                // terms to 2^-20 of their magnitudes).  Logits of 16-bit
+                // operands: eight (the loss of 160 rows at 3136 terms was off by
+                // 1.7e-6 with one sum, 2e-7 as FP32 rounds it).
 #pragma unroll
                 for (int c = 0; c < SLAB; ++c) sum[c] = 0.f;
-                for (int kb = 0; ok && kb < w.nkb; ++kb) {
+                for (int kb = 0; ok && kb < w.nkb; kb += CH) {
                     wait_acc();
                     if (!ok) break;
 #pragma unroll
@@ -843,6 +854,18 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                             for (int i = 0; i < 32; ++i) v[i] *= alpha;
                         }
                         const int64_t z = (int64_t)(RAG == kRagK ? w.g : w.s) * p.stride_c;
+                        if (EPI == kEpiDLogits && p.lo != nullptr) {
+                            // What the rounding to 16 bits leaves, in a plane of its own.
+                            float rest[32];
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                rest[i] = v[i] - (p.out == kOutF16 ? __half2float(__float2half_rn(v[i]))
+                                                                   : __bfloat162float(__float2bfloat16_rn(v[i])));
+                            if (p.out == kOutF16)
+                                lm_store_rows(p, static_cast<__half *>(p.lo), row, row0, n, cnt, rest, stg, lane);
+                            else
+                                lm_store_rows(p, static_cast<__nv_bfloat16 *>(p.lo), row, row0, n, cnt, rest, stg, lane);
+                        }
                         if (p.out == kOutF32)
                             lm_store_rows(p, static_cast<float *>(p.C) + z, row, row0, n, cnt, v, stg, lane);
                         else if (p.out == kOutF16)
@@ -872,12 +895,12 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     }
 }
 
-template <class Tile, bool A_MN, bool B_MN, int RAG, int EPI, bool CHUNKED>
+template <class Tile, bool A_MN, bool B_MN, int RAG, int EPI, int MODE>
 LmKernel lm_kernel_info() {
-    static_assert(!CHUNKED || Tile::STAGES >= 6, "two blocks of three planes in flight");
+    static_assert(MODE != kPlanes || Tile::STAGES >= 6, "two blocks of three planes in flight");
     static_assert(RAG == kRagNone || Tile::FIXED + 8 * (kLmMaxGroups + 2) <= 227 * 1024, "room for the group tables");
     LmKernel k;
-    k.fn = reinterpret_cast<const void *>(&lm_mma_kernel<Tile, A_MN, B_MN, RAG, EPI, CHUNKED>);
+    k.fn = reinterpret_cast<const void *>(&lm_mma_kernel<Tile, A_MN, B_MN, RAG, EPI, MODE>);
     k.threads = lm_threads<Tile, RAG>();
     k.smem = Tile::FIXED;
     k.tile_m = Tile::TILE_M;

@@ -5,10 +5,10 @@
 namespace sg {
 LmKernel lm_weight_grad_kernel(int size, bool f32) {
     if (f32) {
-        if (size == 1) return lm_kernel_info<LmMid, true, true, kRagK, kEpiRows, true>();
-        return lm_kernel_info<LmBig, true, true, kRagK, kEpiRows, true>();
+        if (size == 1) return lm_kernel_info<LmMid, true, true, kRagK, kEpiRows, kPlanes>();
+        return lm_kernel_info<LmBig, true, true, kRagK, kEpiRows, kPlanes>();
     }
-    if (size == 1) return lm_kernel_info<LmMid, true, true, kRagK, kEpiRows, false>();
-    return lm_kernel_info<LmBig, true, true, kRagK, kEpiRows, false>();
+    if (size == 1) return lm_kernel_info<LmMid, true, true, kRagK, kEpiRows, kPlain>();
+    return lm_kernel_info<LmBig, true, true, kRagK, kEpiRows, kPlain>();
 }
 }  // namespace sg
