@@ -383,7 +383,8 @@ sgemmStatus_t plan_w4(int type, int64_t M, int64_t N, int64_t K, int group, W4 &
     if (!type_ok(type) || M < 0 || N < 0 || K < 0) return SGEMM_STATUS_INVALID_VALUE;
     if (group != 32 && group != 64 && group != 128) return SGEMM_STATUS_INVALID_VALUE;
     if (K % group != 0) return SGEMM_STATUS_INVALID_VALUE;
-    if (M > kMaxDim - 512 || N > kMaxDim - 512 || K > kMaxDim - 512) return SGEMM_STATUS_NOT_SUPPORTED;
+    // (Row numbers run past N by the rows of one round of CTAs.)
+    if (M > kMaxDim - 512 || N > kMaxDim - (1 << 20) || K > kMaxDim - 512) return SGEMM_STATUS_NOT_SUPPORTED;
     q.type = type;
     q.planes = type == SGEMM_TYPE_F32 ? 3 : 1;
     q.group = group;
@@ -565,7 +566,7 @@ sgemmStatus_t sgemmCrossEntropy(sgemmHandle_t h, sgemmDataType_t type, int64_t T
                                 const void *X, int64_t ldx, const void *W, int64_t ldw, const int64_t *target,
                                 float *loss, float *lse, cudaStream_t stream) {
     Loss q;
-    sgemmStatus_t st = plan_loss(type, T, V, D, X, ldx, W, ldw, h, q);
+    sgemmStatus_t st = plan_loss(type, T, V, D, X, ldx, W, ldw, nullptr, q);      // checks
     if (st != SGEMM_STATUS_SUCCESS) return st;
     if (T == 0) return SGEMM_STATUS_SUCCESS;
     if ((st = check_vector(target, 8)) != SGEMM_STATUS_SUCCESS || (st = check_vector(loss, 4)) != SGEMM_STATUS_SUCCESS ||
@@ -574,6 +575,7 @@ sgemmStatus_t sgemmCrossEntropy(sgemmHandle_t h, sgemmDataType_t type, int64_t T
     if (h == nullptr) return SGEMM_STATUS_INVALID_VALUE;
     st = check_device(h);
     if (st != SGEMM_STATUS_SUCCESS) return st;
+    plan_loss(type, T, V, D, X, ldx, W, ldw, h, q);
     if (h->ws == nullptr || h->ws_bytes < q.forward_bytes()) return SGEMM_STATUS_WORKSPACE_REQUIRED;
 
     const bool f32 = type == SGEMM_TYPE_F32;
@@ -612,7 +614,7 @@ sgemmStatus_t sgemmCrossEntropyGrad(sgemmHandle_t h, sgemmDataType_t type, int64
                                     const float *lse, const float *dloss, void *dX, int64_t lddx, void *dW,
                                     int64_t lddw, cudaStream_t stream) {
     Loss q;
-    sgemmStatus_t st = plan_loss(type, T, V, D, X, ldx, W, ldw, h, q);
+    sgemmStatus_t st = plan_loss(type, T, V, D, X, ldx, W, ldw, nullptr, q);      // checks
     if (st != SGEMM_STATUS_SUCCESS) return st;
     st = check_matrix(dX, T, D, lddx, type, T > 0);
     if (st != SGEMM_STATUS_SUCCESS) return st;
@@ -626,6 +628,7 @@ sgemmStatus_t sgemmCrossEntropyGrad(sgemmHandle_t h, sgemmDataType_t type, int64
     if (h == nullptr) return SGEMM_STATUS_INVALID_VALUE;
     st = check_device(h);
     if (st != SGEMM_STATUS_SUCCESS) return st;
+    plan_loss(type, T, V, D, X, ldx, W, ldw, h, q);
     if (T == 0)
         return sg::lm_launch_zero(dW, lddw, 0, elem, V, D, 1, stream) == cudaSuccess ? SGEMM_STATUS_SUCCESS
                                                                                      : SGEMM_STATUS_LAUNCH_FAILED;

@@ -8,11 +8,14 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
 #include <exception>
+#include <optional>
 
 #include "../../include/sgemm_gb300_lm.h"
 
@@ -134,14 +137,17 @@ void check(sgemmStatus_t st, const char *where) {
     throw Failed{};
 }
 
-// A Handle of this package: its C handle, and a workspace of `need` bytes
-// attached to it.
+// A Handle of this package: its C handle, the stream of the call, and a
+// workspace of `need` bytes attached to the handle.  With a stream given, what
+// the call allocates belongs to that stream, and what it reads is kept from
+// reuse until that stream has passed.
 struct Call {
     sgemmHandle_t handle = nullptr;
     cudaStream_t stream = nullptr;
     PyObject *owner;
+    std::optional<c10::cuda::CUDAStreamGuard> guard;
 
-    Call(PyObject *h, PyObject *s, c10::Device dev) : owner(h) {
+    Call(PyObject *h, PyObject *s, c10::Device dev, std::initializer_list<PyObject *> read) : owner(h) {
         PyObject *p = PyObject_GetAttr(h, g_name_ptr);
         if (p == nullptr) throw Failed{};
         handle = static_cast<sgemmHandle_t>(PyLong_AsVoidPtr(p));
@@ -149,13 +155,20 @@ struct Call {
         if (PyErr_Occurred()) throw Failed{};
         if (s == Py_None) {
             stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
-        } else {
-            PyObject *v = PyObject_CallFunction(g_stream_ptr, "Oi", s, int(dev.index()));
-            if (v == nullptr) throw Failed{};
-            stream = v == Py_None ? nullptr : static_cast<cudaStream_t>(PyLong_AsVoidPtr(v));
-            Py_DECREF(v);
-            if (PyErr_Occurred()) throw Failed{};
+            return;
         }
+        PyObject *v = PyObject_CallFunction(g_stream_ptr, "Oi", s, int(dev.index()));
+        if (v == nullptr) throw Failed{};
+        stream = v == Py_None ? nullptr : static_cast<cudaStream_t>(PyLong_AsVoidPtr(v));
+        Py_DECREF(v);
+        if (PyErr_Occurred()) throw Failed{};
+        const c10::cuda::CUDAStream on = stream == nullptr ? c10::cuda::getDefaultCUDAStream(dev.index())
+                                                           : c10::cuda::getStreamFromExternal(stream, dev.index());
+        if (on == c10::cuda::getCurrentCUDAStream(dev.index())) return;
+        guard.emplace(on);
+        for (PyObject *t : read)
+            if (t != Py_None)
+                c10::cuda::CUDACachingAllocator::recordStream(THPVariable_Unpack(t).storage().data_ptr(), on);
     }
     void workspace(size_t need) const {
         if (need == 0) return;
@@ -205,9 +218,10 @@ PyObject *py_grouped_gemm(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int64_t T = mx.rows, K = mx.cols, G = w.size(0), N = w.size(trans ? 1 : 2);
         const Matrix mw = stack(w, "w", st, dev, G, trans ? N : K, trans ? K : N);
         const int32_t *ends = vector<int32_t>(a[2], "group_ends", at::kInt, dev, G);
+        if (a[4] != Py_None) matrix(tensor(a[4], "out"), "out", st, dev, T, N);   // before it is recorded
+        const Call c(a[5], a[6], dev, {a[0], a[1], a[2], a[4]});
         const at::Tensor out = output(a[4], {T, N}, st, dev);
         const Matrix my = matrix(out, "out", st, dev, T, N);
-        const Call c(a[5], a[6], dev);
         const sgemmOperation_t op = trans ? SGEMM_OP_T : SGEMM_OP_N;
         size_t need = 0;
         check(sgemmGroupedWorkspaceSize(c.handle, ty, op, T, N, K, G, mx.ptr, mx.ld, mw.ptr, mw.ld, mw.stride, &need),
@@ -234,9 +248,10 @@ PyObject *py_grouped_gemm_weight_grad(PyObject *, PyObject *const *a, Py_ssize_t
         const int64_t T = l.rows, M = l.cols, N = r.cols;
         const int32_t *ends = vector<int32_t>(a[2], "group_ends", at::kInt, dev, -1);
         const int64_t G = THPVariable_Unpack(a[2]).size(0);
+        if (a[4] != Py_None) stack(tensor(a[4], "out"), "out", st, dev, G, M, N);   // before it is recorded
+        const Call c(a[5], a[6], dev, {a[0], a[1], a[2], a[4]});
         const at::Tensor out = output(a[4], {G, M, N}, st, dev);
         const Matrix mc = stack(out, "out", st, dev, G, M, N);
-        const Call c(a[5], a[6], dev);
         size_t need = 0;
         check(sgemmGroupedWeightGradWorkspaceSize(c.handle, ty, T, M, N, G, l.ptr, l.ld, r.ptr, r.ld, &need),
               "sgemmGroupedWeightGradWorkspaceSize");
@@ -272,8 +287,8 @@ PyObject *py_linear_cross_entropy(PyObject *, PyObject *const *a, Py_ssize_t n) 
         expect(n, 5);
         const LossOperands o(a[0], a[1], a[2]);
         const int64_t T = o.x.rows, V = o.w.rows, D = o.x.cols;
+        const Call c(a[3], a[4], o.dev, {a[0], a[1], a[2]});
         const at::Tensor loss = make({T}, at::kFloat, o.dev), lse = make({T}, at::kFloat, o.dev);
-        const Call c(a[3], a[4], o.dev);
         size_t need = 0;
         check(sgemmCrossEntropyWorkspaceSize(c.handle, o.ty, T, V, D, o.x.ptr, o.x.ld, o.w.ptr, o.w.ld, &need),
               "sgemmCrossEntropyWorkspaceSize");
@@ -293,8 +308,8 @@ PyObject *py_linear_cross_entropy_grad(PyObject *, PyObject *const *a, Py_ssize_
         const int64_t T = o.x.rows, V = o.w.rows, D = o.x.cols;
         const float *lse = vector<float>(a[3], "lse", at::kFloat, o.dev, T);
         const float *dloss = vector<float>(a[4], "dloss", at::kFloat, o.dev, T);
+        const Call c(a[5], a[6], o.dev, {a[0], a[1], a[2], a[3], a[4]});
         const at::Tensor dx = make({T, D}, o.st, o.dev), dw = make({V, D}, o.st, o.dev);
-        const Call c(a[5], a[6], o.dev);
         size_t need = 0;
         check(sgemmCrossEntropyGradWorkspaceSize(c.handle, o.ty, T, V, D, o.x.ptr, o.x.ld, o.w.ptr, o.w.ld, &need),
               "sgemmCrossEntropyGradWorkspaceSize");
@@ -326,9 +341,10 @@ PyObject *py_w4_gemm(PyObject *, PyObject *const *a, Py_ssize_t n) {
         Matrix mz;
         mz.ld = 0;
         if (a[3] != Py_None) mz = matrix(tensor(a[3], "zeros"), "zeros", at::kByte, dev, N, groups);
+        if (a[4] != Py_None) matrix(tensor(a[4], "out"), "out", st, dev, M, N);   // before it is recorded
+        const Call c(a[5], a[6], dev, {a[0], a[1], a[2], a[3], a[4]});
         const at::Tensor out = output(a[4], {M, N}, st, dev);
         const Matrix my = matrix(out, "out", st, dev, M, N);
-        const Call c(a[5], a[6], dev);
         const int gr = group > 1024 ? 1024 : int(group);       // beyond any that is taken
         size_t need = 0;
         check(sgemmW4WorkspaceSize(c.handle, ty, M, N, K, gr, &need), "sgemmW4WorkspaceSize");
