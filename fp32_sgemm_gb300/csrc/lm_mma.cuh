@@ -304,9 +304,27 @@ __device__ __forceinline__ void lm_store_rows(const LmArgs &p, Out *base, int ro
             for (int i = 0; i < 32; ++i)
                 if (i < cnt) c[i] = lm_cvt<Out>(v[i]);
         }
-    } else {
+    } else if constexpr (sizeof(Out) == 2) {
         // Rows that vector stores cannot reach: turned in shared memory, so
-        // that half a warp writes 16 neighbours of one row at a time.
+        // that a warp writes 32 neighbours of one row at a time (rows 34
+        // elements apart there: no bank is met twice).
+        uint32_t *words = reinterpret_cast<uint32_t *>(stg);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) words[lane * 17 + i] = lm_pack2<Out>(v[2 * i], v[2 * i + 1]);
+        __syncwarp();
+        const Out *from = reinterpret_cast<const Out *>(stg) + lane;
+        Out *to = base + (int64_t)row0 * p.ldc + col + lane;
+        if (lane < cnt) {
+            if (row0 + 32 <= p.M) {
+#pragma unroll
+                for (int r = 0; r < 32; ++r) to[(int64_t)r * p.ldc] = from[r * 34];
+            } else {
+                for (int r = 0; row0 + r < p.M; ++r) to[(int64_t)r * p.ldc] = from[r * 34];
+            }
+        }
+    } else {
+        // The same for FP32, half a warp on 16 neighbours of a row.
         const int c = lane & 15, rr = lane >> 4;
 #pragma unroll
         for (int h = 0; h < 32; h += 16) {
@@ -855,7 +873,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                             for (int i = 0; i < 32; ++i) v[i] *= alpha;
                         }
                         const int64_t z = (int64_t)(RAG == kRagK ? w.g : w.s) * p.stride_c;
-                        if (EPI == kEpiDLogits && p.lo != nullptr) {
+                        if (EPI == kEpiDLogits && !PAIR && p.lo != nullptr) {
                             // What the rounding to 16 bits leaves, in a plane of its own.
                             float rest[32];
 #pragma unroll
