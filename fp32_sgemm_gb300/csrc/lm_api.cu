@@ -270,11 +270,11 @@ struct Loss {
 };
 
 // Columns per tile of a rows x cols product on `slots` CTAs or pairs: the
-// width with the least waves x (width + what a tile costs beside its MMAs).
-int balanced_tile_n(int64_t tiles_m, int64_t cols, int64_t slots, int gran, int most) {
+// width with the least rounds x (width + what a tile costs beside it).
+int balanced_tile_n(int64_t tiles_m, int64_t cols, int64_t slots, int gran, int least, int most) {
     int best = most;
     double best_cost = 0.0;
-    for (int n = most; n >= most / 2; n -= gran) {
+    for (int n = most; n >= least; n -= gran) {
         const double cost = double(ceil_div(tiles_m * ceil_div(cols, n), slots)) * (n + 8.0);
         if (n == most || cost < best_cost) { best_cost = cost; best = n; }
     }
@@ -305,7 +305,7 @@ sgemmStatus_t plan_loss(int type, int64_t T, int64_t V, int64_t D, const void *X
     const int64_t slots = q.big ? h->sm_count / 2 : h->sm_count;
     const int64_t tiles_m = ceil_div(T, q.big ? 256 : 128);
     q.bn = !q.big && f32 ? 128 : 256;
-    q.tile_n = balanced_tile_n(tiles_m, V, slots, q.big ? 32 : 16, q.bn);
+    q.tile_n = balanced_tile_n(tiles_m, V, slots, q.big ? 32 : 16, q.bn / 2, q.bn);
     q.tiles_n = int(ceil_div(V, q.tile_n));
     q.slabs = q.tiles_n * 2;
     q.ws_part = align256(int64_t(q.slabs) * T * 8);
@@ -589,7 +589,7 @@ sgemmStatus_t sgemmCrossEntropy(sgemmHandle_t h, sgemmDataType_t type, int64_t T
     ws += q.ws_part + q.ws_picked;
     if (!q.x.prepare(ws, stream) || !q.w.prepare(ws + q.x.ws, stream)) return SGEMM_STATUS_LAUNCH_FAILED;
     CUtensorMap tm_x, tm_w;
-    if (!q.x.map(&tm_x, k.box_a) || !q.w.map(&tm_w, k.box_b)) return SGEMM_STATUS_LAUNCH_FAILED;
+    if (!q.x.map(&tm_x, k.box_a) || !q.w.map(&tm_w, q.tile_n / (k.pair ? 2 : 1))) return SGEMM_STATUS_LAUNCH_FAILED;
     st = launch_lm(h, k, false, tm_x, tm_w, p, p.num_tiles, stream);
     if (st != SGEMM_STATUS_SUCCESS) return st;
     return sg::lm_launch_lse_join(p.part, q.slabs, int(T), p.picked, target, V, loss, lse, stream) == cudaSuccess
@@ -661,7 +661,15 @@ sgemmStatus_t sgemmCrossEntropyGrad(sgemmHandle_t h, sgemmDataType_t type, int64
         const bool first = i == 0, last = i == q.pieces - 1;
         // d = (softmax - one at the target) * dloss for this piece.
         const int64_t slots = q.big ? h->sm_count / 2 : h->sm_count;
-        const int tn = balanced_tile_n(ceil_div(T, kd.tile_m), width, slots, kd.gran, kd.bn);
+        // A piece of one round of half-wide tiles at most: narrower ones, down
+        // to 32 columns, bring every SM to it.  (Both gradients of one row,
+        // 9600 x 1600: 64.7 -> 57.9 us; of 100 rows, 2000 x 512: 39.8 -> 32.8.
+        // More rounds of them lose, 128 rows, 50257 x 768: 120 -> 133, and so
+        // does the forward pass, which also joins a part for each tile: one
+        // row, 9600 x 1600: 20.3 -> 24.9.)
+        const int64_t tiles_m = ceil_div(T, kd.tile_m);
+        const bool one_round = !q.big && tiles_m * ceil_div(width, kd.bn / 2) <= slots;
+        const int tn = balanced_tile_n(tiles_m, width, slots, kd.gran, one_round ? 32 : kd.bn / 2, kd.bn);
         LmArgs p = loss_args(q, kd, T, width, D, tn);
         p.C = d;
         p.ldc = q.ld_d;
@@ -674,7 +682,7 @@ sgemmStatus_t sgemmCrossEntropyGrad(sgemmHandle_t h, sgemmDataType_t type, int64
         p.grad = dloss;
         p.gscale = scaled ? scale2 : nullptr;
         if (q.d_planes == 2) p.lo = static_cast<char *>(d) + T * q.ld_d * 2;
-        if (!q.w.map_rows(&tm_w, kd.box_b, v0, width)) return SGEMM_STATUS_LAUNCH_FAILED;
+        if (!q.w.map_rows(&tm_w, tn / (kd.pair ? 2 : 1), v0, width)) return SGEMM_STATUS_LAUNCH_FAILED;
         st = launch_lm(h, kd, false, tm_x, tm_w, p, p.num_tiles, stream);
         if (st != SGEMM_STATUS_SUCCESS) return st;
 

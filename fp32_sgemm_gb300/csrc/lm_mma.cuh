@@ -480,9 +480,9 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         int stage = 0, issued = 0;
         uint32_t phase = 0;
         bool ok = true;
-        // kRagN: the copies of B have as many rows as a tile may have.
+        // K-major B is copied in as many rows as a tile may have.
         const uint32_t stage_bytes =
-            RAG == kRagN ? (uint32_t)(Tile::A_BYTES + p.tile_n / (PAIR ? 2 : 1) * 128) : (uint32_t)Tile::STAGE_BYTES;
+            B_MN ? (uint32_t)Tile::STAGE_BYTES : (uint32_t)(Tile::A_BYTES + p.tile_n / (PAIR ? 2 : 1) * 128);
         const uint32_t full_pair = PAIR ? cluster_addr(&full[0], 0) : 0u;   // rank 0's barriers
         for (int t = slot; ok && t < num_tiles; t += slots) {
             const LmWork w = lm_work<Tile, RAG>(p, g_start, g_prefix, t);
@@ -803,7 +803,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
 #pragma unroll
             for (int c0 = 0; c0 < SLAB; c0 += 32) {
                 const int col = slab0 + c0;                 // column in the tile
-                if (col < w.nvalid) {
+                if (col < w.nvalid && (EPI == kEpiCols || row0 < p.M)) {
                     float v[32];
                     if constexpr (CHUNKED) {
 #pragma unroll
