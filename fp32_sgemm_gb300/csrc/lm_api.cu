@@ -43,8 +43,9 @@ struct Operand {
     size_t ws = 0;
     const void *ptr_t = nullptr;
 
-    void plan() {
-        copy = type == SGEMM_TYPE_F32 || !aligned(ptr, 16) || ld % 8 != 0 || (batch > 1 && stride % 8 != 0);
+    // always: copied even where TMA could read in place.
+    void plan(bool always = false) {
+        copy = always || type == SGEMM_TYPE_F32 || !aligned(ptr, 16) || ld % 8 != 0 || (batch > 1 && stride % 8 != 0);
         if (copy) {
             ld_t = round_up(std::max<int64_t>(cols, 1), 8);
             stride_t = rows * ld_t;
@@ -57,8 +58,8 @@ struct Operand {
         }
     }
     int planes() const { return type == SGEMM_TYPE_F32 ? 3 : 1; }
-    // Copies into `at` (ws bytes) if need be.
-    bool prepare(void *at, cudaStream_t s) {
+    // Copies into `at` (ws bytes) if need be; rows left out by `keep` as zeros.
+    bool prepare(void *at, cudaStream_t s, sg::LmRowFilter keep = {}) {
         if (!copy) {
             ptr_t = ptr;
             return true;
@@ -67,8 +68,8 @@ struct Operand {
         const int64_t st = batch > 1 ? stride : 0;
         return (type == SGEMM_TYPE_F32
                     ? sg::lm_launch_split3(static_cast<const float *>(ptr), ld, st, at, ld_t, plane_t, rows, cols,
-                                           batch, s)
-                    : sg::lm_launch_pack16(ptr, ld, st, at, ld_t, rows, cols, batch, s)) == cudaSuccess;
+                                           batch, keep, s)
+                    : sg::lm_launch_pack16(ptr, ld, st, at, ld_t, rows, cols, batch, keep, s)) == cudaSuccess;
     }
     // {cols, rows, batch * planes}, boxes of 64 x box_rows.
     bool map(CUtensorMap *m, int box_rows) const { return map_rows(m, box_rows, 0, rows); }
@@ -255,6 +256,7 @@ struct Loss {
     int type = 0;
     int64_t T = 0, V = 0, D = 0;
     Operand x, w;
+    Operand x_kept;              // gradient: x, rows that take no part as zeros
     bool big = false;
     int bn = 0;                  // columns of a tile at most
     // Forward.
@@ -266,7 +268,7 @@ struct Loss {
     int splits = 1;
     size_t ws_d = 0, ws_planes = 0, ws_acc = 0;
     size_t forward_bytes() const { return x.ws + w.ws + ws_part + ws_picked; }
-    size_t grad_bytes() const { return x.ws + w.ws + ws_d + ws_planes + ws_acc + 256; }
+    size_t grad_bytes() const { return x_kept.ws + w.ws + ws_d + ws_planes + ws_acc + 256; }
 };
 
 // Columns per tile of a rows x cols product on `slots` CTAs or pairs: the
@@ -298,7 +300,9 @@ sgemmStatus_t plan_loss(int type, int64_t T, int64_t V, int64_t D, const void *X
     q.x.ptr = X; q.x.rows = T; q.x.cols = D; q.x.ld = ldx; q.x.type = type;
     q.w.ptr = W; q.w.rows = V; q.w.cols = D; q.w.ld = ldw; q.w.type = type;
     if (T == 0 || h == nullptr) return SGEMM_STATUS_SUCCESS;
+    q.x_kept = q.x;
     q.x.plan();
+    q.x_kept.plan(true);
     q.w.plan();
     const bool f32 = type == SGEMM_TYPE_F32;
     q.big = T > 128;
@@ -641,7 +645,12 @@ sgemmStatus_t sgemmCrossEntropyGrad(sgemmHandle_t h, sgemmDataType_t type, int64
     void *planes = ws + 256 + q.ws_d;
     float *acc = reinterpret_cast<float *>(ws + 256 + q.ws_d + q.ws_planes);
     ws += 256 + q.ws_d + q.ws_planes + q.ws_acc;
-    if (!q.x.prepare(ws, stream) || !q.w.prepare(ws + q.x.ws, stream)) return SGEMM_STATUS_LAUNCH_FAILED;
+    // Rows that take no part may hold anything, infinities and NaN too: the
+    // zeros of d do not keep those out of d^T . X, so X is always a copy
+    // (both gradients of 12 rows, 5000 x 768: 38.1 -> 40.5 us; of 128 rows and
+    // more, within the noise).
+    Operand &x = q.x_kept;
+    if (!x.prepare(ws, stream, {target, V, dloss}) || !q.w.prepare(ws + x.ws, stream)) return SGEMM_STATUS_LAUNCH_FAILED;
     // d is held over the largest |dloss|, taken in again by the gradient
     // products: then the entries of the targets lie at 1 - p, where all of
     // them are not rounded the same way, as they are when dloss is one over
@@ -655,7 +664,7 @@ sgemmStatus_t sgemmCrossEntropyGrad(sgemmHandle_t h, sgemmDataType_t type, int64
     const LmKernel kd = sg::lm_dlogits_kernel(q.big, f32);
     const LmKernel kx = sg::lm_rows_kernel(q.big, false, f32);
     CUtensorMap tm_x, tm_w, tm_d, tm_x_mn, tm_w_mn, tm_d_mn;
-    if (!q.x.map(&tm_x, kd.box_a) || !q.x.map(&tm_x_mn, 64)) return SGEMM_STATUS_LAUNCH_FAILED;
+    if (!x.map(&tm_x, kd.box_a) || !x.map(&tm_x_mn, 64)) return SGEMM_STATUS_LAUNCH_FAILED;
     for (int64_t i = 0; i < q.pieces; ++i) {
         const int64_t v0 = i * q.piece, width = std::min(q.piece, q.V - v0);
         const bool first = i == 0, last = i == q.pieces - 1;

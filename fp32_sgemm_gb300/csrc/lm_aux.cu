@@ -32,9 +32,16 @@ cudaError_t launch(void (*fn)(P...), int64_t blocks, int threads, cudaStream_t s
 constexpr int kThreads = 256;
 constexpr int64_t kMaxBlocks = 152 * 16;
 
+__device__ __forceinline__ bool keeps(const LmRowFilter &f, int64_t row) {
+    if (f.target == nullptr) return true;
+    const int64_t t = f.target[row];
+    return t >= 0 && t < f.vocab && f.grad[row] != 0.f;
+}
+
+template <bool VEC>
 __global__ void __launch_bounds__(kThreads)
 lm_pack16_kernel(const uint16_t *src, int64_t ld, int64_t stride, uint16_t *dst, int64_t ld_dst, int64_t rows,
-                 int64_t cols, int64_t batch) {
+                 int64_t cols, int64_t batch, LmRowFilter keep) {
     griddep_launch_dependents();
     griddep_wait();
     const int64_t per_row = ld_dst / 8, total = per_row * rows * batch;
@@ -42,8 +49,14 @@ lm_pack16_kernel(const uint16_t *src, int64_t ld, int64_t stride, uint16_t *dst,
         const int64_t r = i / per_row, c = (i - r * per_row) * 8, b = r / rows;
         const uint16_t *s = src + b * stride + (r - b * rows) * ld + c;
         alignas(16) uint16_t v[8];
+        if (!keeps(keep, r)) {
+            *reinterpret_cast<uint4 *>(v) = make_uint4(0, 0, 0, 0);
+        } else if (VEC && c + 8 <= cols) {
+            *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(s);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? s[e] : (uint16_t)0;
+            for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? s[e] : (uint16_t)0;
+        }
         *reinterpret_cast<uint4 *>(dst + r * ld_dst + c) = *reinterpret_cast<const uint4 *>(v);
     }
 }
@@ -67,7 +80,7 @@ __device__ __forceinline__ void split3(float x, uint16_t &a, uint16_t &b, uint16
 template <bool VEC>
 __global__ void __launch_bounds__(kThreads)
 lm_split3_kernel(const float *src, int64_t ld, int64_t stride, uint16_t *dst, int64_t ld_dst, int64_t plane,
-                 int64_t rows, int64_t cols, int64_t batch) {
+                 int64_t rows, int64_t cols, int64_t batch, LmRowFilter keep) {
     griddep_launch_dependents();
     griddep_wait();
     const int64_t per_row = ld_dst / 8, total = per_row * rows * batch;
@@ -75,7 +88,10 @@ lm_split3_kernel(const float *src, int64_t ld, int64_t stride, uint16_t *dst, in
         const int64_t r = i / per_row, c = (i - r * per_row) * 8, b = r / rows;
         const float *s = src + b * stride + (r - b * rows) * ld + c;
         float x[8];
-        if (VEC && c + 8 <= cols) {
+        if (!keeps(keep, r)) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = 0.f;
+        } else if (VEC && c + 8 <= cols) {
             *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(s);
             *reinterpret_cast<float4 *>(x + 4) = *reinterpret_cast<const float4 *>(s + 4);
         } else {
@@ -204,17 +220,19 @@ int64_t blocks_for(int64_t threads) { return std::min<int64_t>((threads + kThrea
 }  // namespace
 
 cudaError_t lm_launch_pack16(const void *src, int64_t ld, int64_t stride, void *dst, int64_t ld_dst, int64_t rows,
-                             int64_t cols, int64_t batch, cudaStream_t s) {
-    return launch(lm_pack16_kernel, blocks_for(ld_dst / 8 * rows * batch), kThreads, s,
-                  static_cast<const uint16_t *>(src), ld, stride, static_cast<uint16_t *>(dst), ld_dst, rows, cols,
-                  batch);
+                             int64_t cols, int64_t batch, LmRowFilter keep, cudaStream_t s) {
+    const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && ld % 8 == 0 && stride % 8 == 0;
+    return launch(vec ? lm_pack16_kernel<true> : lm_pack16_kernel<false>, blocks_for(ld_dst / 8 * rows * batch),
+                  kThreads, s, static_cast<const uint16_t *>(src), ld, stride, static_cast<uint16_t *>(dst), ld_dst,
+                  rows, cols, batch, keep);
 }
 
 cudaError_t lm_launch_split3(const float *src, int64_t ld, int64_t stride, void *dst, int64_t ld_dst,
-                             int64_t plane, int64_t rows, int64_t cols, int64_t batch, cudaStream_t s) {
+                             int64_t plane, int64_t rows, int64_t cols, int64_t batch, LmRowFilter keep,
+                             cudaStream_t s) {
     const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && ld % 4 == 0 && stride % 4 == 0;
     return launch(vec ? lm_split3_kernel<true> : lm_split3_kernel<false>, blocks_for(ld_dst / 8 * rows * batch),
-                  kThreads, s, src, ld, stride, static_cast<uint16_t *>(dst), ld_dst, plane, rows, cols, batch);
+                  kThreads, s, src, ld, stride, static_cast<uint16_t *>(dst), ld_dst, plane, rows, cols, batch, keep);
 }
 
 cudaError_t lm_launch_lse_join(const float2 *part, int slabs, int rows, const float *picked, const int64_t *target,

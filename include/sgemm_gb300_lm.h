@@ -112,7 +112,8 @@ sgemmStatus_t sgemmGroupedWeightGradWorkspaceSize(sgemmHandle_t handle, sgemmDat
  * computed, and the partial results are joined in a fixed order.  A target
  * outside [0, V) marks a token that is not counted: its loss is 0 (its lse
  * is computed).  loss and lse are FP32 in every type.  Arithmetic of the
- * products as for sgemmGrouped().  INVALID_VALUE also for V < 1 or D < 1;
+ * products as for sgemmGrouped(), 16-bit ones here in sums of 1024 terms of
+ * the contraction, added in FP32.  INVALID_VALUE also for V < 1 or D < 1;
  * T == 0 is a no-op.  A workspace is always required (the partial results).
  */
 sgemmStatus_t sgemmCrossEntropy(sgemmHandle_t handle, sgemmDataType_t type, int64_t T, int64_t V, int64_t D,
@@ -131,11 +132,21 @@ sgemmStatus_t sgemmCrossEntropyWorkspaceSize(sgemmHandle_t handle, sgemmDataType
  *   dX = d . W        dW = d^T . X
  *
  * in pieces of the vocabulary: d is computed for one piece at a time (512 MB
- * at most, or 2048 columns), in the type of the matrices (F16: times a power
- * of two that keeps it in range; F32: FP32, then three bf16 planes), and
- * both products over the piece follow; dX is summed over the pieces in FP32.
+ * at most, or 2048 columns) and both products over the piece follow; dX is
+ * summed over the pieces in FP32.  How d is held:
+ *   F32              FP32, then three bf16 planes;
+ *   up to 128 rows   two planes of the call's type, d and what its rounding
+ *                    left (16 bits and more of significand);
+ *   more rows        one plane of the call's type.
+ * F16 in either, and BF16 in one plane, hold d divided by the largest
+ * |dloss| of a counted token (F16: times 2^13 besides, above f16's subnormal
+ * numbers), taken in again in FP32 by the products.  (Where that largest is
+ * outside [1e-30, 1e30], d is held as it is.)
+ *
  * Tokens that are not counted, and those with dloss 0, have no part in
- * either gradient.  T == 0 sets dW to zero.
+ * either gradient whatever their rows of X hold, infinities and NaN too (X
+ * is always copied into the workspace, with zeros in their place); their dX
+ * is zero.  T == 0 sets dW to zero.
  */
 sgemmStatus_t sgemmCrossEntropyGrad(sgemmHandle_t handle, sgemmDataType_t type, int64_t T, int64_t V, int64_t D,
                                     const void *X, int64_t ldx, const void *W, int64_t ldw, const int64_t *target,

@@ -127,6 +127,24 @@ def test_rows_not_counted_may_hold_anything(sg):
     assert (dx[3:5] == 0).all() and not torch.isnan(dx[keep]).any()
 
 
+@pytest.mark.parametrize("tokens", [20, 200])
+@pytest.mark.parametrize("pad", [0, 3])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_rows_without_a_part_reach_no_gradient(sg, dtype, pad, tokens):
+    # Whatever they hold: the gradients are the ones of zeros in their place.
+    x, w, target, dloss = _problem(tokens, 300, 64, dtype, 12, pad=pad)
+    target[5], target[tokens - 1], dloss[9] = -100, 300, 0.0
+    out = [5, 9, tokens - 1]
+    x[out] = 0
+    _, lse = sg.linear_cross_entropy(x, w, target)
+    want = sg.linear_cross_entropy_grad(x, w, target, lse, dloss)
+    x[5], x[9], x[tokens - 1] = float("nan"), float("inf"), -float("inf")
+    _, lse = sg.linear_cross_entropy(x, w, target)
+    got = sg.linear_cross_entropy_grad(x, w, target, lse, dloss)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert (got[0][out] == 0).all() and torch.isfinite(got[1]).all()
+
+
 def test_large_logits_do_not_overflow(sg):
     for dtype in ("bf16", "f32"):
         x, w, target, dloss = _problem(40, 600, 128, dtype, 9, scale=60.0)
