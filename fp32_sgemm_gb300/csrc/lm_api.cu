@@ -217,6 +217,45 @@ sgemmStatus_t plan_grouped(int type, int op, int64_t T, int64_t N, int64_t K, in
     return SGEMM_STATUS_SUCCESS;
 }
 
+// Tiles of a grouped product: size as in lm_kernels.h, rows of a group in one
+// tile.  The groups' sizes are on the device; half a tile of each group is
+// taken to be left over.  Measured, us, with tiles of 128 columns by 32 / 64 /
+// 128 rows and 256 columns by 64 / 256 rows:
+//   the smallest tiles with which every SM has at most one: 8 groups of 200
+//     rows, 512 x 512: 9.0 / 6.9 / 7.6 / 7.6 / 9.6; 4 of 128, 1024 x 1024:
+//     8.3 / 9.0 / 9.6 / 9.0 / 10.3;
+//   otherwise those of a pair, whose W is read in the fewest and longest
+//     pieces: 64 groups of 64, 1408 x 2048: 110 / 73 / 63 / 69 / 61; 8 of 32,
+//     4096 x 14336: 159 / 132 / 121 / 128 / 116;
+//   with fewer than two for each pair, of as many rows as a group has in the
+//     mean, so that the largest groups are cut: 16 of 64, 2048 x 1408 stored
+//     1408 x 2048: 31 / 25 / 27 / 24 / 26;
+//   and no more rows than there are (8 rows, 8 groups, 4096 x 14336, 256
+//     columns by 32 / 256 rows: 96 / 137).
+// FP32, whose six products weigh more than reading W, 32 / 128 / 256 rows:
+// thin tiles also for few rows in a group (32 groups of 2, 1024 x 1408: 115 /
+// 118 / 147), those of one SM up to 256 rows (16 of 192, 2048 x 1408: 291 / 202
+// / 222; of 512: 659 / 307 / 304) and where the pairs' leave SMs idle (2 groups
+// of 632, 1024 x 1408: 57 / 34 / 45).
+struct Tiling {
+    int size, tile_n;
+};
+
+Tiling grouped_tiling(int type, int64_t T, int64_t N, int64_t G, int sms) {
+    const int64_t mean = T / G, touched = std::min(G, T);
+    auto tiles = [&](int64_t height, int64_t rows) { return ceil_div(N, height) * (2 * T / rows + touched) / 2; };
+    if (tiles(128, 32) <= sms) return {0, 32};
+    if (type == SGEMM_TYPE_F32) {
+        if (mean <= 24) return {0, 32};
+        return mean <= 256 || tiles(256, 256) < sms / 2 ? Tiling{1, 128} : Tiling{2, 256};
+    }
+    if (tiles(128, 64) <= sms) return {1, 64};
+    if (tiles(128, 128) <= sms) return {1, 128};
+    int rows = 256;
+    if (ceil_div(N, 256) * G < sms) rows = mean <= 64 ? 64 : mean <= 128 ? 128 : 256;
+    return {2, int(std::min<int64_t>(rows, round_up(T, 32)))};
+}
+
 struct WeightGrad {
     int type = 0;
     int64_t T = 0, M = 0, N = 0, G = 0;
@@ -446,12 +485,8 @@ sgemmStatus_t sgemmGrouped(sgemmHandle_t h, sgemmDataType_t type, sgemmOperation
     if (q.a.ws + q.b.ws > 0 && (h->ws == nullptr || h->ws_bytes < q.a.ws + q.b.ws))
         return SGEMM_STATUS_WORKSPACE_REQUIRED;
 
-    // Tile by the mean number of rows of a group; the middle one also where
-    // the big one would leave SM pairs without a tile (2001 x 1023 x 777 in
-    // 7 groups, FP32: 58 us with 60 big tiles, 49 with the middle one).
-    const int64_t mean = T / G;
-    const bool fills = ceil_div(N, 256) * (T / 256 + std::min(G, T)) >= h->sm_count / 2;
-    const int size = mean <= 24 ? 0 : mean <= 128 || !fills ? 1 : 2;
+    const Tiling tiling = grouped_tiling(type, T, N, G, h->sm_count);
+    const int size = tiling.size;
     const LmKernel k = sg::lm_grouped_kernel(size, opB == SGEMM_OP_N, type == SGEMM_TYPE_F32);
     LmArgs p{};
     p.M = int(N);
@@ -460,10 +495,7 @@ sgemmStatus_t sgemmGrouped(sgemmHandle_t h, sgemmDataType_t type, sgemmOperation
     p.G = int(G);
     p.ends = groupEnds;
     p.tiles_m = int(ceil_div(N, k.tile_m));
-    // Groups of about 64 rows: 16-bit tiles (and TMA boxes) of 64 rows, bound by
-    // reading (1024 rows over 16 groups of 1408 x 2048: 26.9 -> 24.9 us).
-    // Otherwise narrower tiles only add tiles.
-    p.tile_n = size == 1 && mean <= 64 && type != SGEMM_TYPE_F32 ? 64 : k.bn;
+    p.tile_n = tiling.tile_n;
     p.group_m = 8;
     p.splits = 1;
     p.bf16 = type == SGEMM_TYPE_F16 ? 0 : 1;
@@ -524,7 +556,11 @@ sgemmStatus_t sgemmGroupedWeightGrad(sgemmHandle_t h, sgemmDataType_t type, int6
     if (q.a.ws + q.b.ws > 0 && (h->ws == nullptr || h->ws_bytes < q.a.ws + q.b.ws))
         return SGEMM_STATUS_WORKSPACE_REQUIRED;
 
-    const int size = M > 128 && N > 128 ? 2 : 1;
+    // Pairs' tiles unless most would have none (8 groups of 512 rows, BF16, 128
+    // x 128 / 256 x 256: 512 x 512 7.7 / 9.6 us, 768 x 768 10.3 / 10.3, 1024 x
+    // 1024 15.8 / 14.1).
+    const bool fills = 3 * ceil_div(M, 256) * ceil_div(N, 256) * G >= h->sm_count;
+    const int size = M > 128 && N > 128 && fills ? 2 : 1;
     const LmKernel k = sg::lm_weight_grad_kernel(size, type == SGEMM_TYPE_F32);
     LmArgs p{};
     p.M = int(M);
