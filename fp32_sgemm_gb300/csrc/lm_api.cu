@@ -58,8 +58,8 @@ struct Operand {
         }
     }
     int planes() const { return type == SGEMM_TYPE_F32 ? 3 : 1; }
-    // Copies into `at` (ws bytes) if need be; rows left out by `keep` as zeros.
-    bool prepare(void *at, cudaStream_t s, sg::LmRowFilter keep = {}) {
+    // Copies what `keep` asks for into `at` (ws bytes) if need be.
+    bool prepare(void *at, cudaStream_t s, sg::LmCopyFilter keep = {}) {
         if (!copy) {
             ptr_t = ptr;
             return true;
@@ -506,7 +506,9 @@ sgemmStatus_t sgemmGrouped(sgemmHandle_t h, sgemmDataType_t type, sgemmOperation
     const int64_t tiles = int64_t(p.tiles_m) * (ceil_div(T, p.tile_n) + G + 1);
     if (tiles > kMaxDim) return SGEMM_STATUS_NOT_SUPPORTED;
     char *ws = static_cast<char *>(h->ws);
-    if (!q.a.prepare(ws, stream) || !q.b.prepare(ws + q.a.ws, stream)) return SGEMM_STATUS_LAUNCH_FAILED;
+    sg::LmCopyFilter touched;           // matrices of groups that have rows
+    touched.ends = groupEnds;
+    if (!q.a.prepare(ws, stream) || !q.b.prepare(ws + q.a.ws, stream, touched)) return SGEMM_STATUS_LAUNCH_FAILED;
     CUtensorMap tm_w, tm_x;
     if (!q.b.map(&tm_w, k.a_mn ? 64 : k.box_a) || !q.a.map(&tm_x, p.tile_n / (k.pair ? 2 : 1))) return SGEMM_STATUS_LAUNCH_FAILED;
     return launch_lm(h, k, true, tm_w, tm_x, p, tiles, stream);

@@ -32,7 +32,13 @@ cudaError_t launch(void (*fn)(P...), int64_t blocks, int threads, cudaStream_t s
 constexpr int kThreads = 256;
 constexpr int64_t kMaxBlocks = 152 * 16;
 
-__device__ __forceinline__ bool keeps(const LmRowFilter &f, int64_t row) {
+// Ends out of order are put in order by the kernel that reads the copy: a
+// group that does not end behind the one before it is empty there too.
+__device__ __forceinline__ bool unused(const LmCopyFilter &f, int64_t b) {
+    return f.ends != nullptr && f.ends[b] <= (b > 0 ? f.ends[b - 1] : 0);
+}
+
+__device__ __forceinline__ bool keeps(const LmCopyFilter &f, int64_t row) {
     if (f.target == nullptr) return true;
     const int64_t t = f.target[row];
     return t >= 0 && t < f.vocab && f.grad[row] != 0.f;
@@ -41,12 +47,13 @@ __device__ __forceinline__ bool keeps(const LmRowFilter &f, int64_t row) {
 template <bool VEC>
 __global__ void __launch_bounds__(kThreads)
 lm_pack16_kernel(const uint16_t *src, int64_t ld, int64_t stride, uint16_t *dst, int64_t ld_dst, int64_t rows,
-                 int64_t cols, int64_t batch, LmRowFilter keep) {
+                 int64_t cols, int64_t batch, LmCopyFilter keep) {
     griddep_launch_dependents();
     griddep_wait();
     const int64_t per_row = ld_dst / 8, total = per_row * rows * batch;
     for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < total; i += gridDim.x * (int64_t)kThreads) {
         const int64_t r = i / per_row, c = (i - r * per_row) * 8, b = r / rows;
+        if (unused(keep, b)) continue;
         const uint16_t *s = src + b * stride + (r - b * rows) * ld + c;
         alignas(16) uint16_t v[8];
         if (!keeps(keep, r)) {
@@ -80,12 +87,13 @@ __device__ __forceinline__ void split3(float x, uint16_t &a, uint16_t &b, uint16
 template <bool VEC>
 __global__ void __launch_bounds__(kThreads)
 lm_split3_kernel(const float *src, int64_t ld, int64_t stride, uint16_t *dst, int64_t ld_dst, int64_t plane,
-                 int64_t rows, int64_t cols, int64_t batch, LmRowFilter keep) {
+                 int64_t rows, int64_t cols, int64_t batch, LmCopyFilter keep) {
     griddep_launch_dependents();
     griddep_wait();
     const int64_t per_row = ld_dst / 8, total = per_row * rows * batch;
     for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < total; i += gridDim.x * (int64_t)kThreads) {
         const int64_t r = i / per_row, c = (i - r * per_row) * 8, b = r / rows;
+        if (unused(keep, b)) continue;
         const float *s = src + b * stride + (r - b * rows) * ld + c;
         float x[8];
         if (!keeps(keep, r)) {
@@ -220,7 +228,7 @@ int64_t blocks_for(int64_t threads) { return std::min<int64_t>((threads + kThrea
 }  // namespace
 
 cudaError_t lm_launch_pack16(const void *src, int64_t ld, int64_t stride, void *dst, int64_t ld_dst, int64_t rows,
-                             int64_t cols, int64_t batch, LmRowFilter keep, cudaStream_t s) {
+                             int64_t cols, int64_t batch, LmCopyFilter keep, cudaStream_t s) {
     const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && ld % 8 == 0 && stride % 8 == 0;
     return launch(vec ? lm_pack16_kernel<true> : lm_pack16_kernel<false>, blocks_for(ld_dst / 8 * rows * batch),
                   kThreads, s, static_cast<const uint16_t *>(src), ld, stride, static_cast<uint16_t *>(dst), ld_dst,
@@ -228,7 +236,7 @@ cudaError_t lm_launch_pack16(const void *src, int64_t ld, int64_t stride, void *
 }
 
 cudaError_t lm_launch_split3(const float *src, int64_t ld, int64_t stride, void *dst, int64_t ld_dst,
-                             int64_t plane, int64_t rows, int64_t cols, int64_t batch, LmRowFilter keep,
+                             int64_t plane, int64_t rows, int64_t cols, int64_t batch, LmCopyFilter keep,
                              cudaStream_t s) {
     const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && ld % 4 == 0 && stride % 4 == 0;
     return launch(vec ? lm_split3_kernel<true> : lm_split3_kernel<false>, blocks_for(ld_dst / 8 * rows * batch),

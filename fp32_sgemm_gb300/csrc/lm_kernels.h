@@ -64,22 +64,24 @@ LmKernel lm_lse_kernel(bool big, bool f32);                     // lm_loss*.cu
 LmKernel lm_dlogits_kernel(bool big, bool f32);
 LmKernel lm_rows_kernel(bool big, bool a_mn, bool f32);         // B MN-major
 
-// The rows of a copy that are kept: those whose target is an entry of the
-// vocabulary and whose gradient is not zero (all, without targets).
-struct LmRowFilter {
+// What of an operand a copy needs.  With targets: the rows whose target is an
+// entry of the vocabulary and whose gradient is not zero, the others become
+// zeros.  With ends: the matrices of a batch whose group has rows, the others
+// are left as they are (no tile reads them).
+struct LmCopyFilter {
     const int64_t *target = nullptr;
     int64_t vocab = 0;
     const float *grad = nullptr;
+    const int32_t *ends = nullptr;
 };
 
 // lm_aux.cu.  Operand copies TMA can address: rows x cols (x batch) with
 // pitch ld -> pitch ld_dst (a multiple of 8), 16-bit copied as they are,
-// FP32 as three bf16 planes (plane stride in elements).  Rows that `keep`
-// leaves out become zeros.
+// FP32 as three bf16 planes (plane stride in elements).
 cudaError_t lm_launch_pack16(const void *src, int64_t ld, int64_t stride, void *dst, int64_t ld_dst, int64_t rows,
-                             int64_t cols, int64_t batch, LmRowFilter keep, cudaStream_t s);
+                             int64_t cols, int64_t batch, LmCopyFilter keep, cudaStream_t s);
 cudaError_t lm_launch_split3(const float *src, int64_t ld, int64_t stride, void *dst, int64_t ld_dst,
-                             int64_t plane, int64_t rows, int64_t cols, int64_t batch, LmRowFilter keep,
+                             int64_t plane, int64_t rows, int64_t cols, int64_t batch, LmCopyFilter keep,
                              cudaStream_t s);
 // Joins the slabs' maxima and sums: lse and loss of each row.
 cudaError_t lm_launch_lse_join(const float2 *part, int slabs, int rows, const float *picked, const int64_t *target,

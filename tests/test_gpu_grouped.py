@@ -230,6 +230,26 @@ def test_gradients_against_differences(sg):
     assert abs(along(x, w + v, x, w - v) - (dw.double() * v.double()).sum().item()) <= 1e-5 * scale
 
 
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_matrices_without_rows_are_not_read(sg, dtype, trans):
+    # Odd pitches, so that the matrices are copied first; those of groups
+    # without a row hold NaN, and so does the workspace from an earlier call.
+    g = torch.Generator(device="cuda").manual_seed(31)
+    K, N, G = 77, 53, 9
+    x = torch.randn(40, K, generator=g, device="cuda").to(DTYPES[dtype])
+    w = torch.randn(*((G, N, K) if trans else (G, K, N)), generator=g, device="cuda").to(DTYPES[dtype])
+    ends = torch.tensor([0, 13, 13, 13, 20, 20, 40, 40, 40], dtype=torch.int32, device="cuda")
+    bad = w.clone()
+    for i in (0, 2, 3, 5, 7, 8):
+        bad[i] = float("nan")
+    want = sg.grouped_gemm(x, w, ends, trans_w=trans)
+    sg.grouped_gemm(x, torch.full_like(w, float("nan")), torch.arange(1, G + 1, dtype=torch.int32, device="cuda"),
+                    trans_w=trans)
+    got = sg.grouped_gemm(x, bad, ends, trans_w=trans)
+    assert torch.isfinite(want).all() and torch.equal(want, got)
+
+
 def test_other_stream(sg):
     sizes, K, N = [100, 28], 256, 512
     x, w = _rand((128, K), "bf16", 31), _rand((2, K, N), "bf16", 32)
