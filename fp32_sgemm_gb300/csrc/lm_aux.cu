@@ -1,7 +1,12 @@
 // Small kernels around the tensor-core products of the language-model
 // operators: operand copies TMA can address, FP32 split into bf16 planes,
-// the joins of partial results.  All are bound by memory; each thread moves
-// 8 neighbouring elements, so that writes are whole 16-byte words.
+// the joins of partial results.  All are bound by memory, or by being a launch
+// of a few microseconds; the copies move 8 neighbouring elements a thread, so
+// that writes are whole 16-byte words.  Measured on one GB300, each launch by
+// itself from cold caches: 50001 x 1001 f16 copied to a pitch of 1008 (201 MB)
+// 40.6 us, 4.9 TB/s; 16.8 M FP32 values split (168 MB) 24.7 us, 6.8 TB/s; 7 x
+// 1023 x 777 split from an odd pitch (56 MB) 11.4 us, 4.9 TB/s; 286 slabs of 16
+// rows joined 7.0 us, the largest |dloss| of 1023 rows 4.2 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -53,8 +53,8 @@ struct LmArgs {
 
 struct LmKernel {
     const void *fn = nullptr;
-    int threads = 0, smem = 0, tile_m = 0, bn = 0, gran = 0, pair = 0, box_a = 0, box_b = 0, slabs = 0;
-    int a_mn = 0, b_mn = 0;
+    int threads = 0, smem = 0, tile_m = 0, bn = 0, gran = 0, pair = 0, box_a = 0;
+    int a_mn = 0;                   // A is read MN-major (boxes of 64 x 64)
 };
 
 // Kernel tables.  size: 0 thin, 1 middle, 2 big (SM pair).
@@ -62,7 +62,7 @@ LmKernel lm_grouped_kernel(int size, bool w_mn, bool f32);      // lm_grouped*.c
 LmKernel lm_weight_grad_kernel(int size, bool f32);             // size 1 or 2
 LmKernel lm_lse_kernel(bool big, bool f32);                     // lm_loss*.cu
 LmKernel lm_dlogits_kernel(bool big, bool f32);
-LmKernel lm_rows_kernel(bool big, bool a_mn, bool f32);         // B MN-major
+LmKernel lm_rows_kernel(bool big, bool a_mn, bool f32);         // B MN-major; MN-major A is big
 
 // What of an operand a copy needs.  With targets: the rows whose target is an
 // entry of the vocabulary and whose gradient is not zero, the others become

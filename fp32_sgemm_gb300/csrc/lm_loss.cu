@@ -19,10 +19,7 @@ LmKernel lm_dlogits_kernel(bool big, bool f32) {
 }
 LmKernel lm_rows_kernel(bool big, bool a_mn, bool f32) {
     if (f32) return lm_rows_kernel32(big, a_mn);
-    if (a_mn) {
-        if (big) return lm_kernel_info<LmBig, true, true, kRagNone, kEpiRows, kPlain>();
-        return lm_kernel_info<LmWide, true, true, kRagNone, kEpiRows, kPlain>();
-    }
+    if (a_mn) return lm_kernel_info<LmBig, true, true, kRagNone, kEpiRows, kPlain>();
     if (big) return lm_kernel_info<LmBig, false, true, kRagNone, kEpiRows, kPlain>();
     return lm_kernel_info<LmWide, false, true, kRagNone, kEpiRows, kPlain>();
 }

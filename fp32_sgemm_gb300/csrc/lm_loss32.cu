@@ -12,10 +12,7 @@ LmKernel lm_dlogits_kernel32(bool big) {
     return lm_kernel_info<LmMid, false, false, kRagNone, kEpiDLogits, kPlanes>();
 }
 LmKernel lm_rows_kernel32(bool big, bool a_mn) {
-    if (a_mn) {
-        if (big) return lm_kernel_info<LmBig, true, true, kRagNone, kEpiRows, kPlanes>();
-        return lm_kernel_info<LmMid, true, true, kRagNone, kEpiRows, kPlanes>();
-    }
+    if (a_mn) return lm_kernel_info<LmBig, true, true, kRagNone, kEpiRows, kPlanes>();
     if (big) return lm_kernel_info<LmBig, false, true, kRagNone, kEpiRows, kPlanes>();
     return lm_kernel_info<LmMid, false, true, kRagNone, kEpiRows, kPlanes>();
 }
