@@ -58,18 +58,23 @@ struct Operand {
         }
     }
     int planes() const { return type == SGEMM_TYPE_F32 ? 3 : 1; }
-    // Copies what `keep` asks for into `at` (ws bytes) if need be.
-    bool prepare(void *at, cudaStream_t s, sg::LmCopyFilter keep = {}) {
-        if (!copy) {
-            ptr_t = ptr;
-            return true;
+    // The copy into `at` (ws bytes), if there is one.
+    sg::LmCopy place(void *at, sg::LmCopyFilter keep = {}) {
+        sg::LmCopy j;
+        ptr_t = copy ? at : ptr;
+        if (copy) {
+            j.src = ptr;
+            j.ld = ld;
+            j.stride = batch > 1 ? stride : 0;
+            j.dst = at;
+            j.ld_dst = ld_t;
+            j.plane = plane_t;
+            j.rows = rows;
+            j.cols = cols;
+            j.batch = batch;
+            j.keep = keep;
         }
-        ptr_t = at;
-        const int64_t st = batch > 1 ? stride : 0;
-        return (type == SGEMM_TYPE_F32
-                    ? sg::lm_launch_split3(static_cast<const float *>(ptr), ld, st, at, ld_t, plane_t, rows, cols,
-                                           batch, keep, s)
-                    : sg::lm_launch_pack16(ptr, ld, st, at, ld_t, rows, cols, batch, keep, s)) == cudaSuccess;
+        return j;
     }
     // {cols, rows, batch * planes}, boxes of 64 x box_rows.
     bool map(CUtensorMap *m, int box_rows) const { return map_rows(m, box_rows, 0, rows); }
@@ -88,6 +93,14 @@ struct Operand {
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     }
 };
+
+// The copies of two operands (and the scale of a gradient) in one launch, if
+// there is anything to do.
+bool copy_operands(int type, const sg::LmCopy &a, const sg::LmCopy &b, cudaStream_t s,
+                   const sg::LmGradScale &scale = {}) {
+    if (a.src == nullptr && b.src == nullptr && scale.scale2 == nullptr) return true;
+    return sg::lm_launch_copy(type == SGEMM_TYPE_F32, a, b, scale, s) == cudaSuccess;
+}
 
 sgemmStatus_t check_matrix(const void *p, int64_t rows, int64_t cols, int64_t ld, int type, bool used) {
     if (ld < std::max<int64_t>(1, cols)) return SGEMM_STATUS_INVALID_VALUE;
@@ -514,7 +527,7 @@ sgemmStatus_t sgemmGrouped(sgemmHandle_t h, sgemmDataType_t type, sgemmOperation
     char *ws = static_cast<char *>(h->ws);
     sg::LmCopyFilter touched;           // matrices of groups that have rows
     touched.ends = groupEnds;
-    if (!q.a.prepare(ws, stream) || !q.b.prepare(ws + q.a.ws, stream, touched)) return SGEMM_STATUS_LAUNCH_FAILED;
+    if (!copy_operands(type, q.a.place(ws), q.b.place(ws + q.a.ws, touched), stream)) return SGEMM_STATUS_LAUNCH_FAILED;
     CUtensorMap tm_w, tm_x;
     if (!q.b.map(&tm_w, k.a_mn ? 64 : k.box_a) || !q.a.map(&tm_x, p.tile_n / (k.pair ? 2 : 1))) return SGEMM_STATUS_LAUNCH_FAILED;
     return launch_lm(h, k, true, tm_w, tm_x, p, tiles, stream);
@@ -591,7 +604,7 @@ sgemmStatus_t sgemmGroupedWeightGrad(sgemmHandle_t h, sgemmDataType_t type, int6
     p.out = out_type(type);
     p.vec = vec_ok(C, ldc, sc, elem, 32);
     char *ws = static_cast<char *>(h->ws);
-    if (!q.a.prepare(ws, stream) || !q.b.prepare(ws + q.a.ws, stream)) return SGEMM_STATUS_LAUNCH_FAILED;
+    if (!copy_operands(type, q.a.place(ws), q.b.place(ws + q.a.ws), stream)) return SGEMM_STATUS_LAUNCH_FAILED;
     CUtensorMap tm_a, tm_b;
     if (!q.a.map(&tm_a, 64) || !q.b.map(&tm_b, 64)) return SGEMM_STATUS_LAUNCH_FAILED;
     return launch_lm(h, k, true, tm_a, tm_b, p, tiles, stream);
@@ -635,7 +648,7 @@ sgemmStatus_t sgemmCrossEntropy(sgemmHandle_t h, sgemmDataType_t type, int64_t T
     p.part = reinterpret_cast<float2 *>(ws);
     p.picked = reinterpret_cast<float *>(ws + q.ws_part);
     ws += q.ws_part + q.ws_picked;
-    if (!q.x.prepare(ws, stream) || !q.w.prepare(ws + q.x.ws, stream)) return SGEMM_STATUS_LAUNCH_FAILED;
+    if (!copy_operands(type, q.x.place(ws), q.w.place(ws + q.x.ws), stream)) return SGEMM_STATUS_LAUNCH_FAILED;
     CUtensorMap tm_x, tm_w;
     if (!q.x.map(&tm_x, k.box_a) || !q.w.map(&tm_w, q.tile_n / (k.pair ? 2 : 1))) return SGEMM_STATUS_LAUNCH_FAILED;
     st = launch_lm(h, k, false, tm_x, tm_w, p, p.num_tiles, stream);
@@ -694,7 +707,6 @@ sgemmStatus_t sgemmCrossEntropyGrad(sgemmHandle_t h, sgemmDataType_t type, int64
     // (both gradients of 12 rows, 5000 x 768: 38.1 -> 40.5 us; of 128 rows and
     // more, within the noise).
     Operand &x = q.x_kept;
-    if (!x.prepare(ws, stream, {target, V, dloss}) || !q.w.prepare(ws + x.ws, stream)) return SGEMM_STATUS_LAUNCH_FAILED;
     // d is held over the largest |dloss|, taken in again by the gradient
     // products: then the entries of the targets lie at 1 - p, where all of
     // them are not rounded the same way, as they are when dloss is one over
@@ -702,8 +714,20 @@ sgemmStatus_t sgemmCrossEntropyGrad(sgemmHandle_t h, sgemmDataType_t type, int64
     // one direction).  F16 besides times 2^13: its smallest normal number,
     // 2^-14, is above most softmax values over a long vocabulary.
     const bool scaled = f16 || (!f32 && q.d_planes == 1);
-    if (scaled && sg::lm_launch_grad_scale(dloss, target, V, int(T), f16 ? 8192.f : 1.f, scale2, stream) != cudaSuccess)
-        return SGEMM_STATUS_LAUNCH_FAILED;
+    sg::LmCopyFilter part;
+    part.target = target;
+    part.vocab = V;
+    part.grad = dloss;
+    sg::LmGradScale scale;
+    if (scaled) {
+        scale.grad = dloss;
+        scale.target = target;
+        scale.vocab = V;
+        scale.rows = int(T);
+        scale.top = f16 ? 8192.f : 1.f;
+        scale.scale2 = scale2;
+    }
+    if (!copy_operands(type, x.place(ws, part), q.w.place(ws + x.ws), stream, scale)) return SGEMM_STATUS_LAUNCH_FAILED;
 
     const LmKernel kd = sg::lm_dlogits_kernel(q.big, f32);
     const LmKernel kx = sg::lm_rows_kernel(q.big, false, f32);
@@ -748,7 +772,7 @@ sgemmStatus_t sgemmCrossEntropyGrad(sgemmHandle_t h, sgemmDataType_t type, int64
         dd.batch = q.d_planes;
         dd.stride = T * q.ld_d;
         dd.plan();
-        if (!dd.prepare(planes, stream)) return SGEMM_STATUS_LAUNCH_FAILED;
+        if (!copy_operands(type, dd.place(planes), {}, stream)) return SGEMM_STATUS_LAUNCH_FAILED;
         if (!dd.map(&tm_d, kx.box_a) || !dd.map(&tm_d_mn, 64) || !q.w.map_rows(&tm_w_mn, 64, v0, width))
             return SGEMM_STATUS_LAUNCH_FAILED;
 

@@ -49,30 +49,6 @@ __device__ __forceinline__ bool keeps(const LmCopyFilter &f, int64_t row) {
     return t >= 0 && t < f.vocab && f.grad[row] != 0.f;
 }
 
-template <bool VEC>
-__global__ void __launch_bounds__(kThreads)
-lm_pack16_kernel(const uint16_t *src, int64_t ld, int64_t stride, uint16_t *dst, int64_t ld_dst, int64_t rows,
-                 int64_t cols, int64_t batch, LmCopyFilter keep) {
-    griddep_launch_dependents();
-    griddep_wait();
-    const int64_t per_row = ld_dst / 8, total = per_row * rows * batch;
-    for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < total; i += gridDim.x * (int64_t)kThreads) {
-        const int64_t r = i / per_row, c = (i - r * per_row) * 8, b = r / rows;
-        if (unused(keep, b)) continue;
-        const uint16_t *s = src + b * stride + (r - b * rows) * ld + c;
-        alignas(16) uint16_t v[8];
-        if (!keeps(keep, r)) {
-            *reinterpret_cast<uint4 *>(v) = make_uint4(0, 0, 0, 0);
-        } else if (VEC && c + 8 <= cols) {
-            *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(s);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? s[e] : (uint16_t)0;
-        }
-        *reinterpret_cast<uint4 *>(dst + r * ld_dst + c) = *reinterpret_cast<const uint4 *>(v);
-    }
-}
-
 // x = p0 + p1 + p2 exactly: the leading 8, the next 8 and the last 8 bits of
 // its significand (each plane truncated, so that the rest keeps x's sign and
 // p0 never rounds up to infinity).  Values that are not finite stay in p0.
@@ -89,41 +65,89 @@ __device__ __forceinline__ void split3(float x, uint16_t &a, uint16_t &b, uint16
     c = (uint16_t)(__float_as_uint(r2) >> 16);
 }
 
-template <bool VEC>
-__global__ void __launch_bounds__(kThreads)
-lm_split3_kernel(const float *src, int64_t ld, int64_t stride, uint16_t *dst, int64_t ld_dst, int64_t plane,
-                 int64_t rows, int64_t cols, int64_t batch, LmCopyFilter keep) {
-    griddep_launch_dependents();
-    griddep_wait();
-    const int64_t per_row = ld_dst / 8, total = per_row * rows * batch;
-    for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < total; i += gridDim.x * (int64_t)kThreads) {
-        const int64_t r = i / per_row, c = (i - r * per_row) * 8, b = r / rows;
-        if (unused(keep, b)) continue;
-        const float *s = src + b * stride + (r - b * rows) * ld + c;
+// Chunk i of a copy: 8 neighbours of one row.
+template <bool F32>
+__device__ __forceinline__ void copy_chunk(const LmCopy &j, int64_t i) {
+    const int64_t per_row = j.ld_dst / 8;
+    const int64_t r = i / per_row, c = (i - r * per_row) * 8, b = r / j.rows;
+    if (unused(j.keep, b)) return;
+    const bool kept = keeps(j.keep, r);
+    const int64_t from = b * j.stride + (r - b * j.rows) * j.ld + c, to = r * j.ld_dst + c;
+    const bool wide = j.vec && c + 8 <= j.cols;
+    if constexpr (F32) {
+        const float *s = static_cast<const float *>(j.src) + from;
         float x[8];
-        if (!keeps(keep, r)) {
+        if (!kept) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = 0.f;
-        } else if (VEC && c + 8 <= cols) {
+        } else if (wide) {
             *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(s);
             *reinterpret_cast<float4 *>(x + 4) = *reinterpret_cast<const float4 *>(s + 4);
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = c + e < cols ? s[e] : 0.f;
+            for (int e = 0; e < 8; ++e) x[e] = c + e < j.cols ? s[e] : 0.f;
         }
         alignas(16) uint16_t v[3][8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) split3(x[e], v[0][e], v[1][e], v[2][e]);
 #pragma unroll
         for (int q = 0; q < 3; ++q)
-            *reinterpret_cast<uint4 *>(dst + q * plane + r * ld_dst + c) = *reinterpret_cast<const uint4 *>(v[q]);
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(j.dst) + q * j.plane + to) =
+                *reinterpret_cast<const uint4 *>(v[q]);
+    } else {
+        const uint16_t *s = static_cast<const uint16_t *>(j.src) + from;
+        alignas(16) uint16_t v[8];
+        if (!kept) {
+            *reinterpret_cast<uint4 *>(v) = make_uint4(0, 0, 0, 0);
+        } else if (wide) {
+            *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(s);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = c + e < j.cols ? s[e] : (uint16_t)0;
+        }
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(j.dst) + to) = *reinterpret_cast<const uint4 *>(v);
     }
+}
+
+// One CTA: the largest |grad| of a counted row.
+__device__ void grad_scale(const LmGradScale &g) {
+    __shared__ float most[kThreads / 32];
+    float m = 0.f;
+    for (int i = threadIdx.x; i < g.rows; i += kThreads) {
+        const int64_t t = g.target[i];
+        if (t >= 0 && t < g.vocab) m = fmaxf(m, fabsf(g.grad[i]));
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+    if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = m;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) m = fmaxf(m, most[w]);
+        const bool usable = m > 1.0e-30f && m < 1.0e30f;
+        g.scale2[0] = usable ? g.top / m : 1.f;
+        g.scale2[1] = usable ? m / g.top : 1.f;
+    }
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(kThreads)
+lm_copy_kernel(const __grid_constant__ LmCopy a, const __grid_constant__ LmCopy b,
+               const __grid_constant__ LmGradScale scale) {
+    griddep_launch_dependents();
+    griddep_wait();
+    if (blockIdx.x == 0 && scale.scale2 != nullptr) grad_scale(scale);
+    const int64_t step = gridDim.x * (int64_t)kThreads;
+    int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x;
+    for (; i < a.chunks; i += step) copy_chunk<F32>(a, i);
+    for (i -= a.chunks; i < b.chunks; i += step) copy_chunk<F32>(b, i);
 }
 
 // Joins the slabs' {maximum, sum of exp(l - maximum)} of each row in a fixed
 // order: 32 rows per CTA, one per lane (neighbouring rows are neighbours in
-// memory), the slabs dealt to 32 warps; first the maximum, then the sum, so
-// that the exponentials do not wait for one another.
+// memory), the slabs dealt to 32 warps, 8 of a warp loaded at a time and
+// joined to what it has (their maximum first, so that the exponentials do not
+// wait for one another).
 constexpr int kJoinWarps = 32;
 __global__ void __launch_bounds__(kJoinWarps * 32)
 lm_lse_join_kernel(const float2 *part, int slabs, int rows, const float *picked, const int64_t *target,
@@ -134,26 +158,29 @@ lm_lse_join_kernel(const float2 *part, int slabs, int rows, const float *picked,
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int row = min(blockIdx.x * 32 + lane, rows - 1);
     constexpr int U = 8;                            // loads in flight
-    auto each = [&](auto &&f) {
-        for (int i = warp; i < slabs; i += U * kJoinWarps) {
-            float2 v[U];
+    float m = -INFINITY, s = 0.f;
+    for (int i = warp; i < slabs; i += U * kJoinWarps) {
+        float2 v[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                v[u] = part[(int64_t)min(i + u * kJoinWarps, slabs - 1) * rows + row];
+        for (int u = 0; u < U; ++u)
+            v[u] = i + u * kJoinWarps < slabs ? part[(int64_t)(i + u * kJoinWarps) * rows + row]
+                                              : make_float2(-INFINITY, 0.f);
+        const float before = m;
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (i + u * kJoinWarps < slabs) f(v[u]);
-        }
-    };
-    float m = -INFINITY;
-    each([&](float2 v) { m = fmaxf(m, v.x); });
+        for (int u = 0; u < U; ++u) m = fmaxf(m, v[u].x);
+        const float ref = m == -INFINITY ? 0.f : m;
+        s *= expf(before - ref);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i + u * kJoinWarps < slabs) s += v[u].y * expf(v[u].x - ref);
+    }
     met[warp][lane] = m;
     __syncthreads();
+    const float own = m;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, met[w][lane]);
     const float ref = m == -INFINITY ? 0.f : m;
-    float s = 0.f;
-    each([&](float2 v) { s += v.y * expf(v.x - ref); });
+    s *= expf(own - ref);
     __syncthreads();
     met[warp][lane] = s;
     __syncthreads();
@@ -165,33 +192,6 @@ lm_lse_join_kernel(const float2 *part, int slabs, int rows, const float *picked,
         lse[row] = l;
         const int64_t t = target[row];
         loss[row] = t >= 0 && t < vocab ? l - picked[row] : 0.f;
-    }
-}
-
-// scale2 = {top / m, m / top}, m the largest |grad| of a counted row.
-__global__ void __launch_bounds__(1024)
-lm_grad_scale_kernel(const float *grad, const int64_t *target, int64_t vocab, int rows, float top, float *scale2) {
-    griddep_launch_dependents();
-    griddep_wait();
-    __shared__ float most[32];
-    float m = 0.f;
-    for (int i = threadIdx.x; i < rows; i += 1024) {
-        const int64_t t = target[i];
-        if (t >= 0 && t < vocab) m = fmaxf(m, fabsf(grad[i]));
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-    if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = m;
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        m = most[threadIdx.x];
-#pragma unroll
-        for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-        if (threadIdx.x == 0) {
-            const bool usable = m > 1.0e-30f && m < 1.0e30f;
-            scale2[0] = usable ? top / m : 1.f;
-            scale2[1] = usable ? m / top : 1.f;
-        }
     }
 }
 
@@ -232,31 +232,21 @@ int64_t blocks_for(int64_t threads) { return std::min<int64_t>((threads + kThrea
 
 }  // namespace
 
-cudaError_t lm_launch_pack16(const void *src, int64_t ld, int64_t stride, void *dst, int64_t ld_dst, int64_t rows,
-                             int64_t cols, int64_t batch, LmCopyFilter keep, cudaStream_t s) {
-    const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && ld % 8 == 0 && stride % 8 == 0;
-    return launch(vec ? lm_pack16_kernel<true> : lm_pack16_kernel<false>, blocks_for(ld_dst / 8 * rows * batch),
-                  kThreads, s, static_cast<const uint16_t *>(src), ld, stride, static_cast<uint16_t *>(dst), ld_dst,
-                  rows, cols, batch, keep);
-}
-
-cudaError_t lm_launch_split3(const float *src, int64_t ld, int64_t stride, void *dst, int64_t ld_dst,
-                             int64_t plane, int64_t rows, int64_t cols, int64_t batch, LmCopyFilter keep,
-                             cudaStream_t s) {
-    const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && ld % 4 == 0 && stride % 4 == 0;
-    return launch(vec ? lm_split3_kernel<true> : lm_split3_kernel<false>, blocks_for(ld_dst / 8 * rows * batch),
-                  kThreads, s, src, ld, stride, static_cast<uint16_t *>(dst), ld_dst, plane, rows, cols, batch, keep);
+cudaError_t lm_launch_copy(bool f32, LmCopy a, LmCopy b, const LmGradScale &scale, cudaStream_t s) {
+    for (LmCopy *j : {&a, &b}) {
+        if (j->src == nullptr) continue;
+        const int64_t words = f32 ? 4 : 8;          // elements of a 16-byte load
+        j->chunks = j->ld_dst / 8 * j->rows * j->batch;
+        j->vec = reinterpret_cast<uintptr_t>(j->src) % 16 == 0 && j->ld % words == 0 && j->stride % words == 0;
+    }
+    return launch(f32 ? lm_copy_kernel<true> : lm_copy_kernel<false>, blocks_for(a.chunks + b.chunks), kThreads, s, a,
+                  b, scale);
 }
 
 cudaError_t lm_launch_lse_join(const float2 *part, int slabs, int rows, const float *picked, const int64_t *target,
                                int64_t vocab, float *loss, float *lse, cudaStream_t s) {
     return launch(lm_lse_join_kernel, (rows + 31) / 32, kJoinWarps * 32, s, part, slabs, rows, picked, target,
                   vocab, loss, lse);
-}
-
-cudaError_t lm_launch_grad_scale(const float *grad, const int64_t *target, int64_t vocab, int rows, float top,
-                                 float *scale2, cudaStream_t s) {
-    return launch(lm_grad_scale_kernel, 1, 1024, s, grad, target, vocab, rows, top, scale2);
 }
 
 cudaError_t lm_launch_join_splits(const float *part, int64_t ld_part, int64_t plane, int splits, const float *alpha,

@@ -75,20 +75,32 @@ struct LmCopyFilter {
     const int32_t *ends = nullptr;
 };
 
-// lm_aux.cu.  Operand copies TMA can address: rows x cols (x batch) with
-// pitch ld -> pitch ld_dst (a multiple of 8), 16-bit copied as they are,
-// FP32 as three bf16 planes (plane stride in elements).
-cudaError_t lm_launch_pack16(const void *src, int64_t ld, int64_t stride, void *dst, int64_t ld_dst, int64_t rows,
-                             int64_t cols, int64_t batch, LmCopyFilter keep, cudaStream_t s);
-cudaError_t lm_launch_split3(const float *src, int64_t ld, int64_t stride, void *dst, int64_t ld_dst,
-                             int64_t plane, int64_t rows, int64_t cols, int64_t batch, LmCopyFilter keep,
-                             cudaStream_t s);
+// lm_aux.cu.  An operand copy TMA can address: rows x cols (x batch) with
+// pitch ld -> pitch ld_dst (a multiple of 8), 16-bit copied as they are, FP32
+// as three bf16 planes (plane stride in elements).
+struct LmCopy {
+    const void *src = nullptr;       // NULL: nothing to copy
+    int64_t ld = 0, stride = 0;
+    void *dst = nullptr;
+    int64_t ld_dst = 0, plane = 0, rows = 0, cols = 0, batch = 0;
+    LmCopyFilter keep;
+    int64_t chunks = 0;              // of 8 elements, and whether they take vector loads (set by the launch)
+    int vec = 0;
+};
+// scale2 = {top / m, m / top} for the largest |grad| m of a counted row.
+struct LmGradScale {
+    const float *grad = nullptr;
+    const int64_t *target = nullptr;
+    int64_t vocab = 0;
+    int rows = 0;
+    float top = 1.f;
+    float *scale2 = nullptr;         // NULL: not wanted
+};
+// Both copies and the scale in one launch.
+cudaError_t lm_launch_copy(bool f32, LmCopy a, LmCopy b, const LmGradScale &scale, cudaStream_t s);
 // Joins the slabs' maxima and sums: lse and loss of each row.
 cudaError_t lm_launch_lse_join(const float2 *part, int slabs, int rows, const float *picked, const int64_t *target,
                                int64_t vocab, float *loss, float *lse, cudaStream_t s);
-// scale2 = {top / m, m / top} for the largest |grad| m of a counted row.
-cudaError_t lm_launch_grad_scale(const float *grad, const int64_t *target, int64_t vocab, int rows, float top,
-                                 float *scale2, cudaStream_t s);
 // out = alpha * (sum of `splits` FP32 planes), rounded to `out_type`.
 cudaError_t lm_launch_join_splits(const float *part, int64_t ld_part, int64_t plane, int splits, const float *alpha,
                                   int rows, int cols, void *out, int64_t ldo, int out_type, cudaStream_t s);
