@@ -2,11 +2,9 @@
 // operators: operand copies TMA can address, FP32 split into bf16 planes,
 // the joins of partial results.  All are bound by memory, or by being a launch
 // of a few microseconds; the copies move 8 neighbouring elements a thread, so
-// that writes are whole 16-byte words.  Measured on one GB300, each launch by
-// itself from cold caches: 50001 x 1001 f16 copied to a pitch of 1008 (201 MB)
-// 40.6 us, 4.9 TB/s; 16.8 M FP32 values split (168 MB) 24.7 us, 6.8 TB/s; 7 x
-// 1023 x 777 split from an odd pitch (56 MB) 11.4 us, 4.9 TB/s; 286 slabs of 16
-// rows joined 7.0 us, the largest |dloss| of 1023 rows 4.2 us.
+// that writes are whole 16-byte words.  On
+// one GB300 the copy of 50001 x 1001 f16 to a pitch of 1008 (200 MB moved) adds
+// 35 us to the call that needs it, 5.7 TB/s; a copy of little, 1 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -65,47 +63,77 @@ __device__ __forceinline__ void split3(float x, uint16_t &a, uint16_t &b, uint16
     c = (uint16_t)(__float_as_uint(r2) >> 16);
 }
 
+__device__ __forceinline__ void load16(const void *p, uint32_t *w) {
+    const uint4 v = *static_cast<const uint4 *>(p);
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+}
+
 // Chunk i of a copy: 8 neighbours of one row.
 template <bool F32>
 __device__ __forceinline__ void copy_chunk(const LmCopy &j, int64_t i) {
     const int64_t per_row = j.ld_dst / 8;
-    const int64_t r = i / per_row, c = (i - r * per_row) * 8, b = r / j.rows;
+    int64_t r, b;
+    if (j.chunks <= 0xFFFFFFFFll) {                 // 32-bit divisions
+        r = (uint32_t)i / (uint32_t)per_row;
+        b = j.batch == 1 ? 0 : (uint32_t)r / (uint32_t)j.rows;
+    } else {
+        r = i / per_row;
+        b = r / j.rows;
+    }
+    const int64_t c = (i - r * per_row) * 8;
     if (unused(j.keep, b)) return;
     const bool kept = keeps(j.keep, r);
-    const int64_t from = b * j.stride + (r - b * j.rows) * j.ld + c, to = r * j.ld_dst + c;
-    const bool wide = j.vec && c + 8 <= j.cols;
-    if constexpr (F32) {
-        const float *s = static_cast<const float *>(j.src) + from;
-        float x[8];
-        if (!kept) {
+    const int64_t to = r * j.ld_dst + c;
+    constexpr int ELEM = F32 ? 4 : 2, WORDS = 2 * ELEM;        // 32-bit words of 8 elements
+    const unsigned char *base = static_cast<const unsigned char *>(j.src);
+    const int64_t at = (b * j.stride + (r - b * j.rows) * j.ld + c) * ELEM;
+    // Rows of an odd pitch start anywhere in 16 bytes: the aligned words that
+    // hold the chunk are loaded whole and shifted, unless they reach beyond
+    // the operand.  (Forward pass of 1023 rows, 50001 x 1001 f16, of which 73 us
+    // are not the copies: 118 -> 108 us.)
+    const int skip = (int)(reinterpret_cast<uintptr_t>(base + at) & 15);
+    const int64_t first = at - skip;
+    uint32_t w[WORDS];
+    if (!kept) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = 0.f;
-        } else if (wide) {
-            *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(s);
-            *reinterpret_cast<float4 *>(x + 4) = *reinterpret_cast<const float4 *>(s + 4);
-        } else {
+        for (int i = 0; i < WORDS; ++i) w[i] = 0u;
+    } else if (c + 8 <= j.cols && first >= 0 && (skip == 0 || first + WORDS * 4 + 16 <= j.bytes)) {
+        uint32_t l[WORDS + 4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = c + e < j.cols ? s[e] : 0.f;
+        for (int i = 0; i < WORDS; i += 4)
+            load16(base + first + 4 * i, l + i);
+        if (skip != 0) {
+            load16(base + first + 4 * WORDS, l + WORDS);
+#pragma unroll
+            for (int i = 0; i < WORDS + 2; ++i) l[i] = skip & 8 ? l[i + 2] : l[i];
+#pragma unroll
+            for (int i = 0; i < WORDS + 1; ++i) l[i] = skip & 4 ? l[i + 1] : l[i];
+            if constexpr (!F32) {
+#pragma unroll
+                for (int i = 0; i < WORDS; ++i) l[i] = __funnelshift_r(l[i], l[i + 1], 8 * (skip & 2));
+            }
         }
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[i] = l[i];
+    } else if constexpr (F32) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = c + e < j.cols ? reinterpret_cast<const uint32_t *>(base + at)[e] : 0u;
+    } else {
+        const uint16_t *s = reinterpret_cast<const uint16_t *>(base + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = (c + 2 * i < j.cols ? s[2 * i] : 0u) | (uint32_t)(c + 2 * i + 1 < j.cols ? s[2 * i + 1] : 0u) << 16;
+    }
+    uint16_t *dst = static_cast<uint16_t *>(j.dst) + to;
+    if constexpr (F32) {
         alignas(16) uint16_t v[3][8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) split3(x[e], v[0][e], v[1][e], v[2][e]);
+        for (int e = 0; e < 8; ++e) split3(__uint_as_float(w[e]), v[0][e], v[1][e], v[2][e]);
 #pragma unroll
         for (int q = 0; q < 3; ++q)
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(j.dst) + q * j.plane + to) =
-                *reinterpret_cast<const uint4 *>(v[q]);
+            *reinterpret_cast<uint4 *>(dst + q * j.plane) = *reinterpret_cast<const uint4 *>(v[q]);
     } else {
-        const uint16_t *s = static_cast<const uint16_t *>(j.src) + from;
-        alignas(16) uint16_t v[8];
-        if (!kept) {
-            *reinterpret_cast<uint4 *>(v) = make_uint4(0, 0, 0, 0);
-        } else if (wide) {
-            *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(s);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = c + e < j.cols ? s[e] : (uint16_t)0;
-        }
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(j.dst) + to) = *reinterpret_cast<const uint4 *>(v);
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -209,7 +237,7 @@ lm_join_splits_kernel(const float *part, int64_t ld, int64_t plane, int splits, 
     const float a = alpha != nullptr ? *alpha : 1.f;
     const int64_t total = (int64_t)rows * cols;
     for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < total; i += gridDim.x * (int64_t)kThreads) {
-        const int64_t r = i / cols, c = i - r * cols;
+        const int64_t r = total <= 0xFFFFFFFFll ? (uint32_t)i / (uint32_t)cols : i / cols, c = i - r * cols;
         float s = 0.f;
         for (int z = 0; z < splits; ++z) s += part[z * plane + r * ld + c];
         out[r * ldo + c] = to_out<Out>(a * s);
@@ -235,9 +263,8 @@ int64_t blocks_for(int64_t threads) { return std::min<int64_t>((threads + kThrea
 cudaError_t lm_launch_copy(bool f32, LmCopy a, LmCopy b, const LmGradScale &scale, cudaStream_t s) {
     for (LmCopy *j : {&a, &b}) {
         if (j->src == nullptr) continue;
-        const int64_t words = f32 ? 4 : 8;          // elements of a 16-byte load
         j->chunks = j->ld_dst / 8 * j->rows * j->batch;
-        j->vec = reinterpret_cast<uintptr_t>(j->src) % 16 == 0 && j->ld % words == 0 && j->stride % words == 0;
+        j->bytes = ((j->batch - 1) * j->stride + (j->rows - 1) * j->ld + j->cols) * (f32 ? 4 : 2);
     }
     return launch(f32 ? lm_copy_kernel<true> : lm_copy_kernel<false>, blocks_for(a.chunks + b.chunks), kThreads, s, a,
                   b, scale);

@@ -84,8 +84,7 @@ struct LmCopy {
     void *dst = nullptr;
     int64_t ld_dst = 0, plane = 0, rows = 0, cols = 0, batch = 0;
     LmCopyFilter keep;
-    int64_t chunks = 0;              // of 8 elements, and whether they take vector loads (set by the launch)
-    int vec = 0;
+    int64_t chunks = 0, bytes = 0;   // chunks of 8 elements; from the first element to the last (set by the launch)
 };
 // scale2 = {top / m, m / top} for the largest |grad| m of a counted row.
 struct LmGradScale {
