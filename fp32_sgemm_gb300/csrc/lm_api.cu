@@ -195,41 +195,6 @@ int vec_ok(const void *p, int64_t ld, int64_t stride, int elem, int bytes) {
 
 // ------------------------------------------------------------ grouped
 
-struct Grouped {
-    int type = 0, op = 0;
-    int64_t T = 0, N = 0, K = 0, G = 0;
-    Operand a, b;
-};
-
-sgemmStatus_t plan_grouped(int type, int op, int64_t T, int64_t N, int64_t K, int64_t G, const void *A, int64_t lda,
-                           const void *B, int64_t ldb, int64_t strideB, Grouped &q) {
-    if (!type_ok(type) || (op != SGEMM_OP_N && op != SGEMM_OP_T)) return SGEMM_STATUS_INVALID_VALUE;
-    if (T < 0 || N < 0 || K < 0 || G < 0 || strideB < 0) return SGEMM_STATUS_INVALID_VALUE;
-    if (T > kMaxDim - 512 || N > kMaxDim - 512 || K > kMaxDim - 512 || G > SGEMM_MAX_GROUPS)
-        return SGEMM_STATUS_NOT_SUPPORTED;
-    const bool used = T > 0 && N > 0 && K > 0 && G > 0;
-    const int64_t br = op ? N : K, bc = op ? K : N;
-    sgemmStatus_t st = check_matrix(A, T, K, lda, type, used);
-    if (st != SGEMM_STATUS_SUCCESS) return st;
-    st = check_matrix(B, br, bc, ldb, type, used);
-    if (st != SGEMM_STATUS_SUCCESS) return st;
-    if (used && G > 1) {
-        if (strideB < (br - 1) * ldb + bc) return SGEMM_STATUS_INVALID_VALUE;
-        if (strideB > kMaxBytes / 4 / G) return SGEMM_STATUS_NOT_SUPPORTED;
-    }
-    q.type = type;
-    q.op = op;
-    q.T = T; q.N = N; q.K = K; q.G = G;
-    q.a.ptr = A; q.a.rows = T; q.a.cols = K; q.a.ld = lda; q.a.type = type;
-    q.b.ptr = B; q.b.rows = br; q.b.cols = bc; q.b.ld = ldb; q.b.type = type;
-    q.b.batch = G; q.b.stride = strideB;
-    if (used) {
-        q.a.plan();
-        q.b.plan();
-    }
-    return SGEMM_STATUS_SUCCESS;
-}
-
 // Tiles of a grouped product: size as in lm_kernels.h, rows of a group in one
 // tile.  The groups' sizes are on the device; half a tile of each group is
 // taken to be left over.  Measured, us, with tiles of 128 columns by 32 / 64 /
@@ -267,6 +232,66 @@ Tiling grouped_tiling(int type, int64_t T, int64_t N, int64_t G, int sms) {
     int rows = 256;
     if (ceil_div(N, 256) * G < sms) rows = mean <= 64 ? 64 : mean <= 128 ? 128 : 256;
     return {2, int(std::min<int64_t>(rows, round_up(T, 32)))};
+}
+
+// Parts the contraction is cut into where the tiles of a few rows leave most
+// SMs without one, each longer than the ring of stages (FP32 takes three a
+// block); a launch of its own joins them.  2 rows in 2 of 8 groups, 4096 x 2048:
+// 20.3 -> 11.1 us, FP32 99.9 -> 61.0; 2 rows in 2 of 4, 1024 x 1024 (not cut,
+// FP32 in 4): 8.0 -> 8.3, FP32 24.7 -> 15.8.
+int64_t grouped_parts(int type, int64_t K) { return ceil_div(K, 64) / (type == SGEMM_TYPE_F32 ? 4 : 12); }
+int grouped_splits(int type, const Tiling &t, int64_t T, int64_t N, int64_t K, int64_t G, int sms) {
+    if (t.size == 2) return 1;
+    const int64_t most = ceil_div(N, 128) * (T / t.tile_n + std::min(G, T));
+    return int(std::max<int64_t>(1, std::min(sms / std::max<int64_t>(1, most), grouped_parts(type, K))));
+}
+
+struct Grouped {
+    int type = 0, op = 0;
+    int64_t T = 0, N = 0, K = 0, G = 0;
+    Operand a, b;
+    // The rest of the plan, on a device of `sms` SMs.
+    Tiling tiling{};
+    int splits = 1;
+    int64_t ld_part = 0;
+    size_t ws_part = 0;
+    void tile(int sms) {
+        if (T == 0 || N == 0 || K == 0 || G == 0) return;
+        tiling = grouped_tiling(type, T, N, G, sms);
+        splits = grouped_splits(type, tiling, T, N, K, G, sms);
+        ld_part = round_up(N, 8);
+        ws_part = splits > 1 ? align256(splits * T * ld_part * 4) : 0;
+    }
+    size_t bytes() const { return a.ws + b.ws + ws_part; }
+};
+
+sgemmStatus_t plan_grouped(int type, int op, int64_t T, int64_t N, int64_t K, int64_t G, const void *A, int64_t lda,
+                           const void *B, int64_t ldb, int64_t strideB, Grouped &q) {
+    if (!type_ok(type) || (op != SGEMM_OP_N && op != SGEMM_OP_T)) return SGEMM_STATUS_INVALID_VALUE;
+    if (T < 0 || N < 0 || K < 0 || G < 0 || strideB < 0) return SGEMM_STATUS_INVALID_VALUE;
+    if (T > kMaxDim - 512 || N > kMaxDim - 512 || K > kMaxDim - 512 || G > SGEMM_MAX_GROUPS)
+        return SGEMM_STATUS_NOT_SUPPORTED;
+    const bool used = T > 0 && N > 0 && K > 0 && G > 0;
+    const int64_t br = op ? N : K, bc = op ? K : N;
+    sgemmStatus_t st = check_matrix(A, T, K, lda, type, used);
+    if (st != SGEMM_STATUS_SUCCESS) return st;
+    st = check_matrix(B, br, bc, ldb, type, used);
+    if (st != SGEMM_STATUS_SUCCESS) return st;
+    if (used && G > 1) {
+        if (strideB < (br - 1) * ldb + bc) return SGEMM_STATUS_INVALID_VALUE;
+        if (strideB > kMaxBytes / 4 / G) return SGEMM_STATUS_NOT_SUPPORTED;
+    }
+    q.type = type;
+    q.op = op;
+    q.T = T; q.N = N; q.K = K; q.G = G;
+    q.a.ptr = A; q.a.rows = T; q.a.cols = K; q.a.ld = lda; q.a.type = type;
+    q.b.ptr = B; q.b.rows = br; q.b.cols = bc; q.b.ld = ldb; q.b.type = type;
+    q.b.batch = G; q.b.stride = strideB;
+    if (used) {
+        q.a.plan();
+        q.b.plan();
+    }
+    return SGEMM_STATUS_SUCCESS;
 }
 
 struct WeightGrad {
@@ -477,7 +502,9 @@ sgemmStatus_t sgemmGroupedWorkspaceSize(sgemmHandle_t h, sgemmDataType_t type, s
     sgemmStatus_t st = plan_grouped(type, opB, T, N, K, G, A, lda, B, ldb, strideB, q);
     if (st != SGEMM_STATUS_SUCCESS) return st;
     if (h == nullptr) return SGEMM_STATUS_INVALID_VALUE;
-    *bytes = q.a.ws + q.b.ws;
+    // (A short contraction is cut on no device.)
+    if (grouped_parts(type, K) > 1) q.tile(h->sm_count);
+    *bytes = q.bytes();
     return SGEMM_STATUS_SUCCESS;
 }
 
@@ -501,12 +528,10 @@ sgemmStatus_t sgemmGrouped(sgemmHandle_t h, sgemmDataType_t type, sgemmOperation
     if (K == 0 || G == 0)
         return sg::lm_launch_zero(C, ldc, 0, elem, T, N, 1, stream) == cudaSuccess ? SGEMM_STATUS_SUCCESS
                                                                                    : SGEMM_STATUS_LAUNCH_FAILED;
-    if (q.a.ws + q.b.ws > 0 && (h->ws == nullptr || h->ws_bytes < q.a.ws + q.b.ws))
-        return SGEMM_STATUS_WORKSPACE_REQUIRED;
+    q.tile(h->sm_count);
+    if (q.bytes() > 0 && (h->ws == nullptr || h->ws_bytes < q.bytes())) return SGEMM_STATUS_WORKSPACE_REQUIRED;
 
-    const Tiling tiling = grouped_tiling(type, T, N, G, h->sm_count);
-    const int size = tiling.size;
-    const LmKernel k = sg::lm_grouped_kernel(size, opB == SGEMM_OP_N, type == SGEMM_TYPE_F32);
+    const LmKernel k = sg::lm_grouped_kernel(q.tiling.size, opB == SGEMM_OP_N, type == SGEMM_TYPE_F32);
     LmArgs p{};
     p.M = int(N);
     p.T = int(T);
@@ -514,23 +539,35 @@ sgemmStatus_t sgemmGrouped(sgemmHandle_t h, sgemmDataType_t type, sgemmOperation
     p.G = int(G);
     p.ends = groupEnds;
     p.tiles_m = int(ceil_div(N, k.tile_m));
-    p.tile_n = tiling.tile_n;
+    p.tile_n = q.tiling.tile_n;
     p.group_m = 8;
-    p.splits = 1;
+    p.splits = q.splits;
     p.bf16 = type == SGEMM_TYPE_F16 ? 0 : 1;
-    p.C = C;
-    p.ldc = ldc;
-    p.out = out_type(type);
-    p.vec = vec_ok(C, ldc, 0, elem, 16);
-    const int64_t tiles = int64_t(p.tiles_m) * (ceil_div(T, p.tile_n) + G + 1);
-    if (tiles > kMaxDim) return SGEMM_STATUS_NOT_SUPPORTED;
     char *ws = static_cast<char *>(h->ws);
+    float *part = reinterpret_cast<float *>(ws + q.a.ws + q.b.ws);
+    if (q.splits > 1) {
+        p.C = part;
+        p.ldc = q.ld_part;
+        p.stride_c = T * q.ld_part;
+        p.out = sg::kOutF32;
+    } else {
+        p.C = C;
+        p.ldc = ldc;
+        p.out = out_type(type);
+        p.vec = vec_ok(C, ldc, 0, elem, 16);
+    }
+    const int64_t tiles = int64_t(p.tiles_m) * (ceil_div(T, p.tile_n) + G + 1) * q.splits;
+    if (tiles > kMaxDim) return SGEMM_STATUS_NOT_SUPPORTED;
     sg::LmCopyFilter touched;           // matrices of groups that have rows
     touched.ends = groupEnds;
     if (!copy_operands(type, q.a.place(ws), q.b.place(ws + q.a.ws, touched), stream)) return SGEMM_STATUS_LAUNCH_FAILED;
     CUtensorMap tm_w, tm_x;
     if (!q.b.map(&tm_w, k.a_mn ? 64 : k.box_a) || !q.a.map(&tm_x, p.tile_n / (k.pair ? 2 : 1))) return SGEMM_STATUS_LAUNCH_FAILED;
-    return launch_lm(h, k, true, tm_w, tm_x, p, tiles, stream);
+    st = launch_lm(h, k, true, tm_w, tm_x, p, tiles, stream);
+    if (st != SGEMM_STATUS_SUCCESS || q.splits == 1) return st;
+    return sg::lm_launch_join_splits(part, q.ld_part, T * q.ld_part, q.splits, nullptr, int(T), int(N), C, ldc,
+                                     out_type(type), stream) == cudaSuccess
+               ? SGEMM_STATUS_SUCCESS : SGEMM_STATUS_LAUNCH_FAILED;
 }
 
 sgemmStatus_t sgemmGroupedWeightGradWorkspaceSize(sgemmHandle_t h, sgemmDataType_t type, int64_t T, int64_t M,

@@ -34,7 +34,7 @@ struct LmArgs {
     int tiles_m, tiles_n, tile_n, num_tiles, splits, group_m;
     uint32_t bf16;        // operands bf16 (else f16)
     void *C;
-    int64_t ldc, stride_c;   // stride_c: per group (kRagK) or per K split
+    int64_t ldc, stride_c;   // stride_c: per group (kRagK) or per K split (FP32 partial sums)
     int out, vec;            // LmOut; vec: rows take aligned vector stores
     const float *acc_in;     // added to D before alpha, or NULL
     int64_t ld_acc;

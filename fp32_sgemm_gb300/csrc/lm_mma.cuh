@@ -236,6 +236,8 @@ __device__ __forceinline__ LmWork lm_work(const LmArgs &p, const int *start, con
     w.krow0 = 0;
     w.klast = 64;
     if constexpr (RAG == kRagN) {
+        w.s = t % p.splits;
+        t /= p.splits;
         int lo = 0, hi = p.G;                   // last g with prefix[g] <= t
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -255,7 +257,8 @@ __device__ __forceinline__ LmWork lm_work(const LmArgs &p, const int *start, con
         w.n0 = r0 + tn * per;
         w.nvalid = min(per, rows - tn * per);
         w.nmma = (w.nvalid + Tile::GRAN - 1) / Tile::GRAN * Tile::GRAN;
-        w.nkb = lo == p.G ? 0 : p.kb;
+        w.kb0 = (int)((int64_t)p.kb * w.s / p.splits);
+        w.nkb = lo == p.G ? 0 : (int)((int64_t)p.kb * (w.s + 1) / p.splits) - w.kb0;
     } else if constexpr (RAG == kRagK) {
         const int per_g = p.tiles_m * p.tiles_n, at = t / per_g;
         w.g = (int)prefix[at];                  // the groups in their order of work
@@ -523,7 +526,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
     const int slot = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
     const int slots = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
-    const int num_tiles = RAG == kRagN ? (int)g_prefix[p.G + 1] : p.num_tiles;
+    const int num_tiles = RAG == kRagN ? (int)g_prefix[p.G + 1] * p.splits : p.num_tiles;
 
     if (warp == 0) {
         // ---------------- TMA producer (one elected lane issues) ----------------
@@ -875,7 +878,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                     const int n = w.n0 + col;               // column of D
                     if constexpr (EPI == kEpiCols) {
                         if (p.out == kOutF32)
-                            lm_store_cols(p, static_cast<float *>(p.C), row0, n, cnt, v, stg, lane);
+                            lm_store_cols(p, static_cast<float *>(p.C) + w.s * p.stride_c, row0, n, cnt, v, stg, lane);
                         else if (p.out == kOutF16)
                             lm_store_cols(p, static_cast<__half *>(p.C), row0, n, cnt, v, stg, lane);
                         else

@@ -74,7 +74,8 @@ sgemmStatus_t sgemmGrouped(sgemmHandle_t handle, sgemmDataType_t type, sgemmOper
                            int64_t K, int64_t G, const void *A, int64_t lda, const void *B, int64_t ldb,
                            int64_t strideB, const int32_t *groupEnds, void *C, int64_t ldc, cudaStream_t stream);
 
-/* Workspace sgemmGrouped() requires (0 for 16-bit operands read in place). */
+/* Workspace sgemmGrouped() requires: copies of operands that are not read in
+   place, partial sums where few rows leave the contraction to be cut. */
 sgemmStatus_t sgemmGroupedWorkspaceSize(sgemmHandle_t handle, sgemmDataType_t type, sgemmOperation_t opB, int64_t T,
                                         int64_t N, int64_t K, int64_t G, const void *A, int64_t lda, const void *B,
                                         int64_t ldb, int64_t strideB, size_t *bytes);

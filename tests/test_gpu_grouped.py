@@ -230,6 +230,23 @@ def test_gradients_against_differences(sg):
     assert abs(along(x, w + v, x, w - v) - (dw.double() * v.double()).sum().item()) <= 1e-5 * scale
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("K,N", [(4100, 72), (1537, 129), (8192, 256)])
+@pytest.mark.parametrize("sizes", [[1], [0, 2, 0, 3, 0], [5, 40]], ids=["1", "2-3", "5-40"])
+def test_few_rows_of_a_long_contraction(sg, dtype, trans, K, N, sizes):
+    # (Cut along the contraction and joined.)  Two rows behind the last end.
+    n = sum(sizes)
+    x = _rand((n + 2, K), dtype, 40, pitch_pad=3)
+    w = _rand((len(sizes), N, K) if trans else (len(sizes), K, N), dtype, 41)
+    out = torch.full((n + 2, N + 5), 7.0, device="cuda").to(DTYPES[dtype])
+    y = sg.grouped_gemm(x, w, _ends(sizes), trans_w=trans, out=out[:, :N])
+    ref, mag = _forward_ref(x[:n], w, sizes, trans)
+    _close(y[:n], ref, mag, dtype)
+    assert (y[n:] == 0).all() and (out[:, N:] == 7.0).all()
+    assert torch.equal(y, sg.grouped_gemm(x, w, _ends(sizes), trans_w=trans))
+
+
 @pytest.mark.parametrize("trans", [False, True])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_matrices_without_rows_are_not_read(sg, dtype, trans):
