@@ -160,8 +160,8 @@ int resident_slots(const sgemmContext *h, const LmKernel &k, int smem) {
 // table (the opt-in is made once per kernel).
 int smem_of(const LmKernel &k, bool groups) { return k.smem + (groups ? 8 * (sg::kLmMaxGroups + 2) : 0); }
 
-sgemmStatus_t launch_lm(sgemmContext *h, const LmKernel &k, bool groups, const CUtensorMap &a, const CUtensorMap &b,
-                        LmArgs &args, int64_t tiles, cudaStream_t stream) {
+sgemmStatus_t launch_lm(sgemmContext *h, const LmKernel &k, bool groups, const CUtensorMap *a, const CUtensorMap *b,
+                        LmArgs &args, int64_t tiles, cudaStream_t stream, sg::LmRows *rows = nullptr) {
     const int smem = smem_of(k, groups);
     const int slots = resident_slots(h, k, smem);
     if (slots < 1) return SGEMM_STATUS_LAUNCH_FAILED;
@@ -182,8 +182,8 @@ sgemmStatus_t launch_lm(sgemmContext *h, const LmKernel &k, bool groups, const C
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = k.pair ? 2 : 1;
-    void *kargs[] = {const_cast<CUtensorMap *>(&a), const_cast<CUtensorMap *>(&b), &args};
-    return cudaLaunchKernelExC(&cfg, k.fn, kargs) == cudaSuccess ? SGEMM_STATUS_SUCCESS
+    void *kargs[] = {const_cast<CUtensorMap *>(a), const_cast<CUtensorMap *>(b), &args}, *rargs[] = {&args, rows};
+    return cudaLaunchKernelExC(&cfg, k.fn, rows != nullptr ? rargs : kargs) == cudaSuccess ? SGEMM_STATUS_SUCCESS
                                                                  : SGEMM_STATUS_LAUNCH_FAILED;
 }
 
@@ -211,8 +211,8 @@ int vec_ok(const void *p, int64_t ld, int64_t stride, int elem, int bytes) {
 //   and no more rows than there are (8 rows, 8 groups, 4096 x 14336, 256
 //     columns by 32 / 256 rows: 96 / 137).
 // FP32, whose six products weigh more than reading W, 32 / 128 / 256 rows:
-// thin tiles also for few rows in a group (32 groups of 2, 1024 x 1408: 115 /
-// 118 / 147), those of one SM up to 256 rows (16 of 192, 2048 x 1408: 291 / 202
+// thin tiles also for few rows in a group (16 of 16, 2048 x 1408: 147 / 150 /
+// 174), those of one SM up to 256 rows (16 of 192, 2048 x 1408: 291 / 202
 // / 222; of 512: 659 / 307 / 304) and where the pairs' leave SMs idle (2 groups
 // of 632, 1024 x 1408: 57 / 34 / 45).
 struct Tiling {
@@ -237,8 +237,8 @@ Tiling grouped_tiling(int type, int64_t T, int64_t N, int64_t G, int sms) {
 // Parts the contraction is cut into where the tiles of a few rows leave most
 // SMs without one, each longer than the ring of stages (FP32 takes three a
 // block); a launch of its own joins them.  2 rows in 2 of 8 groups, 4096 x 2048:
-// 20.3 -> 11.1 us, FP32 99.9 -> 61.0; 2 rows in 2 of 4, 1024 x 1024 (not cut,
-// FP32 in 4): 8.0 -> 8.3, FP32 24.7 -> 15.8.
+// 20.3 -> 11.1 us; 128 rows in 2 groups, 4096 x 1024: 19.9 -> 12.4, FP32 75.5 ->
+// 39.8; 64 rows in one, 2048 x 2048: 12.4 -> 11.0, FP32 41.0 -> 24.0.
 int64_t grouped_parts(int type, int64_t K) { return ceil_div(K, 64) / (type == SGEMM_TYPE_F32 ? 4 : 12); }
 int grouped_splits(int type, const Tiling &t, int64_t T, int64_t N, int64_t K, int64_t G, int sms) {
     if (t.size == 2) return 1;
@@ -246,17 +246,24 @@ int grouped_splits(int type, const Tiling &t, int64_t T, int64_t N, int64_t K, i
     return int(std::max<int64_t>(1, std::min(sms / std::max<int64_t>(1, most), grouped_parts(type, K))));
 }
 
+// Few FP32 rows a group: W as it is, on the FP32 pipes (lm_rows32.cu has both
+// sides), unless the contraction is too short for a CTA's warps.
+bool few_rows32(int type, int64_t T, int64_t K, int64_t G) {
+    return type == SGEMM_TYPE_F32 && T / G <= 8 && K >= 256;
+}
+
 struct Grouped {
     int type = 0, op = 0;
     int64_t T = 0, N = 0, K = 0, G = 0;
     Operand a, b;
+    bool rows32 = false;         // read as they are, on the FP32 pipes
     // The rest of the plan, on a device of `sms` SMs.
     Tiling tiling{};
     int splits = 1;
     int64_t ld_part = 0;
     size_t ws_part = 0;
     void tile(int sms) {
-        if (T == 0 || N == 0 || K == 0 || G == 0) return;
+        if (T == 0 || N == 0 || K == 0 || G == 0 || rows32) return;
         tiling = grouped_tiling(type, T, N, G, sms);
         splits = grouped_splits(type, tiling, T, N, K, G, sms);
         ld_part = round_up(N, 8);
@@ -287,7 +294,8 @@ sgemmStatus_t plan_grouped(int type, int op, int64_t T, int64_t N, int64_t K, in
     q.a.ptr = A; q.a.rows = T; q.a.cols = K; q.a.ld = lda; q.a.type = type;
     q.b.ptr = B; q.b.rows = br; q.b.cols = bc; q.b.ld = ldb; q.b.type = type;
     q.b.batch = G; q.b.stride = strideB;
-    if (used) {
+    q.rows32 = used && few_rows32(type, T, K, G);
+    if (used && !q.rows32) {
         q.a.plan();
         q.b.plan();
     }
@@ -528,6 +536,31 @@ sgemmStatus_t sgemmGrouped(sgemmHandle_t h, sgemmDataType_t type, sgemmOperation
     if (K == 0 || G == 0)
         return sg::lm_launch_zero(C, ldc, 0, elem, T, N, 1, stream) == cudaSuccess ? SGEMM_STATUS_SUCCESS
                                                                                    : SGEMM_STATUS_LAUNCH_FAILED;
+    if (q.rows32) {
+        const bool few = ceil_div(N, 32) * std::min(G, T) < h->sm_count;
+        const LmKernel k = sg::lm_rows32_kernel_info(opB == SGEMM_OP_T, few);
+        LmArgs p{};
+        p.M = int(N);
+        p.T = int(T);
+        p.G = int(G);
+        p.ends = groupEnds;
+        p.tile_n = k.bn;
+        p.tiles_m = int(ceil_div(N, k.tile_m));
+        p.C = C;
+        p.ldc = ldc;
+        sg::LmRows rows{};
+        rows.X = static_cast<const float *>(A);
+        rows.W = static_cast<const float *>(B);
+        rows.ldx = lda;
+        rows.ldw = ldb;
+        rows.stride = G > 1 ? strideB : 0;
+        rows.K = int(K);
+        rows.x_vec = vec_ok(A, lda, 0, 4, 16);
+        rows.w_vec = vec_ok(B, ldb, rows.stride, 4, 16);
+        const int64_t tiles = int64_t(p.tiles_m) * (ceil_div(T, k.bn) + G + 1);
+        if (tiles > kMaxDim) return SGEMM_STATUS_NOT_SUPPORTED;
+        return launch_lm(h, k, true, nullptr, nullptr, p, tiles, stream, &rows);
+    }
     q.tile(h->sm_count);
     if (q.bytes() > 0 && (h->ws == nullptr || h->ws_bytes < q.bytes())) return SGEMM_STATUS_WORKSPACE_REQUIRED;
 
@@ -563,7 +596,7 @@ sgemmStatus_t sgemmGrouped(sgemmHandle_t h, sgemmDataType_t type, sgemmOperation
     if (!copy_operands(type, q.a.place(ws), q.b.place(ws + q.a.ws, touched), stream)) return SGEMM_STATUS_LAUNCH_FAILED;
     CUtensorMap tm_w, tm_x;
     if (!q.b.map(&tm_w, k.a_mn ? 64 : k.box_a) || !q.a.map(&tm_x, p.tile_n / (k.pair ? 2 : 1))) return SGEMM_STATUS_LAUNCH_FAILED;
-    st = launch_lm(h, k, true, tm_w, tm_x, p, tiles, stream);
+    st = launch_lm(h, k, true, &tm_w, &tm_x, p, tiles, stream);
     if (st != SGEMM_STATUS_SUCCESS || q.splits == 1) return st;
     return sg::lm_launch_join_splits(part, q.ld_part, T * q.ld_part, q.splits, nullptr, int(T), int(N), C, ldc,
                                      out_type(type), stream) == cudaSuccess
@@ -644,7 +677,7 @@ sgemmStatus_t sgemmGroupedWeightGrad(sgemmHandle_t h, sgemmDataType_t type, int6
     if (!copy_operands(type, q.a.place(ws), q.b.place(ws + q.a.ws), stream)) return SGEMM_STATUS_LAUNCH_FAILED;
     CUtensorMap tm_a, tm_b;
     if (!q.a.map(&tm_a, 64) || !q.b.map(&tm_b, 64)) return SGEMM_STATUS_LAUNCH_FAILED;
-    return launch_lm(h, k, true, tm_a, tm_b, p, tiles, stream);
+    return launch_lm(h, k, true, &tm_a, &tm_b, p, tiles, stream);
 }
 
 sgemmStatus_t sgemmCrossEntropyWorkspaceSize(sgemmHandle_t h, sgemmDataType_t type, int64_t T, int64_t V, int64_t D,
@@ -688,7 +721,7 @@ sgemmStatus_t sgemmCrossEntropy(sgemmHandle_t h, sgemmDataType_t type, int64_t T
     if (!copy_operands(type, q.x.place(ws), q.w.place(ws + q.x.ws), stream)) return SGEMM_STATUS_LAUNCH_FAILED;
     CUtensorMap tm_x, tm_w;
     if (!q.x.map(&tm_x, k.box_a) || !q.w.map(&tm_w, q.tile_n / (k.pair ? 2 : 1))) return SGEMM_STATUS_LAUNCH_FAILED;
-    st = launch_lm(h, k, false, tm_x, tm_w, p, p.num_tiles, stream);
+    st = launch_lm(h, k, false, &tm_x, &tm_w, p, p.num_tiles, stream);
     if (st != SGEMM_STATUS_SUCCESS) return st;
     return sg::lm_launch_lse_join(p.part, q.slabs, int(T), p.picked, target, V, loss, lse, stream) == cudaSuccess
                ? SGEMM_STATUS_SUCCESS : SGEMM_STATUS_LAUNCH_FAILED;
@@ -797,7 +830,7 @@ sgemmStatus_t sgemmCrossEntropyGrad(sgemmHandle_t h, sgemmDataType_t type, int64
         p.gscale = scaled ? scale2 : nullptr;
         if (q.d_planes == 2) p.lo = static_cast<char *>(d) + T * q.ld_d * 2;
         if (!q.w.map_rows(&tm_w, tn / (kd.pair ? 2 : 1), v0, width)) return SGEMM_STATUS_LAUNCH_FAILED;
-        st = launch_lm(h, kd, false, tm_x, tm_w, p, p.num_tiles, stream);
+        st = launch_lm(h, kd, false, &tm_x, &tm_w, p, p.num_tiles, stream);
         if (st != SGEMM_STATUS_SUCCESS) return st;
 
         Operand dd;
@@ -833,7 +866,7 @@ sgemmStatus_t sgemmCrossEntropyGrad(sgemmHandle_t h, sgemmDataType_t type, int64
         }
         p.acc_in = first ? nullptr : acc;
         p.ld_acc = q.ld_acc;
-        st = launch_lm(h, kx, false, tm_d, tm_w_mn, p, p.num_tiles, stream);
+        st = launch_lm(h, kx, false, &tm_d, &tm_w_mn, p, p.num_tiles, stream);
         if (st != SGEMM_STATUS_SUCCESS) return st;
         if (q.splits > 1 &&
             sg::lm_launch_join_splits(acc, q.ld_acc, T * q.ld_acc, q.splits, scaled ? scale2 + 1 : nullptr, int(T),
@@ -851,7 +884,7 @@ sgemmStatus_t sgemmCrossEntropyGrad(sgemmHandle_t h, sgemmDataType_t type, int64
         p.out = out_type(type);
         p.vec = vec_ok(p.C, lddw, 0, elem, 32);
         p.alpha = scaled ? scale2 + 1 : nullptr;
-        st = launch_lm(h, kw, false, tm_d_mn, tm_x_mn, p, p.num_tiles, stream);
+        st = launch_lm(h, kw, false, &tm_d_mn, &tm_x_mn, p, p.num_tiles, stream);
         if (st != SGEMM_STATUS_SUCCESS) return st;
     }
     return SGEMM_STATUS_SUCCESS;

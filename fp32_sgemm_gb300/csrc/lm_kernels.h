@@ -57,6 +57,15 @@ struct LmKernel {
     int a_mn = 0;                   // A is read MN-major (boxes of 64 x 64)
 };
 
+// Operands of lm_rows32.cu as they lie in memory.
+struct LmRows {
+    const float *X, *W;
+    int64_t ldx, ldw, stride;
+    int K, x_vec, w_vec;            // rows take 16-byte loads
+};
+// tile_m columns by bn rows; few: fewer tiles than SMs.
+LmKernel lm_rows32_kernel_info(bool trans, bool few);
+
 // Kernel tables.  size: 0 thin, 1 middle, 2 big (SM pair).
 LmKernel lm_grouped_kernel(int size, bool w_mn, bool f32);      // lm_grouped*.cu
 LmKernel lm_weight_grad_kernel(int size, bool f32);             // size 1 or 2

@@ -57,10 +57,11 @@ typedef enum sgemmDataType {
  * gradient as A and the other opB.
  *
  * F16 and BF16 products run on the tensor cores with FP32 sums.  F32
- * operands are split into three bf16 planes each (x = p0 + p1 + p2 exactly)
- * in the workspace and multiplied as the six products p_i q_j, i + j <= 2,
+ * products of up to 8 rows a group in the mean (T / G) and K >= 256 are
+ * FP32 multiply-adds.  For the others F32 operands are split into three bf16
+ * planes each (x = p0 + p1 + p2 exactly) in the workspace and multiplied as the six products p_i q_j, i + j <= 2,
  * with FP32 sums of 64-long pieces; the planes left out are below 2^-23 of
- * a product.  Infinite F32 inputs give NaN or infinity.
+ * a product.  There infinite F32 inputs give NaN or infinity.
  *
  * INVALID_VALUE: negative sizes, a pitch below the row length, strideB
  * below one matrix when G > 1, unknown type or op, NULL pointers with

@@ -248,6 +248,29 @@ def test_few_rows_of_a_long_contraction(sg, dtype, trans, K, N, sizes):
 
 
 @pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("K", [256, 259, 2048, 2053])
+@pytest.mark.parametrize("N", [1, 31, 100, 130])
+def test_few_f32_rows(sg, trans, K, N):
+    # Up to eight rows a group in the mean: groups around eight rows, NaN in
+    # the rows behind the last end and in the matrices of empty groups.
+    sizes = [8, 0, 1, 9, 17, 3, 0]
+    n = sum(sizes)
+    x = _rand((n + 3, K), "f32", 50)
+    w = _rand((len(sizes), N, K) if trans else (len(sizes), K, N), "f32", 51)
+    ref, mag = _forward_ref(x[:n], w, sizes, trans)
+    x[n:], w[1], w[6] = float("nan"), float("nan"), float("nan")
+    out = torch.full((n + 3, N + 2), 7.0, device="cuda")
+    y = sg.grouped_gemm(x, w, _ends(sizes), trans_w=trans, out=out[:, :N])
+    _close(y[:n], ref, mag, "f32")
+    assert (y[n:] == 0).all() and (out[:, N:] == 7.0).all()
+    ends = _ends(sizes)
+    h = sg.Handle()
+    ends[2] = 4                                      # runs backwards
+    sg.grouped_gemm(x, w, ends, trans_w=trans, out=out[:, :N], handle=h)
+    assert h.device_error() >> 24 == 6 and (out[:, N:] == 7.0).all()
+
+
+@pytest.mark.parametrize("trans", [False, True])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_matrices_without_rows_are_not_read(sg, dtype, trans):
     # Odd pitches, so that the matrices are copied first; those of groups

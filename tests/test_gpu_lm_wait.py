@@ -31,7 +31,7 @@ def _calls(sg, dtype):
     target = torch.randint(0, 3000, (400,), generator=g, device="cuda")
     dy = rand(3000, 512)
     return {
-        "thin": lambda h: sg.grouped_gemm(few, w, ends(3, 5, 9, 16), trans_w=True, handle=h),
+        "thin": lambda h: sg.grouped_gemm(some[:160], w, ends(30, 50, 90, 160), trans_w=True, handle=h),
         "middle": lambda h: sg.grouped_gemm(some, w, ends(100, 200, 300, 400), trans_w=True, handle=h),
         "pair": lambda h: sg.grouped_gemm(many, w, ends(700, 1500, 2100, 3000), trans_w=True, handle=h),
         "weight_grad": lambda h: sg.grouped_gemm_weight_grad(many, dy, ends(703, 1501, 2100, 3000), handle=h),
