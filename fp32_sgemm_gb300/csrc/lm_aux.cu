@@ -2,9 +2,9 @@
 // operators: operand copies TMA can address, FP32 split into bf16 planes,
 // the joins of partial results.  All are bound by memory, or by being a launch
 // of a few microseconds; the copies move 8 neighbouring elements a thread, so
-// that writes are whole 16-byte words.  On
-// one GB300 the copy of 50001 x 1001 f16 to a pitch of 1008 (200 MB moved) adds
-// 35 us to the call that needs it, 5.7 TB/s; a copy of little, 1 us.
+// that writes are whole 16-byte words.  On one GB300 the copy of 50001 x 1001
+// f16 to a pitch of 1008 (200 MB moved) adds 35 us to the call that needs it,
+// 5.7 TB/s; a copy of little, 1 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -32,7 +32,7 @@
 //     pipe is busy 98.6% of the active cycles of the forward pass, 96.1 to
 //     98.5% of the gradient's three products (the SMs run at 1.7 of 2.07 GHz
 //     then).  8192 tokens against 131072 x 4096, loss and gradients: 19.3 to
-//     20.0 ms for 35.2 TFLOP, 1760 to 1820 TFLOP/s.  32768 rows in 8 groups, 4096 x 2048: 290 us,
+//     20.2 ms for 35.2 TFLOP, 1740 to 1820 TFLOP/s.  32768 rows in 8 groups, 4096 x 2048: 290 us,
 //     1890 TFLOP/s forward, 291 us weight gradient.  With fewer tiles the last
 //     round leaves pairs idle (8192 rows: 85 us, 1610 TFLOP/s, 256 tiles on 76
 //     pairs);
@@ -41,7 +41,7 @@
 //     tokens against 32000 x 1024 (66 MB): 18 us and 3.5 for the join;
 //   * FP32: six bf16 products for one, and the three planes of both operands
 //     written and read again: 4096 rows in 8 groups, 1024 x 2048, both
-//     gradients 250 to 268 us (206 GFLOP of bf16, 108 us; splitting 60 us).
+//     gradients 245 to 265 us (206 GFLOP of bf16, 108 us).
 #pragma once
 
 #include <cuda_bf16.h>
