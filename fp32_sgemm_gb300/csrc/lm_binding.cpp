@@ -68,6 +68,17 @@ void check_kind(const at::Tensor &t, const char *name, at::ScalarType type, c10:
     if (t.device() != dev) fail(PyExc_ValueError, "%s must be on %s", name, dev.str().c_str());
 }
 
+// Row pitch of the matrices whose rows are dimension `d` of t.  Rows that are
+// the same memory (a broadcast) have none: with one column, too, whose stride
+// of 0 must not pass for a pitch of 1, with which the rows would be read beyond
+// the tensor.
+int64_t pitch(const at::Tensor &t, int d, const char *name) {
+    const int64_t rows = t.size(d), cols = t.size(d + 1);
+    if (rows <= 1 || cols == 0) return std::max<int64_t>(1, cols);
+    if (t.stride(d) < cols) fail(PyExc_ValueError, "%s has overlapping rows", name);
+    return t.stride(d);
+}
+
 // Row-major matrix of the call's type and device; rows, cols < 0: any.
 Matrix matrix(const at::Tensor &t, const char *name, at::ScalarType type, c10::Device dev, int64_t rows = -1,
               int64_t cols = -1) {
@@ -81,8 +92,7 @@ Matrix matrix(const at::Tensor &t, const char *name, at::ScalarType type, c10::D
              (long long)m.cols, (long long)(rows < 0 ? m.rows : rows), (long long)(cols < 0 ? m.cols : cols));
     if (m.rows > 0 && m.cols > 1 && t.stride(1) != 1)
         fail(PyExc_ValueError, "%s must be row major (stride(1) == 1)", name);
-    m.ld = std::max<int64_t>(1, m.rows > 1 ? t.stride(0) : m.cols);
-    if (m.rows > 1 && m.ld < m.cols) fail(PyExc_ValueError, "%s has overlapping rows", name);
+    m.ld = pitch(t, 0, name);
     m.ptr = const_cast<void *>(t.const_data_ptr());
     return m;
 }
@@ -101,8 +111,7 @@ Matrix stack(const at::Tensor &t, const char *name, at::ScalarType type, c10::De
     m.cols = cols;
     if (rows > 0 && cols > 1 && t.stride(2) != 1)
         fail(PyExc_ValueError, "%s must be row major (stride(2) == 1)", name);
-    m.ld = std::max<int64_t>(1, rows > 1 ? t.stride(1) : cols);
-    if (rows > 1 && m.ld < cols) fail(PyExc_ValueError, "%s has overlapping rows", name);
+    m.ld = pitch(t, 1, name);
     m.stride = n > 1 ? t.stride(0) : 0;
     if (n > 1 && rows > 0 && cols > 0 && m.stride < (rows - 1) * m.ld + cols)
         fail(PyExc_ValueError, "%s must hold one matrix per group (no broadcast)", name);
