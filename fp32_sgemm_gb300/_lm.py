@@ -85,7 +85,7 @@ def w4_gemm(x, q, scales, zeros=None, *, out=None, handle=None, stream=None):
 
     x [M, K] (a few rows); q [N, K // 2] uint8, column 2 i of W in the low
     four bits of byte i, column 2 i + 1 in the high four; scales [N, groups]
-    of x's type and zeros [N, groups] uint8 or None (8 everywhere), groups of
+    of x's type and zeros [N, groups] uint8 (0 to 255) or None (8 everywhere), groups of
     K // groups = 32, 64 or 128 columns:
     W[n, k] = scales[n, k // group] * (q[n, k] - zeros[n, k // group]).
     """

@@ -6,12 +6,12 @@
 // product, so everything else is kept off its way:
 //   * each warp streams 16 weight rows, 256 columns (2 KB) at a time, through
 //     its own ring of TMA copies;
-//   * q - z is an integer of at most 5 bits, exact in f16 and bf16, so the
-//     weights meet x in the tensor core unscaled (mma.sync m16n8k16, the rows
-//     of W on the M side, 8 tokens on the N side) and the scale is applied to
-//     the FP32 sum of its group: no weight is ever rounded.  A nibble becomes
-//     a float by one logic operation (its bits under those of 128 or 1024)
-//     and one subtraction, for two weights at a time;
+//   * q - z is an integer of magnitude below 256 (z is any byte), exact in
+//     f16 and bf16, so the weights meet x in the tensor core unscaled
+//     (mma.sync m16n8k16, the rows of W on the M side, 8 tokens on the N side)
+//     and the scale is applied to the FP32 sum of its group: no weight is ever
+//     rounded.  A nibble becomes a float by one logic operation (its bits under
+//     those of 128 or 1024) and one subtraction, for two weights at a time;
 //   * the order of k inside a group is free as long as both operands agree.
 //     A lane multiplies the 8 weights of a 32-bit word with the 8 x values
 //     of the same columns, kept in shared memory in the order in which the
@@ -35,6 +35,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "lm_ptx.cuh"
 #include "lm_w4.h"
 
@@ -55,16 +57,47 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
-// (w & mask) | magic in one operation, with both constants in registers.
-__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
+// (w & mask) ^ magic in one operation, with both constants in registers.
+__device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t mask, uint32_t magic) {
     uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));
+    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));
     return r;
 }
 __device__ __forceinline__ uint32_t in_register(uint32_t v) {
     uint32_t r;
     asm volatile("mov.b32 %0, %1;" : "=r"(r) : "r"(v));
     return r;
+}
+
+// What the unpacking subtracts for one zero point z, twice in a register each.
+// Any byte is a zero point: q - z is in [-255, 15], exact in both types.
+//   f16: 1024 + z, and 64 + z for the nibbles four bits higher.
+//   bf16 holds 128 + q beside a nibble, and 128 + z exactly only for z < 128;
+//   from 128 on the nibble is complemented and the sign set, which makes it
+//   -(128 + 15 - q) = q - 143, and z - 143 is subtracted.  `other` is what the
+//   masked nibble is combined with (and_xor) to get there.  As that takes five
+//   operations more, a step none of whose zero points is above 127 (ANY false)
+//   goes without (14335 x 4096, groups of 32, seven rows: 14.8 us with it in
+//   every step).
+struct W4Zero {
+    uint32_t zero, other;
+};
+// Byte `at` of z.
+template <bool BF16, bool ANY>
+__device__ __forceinline__ W4Zero w4_zero(uint32_t z, int at, uint32_t magic) {
+    if constexpr (BF16 && !ANY) {
+        return {__byte_perm(z, 0x43434343u, 0x4040u | (uint32_t)at * 0x101u), magic};
+    } else if constexpr (BF16) {
+        const uint32_t u = __byte_perm(z, 0x4B000000u, 0x7440u | (uint32_t)at);       // 2^23 + z
+        const bool high = (u & 0x80u) != 0;
+        const float c = __uint_as_float(u) - (high ? 8388608.f + 143.f : 8388608.f - 128.f);
+        return {__byte_perm(__float_as_uint(c), 0u, 0x3232u), high ? 0xC30FC30Fu : 0x43004300u};
+    } else {
+        const uint32_t u = __byte_perm(z, 0x64646464u, 0x4040u | (uint32_t)at * 0x101u);
+        const uint32_t sub = 0x63806380u;                                             // 960 twice
+        const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&u), *reinterpret_cast<const __half2 *>(&sub));
+        return {u, *reinterpret_cast<const uint32_t *>(&d)};
+    }
 }
 
 // The constants of the unpacking, kept in registers.
@@ -77,27 +110,33 @@ struct W4Unpack {
         mask4 = in_register(0x00F000F0u);
         sixteenth = 0x2C002C00u;     // 1 / 16 twice, f16
     }
-    // The 8 nibbles of w as four pairs (0,4) (1,5) (2,6) (3,7) of q - z.
-    // `zero`: 128 + z (bf16) or 1024 + z (f16), twice.  f16 has room for the
-    // nibble four bits higher, as 1024 + 16 q, which one fused operation
-    // brings to q - z (`zero4` = 64 + z): two shifts fewer.
-    __device__ __forceinline__ void operator()(uint32_t w, uint32_t zero, uint32_t zero4, uint32_t (&o)[4]) const {
+    // A zero point of 8.
+    __device__ __forceinline__ W4Zero eight() const {
+        if constexpr (BF16) return {0x43084308u, magic};
+        else return {0x64086408u, 0x54805480u};
+    }
+    // The 8 nibbles of w as four pairs (0,4) (1,5) (2,6) (3,7) of q - z: each
+    // nibble in the low bits of a float whose unit there is one, less that
+    // float and z (a published conversion: Kim et al., 2022).  f16 has room
+    // for the nibble four bits higher, as 1024 + 16 q, which one fused
+    // operation brings to q - z: two shifts fewer.
+    __device__ __forceinline__ void operator()(uint32_t w, const W4Zero &zero, uint32_t (&o)[4]) const {
         if constexpr (BF16) {
-            const __nv_bfloat162 z = *reinterpret_cast<const __nv_bfloat162 *>(&zero);
+            const __nv_bfloat162 z = *reinterpret_cast<const __nv_bfloat162 *>(&zero.zero);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t v = and_or(w >> (4 * i), mask, magic);
+                const uint32_t v = and_xor(w >> (4 * i), mask, zero.other);
                 const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), z);
                 o[i] = *reinterpret_cast<const uint32_t *>(&d);
             }
         } else {
-            const __half2 z = *reinterpret_cast<const __half2 *>(&zero);
-            const __half2 z4 = *reinterpret_cast<const __half2 *>(&zero4);
+            const __half2 z = *reinterpret_cast<const __half2 *>(&zero.zero);
+            const __half2 z4 = *reinterpret_cast<const __half2 *>(&zero.other);
             const __half2 s = *reinterpret_cast<const __half2 *>(&sixteenth);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const uint32_t u = i ? w >> 8 : w;
-                const uint32_t v = and_or(u, mask, magic), v4 = and_or(u, mask4, magic);
+                const uint32_t v = and_xor(u, mask, magic), v4 = and_xor(u, mask4, magic);
                 const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&v), z);
                 const __half2 d4 = __hfma2(*reinterpret_cast<const __half2 *>(&v4), s, __hneg2(z4));
                 o[2 * i] = *reinterpret_cast<const uint32_t *>(&d);
@@ -166,10 +205,17 @@ struct W4Meta {
             return (j & 1) ? __high2float(h) : __low2float(h);
         }
     }
-    // z twice in the low bits of two halves.
-    __device__ __forceinline__ uint32_t zero(int j) const {
-        if constexpr (!ZEROS) return 0x00080008u;
-        else return ((z[j / 4] >> (8 * (j & 3))) & 15u) * 0x10001u;
+    template <bool ANY>
+    __device__ __forceinline__ W4Zero zero(const W4Unpack<TYPE != 1> &unpack, int j) const {
+        if constexpr (!ZEROS) return unpack.eight();
+        else return w4_zero<TYPE != 1, ANY>(z[j / 4], j & 3, unpack.magic);
+    }
+    // Whether a zero point is above 127.
+    __device__ __forceinline__ bool high() const {
+        uint32_t any = 0;
+#pragma unroll
+        for (int i = 0; i < (N + 3) / 4; ++i) any |= z[i];
+        return (any & 0x80808080u) != 0;
     }
 };
 
@@ -403,33 +449,38 @@ lm_w4_kernel(const __grid_constant__ CUtensorMap tmQ, const W4Args p) {
             __syncwarp();
             issue();
             // Past the end of K the words are 0 and x is 0: they add nothing.
-            float c[NB][4];
+            auto multiply = [&](auto any) {
+                float c[NB][4];
 #pragma unroll
-            for (int w = 0; w < 8; ++w) {
-                const int j = w / SLOTS;
-                const bool first = w % SLOTS == 0;
-                const uint32_t z0 = ma.zero(j), z1 = mb.zero(j);
-                uint32_t a[4], d[4];
-                unpack(wa[w], z0 | (BF16 ? 0x43004300u : 0x64006400u), (z0 << 4) | 0x54005400u, a);
-                unpack(wb[w], z1 | (BF16 ? 0x43004300u : 0x64006400u), (z1 << 4) | 0x54005400u, d);
-#pragma unroll
-                for (int n = 0; n < NB; ++n) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(x_lane[n] + s * 512 + w * 64);
-                    if (first) mma16816<BF16>(c[n], a[0], d[0], a[1], d[1], x.x, x.y, 0.f, 0.f, 0.f, 0.f);
-                    else mma16816<BF16>(c[n], a[0], d[0], a[1], d[1], x.x, x.y, c[n][0], c[n][1], c[n][2], c[n][3]);
-                    mma16816<BF16>(c[n], a[2], d[2], a[3], d[3], x.z, x.w, c[n][0], c[n][1], c[n][2], c[n][3]);
-                }
-                if (w % SLOTS == SLOTS - 1) {
-                    const float f0 = ma.scale(j), f1 = mb.scale(j);
+                for (int w = 0; w < 8; ++w) {
+                    const int j = w / SLOTS;
+                    const bool first = w % SLOTS == 0;
+                    uint32_t a[4], d[4];
+                    unpack(wa[w], ma.template zero<decltype(any)::value>(unpack, j), a);
+                    unpack(wb[w], mb.template zero<decltype(any)::value>(unpack, j), d);
 #pragma unroll
                     for (int n = 0; n < NB; ++n) {
-                        sum[n][0] = fmaf(f0, c[n][0], sum[n][0]);
-                        sum[n][1] = fmaf(f0, c[n][1], sum[n][1]);
-                        sum[n][2] = fmaf(f1, c[n][2], sum[n][2]);
-                        sum[n][3] = fmaf(f1, c[n][3], sum[n][3]);
+                        const uint4 x = *reinterpret_cast<const uint4 *>(x_lane[n] + s * 512 + w * 64);
+                        if (first) mma16816<BF16>(c[n], a[0], d[0], a[1], d[1], x.x, x.y, 0.f, 0.f, 0.f, 0.f);
+                        else mma16816<BF16>(c[n], a[0], d[0], a[1], d[1], x.x, x.y, c[n][0], c[n][1], c[n][2], c[n][3]);
+                        mma16816<BF16>(c[n], a[2], d[2], a[3], d[3], x.z, x.w, c[n][0], c[n][1], c[n][2], c[n][3]);
+                    }
+                    if (w % SLOTS == SLOTS - 1) {
+                        const float f0 = ma.scale(j), f1 = mb.scale(j);
+#pragma unroll
+                        for (int n = 0; n < NB; ++n) {
+                            sum[n][0] = fmaf(f0, c[n][0], sum[n][0]);
+                            sum[n][1] = fmaf(f0, c[n][1], sum[n][1]);
+                            sum[n][2] = fmaf(f1, c[n][2], sum[n][2]);
+                            sum[n][3] = fmaf(f1, c[n][3], sum[n][3]);
+                        }
                     }
                 }
-            }
+            };
+            bool high = false;
+            if constexpr (ZEROS && BF16) high = __any_sync(~0u, ma.high() || mb.high());
+            if (ZEROS && BF16 && high) multiply(std::true_type());
+            else multiply(std::false_type());
         }
         // Join the warps' sums (two buffers: a warp may be one block ahead).
         float *buf = red + (b & 1) * (WARPS * NB * 128);

@@ -164,8 +164,8 @@ sgemmStatus_t sgemmCrossEntropyGradWorkspaceSize(sgemmHandle_t handle, sgemmData
  * the weights are N x K (one row per output column), two to a byte along K:
  * Q is N rows of K / 2 bytes (pitch ldq BYTES), column 2 i in the low four
  * bits of byte i, column 2 i + 1 in the high four.  Each row has a scale (of
- * the call's type; pitch lds) and, if `zeros` is not NULL, a zero point (a
- * byte, its low four bits; pitch ldz; otherwise 8) for every `group` columns:
+ * the call's type; pitch lds) and, if `zeros` is not NULL, a zero point (any
+ * byte, 0 to 255; pitch ldz; otherwise 8) for every `group` columns:
  *
  *   Y[t, n] = sum_k scales[n, k / group] * (q[n, k] - zeros[n, k / group]) * X[t, k]
  *
