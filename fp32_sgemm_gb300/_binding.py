@@ -212,7 +212,6 @@ class Handle:
             _check(self._lib.sgemmCreate(ctypes.byref(self._h)), "sgemmCreate")
         self._ws = None
         self.address = self._h.value or 0      # the C handle, as a number
-        self.workspace_bytes = 0
         # Workspace sizes already asked for, by shape, pitches and operand
         # alignment; the handle's settings enter the size, so their setters
         # clear it.
@@ -227,7 +226,7 @@ class Handle:
             self._lib.sgemmDestroy(self._h)
             self._h = _vp()
             self._ws = None
-            self.address = self.workspace_bytes = 0
+            self.address = 0
 
     def __del__(self):
         try:
@@ -294,7 +293,6 @@ class Handle:
             self._ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
             _check(self._lib.sgemmSetWorkspace(self._h, self._ws.data_ptr(), self._ws.numel()),
                    "sgemmSetWorkspace")
-            self.workspace_bytes = nbytes
 
     def plan(self, A, B, C, alpha=1.0, beta=0.0) -> dict:
         M, K = A.shape

@@ -4,7 +4,11 @@ include/sgemm_gb300_lm.h.
 Every function takes float32, float16 or bfloat16 CUDA tensors (the same type
 for all matrices of a call) with any row pitch (stride(-1) == 1), enqueues its
 work on torch's current stream (or `stream`) and returns new tensors unless
-`out` is given.  The checks and the calls are in csrc/lm_binding.cpp.
+`out` is given.  A call's workspace comes from torch's allocator and is its
+own, so calls on several streams or from several threads need no handles of
+their own, and calls can be captured with torch.cuda.graph; a `handle` (the
+device's default one otherwise) carries the wait limit and the error word.
+The checks and the calls are in csrc/lm_binding.cpp.
 """
 
 from __future__ import annotations
