@@ -47,20 +47,28 @@ __device__ __forceinline__ bool keeps(const LmCopyFilter &f, int64_t row) {
     return t >= 0 && t < f.vocab && f.grad[row] != 0.f;
 }
 
-// x = p0 + p1 + p2 exactly: the leading 8, the next 8 and the last 8 bits of
-// its significand (each plane truncated, so that the rest keeps x's sign and
-// p0 never rounds up to infinity).  Values that are not finite stay in p0.
+// x = p0 + p1 + p2, each plane the bf16 nearest to what the ones before it
+// leave: |p1| <= 2^-8 and |p2| <= 2^-17 of x's leading bit, so that the plane
+// products left out of a product are below 2^-23.9 of it, with either sign.
+// (Truncated planes leave up to 2^-21, always on the product's side of zero.)
+// The sum is exact for |x| >= 2^-110; below, p2 meets bf16's smallest step,
+// 2^-133.  x that would round up to infinity has its p0 truncated.  Values
+// that are not finite stay in p0.
+__device__ __forceinline__ float bf16_bits(float x, uint16_t &bits) {
+    const __nv_bfloat16 h = __float2bfloat16_rn(x);
+    bits = *reinterpret_cast<const uint16_t *>(&h);
+    return __uint_as_float((uint32_t)bits << 16);
+}
 __device__ __forceinline__ void split3(float x, uint16_t &a, uint16_t &b, uint16_t &c) {
     const uint32_t u = __float_as_uint(x);
-    // A NaN whose payload lies in the low bits must stay a NaN.
-    const bool odd = (u & 0x7F800000u) == 0x7F800000u;
-    const uint32_t h = odd && (u & 0x7FFFFFu) ? 0x7FC00000u : u & 0xFFFF0000u;
-    const float r1 = odd ? 0.f : x - __uint_as_float(h);
-    const uint32_t m = __float_as_uint(r1) & 0xFFFF0000u;
-    const float r2 = r1 - __uint_as_float(m);
-    a = (uint16_t)(h >> 16);
-    b = (uint16_t)(m >> 16);
-    c = (uint16_t)(__float_as_uint(r2) >> 16);
+    const bool finite = (u & 0x7F800000u) != 0x7F800000u;
+    float h = bf16_bits(x, a);
+    if (finite && (a & 0x7F80u) == 0x7F80u) {
+        a = (uint16_t)(u >> 16);
+        h = __uint_as_float(u & 0xFFFF0000u);
+    }
+    const float r = finite ? x - h : 0.f;
+    bf16_bits(r - bf16_bits(r, b), c);
 }
 
 __device__ __forceinline__ void load16(const void *p, uint32_t *w) {

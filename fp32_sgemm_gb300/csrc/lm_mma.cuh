@@ -320,7 +320,7 @@ __device__ __forceinline__ void lm_order_groups(const LmArgs &p, const int *star
 }
 
 // A product of FP32 operands, each held as three bf16 planes (x = p0 + p1 +
-// p2 exactly): stage i of a block of 64 holds plane i of both, and p_i q_j
+// p2, lm_aux.cu): stage i of a block of 64 holds plane i of both, and p_i q_j
 // with i + j <= 2 are multiplied, smallest first.
 __device__ constexpr int plane_a(int pr) { return (0x046 >> (2 * pr)) & 3; }     // 2 1 0 1 0 0
 __device__ constexpr int plane_b(int pr) { return (0x124 >> (2 * pr)) & 3; }     // 0 1 2 0 1 0

@@ -18,7 +18,7 @@
 //     nibbles come out; which word a lane takes is chosen so that it reads
 //     as many neighbouring words at once as the group allows (16, 8 or 4
 //     bytes for groups of 128, 64, 32);
-//   * FP32 x is held as three bf16 planes (exactly), as three tokens.
+//   * FP32 x is held as three bf16 planes (exactly for |x| >= 2^-110), as three tokens.
 // The warps of a CTA share 16 rows and split K; their sums are joined in a
 // fixed order through shared memory.
 //

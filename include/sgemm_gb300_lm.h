@@ -59,9 +59,11 @@ typedef enum sgemmDataType {
  * F16 and BF16 products run on the tensor cores with FP32 sums.  F32
  * products of up to 8 rows a group in the mean (T / G) and K >= 256 are
  * FP32 multiply-adds.  For the others F32 operands are split into three bf16
- * planes each (x = p0 + p1 + p2 exactly) in the workspace and multiplied as the six products p_i q_j, i + j <= 2,
- * with FP32 sums of 64-long pieces; the planes left out are below 2^-23 of
- * a product.  There infinite F32 inputs give NaN or infinity.
+ * planes each in the workspace (x = p0 + p1 + p2, each plane the nearest to
+ * what is left; exact for |x| >= 2^-110) and multiplied as the six products
+ * p_i q_j, i + j <= 2, with FP32 sums of 64-long pieces; the plane products
+ * left out are below 2^-23 of a product, with either sign (2^-22 if a factor
+ * is above 3.38e38).  There infinite F32 inputs give NaN or infinity.
  *
  * INVALID_VALUE: negative sizes, a pitch below the row length, strideB
  * below one matrix when G > 1, unknown type or op, NULL pointers with
@@ -171,7 +173,7 @@ sgemmStatus_t sgemmCrossEntropyGradWorkspaceSize(sgemmHandle_t handle, sgemmData
  *
  * group is 32, 64 or 128 and divides K.  q - zero meets X unrounded and
  * unscaled, the scale is applied to each group's FP32 sum; F32 X is split
- * into three bf16 planes (exactly).  One pass over the weights serves up to
+ * into three bf16 planes (exactly for |x| >= 2^-110).  One pass over the weights serves up to
  * 32 rows (F32: 10); more rows take further passes.
  *
  * INVALID_VALUE, NOT_SUPPORTED as above, also for another group or a K it
