@@ -994,6 +994,7 @@ sgemmStatus_t sgemmW4(sgemmHandle_t h, sgemmDataType_t type, int64_t M, int64_t 
         cfg.numAttrs = 1;
         p.err = h->d_err;
         p.timeout_ns = h->timeout_ns;
+        p.withhold = h->withhold;
         void *kargs[] = {&tm_q, &p};
         if (cudaLaunchKernelExC(&cfg, k.fn, kargs) != cudaSuccess) return SGEMM_STATUS_LAUNCH_FAILED;
         if (q.slices > 1 &&

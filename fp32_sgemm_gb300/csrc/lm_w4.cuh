@@ -414,10 +414,7 @@ lm_w4_kernel(const __grid_constant__ CUtensorMap tmQ, const W4Args p) {
                 point_meta(row0 + (slots << 4));
                 load_meta(0);
             }
-            if (ok && !mbar_wait_bounded(&full[stage], phase, p.timeout_ns)) {
-                record_error(p.err, kSiteConsumerFull);
-                ok = false;
-            }
+            const bool landed = ok && mbar_wait_bounded(&full[stage], phase, p.timeout_ns);
             const unsigned char *st = ring_w + stage * 2048 + g * 128;
             uint32_t wa[8], wb[8];
             if constexpr (GROUP == 128) {
@@ -445,9 +442,17 @@ lm_w4_kernel(const __grid_constant__ CUtensorMap tmQ, const W4Args p) {
                     wb[h] = *reinterpret_cast<const uint32_t *>(st + 1024 + at);
                 }
             }
-            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
             __syncwarp();
-            issue();
+            // One answer for the warp: where a wait ran out no copy may be issued
+            // into a stage that has one in flight.  (Asked for behind the reads:
+            // 28672 x 8192, one row, 26.8 us, ahead of them 27.5.)
+            if (__all_sync(~0u, landed)) {
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                if (p.withhold != kWithholdRefill) issue();
+            } else {
+                if (ok && lane == 0) record_error(p.err, kSiteConsumerFull);
+                ok = false;
+            }
             // Past the end of K the words are 0 and x is 0: they add nothing.
             auto multiply = [&](auto any) {
                 float c[NB][4];
@@ -520,6 +525,13 @@ lm_w4_kernel(const __grid_constant__ CUtensorMap tmQ, const W4Args p) {
             }
         }
     }
+    // After a wait ran out: the copies still in flight (the stage waited for and
+    // those issued behind it) have to land before the CTA may exit.
+    if (!ok)
+        while (stage != ld_stage) {
+            mbar_wait_bounded(&full[stage], phase, p.timeout_ns);
+            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
 }
 
 template <int TYPE, int GROUP, bool ZEROS>

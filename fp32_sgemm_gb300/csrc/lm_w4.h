@@ -26,6 +26,7 @@ struct W4Args {
     int64_t ld_part;
     uint32_t *err;
     uint64_t timeout_ns;
+    int withhold;
 };
 
 // nb: blocks of 8 columns (1, 2 or 4); alone: one CTA has an SM for itself.
