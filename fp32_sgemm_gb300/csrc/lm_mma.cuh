@@ -427,16 +427,32 @@ __device__ __forceinline__ void lm_store_cols(const LmArgs &p, Out *base, int f0
     }
 }
 
+// A wait that lasts as long as work that goes on (the whole contraction of a
+// tile, or tiles without a tail): its limit starts anew while this SM's
+// producer issues copies, and it gives up when none was issued for as long as
+// the limit.  `issued` only grows, and only as far as there are stages to fill.
+// (A fixed limit ran out in correct calls: 1000001 rows in one group, 1 ms.)
+template <bool CLUSTER>
+__device__ __forceinline__ bool lm_wait_working(uint64_t *bar, uint32_t parity, uint64_t limit,
+                                                const volatile uint32_t *issued) {
+    uint32_t seen = *issued;
+    while (!mbar_wait_bounded<CLUSTER>(bar, parity, limit)) {
+        const uint32_t now = *issued;
+        if (now == seen) return false;
+        seen = now;
+    }
+    return true;
+}
+
 // kRagK, a group's last block of rows: once this SM's copies have landed,
 // the warp clears the rows behind the group (they belong to others) up to the
 // next multiple of 16, where the MMAs stop; both operands, so that an
 // infinity there does not meet a zero.  False if the copies did not land.
 template <class Tile>
 __device__ __forceinline__ bool lm_clear_tail(unsigned char *stage, uint64_t *landed, uint32_t parity, int rows,
-                                              const LmArgs &p, int lane) {
-    // The copies wait for a free stage, that for earlier products: the limit
-    // of a wait behind two others.
-    bool ok = mbar_wait_bounded(landed, parity, 2 * downstream_limit(p.timeout_ns));
+                                              const LmArgs &p, const volatile uint32_t *issued, int lane) {
+    // (All tiles since the last tail lie between: those of other groups too.)
+    bool ok = lm_wait_working<false>(landed, parity, downstream_limit(p.timeout_ns), issued);
     if (!ok && lane == 0) record_error(p.err, kSiteConsumerFull);
     ok = __all_sync(~0u, ok);
     const int r1 = (rows + 15) & ~15, per = (r1 - rows) * 8;      // 16-byte words per chunk of 64 columns
@@ -482,6 +498,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     uint64_t *drain = tempty + 2;           // MMA completion before teardown
     uint64_t *tailbar = drain + 1;          // kRagK, per stage: this SM's copies of a group's last block
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Tile::BARS);
+    volatile uint32_t *progress = tmem_slot + 1;    // stages the producer has issued
     unsigned char *after = reinterpret_cast<unsigned char *>(bars) + ((Tile::BARS * 8 + 16 + 15) / 16) * 16;
     float *staging = reinterpret_cast<float *>(after);
     int *g_start = reinterpret_cast<int *>(after + Tile::STAGING);
@@ -507,6 +524,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             mbar_init(&tempty[b], (PAIR ? 2 : 1) * Tile::EPI_WARPS);
         }
         mbar_init(drain, 1);
+        *progress = 0;
         fence_barrier_init();
         prefetch_tensormap(&tmA);
         prefetch_tensormap(&tmB);
@@ -604,6 +622,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                         __syncwarp();
                     }
                     ++issued;
+                    if (lane == 0) *progress = (uint32_t)issued;
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
             }
@@ -762,7 +781,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             stage = (stage + (w.nkb - (tail ? 1 : 0)) * PLANES) % STAGES;
             for (int pl = 0; tail && ok && pl < PLANES; ++pl) {
                 ok = lm_clear_tail<Tile>(smem + stage * Tile::STAGE_BYTES, &tailbar[stage], (phases >> stage) & 1u,
-                                         w.klast, p, lane);
+                                         w.klast, p, progress, lane);
                 phases ^= 1u << stage;
                 if (ok && lane == 0) {
                     if (rank == 0) mbar_arrive(&full[stage]);
@@ -786,11 +805,9 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             float sum[CHUNKED ? SLAB : 1];
             uint32_t taddr = 0;
             auto wait_acc = [&]() {
-                if (!mbar_wait_bounded<PAIR>(&tfull[gc & 1], (uint32_t)(gc >> 1) & 1u, downstream_limit(p.timeout_ns))) {
-                    record_error(p.err, kSiteConsumerFull);
-                    ok = false;
-                }
-                ok = __all_sync(~0u, ok);
+                ok = __all_sync(~0u, lm_wait_working<PAIR>(&tfull[gc & 1], (uint32_t)(gc >> 1) & 1u,
+                                                           downstream_limit(p.timeout_ns), progress));
+                if (!ok && lane == 0) record_error(p.err, kSiteConsumerFull);
                 tc_fence_after();
                 taddr = lane_base + (uint32_t)((gc & 1) * BN + slab0);
             };
