@@ -538,6 +538,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         lm_order_groups(p, g_start, g_prefix);
     }
     tc_fence_before();
+    __syncwarp();               // (the barriers, too, take whole warps)
     if constexpr (PAIR) cluster_sync();
     else __syncthreads();
     tc_fence_after();
@@ -962,6 +963,9 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                         else
                             lm_store_rows(p, static_cast<__nv_bfloat16 *>(p.C) + z, row, row0, n, cnt, v, stg, lane);
                     }
+                    // Lanes without a row or column to store come back early; the
+                    // next load from tensor memory takes the warp together.
+                    __syncwarp();
                 }
             }
             if constexpr (EPI == kEpiLse) {
@@ -975,6 +979,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
 
     // ---------------- teardown ----------------
     tc_fence_before();
+    __syncwarp();               // (the barriers, too, take whole warps)
     if constexpr (PAIR) cluster_sync();
     else __syncthreads();
     tc_fence_after();
