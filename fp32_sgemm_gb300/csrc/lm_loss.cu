@@ -9,13 +9,13 @@ LmKernel lm_rows_kernel32(bool big, bool a_mn);
 
 LmKernel lm_lse_kernel(bool big, bool f32) {
     if (f32) return lm_lse_kernel32(big);
-    if (big) return lm_kernel_info<LmBigLse, false, false, kRagNone, kEpiLse, kRuns>();
+    if (big) return lm_kernel_info<LmBigBare, false, false, kRagNone, kEpiLse, kRuns>();
     return lm_kernel_info<LmWide, false, false, kRagNone, kEpiLse, kRuns>();
 }
 LmKernel lm_dlogits_kernel(bool big, bool f32) {
     if (f32) return lm_dlogits_kernel32(big);
-    if (big) return lm_kernel_info<LmBig, false, false, kRagNone, kEpiDLogits, kPlain>();
-    return lm_kernel_info<LmWide, false, false, kRagNone, kEpiDLogits, kPlain>();
+    if (big) return lm_kernel_info<LmBigBare, false, false, kRagNone, kEpiDLogits, kRuns>();
+    return lm_kernel_info<LmWide, false, false, kRagNone, kEpiDLogits, kRuns>();
 }
 LmKernel lm_rows_kernel(bool big, bool a_mn, bool f32) {
     if (f32) return lm_rows_kernel32(big, a_mn);

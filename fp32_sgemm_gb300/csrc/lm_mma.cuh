@@ -327,11 +327,12 @@ __device__ constexpr int plane_b(int pr) { return (0x124 >> (2 * pr)) & 3; }    
 
 // -------------------------------------------------------------- epilogues
 
-// 32 columns of this lane's row of D, as a piece of a row-major matrix.
-template <class Out>
+// 32 columns of this lane's row of D, as a piece of a row-major matrix (VEC: of
+// one whose rows always take vector stores).
+template <bool VEC, class Out>
 __device__ __forceinline__ void lm_store_rows(const LmArgs &p, Out *base, int row, int row0, int col, int cnt,
                                               const float (&v)[32], float *stg, int lane) {
-    if (p.vec) {
+    if (VEC || p.vec) {
         if (row >= p.M) return;
         Out *c = base + (int64_t)row * p.ldc + col;
         if (cnt == 32) {
@@ -846,8 +847,11 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 // FP32 operands: one block (two doubled the error, at 40003
                 // terms to 2^-20 of their magnitudes).  Logits of 16-bit
                 // operands: sixteen (losses at 2944 terms off by 4e-7 of
-                // themselves, 2e-7 with eight, which took 15% longer, and
-                // 1.7e-6 with one sum).
+                // themselves, 2e-7 with eight, and 1.7e-6 with one sum), in the
+                // gradient as in the loss: against an lse from other sums all
+                // probabilities are off the same way, by 2% at logits of 2330
+                // (8192 rows, 131072 x 4096, both passes: 20.6 ms with one sum
+                // there, 21.0 so).
 #pragma unroll
                 for (int c = 0; c < SLAB; ++c) sum[c] = 0.f;
                 for (int kb = 0; ok && kb < w.nkb; kb += CH) {
@@ -944,7 +948,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                             for (int i = 0; i < 32; ++i) v[i] *= alpha;
                         }
                         const int64_t z = (int64_t)(RAG == kRagK ? w.g : w.s) * p.stride_c;
-                        if (EPI == kEpiDLogits && !PAIR && p.lo != nullptr) {
+                        if (EPI == kEpiDLogits && MODE != kPlanes && !PAIR && p.lo != nullptr) {
                             // What the rounding to 16 bits leaves, in a plane of its own.
                             float rest[32];
 #pragma unroll
@@ -952,16 +956,17 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                                 rest[i] = v[i] - (p.out == kOutF16 ? __half2float(__float2half_rn(v[i]))
                                                                    : __bfloat162float(__float2bfloat16_rn(v[i])));
                             if (p.out == kOutF16)
-                                lm_store_rows(p, static_cast<__half *>(p.lo), row, row0, n, cnt, rest, stg, lane);
+                                lm_store_rows<true>(p, static_cast<__half *>(p.lo), row, row0, n, cnt, rest, stg, lane);
                             else
-                                lm_store_rows(p, static_cast<__nv_bfloat16 *>(p.lo), row, row0, n, cnt, rest, stg, lane);
+                                lm_store_rows<true>(p, static_cast<__nv_bfloat16 *>(p.lo), row, row0, n, cnt, rest, stg, lane);
                         }
-                        if (p.out == kOutF32)
-                            lm_store_rows(p, static_cast<float *>(p.C) + z, row, row0, n, cnt, v, stg, lane);
+                        // (d has the operands' type.)
+                        if (EPI == kEpiDLogits ? MODE == kPlanes : p.out == kOutF32)
+                            lm_store_rows<EPI == kEpiDLogits>(p, static_cast<float *>(p.C) + z, row, row0, n, cnt, v, stg, lane);
                         else if (p.out == kOutF16)
-                            lm_store_rows(p, static_cast<__half *>(p.C) + z, row, row0, n, cnt, v, stg, lane);
+                            lm_store_rows<EPI == kEpiDLogits>(p, static_cast<__half *>(p.C) + z, row, row0, n, cnt, v, stg, lane);
                         else
-                            lm_store_rows(p, static_cast<__nv_bfloat16 *>(p.C) + z, row, row0, n, cnt, v, stg, lane);
+                            lm_store_rows<EPI == kEpiDLogits>(p, static_cast<__nv_bfloat16 *>(p.C) + z, row, row0, n, cnt, v, stg, lane);
                     }
                     // Lanes without a row or column to store come back early; the
                     // next load from tensor memory takes the warp together.
@@ -1007,7 +1012,7 @@ LmKernel lm_kernel_info() {
 }
 
 using LmBig = LmTile<256, 6, true>;      // 256 x 256 on an SM pair
-using LmBigLse = LmTile<256, 7, true, 0>;
+using LmBigBare = LmTile<256, 7, true, 0>;   // for epilogues without staging
 using LmMid = LmTile<128, 6, false>;     // 128 x 128
 using LmWide = LmTile<256, 4, false>;    // 128 x 256, for few rows against a long matrix
 using LmThin = LmTile<32, 10, false>;    // 128 x 32, for few tokens

@@ -135,6 +135,8 @@ sgemmStatus_t sgemmCrossEntropyWorkspaceSize(sgemmHandle_t handle, sgemmDataType
  *   d[t, v] = dloss[t] * (exp(X[t, :] . W[v, :] - lse[t]) - [v == target[t]])
  *   dX = d . W        dW = d^T . X
  *
+ * with the logits summed as in sgemmCrossEntropy(), so that a row's
+ * probabilities add up to one,
  * in pieces of the vocabulary: d is computed for one piece at a time (512 MB
  * at most, or 2048 columns) and both products over the piece follow; dX is
  * summed over the pieces in FP32.  How d is held:
