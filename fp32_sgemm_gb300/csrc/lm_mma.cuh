@@ -469,7 +469,7 @@ __device__ __forceinline__ bool lm_clear_tail(unsigned char *stage, uint64_t *la
 }
 
 // MODE of a kernel: 16-bit operands in one running sum; the same in runs of
-// sixteen blocks; FP32 operands in three planes, summed block by block.
+// eight blocks; FP32 operands in three planes, summed block by block.
 constexpr int kPlain = 0, kRuns = 1, kPlanes = 3;
 
 // ---------------------------------------------------------------- kernel
@@ -484,7 +484,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     constexpr bool PAIR = Tile::PAIR;
     constexpr int BN = Tile::BN, STAGES = Tile::STAGES, SLAB = Tile::SLAB;
     constexpr bool CHUNKED = MODE != kPlain;
-    constexpr int PLANES = MODE == kPlanes ? 3 : 1, CH = MODE == kRuns ? 16 : 1;
+    constexpr int PLANES = MODE == kPlanes ? 3 : 1, CH = MODE == kRuns ? 8 : 1;
     static_assert((CH & (CH - 1)) == 0, "");
     static_assert(!B_MN || Tile::B_ROWS % 64 == 0, "MN-major B is staged in chunks of 64 columns");
 
@@ -846,12 +846,12 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 // to nearest (the tensor core's own running sum truncates).
                 // FP32 operands: one block (two doubled the error, at 40003
                 // terms to 2^-20 of their magnitudes).  Logits of 16-bit
-                // operands: sixteen (losses at 2944 terms off by 4e-7 of
-                // themselves, 2e-7 with eight, and 1.7e-6 with one sum), in the
-                // gradient as in the loss: against an lse from other sums all
-                // probabilities are off the same way, by 2% at logits of 2330
-                // (8192 rows, 131072 x 4096, both passes: 20.6 ms with one sum
-                // there, 21.0 so).
+                // operands: eight (losses at 4096 terms off by 1.5 to 2e-7 of
+                // themselves, about a unit in the last place, twice that with
+                // sixteen, 1.7e-6 with one sum; loss and gradients of 8192 rows,
+                // 131072 x 4096, 21.8 ms, with sixteen 21.0), in the gradient as
+                // in the loss: against an lse from other sums all probabilities
+                // are off the same way, by 2% at logits of 2330.
 #pragma unroll
                 for (int c = 0; c < SLAB; ++c) sum[c] = 0.f;
                 for (int kb = 0; ok && kb < w.nkb; kb += CH) {

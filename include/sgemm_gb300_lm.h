@@ -116,7 +116,7 @@ sgemmStatus_t sgemmGroupedWeightGradWorkspaceSize(sgemmHandle_t handle, sgemmDat
  * computed, and the partial results are joined in a fixed order.  A target
  * outside [0, V) marks a token that is not counted: its loss is 0 (its lse
  * is computed).  loss and lse are FP32 in every type.  Arithmetic of the
- * products as for sgemmGrouped(), 16-bit ones here in sums of 1024 terms of
+ * products as for sgemmGrouped(), 16-bit ones here in sums of 512 terms of
  * the contraction, added in FP32.  INVALID_VALUE also for V < 1 or D < 1;
  * T == 0 is a no-op.  A workspace is always required (the partial results).
  */
@@ -135,11 +135,11 @@ sgemmStatus_t sgemmCrossEntropyWorkspaceSize(sgemmHandle_t handle, sgemmDataType
  *   d[t, v] = dloss[t] * (exp(X[t, :] . W[v, :] - lse[t]) - [v == target[t]])
  *   dX = d . W        dW = d^T . X
  *
- * with the logits summed as in sgemmCrossEntropy(), so that a row's
- * probabilities add up to one,
- * in pieces of the vocabulary: d is computed for one piece at a time (512 MB
- * at most, or 2048 columns) and both products over the piece follow; dX is
- * summed over the pieces in FP32.  How d is held:
+ * The logits are summed as in sgemmCrossEntropy(), so that a row's
+ * probabilities add up to one.  The vocabulary is taken in pieces: d is
+ * computed for one piece at a time (512 MB at most, or 2048 columns) and both
+ * products over the piece follow; dX is summed over the pieces in FP32.  How d
+ * is held:
  *   F32              FP32, then three bf16 planes;
  *   up to 128 rows   two planes of the call's type, d and what its rounding
  *                    left (16 bits and more of significand);
