@@ -51,6 +51,13 @@ class Plan(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
+class GroupedPlan(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int) for name in ("kernel", "tile_m", "tile_n", "splits", "copies_a", "copies_b")]
+
+    def as_dict(self) -> dict:
+        return {name: getattr(self, name) for name, _ in self._fields_}
+
+
 # name -> (restype, argtypes); must list every function of include/*.h
 SIGNATURES = {
     "sgemmGetStatusString": (ctypes.c_char_p, [_st]),
@@ -90,6 +97,10 @@ SIGNATURES = {
                            _i64, _vp, _vp, _i64, _vp]),
     "sgemmGroupedWorkspaceSize": (_st, [_vp, ctypes.c_int, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, _i64,
                                         _vp, _i64, _i64, ctypes.POINTER(ctypes.c_size_t)]),
+    "sgemmGroupedQueryPlan": (_st, [_vp, ctypes.c_int, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, _i64, _vp,
+                                    _i64, _i64, ctypes.POINTER(GroupedPlan)]),
+    "sgemmGroupedWeightGradQueryPlan": (_st, [_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64,
+                                              ctypes.POINTER(GroupedPlan)]),
     "sgemmGroupedWeightGrad": (_st, [_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp,
                                      _vp, _i64, _i64, _vp]),
     "sgemmGroupedWeightGradWorkspaceSize": (_st, [_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, _i64,

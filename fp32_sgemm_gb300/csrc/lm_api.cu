@@ -302,6 +302,14 @@ sgemmStatus_t plan_grouped(int type, int op, int64_t T, int64_t N, int64_t K, in
     return SGEMM_STATUS_SUCCESS;
 }
 
+// Weight gradients: pairs' tiles unless most pairs would have none (8 groups of
+// 512 rows, BF16, 128 x 128 / 256 x 256: 512 x 512 7.7 / 9.6 us, 768 x 768 10.3 /
+// 10.3, 1024 x 1024 15.8 / 14.1).
+int weight_grad_size(int64_t M, int64_t N, int64_t G, int sms) {
+    const bool fills = 3 * ceil_div(M, 256) * ceil_div(N, 256) * G >= sms;
+    return M > 128 && N > 128 && fills ? 2 : 1;
+}
+
 struct WeightGrad {
     int type = 0;
     int64_t T = 0, M = 0, N = 0, G = 0;
@@ -516,6 +524,35 @@ sgemmStatus_t sgemmGroupedWorkspaceSize(sgemmHandle_t h, sgemmDataType_t type, s
     return SGEMM_STATUS_SUCCESS;
 }
 
+sgemmStatus_t sgemmGroupedQueryPlan(sgemmHandle_t h, sgemmDataType_t type, sgemmOperation_t opB, int64_t T, int64_t N,
+                                    int64_t K, int64_t G, const void *A, int64_t lda, const void *B, int64_t ldb,
+                                    int64_t strideB, sgemmGroupedPlan_t *plan) {
+    if (plan == nullptr) return SGEMM_STATUS_INVALID_VALUE;
+    *plan = sgemmGroupedPlan_t{};
+    Grouped q;
+    sgemmStatus_t st = plan_grouped(type, opB, T, N, K, G, A, lda, B, ldb, strideB, q);
+    if (st != SGEMM_STATUS_SUCCESS) return st;
+    if (h == nullptr) return SGEMM_STATUS_INVALID_VALUE;
+    if (T == 0 || N == 0 || K == 0 || G == 0) return SGEMM_STATUS_SUCCESS;
+    plan->splits = 1;
+    if (q.rows32) {
+        const LmKernel k = sg::lm_rows32_kernel_info(opB == SGEMM_OP_T, false);
+        plan->kernel = 1;
+        plan->tile_m = k.bn;
+        plan->tile_n = k.tile_m;
+        return SGEMM_STATUS_SUCCESS;
+    }
+    q.tile(h->sm_count);
+    const LmKernel k = sg::lm_grouped_kernel(q.tiling.size, opB == SGEMM_OP_N, type == SGEMM_TYPE_F32);
+    plan->kernel = k.pair ? 3 : 2;
+    plan->tile_m = q.tiling.tile_n;     // (the rows are on the MMA's N side)
+    plan->tile_n = k.tile_m;
+    plan->splits = q.splits;
+    plan->copies_a = q.a.copy;
+    plan->copies_b = q.b.copy;
+    return SGEMM_STATUS_SUCCESS;
+}
+
 sgemmStatus_t sgemmGrouped(sgemmHandle_t h, sgemmDataType_t type, sgemmOperation_t opB, int64_t T, int64_t N,
                            int64_t K, int64_t G, const void *A, int64_t lda, const void *B, int64_t ldb,
                            int64_t strideB, const int32_t *groupEnds, void *C, int64_t ldc, cudaStream_t stream) {
@@ -616,6 +653,26 @@ sgemmStatus_t sgemmGroupedWeightGradWorkspaceSize(sgemmHandle_t h, sgemmDataType
     return SGEMM_STATUS_SUCCESS;
 }
 
+sgemmStatus_t sgemmGroupedWeightGradQueryPlan(sgemmHandle_t h, sgemmDataType_t type, int64_t T, int64_t M, int64_t N,
+                                              int64_t G, const void *A, int64_t lda, const void *B, int64_t ldb,
+                                              sgemmGroupedPlan_t *plan) {
+    if (plan == nullptr) return SGEMM_STATUS_INVALID_VALUE;
+    *plan = sgemmGroupedPlan_t{};
+    WeightGrad q;
+    sgemmStatus_t st = plan_weight_grad(type, T, M, N, G, A, lda, B, ldb, q);
+    if (st != SGEMM_STATUS_SUCCESS) return st;
+    if (h == nullptr) return SGEMM_STATUS_INVALID_VALUE;
+    if (T == 0 || M == 0 || N == 0 || G == 0) return SGEMM_STATUS_SUCCESS;
+    const LmKernel k = sg::lm_weight_grad_kernel(weight_grad_size(M, N, G, h->sm_count), type == SGEMM_TYPE_F32);
+    plan->kernel = k.pair ? 3 : 2;
+    plan->tile_m = k.tile_m;
+    plan->tile_n = k.bn;
+    plan->splits = 1;
+    plan->copies_a = q.a.copy;
+    plan->copies_b = q.b.copy;
+    return SGEMM_STATUS_SUCCESS;
+}
+
 sgemmStatus_t sgemmGroupedWeightGrad(sgemmHandle_t h, sgemmDataType_t type, int64_t T, int64_t M, int64_t N,
                                      int64_t G, const void *A, int64_t lda, const void *B, int64_t ldb,
                                      const int32_t *groupEnds, void *C, int64_t ldc, int64_t strideC,
@@ -647,11 +704,7 @@ sgemmStatus_t sgemmGroupedWeightGrad(sgemmHandle_t h, sgemmDataType_t type, int6
     if (q.a.ws + q.b.ws > 0 && (h->ws == nullptr || h->ws_bytes < q.a.ws + q.b.ws))
         return SGEMM_STATUS_WORKSPACE_REQUIRED;
 
-    // Pairs' tiles unless most would have none (8 groups of 512 rows, BF16, 128
-    // x 128 / 256 x 256: 512 x 512 7.7 / 9.6 us, 768 x 768 10.3 / 10.3, 1024 x
-    // 1024 15.8 / 14.1).
-    const bool fills = 3 * ceil_div(M, 256) * ceil_div(N, 256) * G >= h->sm_count;
-    const int size = M > 128 && N > 128 && fills ? 2 : 1;
+    const int size = weight_grad_size(M, N, G, h->sm_count);
     const LmKernel k = sg::lm_weight_grad_kernel(size, type == SGEMM_TYPE_F32);
     LmArgs p{};
     p.M = int(M);

@@ -83,6 +83,20 @@ sgemmStatus_t sgemmGroupedWorkspaceSize(sgemmHandle_t handle, sgemmDataType_t ty
                                         int64_t N, int64_t K, int64_t G, const void *A, int64_t lda, const void *B,
                                         int64_t ldb, int64_t strideB, size_t *bytes);
 
+/* What sgemmGrouped() or sgemmGroupedWeightGrad() runs for a call of these
+   sizes (nothing is launched). */
+typedef struct sgemmGroupedPlan {
+    int kernel;             /* 0 none (an empty product), 1 FP32 multiply-adds, 2 tensor cores, a tile per SM,
+                               3 tensor cores, a tile per pair of SMs */
+    int tile_m, tile_n;     /* rows and columns of C_g in one tile, at most */
+    int splits;             /* parts the contraction is cut into */
+    int copies_a, copies_b; /* 1 if the operand is copied into the workspace */
+} sgemmGroupedPlan_t;
+
+sgemmStatus_t sgemmGroupedQueryPlan(sgemmHandle_t handle, sgemmDataType_t type, sgemmOperation_t opB, int64_t T,
+                                    int64_t N, int64_t K, int64_t G, const void *A, int64_t lda, const void *B,
+                                    int64_t ldb, int64_t strideB, sgemmGroupedPlan_t *plan);
+
 /*
  * Gradient by the groups' matrices: A is T x M, B is T x N, rows sorted by
  * group as for sgemmGrouped(),
@@ -103,6 +117,10 @@ sgemmStatus_t sgemmGroupedWeightGrad(sgemmHandle_t handle, sgemmDataType_t type,
 sgemmStatus_t sgemmGroupedWeightGradWorkspaceSize(sgemmHandle_t handle, sgemmDataType_t type, int64_t T, int64_t M,
                                                   int64_t N, int64_t G, const void *A, int64_t lda, const void *B,
                                                   int64_t ldb, size_t *bytes);
+
+sgemmStatus_t sgemmGroupedWeightGradQueryPlan(sgemmHandle_t handle, sgemmDataType_t type, int64_t T, int64_t M,
+                                              int64_t N, int64_t G, const void *A, int64_t lda, const void *B,
+                                              int64_t ldb, sgemmGroupedPlan_t *plan);
 
 /*
  * Softmax cross entropy over a vocabulary.  X is T x D (one row per token),
