@@ -270,6 +270,10 @@ struct Grouped {
         ws_part = splits > 1 ? align256(splits * T * ld_part * 4) : 0;
     }
     size_t bytes() const { return a.ws + b.ws + ws_part; }
+    LmKernel kernel() const {
+        return sg::lm_grouped_kernel(tiling.size, op == SGEMM_OP_N, type == SGEMM_TYPE_F32,
+                                     K > splits * sg::kLmPlainTerms);
+    }
 };
 
 sgemmStatus_t plan_grouped(int type, int op, int64_t T, int64_t N, int64_t K, int64_t G, const void *A, int64_t lda,
@@ -302,19 +306,20 @@ sgemmStatus_t plan_grouped(int type, int op, int64_t T, int64_t N, int64_t K, in
     return SGEMM_STATUS_SUCCESS;
 }
 
-// Weight gradients: pairs' tiles unless most pairs would have none (8 groups of
-// 512 rows, BF16, 128 x 128 / 256 x 256: 512 x 512 7.7 / 9.6 us, 768 x 768 10.3 /
-// 10.3, 1024 x 1024 15.8 / 14.1).
-int weight_grad_size(int64_t M, int64_t N, int64_t G, int sms) {
-    const bool fills = 3 * ceil_div(M, 256) * ceil_div(N, 256) * G >= sms;
-    return M > 128 && N > 128 && fills ? 2 : 1;
-}
-
 struct WeightGrad {
     int type = 0;
     int64_t T = 0, M = 0, N = 0, G = 0;
     Operand a, b;
 };
+
+// Pairs' tiles unless most pairs would have none (8 groups of 512 rows, BF16, 128
+// x 128 / 256 x 256: 512 x 512 7.7 / 9.6 us, 768 x 768 10.3 / 10.3, 1024 x 1024
+// 15.8 / 14.1).  Sums in runs where a group may be long: one may have all rows.
+LmKernel weight_grad_kernel(const WeightGrad &q, int sms) {
+    const bool fills = 3 * ceil_div(q.M, 256) * ceil_div(q.N, 256) * q.G >= sms;
+    return sg::lm_weight_grad_kernel(q.M > 128 && q.N > 128 && fills ? 2 : 1, q.type == SGEMM_TYPE_F32,
+                                     q.T > sg::kLmPlainTerms);
+}
 
 sgemmStatus_t plan_weight_grad(int type, int64_t T, int64_t M, int64_t N, int64_t G, const void *A, int64_t lda,
                                const void *B, int64_t ldb, WeightGrad &q) {
@@ -543,7 +548,7 @@ sgemmStatus_t sgemmGroupedQueryPlan(sgemmHandle_t h, sgemmDataType_t type, sgemm
         return SGEMM_STATUS_SUCCESS;
     }
     q.tile(h->sm_count);
-    const LmKernel k = sg::lm_grouped_kernel(q.tiling.size, opB == SGEMM_OP_N, type == SGEMM_TYPE_F32);
+    const LmKernel k = q.kernel();
     plan->kernel = k.pair ? 3 : 2;
     plan->tile_m = q.tiling.tile_n;     // (the rows are on the MMA's N side)
     plan->tile_n = k.tile_m;
@@ -601,7 +606,7 @@ sgemmStatus_t sgemmGrouped(sgemmHandle_t h, sgemmDataType_t type, sgemmOperation
     q.tile(h->sm_count);
     if (q.bytes() > 0 && (h->ws == nullptr || h->ws_bytes < q.bytes())) return SGEMM_STATUS_WORKSPACE_REQUIRED;
 
-    const LmKernel k = sg::lm_grouped_kernel(q.tiling.size, opB == SGEMM_OP_N, type == SGEMM_TYPE_F32);
+    const LmKernel k = q.kernel();
     LmArgs p{};
     p.M = int(N);
     p.T = int(T);
@@ -663,7 +668,7 @@ sgemmStatus_t sgemmGroupedWeightGradQueryPlan(sgemmHandle_t h, sgemmDataType_t t
     if (st != SGEMM_STATUS_SUCCESS) return st;
     if (h == nullptr) return SGEMM_STATUS_INVALID_VALUE;
     if (T == 0 || M == 0 || N == 0 || G == 0) return SGEMM_STATUS_SUCCESS;
-    const LmKernel k = sg::lm_weight_grad_kernel(weight_grad_size(M, N, G, h->sm_count), type == SGEMM_TYPE_F32);
+    const LmKernel k = weight_grad_kernel(q, h->sm_count);
     plan->kernel = k.pair ? 3 : 2;
     plan->tile_m = k.tile_m;
     plan->tile_n = k.bn;
@@ -704,8 +709,7 @@ sgemmStatus_t sgemmGroupedWeightGrad(sgemmHandle_t h, sgemmDataType_t type, int6
     if (q.a.ws + q.b.ws > 0 && (h->ws == nullptr || h->ws_bytes < q.a.ws + q.b.ws))
         return SGEMM_STATUS_WORKSPACE_REQUIRED;
 
-    const int size = weight_grad_size(M, N, G, h->sm_count);
-    const LmKernel k = sg::lm_weight_grad_kernel(size, type == SGEMM_TYPE_F32);
+    const LmKernel k = weight_grad_kernel(q, h->sm_count);
     LmArgs p{};
     p.M = int(M);
     p.N = int(N);
@@ -853,7 +857,9 @@ sgemmStatus_t sgemmCrossEntropyGrad(sgemmHandle_t h, sgemmDataType_t type, int64
     if (!copy_operands(type, x.place(ws, part), q.w.place(ws + x.ws), stream, scale)) return SGEMM_STATUS_LAUNCH_FAILED;
 
     const LmKernel kd = sg::lm_dlogits_kernel(q.big, f32);
-    const LmKernel kx = sg::lm_rows_kernel(q.big, false, f32);
+    // (All pieces are as long as the first, or shorter; d in two planes makes two
+    // terms of each.)
+    const LmKernel kx = sg::lm_rows_kernel(q.big, false, f32, q.piece * q.d_planes > q.splits * sg::kLmPlainTerms);
     CUtensorMap tm_x, tm_w, tm_d, tm_x_mn, tm_w_mn, tm_d_mn;
     if (!x.map(&tm_x, kd.box_a) || !x.map(&tm_x_mn, 64)) return SGEMM_STATUS_LAUNCH_FAILED;
     for (int64_t i = 0; i < q.pieces; ++i) {
@@ -929,7 +935,7 @@ sgemmStatus_t sgemmCrossEntropyGrad(sgemmHandle_t h, sgemmDataType_t type, int64
         // Vocabulary rows' gradient: d^T . X, complete for this piece.  In
         // pairs' tiles even where they are half empty (4096 rows, both
         // gradients of 100 x 1024: 72 us, in tiles of one SM 78).
-        const LmKernel kw = sg::lm_rows_kernel(true, true, f32);
+        const LmKernel kw = sg::lm_rows_kernel(true, true, f32, T * q.d_planes > sg::kLmPlainTerms);
         p = loss_args(q, kw, width, D, T, kw.bn);
         p.kb *= q.d_planes;
         p.C = static_cast<char *>(dW) + v0 * lddw * elem;

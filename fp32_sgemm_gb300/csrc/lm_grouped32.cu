@@ -4,9 +4,10 @@
 
 namespace sg {
 LmKernel lm_grouped_kernel16(int size, bool w_mn);
+LmKernel lm_grouped_kernel_long(int size, bool w_mn);
 
-LmKernel lm_grouped_kernel(int size, bool w_mn, bool f32) {
-    if (!f32) return lm_grouped_kernel16(size, w_mn);
+LmKernel lm_grouped_kernel(int size, bool w_mn, bool f32, bool lengthy) {
+    if (!f32) return lengthy ? lm_grouped_kernel_long(size, w_mn) : lm_grouped_kernel16(size, w_mn);
     if (w_mn) {
         if (size == 0) return lm_kernel_info<LmThin, true, false, kRagN, kEpiCols, kPlanes>();
         if (size == 1) return lm_kernel_info<LmMid, true, false, kRagN, kEpiCols, kPlanes>();

@@ -9,6 +9,10 @@
 namespace sg {
 
 constexpr int kLmMaxGroups = 1024;
+// Terms that one running sum of the tensor core may have: it truncates, so that
+// terms of one sign lose up to 1.7e-7 of the sum for every 16 (f16; 9e-5 of it
+// here, below a quarter of a unit in the last place of any 16-bit result).
+constexpr int64_t kLmPlainTerms = 16384;
 constexpr float kLog2E = 1.4426950408889634f;
 
 // Wait / check site of the error word (bits 24..31) beside those of the
@@ -66,12 +70,13 @@ struct LmRows {
 // tile_m columns by bn rows; few: fewer tiles than SMs.
 LmKernel lm_rows32_kernel_info(bool trans, bool few);
 
-// Kernel tables.  size: 0 thin, 1 middle, 2 big (SM pair).
-LmKernel lm_grouped_kernel(int size, bool w_mn, bool f32);      // lm_grouped*.cu
-LmKernel lm_weight_grad_kernel(int size, bool f32);             // size 1 or 2
+// Kernel tables.  size: 0 thin, 1 middle, 2 big (SM pair); lengthy: 16-bit
+// operands are summed in runs (see kLmPlainTerms).
+LmKernel lm_grouped_kernel(int size, bool w_mn, bool f32, bool lengthy);      // lm_grouped*.cu
+LmKernel lm_weight_grad_kernel(int size, bool f32, bool lengthy);             // size 1 or 2
 LmKernel lm_lse_kernel(bool big, bool f32);                     // lm_loss*.cu
 LmKernel lm_dlogits_kernel(bool big, bool f32);
-LmKernel lm_rows_kernel(bool big, bool a_mn, bool f32);         // B MN-major; MN-major A is big
+LmKernel lm_rows_kernel(bool big, bool a_mn, bool f32, bool lengthy);         // B MN-major; MN-major A is big
 
 // What of an operand a copy needs.  With targets: the rows whose target is an
 // entry of the vocabulary and whose gradient is not zero, the others become

@@ -469,8 +469,9 @@ __device__ __forceinline__ bool lm_clear_tail(unsigned char *stage, uint64_t *la
 }
 
 // MODE of a kernel: 16-bit operands in one running sum; the same in runs of
-// eight blocks; FP32 operands in three planes, summed block by block.
-constexpr int kPlain = 0, kRuns = 1, kPlanes = 3;
+// eight blocks, or, where a contraction may be long, of 128; FP32 operands in
+// three planes, summed block by block.
+constexpr int kPlain = 0, kRuns = 1, kLong = 2, kPlanes = 3;
 
 // ---------------------------------------------------------------- kernel
 
@@ -484,7 +485,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     constexpr bool PAIR = Tile::PAIR;
     constexpr int BN = Tile::BN, STAGES = Tile::STAGES, SLAB = Tile::SLAB;
     constexpr bool CHUNKED = MODE != kPlain;
-    constexpr int PLANES = MODE == kPlanes ? 3 : 1, CH = MODE == kRuns ? 8 : 1;
+    constexpr int PLANES = MODE == kPlanes ? 3 : 1, CH = MODE == kRuns ? 8 : MODE == kLong ? 128 : 1;
     static_assert((CH & (CH - 1)) == 0, "");
     static_assert(!B_MN || Tile::B_ROWS % 64 == 0, "MN-major B is staged in chunks of 64 columns");
 
@@ -851,7 +852,10 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 // sixteen, 1.7e-6 with one sum; loss and gradients of 8192 rows,
                 // 131072 x 4096, 21.8 ms, with sixteen 21.0), in the gradient as
                 // in the loss: against an lse from other sums all probabilities
-                // are off the same way, by 2% at logits of 2330.
+                // are off the same way, by 2% at logits of 2330.  Other sums of
+                // 16-bit operands that may have more than 16384 terms: 128 (one
+                // sum of a million terms of one sign is off by 0.6%, of 65536 by
+                // 0.04%, a unit of f16's last place; runs of 8192 by 0.005%).
 #pragma unroll
                 for (int c = 0; c < SLAB; ++c) sum[c] = 0.f;
                 for (int kb = 0; ok && kb < w.nkb; kb += CH) {
