@@ -47,6 +47,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "lm_kernels.h"
 #include "lm_ptx.cuh"
 
@@ -500,7 +502,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     uint64_t *drain = tempty + 2;           // MMA completion before teardown
     uint64_t *tailbar = drain + 1;          // kRagK, per stage: this SM's copies of a group's last block
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Tile::BARS);
-    volatile uint32_t *progress = tmem_slot + 1;    // stages the producer has issued
+    volatile uint32_t *progress = tmem_slot + 1;    // stages the producer has issued, each time round
     unsigned char *after = reinterpret_cast<unsigned char *>(bars) + ((Tile::BARS * 8 + 16 + 15) / 16) * 16;
     float *staging = reinterpret_cast<float *>(after);
     int *g_start = reinterpret_cast<int *>(after + Tile::STAGING);
@@ -625,8 +627,13 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                         __syncwarp();
                     }
                     ++issued;
-                    if (lane == 0) *progress = (uint32_t)issued;
-                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                        // (Each time round, and not by the lane whose arrivals
+                        // would wait for it: every stage cost 3%.)
+                        if (lane == 31) *progress = (uint32_t)issued;
+                    }
                 }
             }
         }
@@ -841,7 +848,109 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                     }
                 }
             }
-            if constexpr (CHUNKED) {
+            // The tile's columns, out of tensor memory or from `sum`.
+            auto store_tile = [&](auto from_sum) {
+                uint32_t next[32];
+#pragma unroll
+                for (int c0 = 0; c0 < SLAB; c0 += 32) {
+                    const int col = slab0 + c0;                 // column in the tile
+                    if (col < w.nvalid && (EPI == kEpiCols || row0 < p.M)) {
+                        float v[32];
+                        if constexpr (decltype(from_sum)::value) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = sum[c0 + i];
+                        } else if (w.nkb > 0) {
+                            // The next 32 columns are on their way while these
+                            // are worked on.
+                            if (c0 == 0) tmem_ld_32cols_nowait(taddr, next);
+                            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(next[i]);
+                            if (c0 + 32 < SLAB && col + 32 < w.nvalid)
+                                tmem_ld_32cols_nowait(taddr + (uint32_t)(c0 + 32), next);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                        }
+                        const int cnt = min(32, w.nvalid - col);
+                        const int n = w.n0 + col;               // column of D
+                        if constexpr (EPI == kEpiCols) {
+                            if (p.out == kOutF32)
+                                lm_store_cols(p, static_cast<float *>(p.C) + w.s * p.stride_c, row0, n, cnt, v, stg, lane);
+                            else if (p.out == kOutF16)
+                                lm_store_cols(p, static_cast<__half *>(p.C), row0, n, cnt, v, stg, lane);
+                            else
+                                lm_store_cols(p, static_cast<__nv_bfloat16 *>(p.C), row0, n, cnt, v, stg, lane);
+                        } else if constexpr (EPI == kEpiLse) {
+                            if (cnt < 32)
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (i >= cnt) v[i] = -INFINITY;
+                            float bm = v[0];
+#pragma unroll
+                            for (int i = 1; i < 32; ++i) bm = fmaxf(bm, v[i]);
+                            const float nm = fmaxf(run_max, bm);
+                            const float ref = (nm == -INFINITY ? 0.f : nm) * kLog2E;
+                            float s = run_sum * exp2_approx(fmaf(run_max, kLog2E, -ref));
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) s += exp2_approx(fmaf(v[i], kLog2E, -ref));
+                            run_sum = s;
+                            run_max = nm;
+                            const int rel = tgt - n;
+                            if (rel >= 0 && rel < cnt) {
+                                float pick = v[0];
+#pragma unroll
+                                for (int i = 1; i < 32; ++i)
+                                    if (i == rel) pick = v[i];
+                                p.picked[row] = pick;
+                            }
+                        } else {
+                            if constexpr (EPI == kEpiDLogits) {
+                                const int rel = tgt - n;
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) {
+                                    float e = exp2_approx_subnormal((v[i] - row_lse) * kLog2E);
+                                    if (i == rel) e -= 1.f;
+                                    v[i] = row_g == 0.f ? 0.f : e * row_g;
+                                }
+                            } else {
+                                if (p.acc_in != nullptr && row < p.M) {
+                                    const float *a = p.acc_in + (int64_t)row * p.ld_acc + n;
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i)
+                                        if (i < cnt) v[i] += a[i];
+                                }
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) v[i] *= alpha;
+                            }
+                            const int64_t z = (int64_t)(RAG == kRagK ? w.g : w.s) * p.stride_c;
+                            if (EPI == kEpiDLogits && MODE != kPlanes && !PAIR && p.lo != nullptr) {
+                                // What the rounding to 16 bits leaves, in a plane of its own.
+                                float rest[32];
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    rest[i] = v[i] - (p.out == kOutF16 ? __half2float(__float2half_rn(v[i]))
+                                                                       : __bfloat162float(__float2bfloat16_rn(v[i])));
+                                if (p.out == kOutF16)
+                                    lm_store_rows<true>(p, static_cast<__half *>(p.lo), row, row0, n, cnt, rest, stg, lane);
+                                else
+                                    lm_store_rows<true>(p, static_cast<__nv_bfloat16 *>(p.lo), row, row0, n, cnt, rest, stg, lane);
+                            }
+                            // (d has the operands' type.)
+                            if (EPI == kEpiDLogits ? MODE == kPlanes : p.out == kOutF32)
+                                lm_store_rows<EPI == kEpiDLogits>(p, static_cast<float *>(p.C) + z, row, row0, n, cnt, v, stg, lane);
+                            else if (p.out == kOutF16)
+                                lm_store_rows<EPI == kEpiDLogits>(p, static_cast<__half *>(p.C) + z, row, row0, n, cnt, v, stg, lane);
+                            else
+                                lm_store_rows<EPI == kEpiDLogits>(p, static_cast<__nv_bfloat16 *>(p.C) + z, row, row0, n, cnt, v, stg, lane);
+                        }
+                        // Lanes without a row or column to store come back early; the
+                        // next load from tensor memory takes the warp together.
+                        __syncwarp();
+                    }
+                }
+            };
+            if (CHUNKED && (MODE != kLong || w.nkb > CH)) {
                 // Runs of CH blocks of the contraction are summed in an
                 // accumulator of their own and added here in FP32 with rounding
                 // to nearest (the tensor core's own running sum truncates).
@@ -855,9 +964,10 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 // are off the same way, by 2% at logits of 2330.  Other sums of
                 // 16-bit operands that may have more than 16384 terms: 128 (one
                 // sum of a million terms of one sign is off by 0.6%, of 65536 by
-                // 0.04%, a unit of f16's last place; runs of 8192 by 0.005%).
+                // 0.04%, a unit of f16's last place; runs of 8192 by 0.005%); a tile of
+                // fewer goes the plain way.
 #pragma unroll
-                for (int c = 0; c < SLAB; ++c) sum[c] = 0.f;
+                for (int c = 0; c < (CHUNKED ? SLAB : 1); ++c) sum[c] = 0.f;
                 for (int kb = 0; ok && kb < w.nkb; kb += CH) {
                     wait_acc();
                     if (!ok) break;
@@ -868,121 +978,24 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                             tmem_ld_32cols_nowait(taddr + (uint32_t)c0, r);
                             asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) sum[c0 + i] += __uint_as_float(r[i]);
+                            for (int i = 0; i < 32; ++i) sum[CHUNKED ? c0 + i : 0] += __uint_as_float(r[i]);
                         }
                     }
                     release_acc();
                 }
-            } else if (w.nkb > 0) {
-                wait_acc();
-            }
-            if (!ok) break;
-
-            uint32_t next[32];
-#pragma unroll
-            for (int c0 = 0; c0 < SLAB; c0 += 32) {
-                const int col = slab0 + c0;                 // column in the tile
-                if (col < w.nvalid && (EPI == kEpiCols || row0 < p.M)) {
-                    float v[32];
-                    if constexpr (CHUNKED) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = sum[c0 + i];
-                    } else if (w.nkb > 0) {
-                        // The next 32 columns are on their way while these
-                        // are worked on.
-                        if (c0 == 0) tmem_ld_32cols_nowait(taddr, next);
-                        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(next[i]);
-                        if (c0 + 32 < SLAB && col + 32 < w.nvalid)
-                            tmem_ld_32cols_nowait(taddr + (uint32_t)(c0 + 32), next);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = 0.f;
-                    }
-                    const int cnt = min(32, w.nvalid - col);
-                    const int n = w.n0 + col;               // column of D
-                    if constexpr (EPI == kEpiCols) {
-                        if (p.out == kOutF32)
-                            lm_store_cols(p, static_cast<float *>(p.C) + w.s * p.stride_c, row0, n, cnt, v, stg, lane);
-                        else if (p.out == kOutF16)
-                            lm_store_cols(p, static_cast<__half *>(p.C), row0, n, cnt, v, stg, lane);
-                        else
-                            lm_store_cols(p, static_cast<__nv_bfloat16 *>(p.C), row0, n, cnt, v, stg, lane);
-                    } else if constexpr (EPI == kEpiLse) {
-                        if (cnt < 32)
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (i >= cnt) v[i] = -INFINITY;
-                        float bm = v[0];
-#pragma unroll
-                        for (int i = 1; i < 32; ++i) bm = fmaxf(bm, v[i]);
-                        const float nm = fmaxf(run_max, bm);
-                        const float ref = (nm == -INFINITY ? 0.f : nm) * kLog2E;
-                        float s = run_sum * exp2_approx(fmaf(run_max, kLog2E, -ref));
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) s += exp2_approx(fmaf(v[i], kLog2E, -ref));
-                        run_sum = s;
-                        run_max = nm;
-                        const int rel = tgt - n;
-                        if (rel >= 0 && rel < cnt) {
-                            float pick = v[0];
-#pragma unroll
-                            for (int i = 1; i < 32; ++i)
-                                if (i == rel) pick = v[i];
-                            p.picked[row] = pick;
-                        }
-                    } else {
-                        if constexpr (EPI == kEpiDLogits) {
-                            const int rel = tgt - n;
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                float e = exp2_approx_subnormal((v[i] - row_lse) * kLog2E);
-                                if (i == rel) e -= 1.f;
-                                v[i] = row_g == 0.f ? 0.f : e * row_g;
-                            }
-                        } else {
-                            if (p.acc_in != nullptr && row < p.M) {
-                                const float *a = p.acc_in + (int64_t)row * p.ld_acc + n;
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if (i < cnt) v[i] += a[i];
-                            }
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] *= alpha;
-                        }
-                        const int64_t z = (int64_t)(RAG == kRagK ? w.g : w.s) * p.stride_c;
-                        if (EPI == kEpiDLogits && MODE != kPlanes && !PAIR && p.lo != nullptr) {
-                            // What the rounding to 16 bits leaves, in a plane of its own.
-                            float rest[32];
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                rest[i] = v[i] - (p.out == kOutF16 ? __half2float(__float2half_rn(v[i]))
-                                                                   : __bfloat162float(__float2bfloat16_rn(v[i])));
-                            if (p.out == kOutF16)
-                                lm_store_rows<true>(p, static_cast<__half *>(p.lo), row, row0, n, cnt, rest, stg, lane);
-                            else
-                                lm_store_rows<true>(p, static_cast<__nv_bfloat16 *>(p.lo), row, row0, n, cnt, rest, stg, lane);
-                        }
-                        // (d has the operands' type.)
-                        if (EPI == kEpiDLogits ? MODE == kPlanes : p.out == kOutF32)
-                            lm_store_rows<EPI == kEpiDLogits>(p, static_cast<float *>(p.C) + z, row, row0, n, cnt, v, stg, lane);
-                        else if (p.out == kOutF16)
-                            lm_store_rows<EPI == kEpiDLogits>(p, static_cast<__half *>(p.C) + z, row, row0, n, cnt, v, stg, lane);
-                        else
-                            lm_store_rows<EPI == kEpiDLogits>(p, static_cast<__nv_bfloat16 *>(p.C) + z, row, row0, n, cnt, v, stg, lane);
-                    }
-                    // Lanes without a row or column to store come back early; the
-                    // next load from tensor memory takes the warp together.
-                    __syncwarp();
-                }
+                if (!ok) break;
+                store_tile(std::integral_constant<bool, CHUNKED>());
+            } else {
+                if (w.nkb > 0) wait_acc();
+                if (!ok) break;
+                store_tile(std::false_type());
+                if (w.nkb > 0) release_acc();
             }
             if constexpr (EPI == kEpiLse) {
                 if (row < p.M)
                     p.part[(int64_t)((w.n0 / p.tile_n) * (BN / SLAB) + (ew >> 2)) * p.M + row] =
                         make_float2(run_max, run_sum);
             }
-            if (!CHUNKED && w.nkb > 0) release_acc();
         }
     }
 
