@@ -4,7 +4,10 @@
 // launches.
 #include <algorithm>
 #include <cstring>
+#include <map>
 #include <mutex>
+#include <new>
+#include <tuple>
 
 #include "../../include/sgemm_gb300_lm.h"
 #include "context.h"
@@ -119,17 +122,18 @@ sgemmStatus_t check_device(const sgemmContext *h) {
 }
 
 // CTAs (or SM pairs) of a kernel that are resident at once on the device,
-// asked for once per kernel, device and size after its shared-memory opt-in.
-int resident_slots(const sgemmContext *h, const LmKernel &k, int smem) {
-    struct Known { const void *fn; int device, smem, threads, slots; };
-    static Known known[256];
-    static int count = 0;
+// asked for once per kernel, device and size (to the next KB) after its
+// shared-memory opt-in.  The 4-bit products' size follows x, so that a server's
+// batches make many.
+int resident_slots(const sgemmContext *h, const LmKernel &k, int exact_smem) {
+    using Key = std::tuple<const void *, int, int, int>;
+    static std::map<Key, int> known;
     static std::mutex mutex;
+    const int smem = std::min(int(round_up(exact_smem, 1024)), kMaxSmem);
+    const Key key(k.fn, h->device, smem, k.threads);
     std::lock_guard<std::mutex> lock(mutex);
-    for (int i = 0; i < count; ++i)
-        if (known[i].fn == k.fn && known[i].device == h->device && known[i].smem == smem &&
-            known[i].threads == k.threads)
-            return known[i].slots;
+    const auto at = known.find(key);
+    if (at != known.end()) return at->second;
     // The opt-in is for the most any launch may ask for, so that one launch
     // never lowers it under another.
     if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess) return -1;
@@ -152,7 +156,10 @@ int resident_slots(const sgemmContext *h, const LmKernel &k, int smem) {
         n *= h->sm_count;
     }
     if (n < 1) return -1;
-    if (count < 256) known[count++] = Known{k.fn, h->device, smem, k.threads, n};
+    try {
+        known.emplace(key, n);
+    } catch (const std::bad_alloc &) {       // (asked for again next time)
+    }
     return n;
 }
 
