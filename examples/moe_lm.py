@@ -3,8 +3,8 @@ and then served.
 
 Training: tokens are sorted by the expert a router picked, each expert
 multiplies its rows (grouped_gemm; the counts stay on the device), and the
-loss over the vocabulary is taken without its logits (linear_cross_entropy).
-Both have their gradients as torch.autograd functions below.  Serving: the
+loss over the vocabulary is taken without its logits (linear_cross_entropy);
+torch's backward pass goes through both.  Serving: the
 head's matrix is quantised to 4 bits and one token at a time goes through
 w4_gemm.
 
@@ -17,37 +17,6 @@ import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import fp32_sgemm_gb300 as sg  # noqa: E402
-
-
-class GroupedLinear(torch.autograd.Function):
-    """y[t] = x[t] @ w[g].T for the rows t of group g; w [groups, out, in]."""
-
-    @staticmethod
-    def forward(ctx, x, w, group_ends):
-        ctx.save_for_backward(x, w, group_ends)
-        return sg.grouped_gemm(x, w, group_ends, trans_w=True)
-
-    @staticmethod
-    def backward(ctx, dy):
-        x, w, group_ends = ctx.saved_tensors
-        dy = dy.contiguous()
-        return (sg.grouped_gemm(dy, w, group_ends),
-                sg.grouped_gemm_weight_grad(x, dy, group_ends, trans_w=True), None)
-
-
-class VocabularyLoss(torch.autograd.Function):
-    """Loss of each token against the rows of w as vocabulary."""
-
-    @staticmethod
-    def forward(ctx, x, w, target):
-        loss, lse = sg.linear_cross_entropy(x, w, target)
-        ctx.save_for_backward(x, w, target, lse)
-        return loss
-
-    @staticmethod
-    def backward(ctx, dloss):
-        dx, dw = sg.linear_cross_entropy_grad(*ctx.saved_tensors, dloss.contiguous().float())
-        return dx, dw, None
 
 
 class ExpertModel(torch.nn.Module):
@@ -74,7 +43,8 @@ class ExpertModel(torch.nn.Module):
         ends = torch.searchsorted(expert[order], torch.arange(self.up.shape[0], device=x.device),
                                   right=True).to(torch.int32)
         rows = x[order]
-        y = GroupedLinear.apply(torch.nn.functional.silu(GroupedLinear.apply(rows, self.up, ends)), self.down, ends)
+        h = torch.nn.functional.silu(sg.grouped_gemm(rows, self.up, ends, trans_w=True))
+        y = sg.grouped_gemm(h, self.down, ends, trans_w=True)
         y = y * gate[order, None].to(y.dtype)
         return x + torch.zeros_like(y).index_copy(0, order, y)
 
@@ -82,7 +52,7 @@ class ExpertModel(torch.nn.Module):
         return self.experts(self.embed[tokens])
 
     def loss(self, tokens, target):
-        losses = VocabularyLoss.apply(self.hidden(tokens), self.head, target)
+        losses, _ = sg.linear_cross_entropy(self.hidden(tokens), self.head, target)
         return losses.sum() / (target >= 0).sum()
 
 

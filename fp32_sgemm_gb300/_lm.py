@@ -9,9 +9,18 @@ own, so calls on several streams or from several threads need no handles of
 their own, and calls can be captured with torch.cuda.graph; a `handle` (the
 device's default one otherwise) carries the wait limit and the error word.
 The checks and the calls are in csrc/lm_binding.cpp.
+
+grouped_gemm() and linear_cross_entropy() are differentiable in x and w: where
+gradients are recorded and one of them requires one, the result carries a graph
+whose backward pass makes the gradient calls below, on the stream current there.
+(A result in `out` carries none.)  What has no gradient here, the products with
+4-bit weights and lse by itself, says so when one is asked for.
 """
 
 from __future__ import annotations
+
+import torch
+from torch.autograd.function import once_differentiable
 
 from . import _build
 from ._binding import _default_handles, default_handle, load_library
@@ -22,7 +31,6 @@ def _load():
     import importlib.util
     import os
 
-    import torch  # noqa: F401  (its libraries, which the module is linked to)
     load_library()
     if not os.path.exists(_build.LM_BINDING_PATH):
         raise RuntimeError(f"{_build.LM_BINDING_PATH} is not built; run fp32_sgemm_gb300.build()")
@@ -49,6 +57,61 @@ def _handle(x, handle):
     return _default_handles.get(index) or default_handle(index)
 
 
+def _recorded(x, w):
+    return torch.is_grad_enabled() and (getattr(x, "requires_grad", False) or getattr(w, "requires_grad", False))
+
+
+class _GroupedGemm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, group_ends, trans_w, handle, stream):
+        y = _c.grouped_gemm(x, w, group_ends, trans_w, None, handle, stream)
+        ctx.save_for_backward(x, w, group_ends)
+        ctx.trans_w, ctx.handle = trans_w, handle
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, w, group_ends = ctx.saved_tensors
+        dy = dy.contiguous()
+        dx = dw = None
+        if ctx.needs_input_grad[0]:
+            dx = _c.grouped_gemm(dy, w, group_ends, not ctx.trans_w, None, ctx.handle, None)
+        if ctx.needs_input_grad[1]:
+            dw = _c.grouped_gemm_weight_grad(x, dy, group_ends, ctx.trans_w, None, ctx.handle, None)
+        return dx, dw, None, None, None, None
+
+
+class _LinearCrossEntropy(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, target, handle, stream):
+        loss, lse = _c.linear_cross_entropy(x, w, target, handle, stream)
+        ctx.save_for_backward(x, w, target, lse)
+        ctx.handle = handle
+        ctx.set_materialize_grads(False)
+        return loss, lse
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dloss, dlse):
+        if dlse is not None:
+            raise NotImplementedError("linear_cross_entropy has no gradient by lse, only by loss")
+        if dloss is None:
+            return None, None, None, None, None
+        dx, dw = _c.linear_cross_entropy_grad(*ctx.saved_tensors, dloss.contiguous(), ctx.handle, None)
+        return (dx if ctx.needs_input_grad[0] else None, dw if ctx.needs_input_grad[1] else None, None, None, None)
+
+
+class _W4Gemm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, q, scales, zeros, handle, stream):
+        return _c.w4_gemm(x, q, scales, zeros, None, handle, stream)
+
+    @staticmethod
+    def backward(ctx, dy):
+        raise NotImplementedError("w4_gemm has no gradient")
+
+
 def grouped_gemm(x, w, group_ends, *, trans_w: bool = False, out=None, handle=None, stream=None):
     """y[t] = x[t] @ op(w[g]) for every row t of group g; returns y [T, N].
 
@@ -58,6 +121,8 @@ def grouped_gemm(x, w, group_ends, *, trans_w: bool = False, out=None, handle=No
     zeros.  The gradient by x is ``grouped_gemm(dy, w, group_ends,
     trans_w=not trans_w)``; that by w, grouped_gemm_weight_grad().
     """
+    if out is None and _recorded(x, w):
+        return _GroupedGemm.apply(x, w, group_ends, trans_w, _handle(x, handle), stream)
     return _c.grouped_gemm(x, w, group_ends, trans_w, out, _handle(x, handle), stream)
 
 
@@ -75,6 +140,8 @@ def linear_cross_entropy(x, w, target, *, handle=None, stream=None):
     0); returns (loss, lse), float32 [T]: lse[t] = log sum_v exp(x_t . w_v),
     loss[t] = lse[t] - x_t . w_target.
     """
+    if _recorded(x, w):
+        return _LinearCrossEntropy.apply(x, w, target, _handle(x, handle), stream)
     return _c.linear_cross_entropy(x, w, target, _handle(x, handle), stream)
 
 
@@ -93,4 +160,6 @@ def w4_gemm(x, q, scales, zeros=None, *, out=None, handle=None, stream=None):
     K // groups = 32, 64 or 128 columns:
     W[n, k] = scales[n, k // group] * (q[n, k] - zeros[n, k // group]).
     """
+    if out is None and _recorded(x, scales):
+        return _W4Gemm.apply(x, q, scales, zeros, _handle(x, handle), stream)
     return _c.w4_gemm(x, q, scales, zeros, out, _handle(x, handle), stream)
