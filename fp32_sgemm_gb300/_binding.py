@@ -202,6 +202,9 @@ def _matrix(t, name: str, rows: int | None = None, cols: int | None = None):
     stride = t.stride()
     if r > 1 and c > 0 and stride[1] != 1:
         raise ValueError(f"{name} must be row major (stride(1) == 1)")
+    if r > 1 and stride[0] < c:
+        # A broadcast row has no pitch: read with one, it ends beyond the tensor.
+        raise ValueError(f"{name} has overlapping rows")
     ld = stride[0] if r > 1 else max(c, 1)
     if rows is not None and r != rows or cols is not None and c != cols:
         raise ValueError(f"{name} has shape {tuple(shape)}, expected ({rows}, {cols})")

@@ -68,3 +68,15 @@ def test_one_column_with_a_pitch(sg, dtype):
     ends = torch.tensor([15, T], dtype=torch.int32, device="cuda")
     want = torch.cat((x[:15].double() @ w[0].double(), x[15:].double() @ w[1].double()))
     assert torch.equal(sg.grouped_gemm(x, w, ends).double(), want)
+
+
+def test_broadcast_rows_of_an_fp32_product_are_refused(sg):
+    full = torch.ones(40, 40, device="cuda")
+    for rows in (torch.ones(1, 40, device="cuda").expand(40, 40), full.as_strided((40, 40), (8, 1))):
+        with pytest.raises(ValueError):
+            sg.sgemm(rows, full)
+        with pytest.raises(ValueError):
+            sg.sgemm(full, rows)
+        with pytest.raises(ValueError):
+            sg.sgemm(full, full, rows)
+    assert (sg.sgemm(torch.ones(1, 40, device="cuda"), full) == 40).all()
