@@ -219,6 +219,12 @@ PyObject *guarded(F &&f) {
     }
 }
 
+bool truth(PyObject *o) {
+    const int is = PyObject_IsTrue(o);
+    if (is < 0) throw Failed{};
+    return is != 0;
+}
+
 PyObject *wrap(const at::Tensor &t) { return THPVariable_Wrap(t); }
 
 // (x, w, group_ends, trans_w, out, handle, stream)
@@ -231,7 +237,7 @@ PyObject *py_grouped_gemm(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const at::ScalarType st = x.scalar_type();
         const Matrix mx = matrix(x, "x", st, dev);
         if (w.dim() != 3) fail(PyExc_ValueError, "w must be a 3-D tensor [groups, rows, cols]");
-        const bool trans = PyObject_IsTrue(a[3]);
+        const bool trans = truth(a[3]);
         const int64_t T = mx.rows, K = mx.cols, G = w.size(0), N = w.size(trans ? 1 : 2);
         const Matrix mw = stack(w, "w", st, dev, G, trans ? N : K, trans ? K : N);
         const int32_t *ends = vector<int32_t>(a[2], "group_ends", at::kInt, dev, G);
@@ -261,7 +267,7 @@ PyObject *py_grouped_gemm_weight_grad(PyObject *, PyObject *const *a, Py_ssize_t
         Matrix l = matrix(x, "x", st, dev), r = matrix(dy, "dy", st, dev);
         if (l.rows != r.rows)
             fail(PyExc_ValueError, "x has %lld rows, dy has %lld", (long long)l.rows, (long long)r.rows);
-        if (PyObject_IsTrue(a[3])) std::swap(l, r);
+        if (truth(a[3])) std::swap(l, r);
         const int64_t T = l.rows, M = l.cols, N = r.cols;
         const int32_t *ends = vector<int32_t>(a[2], "group_ends", at::kInt, dev, -1);
         const int64_t G = THPVariable_Unpack(a[2]).size(0);

@@ -80,3 +80,13 @@ def test_broadcast_rows_of_an_fp32_product_are_refused(sg):
         with pytest.raises(ValueError):
             sg.sgemm(full, full, rows)
     assert (sg.sgemm(torch.ones(1, 40, device="cuda"), full) == 40).all()
+
+
+def test_a_flag_without_a_truth_value_raises_its_own_error(sg):
+    x, w = torch.ones(8, 16, device="cuda"), torch.ones(1, 16, 16, device="cuda")
+    ends = torch.tensor([8], dtype=torch.int32, device="cuda")
+    two = torch.ones(2)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        sg.grouped_gemm(x, w, ends, trans_w=two)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        sg.grouped_gemm_weight_grad(x, x, ends, trans_w=two)
