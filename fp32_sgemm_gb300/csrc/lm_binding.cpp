@@ -24,6 +24,7 @@ namespace {
 
 PyObject *g_check = nullptr;        // _binding._check(status, where)
 PyObject *g_stream_ptr = nullptr;   // _binding._stream_ptr(stream, device index)
+PyObject *g_out_of_memory = nullptr;   // torch.OutOfMemoryError
 PyObject *g_name_ptr = nullptr;
 
 struct Failed {};                   // a Python error is set
@@ -213,6 +214,9 @@ PyObject *guarded(F &&f) {
         return f();
     } catch (const Failed &) {
         return nullptr;
+    } catch (const c10::OutOfMemoryError &e) {
+        PyErr_SetString(g_out_of_memory, e.what_without_backtrace());
+        return nullptr;
     } catch (const std::exception &e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
         return nullptr;
@@ -397,7 +401,12 @@ PyMODINIT_FUNC PyInit__lm_binding(void) {
     g_check = PyObject_GetAttrString(b, "_check");
     g_stream_ptr = PyObject_GetAttrString(b, "_stream_ptr");
     Py_DECREF(b);
+    PyObject *t = PyImport_ImportModule("torch");
+    if (t == nullptr) return nullptr;
+    g_out_of_memory = PyObject_GetAttrString(t, "OutOfMemoryError");
+    Py_DECREF(t);
     g_name_ptr = PyUnicode_InternFromString("address");
-    if (g_check == nullptr || g_stream_ptr == nullptr || g_name_ptr == nullptr) return nullptr;
+    if (g_check == nullptr || g_stream_ptr == nullptr || g_out_of_memory == nullptr || g_name_ptr == nullptr)
+        return nullptr;
     return PyModule_Create(&module);
 }

@@ -90,3 +90,20 @@ def test_a_flag_without_a_truth_value_raises_its_own_error(sg):
         sg.grouped_gemm(x, w, ends, trans_w=two)
     with pytest.raises(RuntimeError, match="ambiguous"):
         sg.grouped_gemm_weight_grad(x, x, ends, trans_w=two)
+
+
+def test_what_does_not_fit_raises_torchs_own_error(sg):
+    # 1024 gradients of 65536 x 65536: nothing is launched.
+    x = torch.zeros(8, 65536, dtype=torch.bfloat16, device="cuda")
+    ends = torch.full((1024,), 8, dtype=torch.int32, device="cuda")
+    with pytest.raises(torch.OutOfMemoryError):
+        sg.grouped_gemm_weight_grad(x, x, ends)
+    # (An operand that fits, and the three planes of it that do not.)
+    free = torch.cuda.mem_get_info()[0]
+    rows = int(free * 0.55) // (4 * 65537)
+    w = torch.empty(rows, 65537, device="cuda")
+    target = torch.zeros(8, dtype=torch.int64, device="cuda")
+    with pytest.raises(torch.OutOfMemoryError):
+        sg.linear_cross_entropy(torch.zeros(8, 65537, device="cuda"), w, target)
+    del w
+    torch.cuda.empty_cache()
