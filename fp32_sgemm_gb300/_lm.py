@@ -58,7 +58,7 @@ def _handle(x, handle):
 
 
 def _recorded(x, w):
-    return torch.is_grad_enabled() and (getattr(x, "requires_grad", False) or getattr(w, "requires_grad", False))
+    return (getattr(x, "requires_grad", False) or getattr(w, "requires_grad", False)) and torch.is_grad_enabled()
 
 
 class _GroupedGemm(torch.autograd.Function):
