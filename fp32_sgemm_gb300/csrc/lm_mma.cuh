@@ -825,7 +825,10 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if constexpr (PAIR) mbar_arrive_cluster(cluster_addr(&tempty[gc & 1], 0));
+                    // Only the loads from tensor memory have to come before (they
+                    // are complete, and fenced); a release would wait for the
+                    // stores of the tile before, too.
+                    if constexpr (PAIR) mbar_arrive_cluster_relaxed(cluster_addr(&tempty[gc & 1], 0));
                     else mbar_arrive(&tempty[gc & 1]);
                 }
                 ++gc;
