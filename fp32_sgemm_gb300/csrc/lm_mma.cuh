@@ -129,14 +129,6 @@ __device__ __forceinline__ float exp2_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// The same without flushing results below 2^-126 (gradients of improbable
-// entries).
-__device__ __forceinline__ float exp2_approx_subnormal(float x) {
-    float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 template <class T> __device__ __forceinline__ T lm_cvt(float x);
 template <> __device__ __forceinline__ float lm_cvt<float>(float x) { return x; }
 template <> __device__ __forceinline__ __half lm_cvt<__half>(float x) { return __float2half_rn(x); }
@@ -810,6 +802,7 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         bool ok = true;
         float alpha = 1.f;
         if (EPI == kEpiRows && p.alpha != nullptr) alpha = *p.alpha;
+        if (EPI == kEpiDLogits && p.gscale != nullptr) alpha = *p.gscale;
         for (int t = slot; ok && t < num_tiles; t += slots) {
             const LmWork w = lm_work<Tile, RAG>(p, g_start, g_prefix, t);
             float sum[CHUNKED ? SLAB : 1];
@@ -841,13 +834,18 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             if constexpr (EPI == kEpiLse || EPI == kEpiDLogits) {
                 if (row < p.M) {
                     const int64_t tv = p.target[row];
+                    // (All on their way together; of a token that is not
+                    // counted they are not used.)
+                    float lse = 0.f, grad = 0.f;
+                    if constexpr (EPI == kEpiDLogits) {
+                        lse = p.lse[row];
+                        grad = p.grad[row];
+                    }
                     if (tv >= 0 && tv < p.vocab) {
                         const int64_t rel = tv - p.v0;
                         tgt = rel >= 0 && rel < p.N ? (int)rel : -1;
-                        if constexpr (EPI == kEpiDLogits) {
-                            row_lse = p.lse[row];
-                            row_g = p.grad[row] * (p.gscale != nullptr ? *p.gscale : 1.f);
-                        }
+                        row_lse = lse;
+                        row_g = grad * alpha;
                     }
                 }
             }
@@ -909,13 +907,24 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                             }
                         } else {
                             if constexpr (EPI == kEpiDLogits) {
+                                // exp(x) as the square of exp(x / 2), whose product
+                                // keeps results below 2^-126 (gradients of
+                                // improbable entries).
                                 const int rel = tgt - n;
 #pragma unroll
                                 for (int i = 0; i < 32; ++i) {
-                                    float e = exp2_approx_subnormal((v[i] - row_lse) * kLog2E);
-                                    if (i == rel) e -= 1.f;
-                                    v[i] = row_g == 0.f ? 0.f : e * row_g;
+                                    const float h = exp2_approx((v[i] - row_lse) * (0.5f * kLog2E));
+                                    v[i] = h * h;
                                 }
+                                if (rel >= 0 && rel < 32)
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i)
+                                        if (i == rel) v[i] -= 1.f;
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) v[i] *= row_g;
+                                if (row_g == 0.f)
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i) v[i] = 0.f;
                             } else {
                                 if (p.acc_in != nullptr && row < p.M) {
                                     const float *a = p.acc_in + (int64_t)row * p.ld_acc + n;
