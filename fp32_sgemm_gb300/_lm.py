@@ -57,10 +57,6 @@ def _handle(x, handle):
     return _default_handles.get(index) or default_handle(index)
 
 
-def _recorded(x, w):
-    return (getattr(x, "requires_grad", False) or getattr(w, "requires_grad", False)) and torch.is_grad_enabled()
-
-
 class _GroupedGemm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, group_ends, trans_w, handle, stream):
@@ -121,9 +117,9 @@ def grouped_gemm(x, w, group_ends, *, trans_w: bool = False, out=None, handle=No
     zeros.  The gradient by x is ``grouped_gemm(dy, w, group_ends,
     trans_w=not trans_w)``; that by w, grouped_gemm_weight_grad().
     """
-    if out is None and _recorded(x, w):
-        return _GroupedGemm.apply(x, w, group_ends, trans_w, _handle(x, handle), stream)
-    return _c.grouped_gemm(x, w, group_ends, trans_w, out, _handle(x, handle), stream)
+    handle = _handle(x, handle)
+    y = _c.grouped_gemm(x, w, group_ends, trans_w, out, handle, stream)
+    return _GroupedGemm.apply(x, w, group_ends, trans_w, handle, stream) if y is None else y
 
 
 def grouped_gemm_weight_grad(x, dy, group_ends, *, trans_w: bool = False, out=None, handle=None,
@@ -140,9 +136,9 @@ def linear_cross_entropy(x, w, target, *, handle=None, stream=None):
     0); returns (loss, lse), float32 [T]: lse[t] = log sum_v exp(x_t . w_v),
     loss[t] = lse[t] - x_t . w_target.
     """
-    if _recorded(x, w):
-        return _LinearCrossEntropy.apply(x, w, target, _handle(x, handle), stream)
-    return _c.linear_cross_entropy(x, w, target, _handle(x, handle), stream)
+    handle = _handle(x, handle)
+    both = _c.linear_cross_entropy(x, w, target, handle, stream)
+    return _LinearCrossEntropy.apply(x, w, target, handle, stream) if both is None else both
 
 
 def linear_cross_entropy_grad(x, w, target, lse, dloss, *, handle=None, stream=None):
@@ -160,6 +156,6 @@ def w4_gemm(x, q, scales, zeros=None, *, out=None, handle=None, stream=None):
     K // groups = 32, 64 or 128 columns:
     W[n, k] = scales[n, k // group] * (q[n, k] - zeros[n, k // group]).
     """
-    if out is None and _recorded(x, scales):
-        return _W4Gemm.apply(x, q, scales, zeros, _handle(x, handle), stream)
-    return _c.w4_gemm(x, q, scales, zeros, out, _handle(x, handle), stream)
+    handle = _handle(x, handle)
+    y = _c.w4_gemm(x, q, scales, zeros, out, handle, stream)
+    return _W4Gemm.apply(x, q, scales, zeros, handle, stream) if y is None else y

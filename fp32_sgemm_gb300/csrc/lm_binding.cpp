@@ -8,6 +8,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -157,9 +158,8 @@ void check(sgemmStatus_t st, const char *where) {
 // different streams or from different threads share none of it, whatever
 // handle they go through, and a captured call's stays in its graph's memory.
 // (A buffer kept by the handle would have to be one for each stream and each
-// capture.  Asking takes some 1 us of the host's time, 6.9 us a call instead of
-// 5.8, which the device's hides: loss of 16 rows, 32000 x 1024, 21.2 us with a
-// kept buffer and 21.4.)
+// capture.  Asking takes some tenths of a microsecond of the host's time; loss of
+// 16 rows, 32000 x 1024, 21.1 us with a kept buffer and 21.3.)
 struct Call {
     sgemmContext context;           // the handle's, but for the workspace
     sgemmHandle_t handle = nullptr;
@@ -230,6 +230,12 @@ bool truth(PyObject *o) {
     return is != 0;
 }
 
+// Whether the call belongs into torch's graph: then it answers None, and
+// _lm.py takes it there (inside, nothing is recorded).
+bool recorded(const at::Tensor &a, const at::Tensor &b) {
+    return (a.requires_grad() || b.requires_grad()) && c10::GradMode::is_enabled();
+}
+
 PyObject *wrap(const at::Tensor &t) { return THPVariable_Wrap(t); }
 
 // (x, w, group_ends, trans_w, out, handle, stream)
@@ -237,6 +243,7 @@ PyObject *py_grouped_gemm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&] {
         expect(n, 7);
         const at::Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "w");
+        if (a[4] == Py_None && recorded(x, w)) Py_RETURN_NONE;
         const sgemmDataType_t ty = type_of(x, "x");
         const c10::Device dev = device_of(x, "x");
         const at::ScalarType st = x.scalar_type();
@@ -313,6 +320,7 @@ struct LossOperands {
 PyObject *py_linear_cross_entropy(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&] {
         expect(n, 5);
+        if (recorded(tensor(a[0], "x"), tensor(a[1], "w"))) Py_RETURN_NONE;
         const LossOperands o(a[0], a[1], a[2]);
         const int64_t T = o.x.rows, V = o.w.rows, D = o.x.cols;
         Call c(a[3], a[4], o.dev, {a[0], a[1], a[2]});
@@ -354,6 +362,7 @@ PyObject *py_w4_gemm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&] {
         expect(n, 7);
         const at::Tensor &x = tensor(a[0], "x"), &q = tensor(a[1], "q"), &s = tensor(a[2], "scales");
+        if (a[4] == Py_None && recorded(x, s)) Py_RETURN_NONE;
         const sgemmDataType_t ty = type_of(x, "x");
         const c10::Device dev = device_of(x, "x");
         const at::ScalarType st = x.scalar_type();
