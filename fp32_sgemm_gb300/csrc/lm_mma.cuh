@@ -117,9 +117,10 @@ __device__ __forceinline__ void tmem_ld_32cols_nowait(uint32_t taddr, uint32_t (
         : "r"(taddr));
 }
 
-// 32 bytes to a 32-byte aligned address in one store: a whole sector.
+// 32 bytes to a 32-byte aligned address in one store: a whole sector.  (Kept out
+// of L1, where it would take the place of what the epilogue has spilled.)
 __device__ __forceinline__ void st_global_32B(void *p, const uint32_t *v) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+    asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
                  :: "l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
                     "r"(v[7]) : "memory");
 }
