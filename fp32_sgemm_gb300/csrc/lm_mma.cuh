@@ -26,22 +26,24 @@
 // out of TMEM while the next tile is multiplied into the other accumulator.
 // Every wait is bounded and reports its site in the handle's error word.
 //
-// What bounds it, measured on one GB300 (copies 6.79 TB/s, a library's bf16
-// product 1900 TFLOP/s), bf16:
+// What bounds it, measured on one GB300 (copies 6.69 TB/s, a library's bf16
+// product 1915 TFLOP/s in a burst, 1730 sustained), bf16:
 //   * many rows: the tensor core.  4096 tokens against 32768 x 4096: the tensor
-//     pipe is busy 98.6% of the active cycles of the forward pass, 96.1 to
-//     98.5% of the gradient's three products (the SMs run at 1.7 of 2.07 GHz
-//     then).  8192 tokens against 131072 x 4096, loss and gradients: 19.3 to
-//     20.2 ms for 35.2 TFLOP, 1740 to 1820 TFLOP/s.  32768 rows in 8 groups, 4096 x 2048: 290 us,
-//     1890 TFLOP/s forward, 291 us weight gradient.  With fewer tiles the last
-//     round leaves pairs idle (8192 rows: 85 us, 1610 TFLOP/s, 256 tiles on 76
+//     pipe is busy 98.7% of the active cycles of the forward pass, 90% of the
+//     kernel of d (its epilogue lasts longer than the two runs of 512 terms the
+//     MMAs may be ahead), 97 to 97.7% of the gradient's two products.  8192
+//     tokens against 131072 x 4096, loss and gradients: 20.8 to 21.2 ms for 35.2
+//     TFLOP, 1660 to 1690 TFLOP/s at the power limit.  32768 rows in 8 groups,
+//     4096 x 2048: 288 to 299 us, 1840 to 1910 TFLOP/s forward, 294 to 299 us
+//     weight gradient.  With fewer tiles the last round leaves pairs idle (8192
+//     rows: 108 and 100 us, 1270 and 1380 TFLOP/s, 256 and 1024 tiles on 76
 //     pairs);
 //   * few rows: reading the matrices.  19 of 64 groups' 1024 x 2048 (80 MB):
-//     18.9 us, 4.2 TB/s, of which the first and last 3.5 us move nothing; 16
+//     19.1 us, 4.2 TB/s, of which the first and last 3.5 us move nothing; 16
 //     tokens against 32000 x 1024 (66 MB): 18 us and 3.5 for the join;
 //   * FP32: six bf16 products for one, and the three planes of both operands
 //     written and read again: 4096 rows in 8 groups, 1024 x 2048, both
-//     gradients 245 to 265 us (206 GFLOP of bf16, 108 us).
+//     gradients 219 to 245 us (206 GFLOP of bf16, 108 us).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -977,10 +979,10 @@ lm_mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 // terms to 2^-20 of their magnitudes).  Logits of 16-bit
                 // operands: eight (losses at 4096 terms off by 1.5 to 2e-7 of
                 // themselves, about a unit in the last place, twice that with
-                // sixteen, 1.7e-6 with one sum; loss and gradients of 8192 rows,
-                // 131072 x 4096, 21.8 ms, with sixteen 21.0), in the gradient as
-                // in the loss: against an lse from other sums all probabilities
-                // are off the same way, by 2% at logits of 2330.  Other sums of
+                // sixteen, 1.7e-6 with one sum; gradients of 8192 rows, 32768 x
+                // 4096, 3.96 ms, with sixteen 3.80), in the gradient as in the
+                // loss: against an lse from other sums all probabilities are off
+                // the same way, by 2% at logits of 2330.  Other sums of
                 // 16-bit operands that may have more than 16384 terms: 128 (one
                 // sum of a million terms of one sign is off by 0.6%, of 65536 by
                 // 0.04%, a unit of f16's last place; runs of 8192 by 0.005%); a tile of

@@ -22,14 +22,16 @@
 // The warps of a CTA share 16 rows and split K; their sums are joined in a
 // fixed order through shared memory.
 //
-// Measured (one GB300; reading alone takes 17.8, 1.3 and 5.2 us): 28672 x 8192,
-// f16, groups of 128, one row 26.4 us, 4.6 TB/s; 4096 x 4096, bf16, one row 4.9
+// Measured (one GB300; reading alone takes 18.1, 1.3 and 5.2 us): 28672 x 8192,
+// f16, groups of 128, one row 26.8 us, 4.5 TB/s; 4096 x 4096, bf16, one row 4.9
 // us, most of it the launch and one pass through the memory; 14335 x 4096
-// with zero points, groups of 32, bf16, seven rows 13.9 us, 2.5 TB/s.  What bounds the
-// long ones is the issue of instructions (60% of the active cycles; the
-// unpacking) beside mma.sync, which takes about 26 cycles on a quarter of an SM
-// whatever the number of rows.  The same on the FP32 pipes took 33.5 us, on
-// tcgen05 with the unpacked weights in tensor memory 44.8.
+// with zero points, groups of 32, bf16, seven rows 13.9 us, 2.5 TB/s.  The long
+// ones are at no unit's limit: instructions issue in 59% of the active cycles,
+// DRAM is at 54%, the matrix pipe at 24%.  What is left is latency: a group's
+// products are a chain of up to eight dependent mma.sync, about 26 cycles each
+// whatever the number of rows, with four warps on a quarter of an SM.  The same
+// on the FP32 pipes took 33.5 us, on tcgen05 with the unpacked weights in tensor
+// memory 44.8.
 #pragma once
 
 #include <cuda_bf16.h>

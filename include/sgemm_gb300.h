@@ -391,7 +391,8 @@ sgemmStatus_t sgemmGetDeviceError(sgemmHandle_t handle, int *code);
  *       expires, on launches whose CTAs take more K slices than stages);
  *   3 = consumers never release a pipeline stage (site 2 expires, same
  *       launches).
- * Only the main kernels (FFMA and 3xTF32) honour it.  Use a short limit
+ * The main kernels (FFMA and 3xTF32) honour it, and of sgemm_gb300_lm.h the
+ * tensor-core kernels (2 and 3) and the 4-bit products (2).  Use a short limit
  * (sgemmSetWaitTimeout) so that the expiries come quickly.  INVALID_VALUE
  * for other values or a NULL handle.
  */

@@ -56,7 +56,9 @@ typedef enum sgemmDataType {
  * touched).  The gradient by the rows is the same call with the output's
  * gradient as A and the other opB.
  *
- * F16 and BF16 products run on the tensor cores with FP32 sums.  F32
+ * F16 and BF16 products run on the tensor cores with FP32 sums, in runs of 8192
+ * terms where the contraction may have more than 16384 (the tensor cores' sums
+ * truncate: by up to 1.7e-7 of the sum for every 16 terms of one sign).  F32
  * products of up to 8 rows a group in the mean (T / G) and K >= 256 are
  * FP32 multiply-adds.  For the others F32 operands are split into three bf16
  * planes each in the workspace (x = p0 + p1 + p2, each plane the nearest to
