@@ -17,7 +17,7 @@ _BINDING_NAMES = {
 
 _LM_NAMES = {
     "grouped_gemm", "grouped_gemm_weight_grad", "linear_cross_entropy", "linear_cross_entropy_grad",
-    "w4_gemm",
+    "w4_gemm", "route_topk", "route_topk_grad", "expert_dispatch", "expert_combine", "expert_combine_grad",
 }
 
 

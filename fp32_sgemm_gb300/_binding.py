@@ -117,6 +117,14 @@ SIGNATURES = {
                       _vp, _i64, _vp, _i64, _vp]),
     "sgemmW4WorkspaceSize": (_st, [_vp, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int,
                                    ctypes.POINTER(ctypes.c_size_t)]),
+    "sgemmRouteTopK": (_st, [_vp, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _vp, _i64, _vp, _vp, _vp]),
+    "sgemmRouteTopKGrad": (_st, [_vp, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _vp, _i64, _vp, _vp, _vp,
+                                 _i64, _vp]),
+    "sgemmExpertDispatch": (_st, [_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp,
+                                  _vp, _vp]),
+    "sgemmExpertCombine": (_st, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp]),
+    "sgemmExpertCombineGrad": (_st, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                                     _i64, _vp, _vp]),
 }
 
 _lock = threading.Lock()

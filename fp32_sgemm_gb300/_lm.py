@@ -45,15 +45,15 @@ def _load():
 _c = _load()
 
 
-def _handle(x, handle):
+def _handle(x, handle, name="x"):
     if handle is not None:
         return handle
     try:
         index = x.get_device()
     except AttributeError:
-        raise TypeError("x must be a torch.Tensor") from None
+        raise TypeError(f"{name} must be a torch.Tensor") from None
     if index < 0:
-        raise ValueError("x must be a CUDA tensor")
+        raise ValueError(f"{name} must be a CUDA tensor")
     return _default_handles.get(index) or default_handle(index)
 
 
@@ -108,6 +108,57 @@ class _W4Gemm(torch.autograd.Function):
         raise NotImplementedError("w4_gemm has no gradient")
 
 
+class _RouteTopK(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, k, normalize, handle, stream):
+        weights, experts = _c.route_topk(logits, k, normalize, handle, stream)
+        ctx.save_for_backward(logits, experts)
+        ctx.mark_non_differentiable(experts)
+        ctx.normalize, ctx.handle = normalize, handle
+        return weights, experts
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dweights, dexperts):
+        logits, experts = ctx.saved_tensors
+        return (_c.route_topk_grad(logits, experts, dweights.contiguous(), ctx.normalize, ctx.handle, None),
+                None, None, None, None)
+
+
+class _ExpertDispatch(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, experts, num_experts, handle, stream):
+        rows, slots, group_ends = _c.expert_dispatch(x, experts, num_experts, handle, stream)
+        ctx.save_for_backward(slots)
+        ctx.mark_non_differentiable(slots, group_ends)
+        ctx.handle = handle
+        return rows, slots, group_ends
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, drows, dslots, dends):
+        slots, = ctx.saved_tensors
+        return _c.expert_combine(drows.contiguous(), slots, None, None, ctx.handle, None), None, None, None, None
+
+
+class _ExpertCombine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, rows, slots, weights, handle, stream):
+        y = _c.expert_combine(rows, slots, weights, None, handle, stream)
+        # (What only the weights' gradient reads is kept for that alone.)
+        ctx.save_for_backward(rows if ctx.needs_input_grad[2] else None, slots, weights)
+        ctx.handle = handle
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        rows, slots, weights = ctx.saved_tensors
+        drows, dweights = _c.expert_combine_grad(dy.contiguous(), rows, slots, weights, ctx.needs_input_grad[0],
+                                                 ctx.needs_input_grad[2], ctx.handle, None)
+        return drows, None, dweights, None, None
+
+
 def grouped_gemm(x, w, group_ends, *, trans_w: bool = False, out=None, handle=None, stream=None):
     """y[t] = x[t] @ op(w[g]) for every row t of group g; returns y [T, N].
 
@@ -159,3 +210,57 @@ def w4_gemm(x, q, scales, zeros=None, *, out=None, handle=None, stream=None):
     handle = _handle(x, handle)
     y = _c.w4_gemm(x, q, scales, zeros, out, handle, stream)
     return _W4Gemm.apply(x, q, scales, zeros, handle, stream) if y is None else y
+
+
+def route_topk(logits, k, *, normalize: bool = True, handle=None, stream=None):
+    """A router's choice: the k largest of each token's logits [T, E], in
+    falling order, the lower index first among equals.
+
+    Returns (weights, experts): float32 [T, k] softmax weights, over the chosen
+    alone with normalize (they add up to 1) and over all E without; int64 [T, k].
+    A logit of -inf is never chosen: where fewer than k are left the expert is -1
+    and its weight 0.  Differentiable in logits; route_topk_grad() by itself.
+    """
+    handle = _handle(logits, handle, "logits")
+    both = _c.route_topk(logits, k, normalize, handle, stream)
+    return _RouteTopK.apply(logits, k, normalize, handle, stream) if both is None else both
+
+
+def route_topk_grad(logits, experts, dweights, *, normalize: bool = True, handle=None, stream=None):
+    """Gradient of route_topk() by the logits, [T, E], for its experts and the
+    gradient dweights [T, k] (float32) by its weights."""
+    return _c.route_topk_grad(logits, experts, dweights, normalize, _handle(logits, handle, "logits"), stream)
+
+
+def expert_dispatch(x, experts, num_experts, *, handle=None, stream=None):
+    """Tokens x [T, D] sorted by expert: experts [T, k] int64, as route_topk()
+    gives them (what is outside [0, num_experts) is no expert).
+
+    Returns (rows, slots, group_ends): rows [T * k, D], each expert's in the
+    order of the choices, those of no expert behind the last end and zero; slots
+    [T, k] int32, the row of each choice (~r for a row r of no expert); group_ends
+    [num_experts] int32, as grouped_gemm() takes them.  Differentiable in x; the
+    gradient is ``expert_combine(drows, slots)``.
+    """
+    handle = _handle(x, handle)
+    parts = _c.expert_dispatch(x, experts, num_experts, handle, stream)
+    return _ExpertDispatch.apply(x, experts, num_experts, handle, stream) if parts is None else parts
+
+
+def expert_combine(rows, slots, weights=None, *, out=None, handle=None, stream=None):
+    """y[t] = sum_j weights[t, j] * rows[slots[t, j]]; returns y [T, D].
+
+    rows [T * k, D] and slots [T, k] as expert_dispatch() lays them out (negative
+    slots add nothing), weights [T, k] float32 or None (1).  Summed in float32 in
+    the order of j.  Differentiable in rows and weights; expert_combine_grad() by
+    itself.
+    """
+    handle = _handle(rows, handle, "rows")
+    y = _c.expert_combine(rows, slots, weights, out, handle, stream)
+    return _ExpertCombine.apply(rows, slots, weights, handle, stream) if y is None else y
+
+
+def expert_combine_grad(dy, rows, slots, weights=None, *, handle=None, stream=None):
+    """Gradients (drows [T * k, D], dweights [T, k] float32) of expert_combine()
+    for the gradient dy [T, D] by y.  Rows behind the last end get zeros."""
+    return _c.expert_combine_grad(dy, rows, slots, weights, True, True, _handle(rows, handle, "rows"), stream)

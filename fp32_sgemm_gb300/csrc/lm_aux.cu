@@ -10,27 +10,12 @@
 
 #include <algorithm>
 
+#include "lm_launch.cuh"
 #include "lm_kernels.h"
 #include "ptx.cuh"
 
 namespace sg {
 namespace {
-
-// A launch that may begin while the kernel before it in the stream ends
-// (griddepcontrol.wait orders its memory accesses).
-template <class... P, class... A>
-cudaError_t launch(void (*fn)(P...), int64_t blocks, int threads, cudaStream_t s, A... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(std::max<int64_t>(1, blocks)));
-    cfg.blockDim = dim3(threads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fn, P(args)...);
-}
 
 constexpr int kThreads = 256;
 constexpr int64_t kMaxBlocks = 152 * 16;

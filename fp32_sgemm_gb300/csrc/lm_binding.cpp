@@ -122,6 +122,16 @@ Matrix stack(const at::Tensor &t, const char *name, at::ScalarType type, c10::De
     return m;
 }
 
+// Contiguous T x k table beside T tokens (k < 0: any).
+template <class T>
+T *table(const at::Tensor &t, const char *name, at::ScalarType type, c10::Device dev, int64_t rows, int64_t k) {
+    check_kind(t, name, type, dev);
+    if (t.dim() != 2 || (rows >= 0 && t.size(0) != rows) || (k >= 0 && t.size(1) != k) || !t.is_contiguous())
+        fail(PyExc_ValueError, "%s must be a contiguous matrix with a row for each token%s", name,
+             k >= 0 ? " and a column for each of its choices" : "");
+    return static_cast<T *>(const_cast<void *>(t.const_data_ptr()));
+}
+
 template <class T>
 T *vector(PyObject *o, const char *name, at::ScalarType type, c10::Device dev, int64_t n) {
     const at::Tensor &t = tensor(o, name);
@@ -224,6 +234,15 @@ PyObject *guarded(F &&f) {
     }
 }
 
+int64_t whole(PyObject *o, const char *name) {
+    const long long v = PyLong_AsLongLong(o);
+    if (v == -1 && PyErr_Occurred()) {
+        PyErr_Clear();
+        fail(PyExc_TypeError, "%s must be an integer", name);
+    }
+    return v;
+}
+
 bool truth(PyObject *o) {
     const int is = PyObject_IsTrue(o);
     if (is < 0) throw Failed{};
@@ -235,6 +254,8 @@ bool truth(PyObject *o) {
 bool recorded(const at::Tensor &a, const at::Tensor &b) {
     return (a.requires_grad() || b.requires_grad()) && c10::GradMode::is_enabled();
 }
+
+bool recorded(const at::Tensor &a) { return a.requires_grad() && c10::GradMode::is_enabled(); }
 
 PyObject *wrap(const at::Tensor &t) { return THPVariable_Wrap(t); }
 
@@ -392,6 +413,139 @@ PyObject *py_w4_gemm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// (logits, k, normalize, handle, stream) -> (weights, experts)
+PyObject *py_route_topk(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&] {
+        expect(n, 5);
+        const at::Tensor &l = tensor(a[0], "logits");
+        if (recorded(l)) Py_RETURN_NONE;
+        const sgemmDataType_t ty = type_of(l, "logits");
+        const c10::Device dev = device_of(l, "logits");
+        const Matrix ml = matrix(l, "logits", l.scalar_type(), dev);
+        const int64_t k = whole(a[1], "k");
+        const bool normalize = truth(a[2]);
+        if (k < 1 || k > ml.cols)
+            fail(PyExc_ValueError, "k is %lld, of %lld experts", (long long)k, (long long)ml.cols);
+        Call c(a[3], a[4], dev, {a[0]});
+        const at::Tensor weights = make({ml.rows, k}, at::kFloat, dev), experts = make({ml.rows, k}, at::kLong, dev);
+        check(sgemmRouteTopK(c.handle, ty, ml.rows, ml.cols, k, normalize, ml.ptr, ml.ld,
+                             static_cast<float *>(weights.mutable_data_ptr()),
+                             static_cast<int64_t *>(experts.mutable_data_ptr()), c.stream), "sgemmRouteTopK");
+        return Py_BuildValue("NN", wrap(weights), wrap(experts));
+    });
+}
+
+// (logits, experts, dweights, normalize, handle, stream)
+PyObject *py_route_topk_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&] {
+        expect(n, 6);
+        const at::Tensor &l = tensor(a[0], "logits"), &e = tensor(a[1], "experts"), &g = tensor(a[2], "dweights");
+        const sgemmDataType_t ty = type_of(l, "logits");
+        const c10::Device dev = device_of(l, "logits");
+        const Matrix ml = matrix(l, "logits", l.scalar_type(), dev);
+        const int64_t *experts = table<int64_t>(e, "experts", at::kLong, dev, ml.rows, -1);
+        const int64_t k = e.size(1);
+        const float *dweights = table<float>(g, "dweights", at::kFloat, dev, ml.rows, k);
+        const bool normalize = truth(a[3]);
+        if (k < 1 || k > ml.cols)
+            fail(PyExc_ValueError, "%lld choices of %lld experts", (long long)k, (long long)ml.cols);
+        Call c(a[4], a[5], dev, {a[0], a[1], a[2]});
+        const at::Tensor out = make({ml.rows, ml.cols}, l.scalar_type(), dev);
+        check(sgemmRouteTopKGrad(c.handle, ty, ml.rows, ml.cols, k, normalize, ml.ptr, ml.ld, experts, dweights,
+                                 out.mutable_data_ptr(), ml.cols, c.stream), "sgemmRouteTopKGrad");
+        return wrap(out);
+    });
+}
+
+// (x, experts, num_experts, handle, stream) -> (rows, slots, group_ends)
+PyObject *py_expert_dispatch(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&] {
+        expect(n, 5);
+        const at::Tensor &x = tensor(a[0], "x"), &e = tensor(a[1], "experts");
+        if (recorded(x)) Py_RETURN_NONE;
+        const sgemmDataType_t ty = type_of(x, "x");
+        const c10::Device dev = device_of(x, "x");
+        const Matrix mx = matrix(x, "x", x.scalar_type(), dev);
+        const int64_t *experts = table<int64_t>(e, "experts", at::kLong, dev, mx.rows, -1);
+        const int64_t k = e.size(1), G = whole(a[2], "num_experts");
+        if (G < 0) fail(PyExc_ValueError, "num_experts is %lld", (long long)G);
+        if (G > SGEMM_MAX_GROUPS) check(SGEMM_STATUS_NOT_SUPPORTED, "sgemmExpertDispatch");
+        Call c(a[3], a[4], dev, {a[0], a[1]});
+        const at::Tensor rows = make({mx.rows * k, mx.cols}, x.scalar_type(), dev);
+        const at::Tensor slots = make({mx.rows, k}, at::kInt, dev), ends = make({G}, at::kInt, dev);
+        check(sgemmExpertDispatch(c.handle, ty, mx.rows, mx.cols, k, G, mx.ptr, mx.ld, experts, rows.mutable_data_ptr(),
+                                  std::max<int64_t>(mx.cols, 1), static_cast<int32_t *>(slots.mutable_data_ptr()),
+                                  static_cast<int32_t *>(ends.mutable_data_ptr()), c.stream), "sgemmExpertDispatch");
+        return Py_BuildValue("NNN", wrap(rows), wrap(slots), wrap(ends));
+    });
+}
+
+// `like`: the rows, or dy in their place where they are not wanted.
+struct CombineOperands {
+    sgemmDataType_t ty;
+    c10::Device dev;
+    at::ScalarType st;
+    Matrix rows;
+    const int32_t *slots;
+    const float *weights = nullptr;
+    int64_t T, k, D;
+    CombineOperands(PyObject *pr, PyObject *ps, PyObject *pw, PyObject *like) : dev(c10::kCPU) {
+        const char *name = like == pr ? "rows" : "dy";
+        const at::Tensor &t = tensor(like, name), &ts = tensor(ps, "slots");
+        ty = type_of(t, name);
+        dev = device_of(t, name);
+        st = t.scalar_type();
+        slots = table<int32_t>(ts, "slots", at::kInt, dev, -1, -1);
+        T = ts.size(0);
+        k = ts.size(1);
+        rows = matrix(t, name, st, dev);
+        D = rows.cols;
+        if (like != pr) rows = Matrix();
+        else if (rows.rows != T * k)
+            fail(PyExc_ValueError, "rows has %lld rows for %lld slots", (long long)rows.rows, (long long)(T * k));
+        if (pw != Py_None) weights = table<float>(tensor(pw, "weights"), "weights", at::kFloat, dev, T, k);
+    }
+};
+
+// (rows, slots, weights, out, handle, stream)
+PyObject *py_expert_combine(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&] {
+        expect(n, 6);
+        if (a[3] == Py_None && (recorded(tensor(a[0], "rows")) || (a[2] != Py_None && recorded(tensor(a[2], "weights")))))
+            Py_RETURN_NONE;
+        const CombineOperands o(a[0], a[1], a[2], a[0]);
+        if (a[3] != Py_None) matrix(tensor(a[3], "out"), "out", o.st, o.dev, o.T, o.D);   // before it is recorded
+        Call c(a[4], a[5], o.dev, {a[0], a[1], a[2], a[3]});
+        const at::Tensor out = output(a[3], {o.T, o.D}, o.st, o.dev);
+        const Matrix my = matrix(out, "out", o.st, o.dev, o.T, o.D);
+        check(sgemmExpertCombine(c.handle, o.ty, o.T, o.D, o.k, o.rows.ptr, o.rows.ld, o.slots, o.weights, my.ptr,
+                                 my.ld, c.stream), "sgemmExpertCombine");
+        return wrap(out);
+    });
+}
+
+// (dy, rows, slots, weights, need_drows, need_dweights, handle, stream) -> (drows, dweights)
+PyObject *py_expert_combine_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&] {
+        expect(n, 8);
+        const at::Tensor &dy = tensor(a[0], "dy");
+        const bool need_rows = truth(a[4]), need_weights = truth(a[5]);
+        const CombineOperands o(a[1], a[2], a[3], a[1] != Py_None || need_weights ? a[1] : a[0]);
+        const Matrix md = matrix(dy, "dy", o.st, o.dev, o.T, o.D);
+        Call c(a[6], a[7], o.dev, {a[0], a[1], a[2], a[3]});
+        at::Tensor drows, dweights;
+        if (need_rows) drows = make({o.T * o.k, o.D}, o.st, o.dev);
+        if (need_weights) dweights = make({o.T, o.k}, at::kFloat, o.dev);
+        check(sgemmExpertCombineGrad(c.handle, o.ty, o.T, o.D, o.k, md.ptr, md.ld, o.rows.ptr, std::max(o.rows.ld, o.D), o.slots,
+                                     o.weights, need_rows ? drows.mutable_data_ptr() : nullptr,
+                                     std::max<int64_t>(o.D, 1),
+                                     need_weights ? static_cast<float *>(dweights.mutable_data_ptr()) : nullptr, c.stream),
+              "sgemmExpertCombineGrad");
+        return Py_BuildValue("NN", need_rows ? wrap(drows) : Py_NewRef(Py_None),
+                             need_weights ? wrap(dweights) : Py_NewRef(Py_None));
+    });
+}
+
 PyMethodDef methods[] = {
     {"grouped_gemm", reinterpret_cast<PyCFunction>(py_grouped_gemm), METH_FASTCALL, nullptr},
     {"grouped_gemm_weight_grad", reinterpret_cast<PyCFunction>(py_grouped_gemm_weight_grad), METH_FASTCALL, nullptr},
@@ -399,6 +553,11 @@ PyMethodDef methods[] = {
     {"linear_cross_entropy_grad", reinterpret_cast<PyCFunction>(py_linear_cross_entropy_grad), METH_FASTCALL,
      nullptr},
     {"w4_gemm", reinterpret_cast<PyCFunction>(py_w4_gemm), METH_FASTCALL, nullptr},
+    {"route_topk", reinterpret_cast<PyCFunction>(py_route_topk), METH_FASTCALL, nullptr},
+    {"route_topk_grad", reinterpret_cast<PyCFunction>(py_route_topk_grad), METH_FASTCALL, nullptr},
+    {"expert_dispatch", reinterpret_cast<PyCFunction>(py_expert_dispatch), METH_FASTCALL, nullptr},
+    {"expert_combine", reinterpret_cast<PyCFunction>(py_expert_combine), METH_FASTCALL, nullptr},
+    {"expert_combine_grad", reinterpret_cast<PyCFunction>(py_expert_combine_grad), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_lm_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

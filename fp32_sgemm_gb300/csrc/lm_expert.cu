@@ -1,0 +1,383 @@
+// Tokens sorted by expert and back.  Choice a = t k + j of token t goes to row
+// slots[a] of the sorted rows: choices of expert 0 first, each expert's in the
+// order of a, those of no expert behind the last end (row r is then written as
+// ~r in slots, and holds zeros), so that slots names every row once.
+//
+//   dispatch       rows[slots[t, j]] = x[t]
+//   combine        y[t] = sum_j w[t, j] rows[slots[t, j]]      (j in order, FP32, rounded once)
+//   its gradient   drows[slots[t, j]] = w[t, j] dy[t],  dw[t, j] = dy[t] . rows[slots[t, j]]
+//
+// The gradient of a dispatch is a combine without weights.  All three are bound
+// by memory and go by token, so that what a token has once (x, y, dy) is moved
+// once.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "../../include/sgemm_gb300_lm.h"
+#include "lm_expert.h"
+#include "lm_launch.cuh"
+#include "lm_ptx.cuh"
+
+namespace sg {
+namespace {
+
+// ------------------------------------------------------------------- sort
+//
+// One cluster of up to 8 CTAs of 32 warps.  Each warp has a run of the choices,
+// counts it by expert (a histogram of its own in shared memory), the histograms
+// are added up over warps and, through distributed shared memory, over CTAs, and
+// each warp goes over its run again with the row at which its choices of each
+// expert start.  No atomics: the order is that of the choices.
+constexpr int kSortThreads = 1024, kSortWarps = 32, kSortCluster = 8;
+
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// Choice a's expert, G for none.
+__device__ __forceinline__ int bin_of(const int64_t *experts, int64_t a, int n, int G) {
+    if (a >= n) return -1;
+    const int64_t e = experts[a];
+    return e >= 0 && e < G ? (int)e : G;
+}
+
+__global__ void __launch_bounds__(kSortThreads, 1)
+lm_expert_sort_kernel(const int64_t *experts, int n, int G, int32_t *slots, int32_t *ends) {
+    extern __shared__ uint32_t sm[];
+    const int bins = G + 1;
+    uint32_t *total = sm;                        // [bins] this CTA's
+    uint32_t *first = total + bins;              // [bins] row of this CTA's first
+    uint32_t *hist = first + bins;               // [warp][bins]
+    __shared__ uint32_t sums[kSortWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank(), ctas = (int)gridDim.x;
+    griddep_launch_dependents();
+    griddep_wait();
+    for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) hist[i] = 0u;
+    __syncthreads();
+    const int64_t warps = (int64_t)ctas * kSortWarps;
+    const int64_t run = ((n + warps - 1) / warps + 31) / 32 * 32;
+    const int64_t a0 = (rank * kSortWarps + warp) * run, a1 = min(a0 + run, (int64_t)n);
+    uint32_t *own = hist + warp * bins;
+    for (int64_t a = a0; a < a1; a += 32) {
+        const int b = bin_of(experts, a + lane, n, G);
+        const uint32_t same = __match_any_sync(~0u, b);
+        if (b >= 0 && lane == __ffs(same) - 1) own[b] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    for (int b = threadIdx.x; b < bins; b += kSortThreads) {
+        uint32_t sum = 0;
+        for (int w = 0; w < kSortWarps; ++w) {
+            const uint32_t c = hist[w * bins + b];
+            hist[w * bins + b] = sum;
+            sum += c;
+        }
+        total[b] = sum;
+    }
+    cluster_sync();
+    // Rows of the experts before, then of the CTAs before.
+    uint32_t before = 0;
+    for (int b0 = 0; b0 < bins; b0 += kSortThreads) {
+        const int b = b0 + (int)threadIdx.x;
+        uint32_t all = 0, earlier = 0;
+        if (b < bins)
+            for (int c = 0; c < ctas; ++c) {
+                const uint32_t v = ld_cluster(cluster_addr(total + b, (uint32_t)c));
+                all += v;
+                if (c < rank) earlier += v;
+            }
+        uint32_t scan = all;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t o = __shfl_up_sync(~0u, scan, d);
+            if (lane >= d) scan += o;
+        }
+        if (lane == 31) sums[warp] = scan;
+        __syncthreads();
+        uint32_t of_warps = before;
+        for (int w = 0; w < kSortWarps; ++w) {
+            if (w < warp) of_warps += sums[w];
+            before += sums[w];
+        }
+        __syncthreads();
+        if (b < bins) {
+            first[b] = of_warps + scan - all + earlier;
+            if (rank == 0 && b < G) ends[b] = (int32_t)(of_warps + scan);
+        }
+    }
+    // (No CTA leaves, or goes on to write, before the others have read.)
+    cluster_sync();
+    for (int64_t a = a0; a < a1; a += 32) {
+        const int b = bin_of(experts, a + lane, n, G);
+        const uint32_t same = __match_any_sync(~0u, b);
+        const uint32_t below = same & ((1u << lane) - 1u);
+        if (b >= 0) {
+            const int32_t r = (int32_t)(first[b] + own[b] + __popc(below));
+            slots[a + lane] = b < G ? r : ~r;
+        }
+        __syncwarp();
+        if (b >= 0 && below == 0u) own[b] += __popc(same);
+        __syncwarp();
+    }
+}
+
+// ------------------------------------------------------------------- rows
+
+// Pieces of a row that one load or store takes: the widest that every row of
+// the call is aligned to.
+int64_t piece_bytes(std::initializer_list<int64_t> all) {
+    int64_t any = 16;
+    for (int64_t v : all) any |= v;
+    return any & -any;
+}
+int64_t address(const void *p) { return (int64_t)reinterpret_cast<uintptr_t>(p); }
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int64_t kMaxBlocks = 152 * 8;
+
+int64_t blocks_for(int64_t tasks) { return std::min((tasks + kWarps - 1) / kWarps, kMaxBlocks); }
+
+// A warp takes U * 32 pieces of one token at a time.
+template <class P, int U>
+__global__ void __launch_bounds__(kThreads)
+lm_expert_dispatch_kernel(const ExpertRows p, int64_t pieces, int64_t parts) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t tasks = p.T * parts;
+    for (int64_t i = blockIdx.x * (int64_t)kWarps + (threadIdx.x >> 5); i < tasks; i += gridDim.x * (int64_t)kWarps) {
+        const int64_t t = i / parts, c0 = (i - t * parts) * (U * 32) + lane;
+        const P *from = reinterpret_cast<const P *>(static_cast<const char *>(p.x) + t * p.ldx);
+        P v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (c0 + u * 32 < pieces) v[u] = from[c0 + u * 32];
+        for (int j = 0; j < p.k; ++j) {
+            const int32_t slot = p.slots[t * p.k + j];
+            P *to = reinterpret_cast<P *>(static_cast<char *>(p.out) + (int64_t)(slot < 0 ? ~slot : slot) * p.ldo);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (c0 + u * 32 < pieces) to[c0 + u * 32] = slot < 0 ? P{} : v[u];
+        }
+    }
+}
+
+// Elements of a piece as FP32 and back.
+template <class T, class P>
+struct Piece {
+    static constexpr int N = sizeof(P) / sizeof(T);
+    union {
+        P p;
+        T e[N];
+    };
+    __device__ __forceinline__ Piece() {}
+    __device__ __forceinline__ float get(int i) const { return (float)e[i]; }
+    __device__ __forceinline__ void set(int i, float v) {
+        if constexpr (std::is_same_v<T, __half>) e[i] = __float2half_rn(v);
+        else if constexpr (std::is_same_v<T, __nv_bfloat16>) e[i] = __float2bfloat16_rn(v);
+        else e[i] = v;
+    }
+};
+
+// rows outside [0, T k) are none.
+__device__ __forceinline__ bool row_of(const ExpertRows &p, int32_t slot) {
+    return slot >= 0 && slot < p.T * p.k;
+}
+
+template <class T, class P, int U>
+__global__ void __launch_bounds__(kThreads)
+lm_expert_combine_kernel(const ExpertRows p, int64_t pieces, int64_t parts) {
+    griddep_launch_dependents();
+    griddep_wait();
+    using Pc = Piece<T, P>;
+    const int lane = threadIdx.x & 31;
+    const int64_t tasks = p.T * parts;
+    for (int64_t i = blockIdx.x * (int64_t)kWarps + (threadIdx.x >> 5); i < tasks; i += gridDim.x * (int64_t)kWarps) {
+        const int64_t t = i / parts, c0 = (i - t * parts) * (U * 32) + lane;
+        float sum[U][Pc::N];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < Pc::N; ++e) sum[u][e] = 0.f;
+#pragma unroll 4
+        for (int j = 0; j < p.k; ++j) {
+            const int32_t slot = p.slots[t * p.k + j];
+            if (!row_of(p, slot)) continue;
+            const float w = p.weights != nullptr ? p.weights[t * p.k + j] : 1.f;
+            const P *from = reinterpret_cast<const P *>(static_cast<const char *>(p.x) + slot * p.ldx);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (c0 + u * 32 < pieces) {
+                    Pc v;
+                    v.p = from[c0 + u * 32];
+#pragma unroll
+                    for (int e = 0; e < Pc::N; ++e) sum[u][e] = fmaf(w, v.get(e), sum[u][e]);
+                }
+        }
+        P *to = reinterpret_cast<P *>(static_cast<char *>(p.out) + t * p.ldo);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (c0 + u * 32 < pieces) {
+                Pc v;
+#pragma unroll
+                for (int e = 0; e < Pc::N; ++e) v.set(e, sum[u][e]);
+                to[c0 + u * 32] = v.p;
+            }
+    }
+}
+
+// A CTA a token: KC choices at a time, so that dy's pieces meet KC rows.
+constexpr int KC = 8;
+template <class T, class P>
+__global__ void __launch_bounds__(kThreads)
+lm_expert_combine_grad_kernel(const ExpertRows p, int64_t pieces) {
+    griddep_launch_dependents();
+    griddep_wait();
+    using Pc = Piece<T, P>;
+    __shared__ float part[kWarps][KC];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = blockIdx.x;
+    const P *dy = reinterpret_cast<const P *>(static_cast<const char *>(p.x) + t * p.ldx);
+    for (int j0 = 0; j0 < p.k; j0 += KC) {
+        float dot[KC], w[KC];
+        int32_t slot[KC];
+#pragma unroll
+        for (int j = 0; j < KC; ++j) {
+            dot[j] = 0.f;
+            w[j] = 0.f;
+            slot[j] = INT32_MIN;                            // no row at all
+            if (j0 + j < p.k) {
+                slot[j] = p.slots[t * p.k + j0 + j];
+                w[j] = p.weights != nullptr ? p.weights[t * p.k + j0 + j] : 1.f;
+            }
+        }
+        for (int64_t c = threadIdx.x; c < pieces; c += blockDim.x) {
+            Pc g, r[KC];
+            g.p = dy[c];
+            if (p.dweights != nullptr) {
+#pragma unroll
+                for (int j = 0; j < KC; ++j)
+                    if (row_of(p, slot[j]))
+                        r[j].p = reinterpret_cast<const P *>(static_cast<const char *>(p.rows) + slot[j] * p.ldr)[c];
+#pragma unroll
+                for (int j = 0; j < KC; ++j)
+                    if (row_of(p, slot[j]))
+#pragma unroll
+                        for (int e = 0; e < Pc::N; ++e) dot[j] = fmaf(g.get(e), r[j].get(e), dot[j]);
+            }
+            if (p.out != nullptr) {
+#pragma unroll
+                for (int j = 0; j < KC; ++j) {
+                    const int32_t at = slot[j] < 0 ? ~slot[j] : slot[j];
+                    if (!row_of(p, at)) continue;
+                    Pc v;
+#pragma unroll
+                    for (int e = 0; e < Pc::N; ++e) v.set(e, slot[j] < 0 ? 0.f : w[j] * g.get(e));
+                    reinterpret_cast<P *>(static_cast<char *>(p.out) + at * p.ldo)[c] = v.p;
+                }
+            }
+        }
+        if (p.dweights != nullptr) {
+#pragma unroll
+            for (int j = 0; j < KC; ++j)
+#pragma unroll
+                for (int d = 16; d; d >>= 1) dot[j] += __shfl_xor_sync(~0u, dot[j], d);
+            if (lane == 0)
+#pragma unroll
+                for (int j = 0; j < KC; ++j) part[warp][j] = dot[j];
+            __syncthreads();
+            if ((int)threadIdx.x < KC && j0 + (int)threadIdx.x < p.k) {
+                float sum = 0.f;
+                for (int v = 0; v < (int)blockDim.x / 32; ++v) sum += part[v][threadIdx.x];
+                p.dweights[t * p.k + j0 + threadIdx.x] = sum;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+template <class P>
+cudaError_t dispatch_by_piece(const ExpertRows &p, cudaStream_t s) {
+    constexpr int U = 4;
+    const int64_t pieces = p.D * p.elem / (int64_t)sizeof(P), parts = (pieces + U * 32 - 1) / (U * 32);
+    return launch(lm_expert_dispatch_kernel<P, U>, blocks_for(p.T * parts), kThreads, s, p, pieces, parts);
+}
+
+template <class T, class P>
+cudaError_t combine_by_piece(const ExpertRows &p, cudaStream_t s) {
+    constexpr int U = 2;
+    const int64_t pieces = p.D * p.elem / (int64_t)sizeof(P), parts = (pieces + U * 32 - 1) / (U * 32);
+    return launch(lm_expert_combine_kernel<T, P, U>, blocks_for(p.T * parts), kThreads, s, p, pieces, parts);
+}
+
+template <class T, class P>
+cudaError_t grad_by_piece(const ExpertRows &p, cudaStream_t s) {
+    const int64_t pieces = p.D * p.elem / (int64_t)sizeof(P);
+    const int threads = (int)std::min<int64_t>(kThreads, std::max<int64_t>(32, (pieces + 31) / 32 * 32));
+    return launch(lm_expert_combine_grad_kernel<T, P>, p.T, threads, s, p, pieces);
+}
+
+}  // namespace
+
+cudaError_t expert_sort_launch(const int64_t *experts, int n, int G, int32_t *slots, int32_t *ends, cudaStream_t s) {
+    const size_t smem = size_t(G + 1) * (kSortWarps + 2) * 4;
+    if (smem > 48 * 1024) {                       // (for any number of experts: another call may ask for more)
+        const cudaError_t opted = cudaFuncSetAttribute(lm_expert_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       (kRouteMaxExperts + 1) * (kSortWarps + 2) * 4);
+        if (opted != cudaSuccess) return opted;
+    }
+    // A warp has at least 64 choices before there is another CTA.
+    int ctas = 1;
+    while (ctas < kSortCluster && (int64_t)ctas * kSortWarps * 64 < n) ctas *= 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(ctas));
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(ctas);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, lm_expert_sort_kernel, experts, n, G, slots, ends);
+}
+
+cudaError_t expert_dispatch_launch(const ExpertRows &p, cudaStream_t s) {
+    switch (piece_bytes({address(p.x), p.ldx, address(p.out), p.ldo, p.D * p.elem})) {
+        case 16: return dispatch_by_piece<uint4>(p, s);
+        case 8: return dispatch_by_piece<uint2>(p, s);
+        case 4: return dispatch_by_piece<uint32_t>(p, s);
+        default: return dispatch_by_piece<uint16_t>(p, s);
+    }
+}
+
+cudaError_t expert_combine_launch(int type, const ExpertRows &p, cudaStream_t s) {
+    const int64_t piece = piece_bytes({address(p.x), p.ldx, address(p.out), p.ldo, p.D * p.elem});
+    if (type == SGEMM_TYPE_F32)
+        return piece == 16 ? combine_by_piece<float, uint4>(p, s) : combine_by_piece<float, uint32_t>(p, s);
+    if (type == SGEMM_TYPE_F16)
+        return piece == 16 ? combine_by_piece<__half, uint4>(p, s) : combine_by_piece<__half, uint16_t>(p, s);
+    return piece == 16 ? combine_by_piece<__nv_bfloat16, uint4>(p, s) : combine_by_piece<__nv_bfloat16, uint16_t>(p, s);
+}
+
+cudaError_t expert_combine_grad_launch(int type, const ExpertRows &p, cudaStream_t s) {
+    int64_t piece = piece_bytes({address(p.x), p.ldx, p.D * p.elem});
+    if (p.out != nullptr) piece = std::min(piece, piece_bytes({address(p.out), p.ldo}));
+    if (p.dweights != nullptr) piece = std::min(piece, piece_bytes({address(p.rows), p.ldr}));
+    if (type == SGEMM_TYPE_F32)
+        return piece == 16 ? grad_by_piece<float, uint4>(p, s) : grad_by_piece<float, uint32_t>(p, s);
+    if (type == SGEMM_TYPE_F16)
+        return piece == 16 ? grad_by_piece<__half, uint4>(p, s) : grad_by_piece<__half, uint16_t>(p, s);
+    return piece == 16 ? grad_by_piece<__nv_bfloat16, uint4>(p, s) : grad_by_piece<__nv_bfloat16, uint16_t>(p, s);
+}
+
+}  // namespace sg

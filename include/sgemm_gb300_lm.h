@@ -7,7 +7,10 @@
  *   - softmax cross entropy over a vocabulary whose logits are never kept,
  *     and its gradients (sgemmCrossEntropy, sgemmCrossEntropyGrad);
  *   - products of a few rows with 4-bit weights and group scales
- *     (sgemmW4).
+ *     (sgemmW4);
+ *   - a router's choice of experts and its gradient (sgemmRouteTopK), tokens
+ *     sorted by expert and brought back, and their gradients
+ *     (sgemmExpertDispatch, sgemmExpertCombine).
  *
  * The conventions of sgemm_gb300.h hold: row-major matrices with explicit
  * row pitches in elements, device pointers, work only enqueued on `stream`,
@@ -210,6 +213,83 @@ sgemmStatus_t sgemmW4(sgemmHandle_t handle, sgemmDataType_t type, int64_t M, int
 
 sgemmStatus_t sgemmW4WorkspaceSize(sgemmHandle_t handle, sgemmDataType_t type, int64_t M, int64_t N, int64_t K,
                                    int group, size_t *bytes);
+
+/*
+ * A router's choice.  Each of T tokens has E logits (pitch ldl); the k largest
+ * are chosen, in falling order, the lower index first among equals (0 and -0
+ * are equal; NaN counts as larger than every number).  With
+ * p = softmax(logits[t, :]):
+ *
+ *   experts[t * k + j] = e_j
+ *   weights[t * k + j] = p[e_j]                            normalize == 0
+ *                      = p[e_j] / sum_i p[e_i]             otherwise
+ *
+ * A logit of -inf is an expert that is masked: it is never chosen, and where
+ * fewer than k are left the remaining choices are -1 with weight 0.  (The lowest
+ * finite value of a type is a number like any other.)  A NaN or +inf among a
+ * token's logits makes its weights NaN.  Weights and sums are FP32 in every type.
+ *
+ * The gradient by the logits from that by the weights, for the same choice,
+ * S being the experts chosen (-1 and what lies outside [0, E) take no part):
+ *
+ *   dlogits[t, e] = p_e ([e in S] dweights_e - sum_S p_i dweights_i)
+ *
+ * with the normalized weights in the place of p, and 0 outside S, if normalize.
+ *
+ * INVALID_VALUE: negative T, E < 1, k < 1, k > E, NULL pointers with nonzero
+ * extent, and as for sgemmGrouped().  NOT_SUPPORTED: E > 1024, k > 32, T * k of
+ * 2^31 or more.  T == 0 is a no-op.  No workspace.
+ */
+sgemmStatus_t sgemmRouteTopK(sgemmHandle_t handle, sgemmDataType_t type, int64_t T, int64_t E, int64_t k,
+                             int normalize, const void *logits, int64_t ldl, float *weights, int64_t *experts,
+                             cudaStream_t stream);
+
+sgemmStatus_t sgemmRouteTopKGrad(sgemmHandle_t handle, sgemmDataType_t type, int64_t T, int64_t E, int64_t k,
+                                 int normalize, const void *logits, int64_t ldl, const int64_t *experts,
+                                 const float *dweights, void *dlogits, int64_t ldd, cudaStream_t stream);
+
+/*
+ * Tokens sorted by expert: X is T x D, experts T x k (any number outside
+ * [0, G) is no expert; a token may choose an expert more than once).  The T * k
+ * choices are sorted by expert, each expert's in their order in `experts`, and
+ *
+ *   rows[slots[t, j], :] = X[t, :]
+ *   groupEnds[g] = the row at which expert g's rows end     (as sgemmGrouped() takes them)
+ *
+ * Choices of no expert come behind the last end: their row r holds zeros and
+ * is written as ~r (that is -1 - r) in slots, which so names each of the T * k
+ * rows once.  rows is (T * k) x D.  The gradient by X is
+ * sgemmExpertCombine() of the rows' gradient without weights.
+ *
+ * Back again, with FP32 weights [T, k] (NULL: 1):
+ *
+ *   Y[t, :] = sum_j weights[t, j] * rows[slots[t, j], :]     over slots[t, j] in [0, T * k)
+ *
+ * in the order of j, in FP32, rounded once.  Its gradients, either of which
+ * may be NULL:
+ *
+ *   dRows[slots[t, j], :] = weights[t, j] * dY[t, :]          (row ~slots[t, j]: zeros)
+ *   dWeights[t, j] = dY[t, :] . rows[slots[t, j], :]          (0 for a negative slot)
+ *
+ * slots are those of sgemmExpertDispatch(), or any that name each row at most
+ * once: rows named by none keep in dRows what was there, of one named twice
+ * either gradient is written, and what lies outside the rows is left out.
+ *
+ * INVALID_VALUE, MISALIGNED as for sgemmGrouped().  NOT_SUPPORTED: T * k, D of
+ * 2^31 or more, G > SGEMM_MAX_GROUPS.  No workspace.
+ */
+sgemmStatus_t sgemmExpertDispatch(sgemmHandle_t handle, sgemmDataType_t type, int64_t T, int64_t D, int64_t k,
+                                  int64_t G, const void *X, int64_t ldx, const int64_t *experts, void *rows,
+                                  int64_t ldr, int32_t *slots, int32_t *groupEnds, cudaStream_t stream);
+
+sgemmStatus_t sgemmExpertCombine(sgemmHandle_t handle, sgemmDataType_t type, int64_t T, int64_t D, int64_t k,
+                                 const void *rows, int64_t ldr, const int32_t *slots, const float *weights, void *Y,
+                                 int64_t ldy, cudaStream_t stream);
+
+sgemmStatus_t sgemmExpertCombineGrad(sgemmHandle_t handle, sgemmDataType_t type, int64_t T, int64_t D, int64_t k,
+                                     const void *dY, int64_t lddy, const void *rows, int64_t ldr,
+                                     const int32_t *slots, const float *weights, void *dRows, int64_t lddr,
+                                     float *dWeights, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
