@@ -18,6 +18,7 @@ _BINDING_NAMES = {
 _LM_NAMES = {
     "grouped_gemm", "grouped_gemm_weight_grad", "linear_cross_entropy", "linear_cross_entropy_grad",
     "w4_gemm", "route_topk", "route_topk_grad", "expert_dispatch", "expert_combine", "expert_combine_grad",
+    "int8_quantize", "int8_gemm", "int8_grouped_gemm",
 }
 
 

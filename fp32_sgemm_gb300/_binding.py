@@ -117,6 +117,11 @@ SIGNATURES = {
                       _vp, _i64, _vp, _i64, _vp]),
     "sgemmW4WorkspaceSize": (_st, [_vp, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int,
                                    ctypes.POINTER(ctypes.c_size_t)]),
+    "sgemmInt8Quantize": (_st, [_vp, ctypes.c_int, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp]),
+    "sgemmInt8": (_st, [_vp, ctypes.c_int, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64,
+                        _i64, _vp, _vp, _vp, _i64, _vp]),
+    "sgemmInt8WorkspaceSize": (_st, [_vp, ctypes.c_int, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, _i64, _vp,
+                                     _i64, _i64, ctypes.POINTER(ctypes.c_size_t)]),
     "sgemmRouteTopK": (_st, [_vp, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _vp, _i64, _vp, _vp, _vp]),
     "sgemmRouteTopKGrad": (_st, [_vp, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _vp, _i64, _vp, _vp, _vp,
                                  _i64, _vp]),

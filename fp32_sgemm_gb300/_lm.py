@@ -108,6 +108,16 @@ class _W4Gemm(torch.autograd.Function):
         raise NotImplementedError("w4_gemm has no gradient")
 
 
+class _Int8Gemm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, scales, x_scales, group_ends, dtype, handle, stream):
+        return _c.int8_gemm(x, w, scales, x_scales, group_ends, dtype, None, handle, stream)
+
+    @staticmethod
+    def backward(ctx, dy):
+        raise NotImplementedError("int8_gemm and int8_grouped_gemm have no gradient")
+
+
 class _RouteTopK(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, k, normalize, handle, stream):
@@ -264,3 +274,40 @@ def expert_combine_grad(dy, rows, slots, weights=None, *, handle=None, stream=No
     """Gradients (drows [T * k, D], dweights [T, k] float32) of expert_combine()
     for the gradient dy [T, D] by y.  Rows behind the last end get zeros."""
     return _c.expert_combine_grad(dy, rows, slots, weights, True, True, _handle(rows, handle, "rows"), stream)
+
+
+def int8_quantize(x, *, handle=None, stream=None):
+    """Rows of x [T, K] as 8-bit integers with a scale each: (q, scales), int8
+    [T, K] and float32 [T].
+
+    scales[t] = max |x[t]| / 127, q = x / scales to the nearest integer (ties to
+    even).  A row with an infinity or a NaN has scale NaN.  Weights are quantised
+    the same way, a row per output channel.
+    """
+    return _c.int8_quantize(x, _handle(x, handle), stream)
+
+
+def int8_gemm(x, w, scales, *, x_scales=None, dtype=None, out=None, handle=None, stream=None):
+    """y = x @ w.T in 8-bit integers with scales for each token and channel;
+    returns y [T, N].
+
+    w [N, K] int8 with scales [N] float32; x [T, K] float32, float16 or bfloat16,
+    each row of which becomes integers as by int8_quantize(), or int8 with
+    x_scales [T] float32 (quantised once for several products).
+    y[t, n] = x_scales[t] * scales[n] * (the exact sum of q[t, k] * w[n, k]), in
+    dtype (x's if it has one).
+    """
+    handle = _handle(x, handle)
+    y = _c.int8_gemm(x, w, scales, x_scales, None, dtype, out, handle, stream)
+    return _Int8Gemm.apply(x, w, scales, x_scales, None, dtype, handle, stream) if y is None else y
+
+
+def int8_grouped_gemm(x, w, scales, group_ends, *, x_scales=None, dtype=None, out=None, handle=None, stream=None):
+    """int8_gemm() by group: w [G, N, K] int8 with scales [G, N], the rows of x
+    sorted by group and group_ends [G] as for grouped_gemm().  Rows behind the
+    last end get zeros."""
+    if group_ends is None:
+        raise TypeError("group_ends must be a torch.Tensor")
+    handle = _handle(x, handle)
+    y = _c.int8_gemm(x, w, scales, x_scales, group_ends, dtype, out, handle, stream)
+    return _Int8Gemm.apply(x, w, scales, x_scales, group_ends, dtype, handle, stream) if y is None else y

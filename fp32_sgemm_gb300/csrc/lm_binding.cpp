@@ -12,6 +12,7 @@
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
@@ -546,6 +547,84 @@ PyObject *py_expert_combine_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// (x, handle, stream) -> (q, scales)
+PyObject *py_int8_quantize(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&] {
+        expect(n, 3);
+        const at::Tensor &x = tensor(a[0], "x");
+        const sgemmDataType_t ty = type_of(x, "x");
+        const c10::Device dev = device_of(x, "x");
+        const Matrix mx = matrix(x, "x", x.scalar_type(), dev);
+        Call c(a[1], a[2], dev, {a[0]});
+        const at::Tensor q = make({mx.rows, mx.cols}, at::kChar, dev), scales = make({mx.rows}, at::kFloat, dev);
+        check(sgemmInt8Quantize(c.handle, ty, mx.rows, mx.cols, mx.ptr, mx.ld,
+                                static_cast<int8_t *>(q.mutable_data_ptr()), std::max<int64_t>(mx.cols, 1),
+                                static_cast<float *>(scales.mutable_data_ptr()), c.stream), "sgemmInt8Quantize");
+        return Py_BuildValue("NN", wrap(q), wrap(scales));
+    });
+}
+
+// (x, w, scales, x_scales, group_ends, dtype, out, handle, stream); group_ends
+// None: one matrix.
+PyObject *py_int8_gemm(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&] {
+        expect(n, 9);
+        const at::Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "w"), &s = tensor(a[2], "scales");
+        const bool integers = a[3] != Py_None, grouped = a[4] != Py_None;
+        if (a[6] == Py_None &&
+            (recorded(x, s) || (integers && recorded(tensor(a[3], "x_scales")))))
+            Py_RETURN_NONE;
+        const c10::Device dev = device_of(x, "x");
+        if (integers && x.scalar_type() != at::kChar)
+            fail(PyExc_TypeError, "x must be int8 where x_scales are given, got %s", type_name(x.scalar_type()));
+        const sgemmDataType_t from = integers ? SGEMM_TYPE_S8 : type_of(x, "x");
+        at::ScalarType st = x.scalar_type();
+        if (a[5] != Py_None) {
+            if (!THPDtype_Check(a[5])) fail(PyExc_TypeError, "dtype must be a torch.dtype");
+            st = reinterpret_cast<THPDtype *>(a[5])->scalar_type;
+        } else if (a[6] != Py_None) {
+            st = tensor(a[6], "out").scalar_type();
+        } else if (integers) {
+            fail(PyExc_TypeError, "dtype (or out) must be given with x of integers");
+        }
+        if (st != at::kFloat && st != at::kHalf && st != at::kBFloat16)
+            fail(PyExc_TypeError, "the result must be float32, float16 or bfloat16, not %s", type_name(st));
+        const sgemmDataType_t to = st == at::kFloat ? SGEMM_TYPE_F32 : st == at::kHalf ? SGEMM_TYPE_F16 : SGEMM_TYPE_BF16;
+        const Matrix mx = matrix(x, "x", x.scalar_type(), dev);
+        const int64_t T = mx.rows, K = mx.cols;
+        Matrix mw;
+        int64_t G = 1, N;
+        if (grouped) {
+            if (w.dim() != 3) fail(PyExc_ValueError, "w must be a 3-D tensor [groups, channels, columns of x]");
+            G = w.size(0);
+            N = w.size(1);
+            mw = stack(w, "w", at::kChar, dev, G, N, K);
+            check_kind(s, "scales", at::kFloat, dev);
+            if (s.dim() != 2 || s.size(0) != G || s.size(1) != N || !s.is_contiguous())
+                fail(PyExc_ValueError, "scales must be a contiguous matrix with a row for each group and a column for "
+                                       "each of w's channels");
+        } else {
+            mw = matrix(w, "w", at::kChar, dev, -1, K);
+            N = mw.rows;
+            vector<float>(a[2], "scales", at::kFloat, dev, N);
+        }
+        const float *scales = static_cast<const float *>(s.const_data_ptr());
+        const float *xs = integers ? vector<float>(a[3], "x_scales", at::kFloat, dev, T) : nullptr;
+        const int32_t *ends = grouped ? vector<int32_t>(a[4], "group_ends", at::kInt, dev, G) : nullptr;
+        if (a[6] != Py_None) matrix(tensor(a[6], "out"), "out", st, dev, T, N);   // before it is recorded
+        Call c(a[7], a[8], dev, {a[0], a[1], a[2], a[3], a[4], a[6]});
+        const at::Tensor out = output(a[6], {T, N}, st, dev);
+        const Matrix my = matrix(out, "out", st, dev, T, N);
+        size_t need = 0;
+        check(sgemmInt8WorkspaceSize(c.handle, from, to, T, N, K, G, mx.ptr, mx.ld, static_cast<const int8_t *>(mw.ptr),
+                                     mw.ld, mw.stride, &need), "sgemmInt8WorkspaceSize");
+        c.workspace(need);
+        check(sgemmInt8(c.handle, from, to, T, N, K, G, mx.ptr, mx.ld, xs, static_cast<const int8_t *>(mw.ptr), mw.ld,
+                        mw.stride, scales, ends, my.ptr, my.ld, c.stream), "sgemmInt8");
+        return wrap(out);
+    });
+}
+
 PyMethodDef methods[] = {
     {"grouped_gemm", reinterpret_cast<PyCFunction>(py_grouped_gemm), METH_FASTCALL, nullptr},
     {"grouped_gemm_weight_grad", reinterpret_cast<PyCFunction>(py_grouped_gemm_weight_grad), METH_FASTCALL, nullptr},
@@ -558,6 +637,8 @@ PyMethodDef methods[] = {
     {"expert_dispatch", reinterpret_cast<PyCFunction>(py_expert_dispatch), METH_FASTCALL, nullptr},
     {"expert_combine", reinterpret_cast<PyCFunction>(py_expert_combine), METH_FASTCALL, nullptr},
     {"expert_combine_grad", reinterpret_cast<PyCFunction>(py_expert_combine_grad), METH_FASTCALL, nullptr},
+    {"int8_quantize", reinterpret_cast<PyCFunction>(py_int8_quantize), METH_FASTCALL, nullptr},
+    {"int8_gemm", reinterpret_cast<PyCFunction>(py_int8_gemm), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_lm_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

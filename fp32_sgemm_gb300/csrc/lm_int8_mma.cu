@@ -1,0 +1,395 @@
+// Products of many rows of 8-bit integers with 8-bit weights, by group or not,
+// on the tcgen05 tensor cores:
+//
+//   y[t, n] = sx[t] sw[n] sum_k x[t, k] w[n, k]
+//
+// sm_103a's tensor cores take no 8-bit integers, so both operands become f16
+// (exactly).  x, which is small or needed by many tiles, is f16 in memory when
+// the kernel begins; the weights are read as the bytes they are and become f16
+// on their way into tensor memory, where the MMA takes its A operand from: four
+// warps load a row of a 128-byte tile each lane, turn four bytes at a time into
+// two pairs of f16 and store them to the lane's columns.  Through shared memory
+// instead, the f16 weights would be written and read there beside x: 80 KB for
+// 512 cycles of MMAs, which is more than it moves.
+//
+// Tiles, groups and SM pairs are those of lm_mma.cuh: 256 rows of W by up to 192
+// tokens (two accumulators of 192 columns and four slots of 64 columns of K fill
+// the 512 columns of tensor memory).  An accumulator takes 1024 terms, whose sum
+// FP32 holds exactly; the epilogue's warps add them up as 32-bit integers.
+//
+// Warps: 0 copies, 1 issues the MMAs, 2 to 5 convert, 6 to 13 are the epilogue.
+#include <type_traits>
+
+#include "lm_int8.h"
+#include "lm_mma.cuh"
+
+namespace sg {
+namespace {
+
+struct Int8Tile {
+    static constexpr int GRAN = 32, TILE_M = 256, BN = kInt8TileN, BK = kInt8BlockK;
+    static constexpr int STAGES = 5, SLOTS = 4;
+    static constexpr int A_BYTES = 128 * BK, B_CHUNK = BN / 2 * 128, STAGE_BYTES = A_BYTES + 2 * B_CHUNK;
+    static constexpr int CONV_WARPS = 4, EPI_WARPS = 8, SLAB = BN / 2;
+    static constexpr int THREADS = (2 + CONV_WARPS + EPI_WARPS) * 32;
+    static constexpr int TMEM_COLS = 512, SLOT0 = 2 * BN, SLOT_COLS = 32;
+    static constexpr int BARS = 3 * STAGES + 2 * SLOTS + 5;
+    static constexpr int STG = 32 * 17, STAGING = EPI_WARPS * STG * 4;
+    static constexpr int FIXED = STAGES * STAGE_BYTES + ((BARS * 8 + 16 + 15) / 16) * 16 + STAGING + 1024;
+    static constexpr int RUN_BLOCKS = kInt8Run / BK;
+    static_assert(SLOT0 + SLOTS * SLOT_COLS <= TMEM_COLS && B_CHUNK % 1024 == 0 && A_BYTES % 1024 == 0, "");
+    static_assert(FIXED + 8 * (kLmMaxGroups + 2) <= 227 * 1024, "room for the group tables");
+};
+
+__device__ __forceinline__ void mma_f16_pair_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// 32 columns of this lane.
+__device__ __forceinline__ void tmem_st_32cols(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+        :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+           "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+           "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Four integers as two pairs of f16: a byte plus 128 under the leading bits of
+// 1024, less 1152.
+__device__ __forceinline__ void to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    w ^= 0x80808080u;
+    const uint32_t magic = 0x64646464u, less = 0x64806480u;
+    const uint32_t l = __byte_perm(w, magic, 0x4140), h = __byte_perm(w, magic, 0x4342);
+    const __half2 dl = __hsub2(*reinterpret_cast<const __half2 *>(&l), *reinterpret_cast<const __half2 *>(&less));
+    const __half2 dh = __hsub2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&less));
+    lo = *reinterpret_cast<const uint32_t *>(&dl);
+    hi = *reinterpret_cast<const uint32_t *>(&dh);
+}
+
+// tmW: bytes {K, N, G}, boxes of 128 x 128.  tmX: f16 {K, T}, boxes of 64 x tile_n / 2.
+__global__ void __launch_bounds__(Int8Tile::THREADS, 1)
+lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                   const __grid_constant__ Int8Args q) {
+    using Tile = Int8Tile;
+    constexpr int STAGES = Tile::STAGES, SLOTS = Tile::SLOTS, BN = Tile::BN, SLAB = Tile::SLAB;
+    const LmArgs &p = q.lm;
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+    unsigned char *smem = smem_raw + pad;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * Tile::STAGE_BYTES);
+    uint64_t *wfull = bars;                     // this SM's bytes of W have landed
+    uint64_t *xfull = wfull + STAGES;           // rank 0: both SMs' x
+    uint64_t *empty = xfull + STAGES;           // MMAs -> copies
+    uint64_t *ready = empty + STAGES;           // rank 0: both SMs' slot of W is converted
+    uint64_t *taken = ready + SLOTS;            // MMAs -> converting warps
+    uint64_t *tfull = taken + SLOTS;            // MMAs -> epilogue, per accumulator
+    uint64_t *tempty = tfull + 2;               // epilogue -> MMAs
+    uint64_t *drain = tempty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Tile::BARS);
+    volatile uint32_t *progress = tmem_slot + 1;
+    unsigned char *after = reinterpret_cast<unsigned char *>(bars) + ((Tile::BARS * 8 + 16 + 15) / 16) * 16;
+    float *staging = reinterpret_cast<float *>(after);
+    int *g_start = reinterpret_cast<int *>(after + Tile::STAGING);
+    uint32_t *g_prefix = reinterpret_cast<uint32_t *>(g_start + p.G + 2);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+
+    if (warp == 0) tmem_alloc_pair(tmem_slot, Tile::TMEM_COLS);
+    if (threadIdx.x == 32) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&wfull[s], 1);
+            mbar_init(&xfull[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < SLOTS; ++s) {
+            mbar_init(&ready[s], 2 * Tile::CONV_WARPS);
+            mbar_init(&taken[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull[b], 1);
+            mbar_init(&tempty[b], 2 * Tile::EPI_WARPS);
+        }
+        mbar_init(drain, 1);
+        *progress = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&tmW);
+        prefetch_tensormap(&tmX);
+    }
+    griddep_launch_dependents();
+    griddep_wait();
+    if (warp == 2) {
+        if (p.ends != nullptr) {
+            lm_group_tables<Tile, kRagN>(p, g_start, g_prefix, lane);
+        } else if (lane == 0) {
+            const uint32_t tiles = (uint32_t)((p.T + p.tile_n - 1) / p.tile_n) * (uint32_t)p.tiles_m;
+            g_start[0] = 0; g_start[1] = g_start[2] = p.T;
+            g_prefix[0] = 0; g_prefix[1] = g_prefix[2] = tiles;
+        }
+    }
+    tc_fence_before();
+    __syncwarp();               // (the barriers, too, take whole warps)
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
+    const int slot0 = (int)(blockIdx.x >> 1), slots = (int)(gridDim.x >> 1);
+    const int num_tiles = (int)g_prefix[p.G + 1] * p.splits;
+
+    if (warp == 0) {
+        // ---------------- copies (one elected lane issues) ----------------
+        int stage = 0, issued = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        const uint32_t x_bytes = (uint32_t)(p.tile_n / 2 * 128) * 2;       // of this SM, both halves of the block
+        const uint32_t xfull0 = cluster_addr(&xfull[0], 0);
+        for (int t = slot0; ok && t < num_tiles; t += slots) {
+            const LmWork w = lm_work<Tile, kRagN>(p, g_start, g_prefix, t);
+            const int mw = w.m0 + (int)rank * 128;
+            const int nx = w.n0 + (int)rank * (w.nmma >> 1);
+            for (int kb = 0; kb < w.nkb; ++kb) {
+                if (p.withhold == kWithholdRefill && issued >= STAGES) { ok = false; break; }
+                if (!mbar_wait_bounded<true>(&empty[stage], phase ^ 1u, p.timeout_ns)) {
+                    if (lane == 0) record_error(p.err, kSiteProducerEmpty);
+                    ok = false;
+                }
+                ok = __all_sync(~0u, ok);
+                if (!ok) break;
+                unsigned char *sw = smem + stage * Tile::STAGE_BYTES, *sx = sw + Tile::A_BYTES;
+                const int kc = (w.kb0 + kb) * Tile::BK;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&wfull[stage], Tile::A_BYTES);
+                    tma_load_3d(sw, &tmW, &wfull[stage], kc, mw, w.g);
+                    if (rank == 0) mbar_arrive_expect_tx(&xfull[stage], 2 * x_bytes);
+                    tma_load_3d_pair(sx, &tmX, xfull0 + (uint32_t)stage * 8u, kc, nx, 0);
+                    tma_load_3d_pair(sx + Tile::B_CHUNK, &tmX, xfull0 + (uint32_t)stage * 8u, kc + 64, nx, 0);
+                }
+                __syncwarp();
+                ++issued;
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                    if (lane == 31) *progress = (uint32_t)issued;
+                }
+            }
+        }
+        if (!ok) {
+            // Let this CTA's own copies land before it can exit (rank 1 sees
+            // those of x as the release of its stages).
+            const int pending = issued < STAGES ? issued : STAGES;
+            for (int back = 1; back <= pending; ++back) {
+                int s = stage - back;
+                uint32_t ph = phase;
+                if (s < 0) { s += STAGES; ph ^= 1u; }
+                mbar_wait_bounded(&wfull[s], ph, p.timeout_ns);
+                mbar_wait_bounded<true>(rank == 0 ? &xfull[s] : &empty[s], ph, p.timeout_ns);
+            }
+        }
+    } else if (warp == 1 && rank == 0) {
+        // ---------------- MMAs (one elected lane of a uniform warp) ----------------
+        const uint64_t db0 = smem_desc_k_sw128(smem_u32(smem) + Tile::A_BYTES);
+        int stage = 0, gc = 0;
+        uint32_t phase = 0, half = 0;            // halves of a block so far: slot and its phase
+        bool ok = true;
+        for (int t = slot0; ok && t < num_tiles; t += slots) {
+            const LmWork w = lm_work<Tile, kRagN>(p, g_start, g_prefix, t);
+            const uint32_t idesc = idesc_f16(0, false, false, Tile::TILE_M, w.nmma);
+            uint32_t d_tmem = 0;
+            for (int kb = 0; kb < w.nkb; ++kb) {
+                const bool first = kb % Tile::RUN_BLOCKS == 0;
+                const bool last = kb == w.nkb - 1 || kb % Tile::RUN_BLOCKS == Tile::RUN_BLOCKS - 1;
+                if (first) {
+                    const int ab = gc & 1;
+                    if (!mbar_wait_bounded<true>(&tempty[ab], ((uint32_t)(gc >> 1) & 1u) ^ 1u, p.timeout_ns)) {
+                        if (lane == 0) record_error(p.err, kSiteConsumerFull);
+                        ok = false;
+                    }
+                    ok = __all_sync(~0u, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    d_tmem = tmem_base + (uint32_t)(ab * BN);
+                }
+                if (!mbar_wait_bounded<true>(&xfull[stage], phase, downstream_limit(p.timeout_ns))) {
+                    if (lane == 0) record_error(p.err, kSiteConsumerFull);
+                    ok = false;
+                }
+                ok = __all_sync(~0u, ok);
+                if (!ok) break;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t s = half % SLOTS, ph = (half / SLOTS) & 1u;
+                    if (ok && !mbar_wait_bounded<true>(&ready[s], ph, 2 * downstream_limit(p.timeout_ns))) {
+                        if (lane == 0) record_error(p.err, kSiteConsumerFull);
+                        ok = false;
+                    }
+                    ok = __all_sync(~0u, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t a = tmem_base + Tile::SLOT0 + s * Tile::SLOT_COLS;
+                        const uint64_t b = db0 + (uint64_t)(stage * (Tile::STAGE_BYTES >> 4) + h * (Tile::B_CHUNK >> 4));
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_f16_pair_ts(d_tmem, a + kk * 8, b + kk * 2, idesc, first && h == 0 && kk == 0 ? 0u : 1u);
+                        mma_commit_pair_mc(&taken[s], 0x3);
+                        if (h == 1) {
+                            if (p.withhold != kWithholdRelease) mma_commit_pair_mc(&empty[stage], 0x3);
+                            if (last) mma_commit_pair_mc(&tfull[gc & 1], 0x3);
+                        }
+                    }
+                    __syncwarp();
+                    ++half;
+                }
+                if (!ok) break;
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                if (last) ++gc;
+            }
+        }
+        if (elect_one()) mma_commit_pair(drain);
+        __syncwarp();
+        mbar_wait_bounded(drain, 0u, p.timeout_ns);
+    } else if (warp >= 2 && warp < 2 + Tile::CONV_WARPS) {
+        // ---------------- W into tensor memory ----------------
+        const int quarter = warp & 3, row = quarter * 32 + lane;
+        const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16) + Tile::SLOT0;
+        const uint32_t ready0 = cluster_addr(&ready[0], 0);
+        int stage = 0;
+        uint32_t phase = 0, half = 0;
+        bool ok = true;
+        for (int t = slot0; ok && t < num_tiles; t += slots) {
+            const LmWork w = lm_work<Tile, kRagN>(p, g_start, g_prefix, t);
+            for (int kb = 0; kb < w.nkb; ++kb) {
+                ok = __all_sync(~0u, mbar_wait_bounded(&wfull[stage], phase, downstream_limit(p.timeout_ns)));
+                if (!ok) {
+                    if (lane == 0) record_error(p.err, kSiteConsumerFull);
+                    break;
+                }
+                const unsigned char *sw = smem + stage * Tile::STAGE_BYTES + row * 128;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t r[32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(sw + (((h * 4 + c) ^ (row & 7)) << 4));
+                        to_f16(v.x, r[8 * c], r[8 * c + 1]);
+                        to_f16(v.y, r[8 * c + 2], r[8 * c + 3]);
+                        to_f16(v.z, r[8 * c + 4], r[8 * c + 5]);
+                        to_f16(v.w, r[8 * c + 6], r[8 * c + 7]);
+                    }
+                    const uint32_t s = half % SLOTS, ph = (half / SLOTS) & 1u;
+                    ok = ok && mbar_wait_bounded<true>(&taken[s], ph ^ 1u, 2 * downstream_limit(p.timeout_ns));
+                    ok = __all_sync(~0u, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    tmem_st_32cols(lane_base + s * Tile::SLOT_COLS, r);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(ready0 + s * 8u);
+                    ++half;
+                }
+                if (!ok) {
+                    if (lane == 0) record_error(p.err, kSiteConsumerFull);
+                    break;
+                }
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+            }
+        }
+    } else if (warp >= 2 + Tile::CONV_WARPS) {
+        // ---------------- epilogue ----------------
+        const int quarter = warp & 3, ew = warp - 2 - Tile::CONV_WARPS;
+        const int slab0 = (ew >> 2) * SLAB;
+        float *stg = staging + ew * Tile::STG;
+        const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
+        int gc = 0;
+        bool ok = true;
+        for (int t = slot0; ok && t < num_tiles; t += slots) {
+            const LmWork w = lm_work<Tile, kRagN>(p, g_start, g_prefix, t);
+            const int row0 = w.m0 + (int)rank * 128 + quarter * 32;       // first channel of this warp
+            int sum[SLAB];
+#pragma unroll
+            for (int c = 0; c < SLAB; ++c) sum[c] = 0;
+            for (int kb = 0; kb < w.nkb; kb += Tile::RUN_BLOCKS) {
+                ok = __all_sync(~0u, lm_wait_working<true>(&tfull[gc & 1], (uint32_t)(gc >> 1) & 1u,
+                                                           downstream_limit(p.timeout_ns), progress));
+                if (!ok) {
+                    if (lane == 0) record_error(p.err, kSiteConsumerFull);
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t taddr = lane_base + (uint32_t)((gc & 1) * BN + slab0);
+#pragma unroll
+                for (int c0 = 0; c0 < SLAB; c0 += 16) {
+                    if (slab0 + c0 < w.nvalid) {
+                        float r[16];
+                        tmem_ld_16cols(taddr + (uint32_t)c0, r);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) sum[c0 + i] += __float2int_rn(r[i]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster_relaxed(cluster_addr(&tempty[gc & 1], 0));
+                ++gc;
+            }
+            if (!ok) break;
+            const int f = min(row0 + lane, p.M - 1);
+            const float ws = w.g < p.G && p.splits == 1 ? q.scales[(int64_t)w.g * p.M + f] : 0.f;
+#pragma unroll
+            for (int c0 = 0; c0 < SLAB; c0 += 32) {
+                const int col = slab0 + c0;
+                if (col < w.nvalid && row0 < p.M) {
+                    const int cnt = min(32, w.nvalid - col), n = w.n0 + col;
+                    float v[32];
+                    if (p.splits > 1) {
+                        // (Bits of the integers: the store does not look at them.)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __int_as_float(sum[c0 + i]);
+                        lm_store_cols(p, static_cast<float *>(p.C) + w.s * p.stride_c, row0, n, cnt, v, stg, lane);
+                        if (w.s == 0 && row0 == 0 && lane < cnt) q.row_group[n + lane] = w.g < p.G ? w.g : -1;
+                    } else {
+                        const float xs = w.g < p.G && lane < cnt ? q.x_scales[n + lane] : 0.f;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = (float)sum[c0 + i] * __shfl_sync(~0u, xs, i) * ws;
+                        if (p.out == kOutF32) lm_store_cols(p, static_cast<float *>(p.C), row0, n, cnt, v, stg, lane);
+                        else if (p.out == kOutF16) lm_store_cols(p, static_cast<__half *>(p.C), row0, n, cnt, v, stg, lane);
+                        else lm_store_cols(p, static_cast<__nv_bfloat16 *>(p.C), row0, n, cnt, v, stg, lane);
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+    }
+
+    // ---------------- teardown ----------------
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc_pair(tmem_base, Tile::TMEM_COLS);
+}
+
+}  // namespace
+
+LmKernel int8_mma_kernel() {
+    LmKernel k;
+    k.fn = reinterpret_cast<const void *>(&lm_int8_mma_kernel);
+    k.threads = Int8Tile::THREADS;
+    k.smem = Int8Tile::FIXED;
+    k.tile_m = Int8Tile::TILE_M;
+    k.bn = Int8Tile::BN;
+    k.gran = Int8Tile::GRAN;
+    k.pair = 1;
+    k.box_a = 128;
+    return k;
+}
+
+}  // namespace sg

@@ -8,6 +8,8 @@
  *     and its gradients (sgemmCrossEntropy, sgemmCrossEntropyGrad);
  *   - products of a few rows with 4-bit weights and group scales
  *     (sgemmW4);
+ *   - products in 8-bit integers with scales for each token and channel, by
+ *     expert or not (sgemmInt8, sgemmInt8Quantize);
  *   - a router's choice of experts and its gradient (sgemmRouteTopK), tokens
  *     sorted by expert and brought back, and their gradients
  *     (sgemmExpertDispatch, sgemmExpertCombine).
@@ -36,7 +38,8 @@ extern "C" {
 typedef enum sgemmDataType {
     SGEMM_TYPE_F32 = 0,
     SGEMM_TYPE_F16 = 1,
-    SGEMM_TYPE_BF16 = 2
+    SGEMM_TYPE_BF16 = 2,
+    SGEMM_TYPE_S8 = 3           /* the rows of sgemmInt8() alone */
 } sgemmDataType_t;
 
 /* Most groups of one call. */
@@ -213,6 +216,52 @@ sgemmStatus_t sgemmW4(sgemmHandle_t handle, sgemmDataType_t type, int64_t M, int
 
 sgemmStatus_t sgemmW4WorkspaceSize(sgemmHandle_t handle, sgemmDataType_t type, int64_t M, int64_t N, int64_t K,
                                    int group, size_t *bytes);
+
+/*
+ * Rows as 8-bit integers with a scale each: X is T x K,
+ *
+ *   scales[t] = max_k |X[t, k]| / 127      (the nearest FP32 number, at least 2^-126; 0 for a row of zeros)
+ *   Q[t, k]   = X[t, k] / scales[t] rounded to the nearest integer, ties to even
+ *
+ * (pitch ldq BYTES; the bytes between K and the pitch are not written.)  A row
+ * with an infinity or a NaN has scale NaN and integers 0, so that its products
+ * are NaN.  T == 0 is a no-op.
+ */
+sgemmStatus_t sgemmInt8Quantize(sgemmHandle_t handle, sgemmDataType_t type, int64_t T, int64_t K, const void *X,
+                                int64_t ldx, int8_t *Q, int64_t ldq, float *scales, cudaStream_t stream);
+
+/*
+ * Products in 8-bit integers.  The weights are N x K integers (one row per
+ * output column, pitch ldb BYTES) with a scale for each row; with G > 1 or
+ * groupEnds there is one such matrix per group, at B + g * strideB, its scales
+ * at scales + g * N, and the rows of X are sorted by group as for
+ * sgemmGrouped().  groupEnds may be NULL if G == 1: then all rows have the one
+ * matrix.  X is T x K, of integers (SGEMM_TYPE_S8, pitch ldx BYTES) with their
+ * scales xScales[t], or of a type of numbers: then xScales is NULL and each row
+ * becomes integers as by sgemmInt8Quantize().
+ *
+ *   C[t, n] = xScales[t] * scales[g, n] * sum_k X[t, k] B_g[n, k]
+ *
+ * The sum is exact (a 32-bit integer); it becomes FP32, is multiplied by the
+ * row's scale, then by the channel's, and is rounded to typeC: the same bits
+ * whatever the number of rows, the groups or the pitches.  Rows behind the last
+ * end become zeros; ends that run backwards are treated as in sgemmGrouped().
+ *
+ * INVALID_VALUE, MISALIGNED, NOT_SUPPORTED as for sgemmGrouped(), also for
+ * xScales that is NULL with integers or not NULL with numbers; NOT_SUPPORTED for
+ * K > 131071, beyond which a sum may pass 32 bits.  W that is not 16-byte aligned
+ * with pitches that are multiples of 16 is read more slowly, or copied.
+ * WORKSPACE_REQUIRED: see the size query.  T == 0 or N == 0 is a no-op; K == 0 or
+ * G == 0 sets C to zero.
+ */
+sgemmStatus_t sgemmInt8(sgemmHandle_t handle, sgemmDataType_t typeX, sgemmDataType_t typeC, int64_t T, int64_t N,
+                        int64_t K, int64_t G, const void *X, int64_t ldx, const float *xScales, const int8_t *B,
+                        int64_t ldb, int64_t strideB, const float *scales, const int32_t *groupEnds, void *C,
+                        int64_t ldc, cudaStream_t stream);
+
+sgemmStatus_t sgemmInt8WorkspaceSize(sgemmHandle_t handle, sgemmDataType_t typeX, sgemmDataType_t typeC, int64_t T,
+                                     int64_t N, int64_t K, int64_t G, const void *X, int64_t ldx, const int8_t *B,
+                                     int64_t ldb, int64_t strideB, size_t *bytes);
 
 /*
  * A router's choice.  Each of T tokens has E logits (pitch ldl); the k largest
