@@ -95,21 +95,21 @@ sgemmStatus_t plan_int8(const sgemmContext *h, int from, int to, int64_t T, int6
             q.stride_w = q.ldw * N;
             q.ws_w = align256(q.stride_w * G);
         }
-        // Widths of a tile in rows of x: the one with the least rounds of tiles
-        // times what a tile costs; for groups, as wide as their mean.
+        // Rows of a tile: as many as a group has in the mean.  A block of W costs
+        // its conversion whatever the rows are, so that few tiles with the
+        // contraction cut between pairs come before more tiles.
         const int64_t pairs = h->sm_count / 2, high = ceil_div(N, 256);
-        if (G == 1) {
+        q.tile_n = int(std::min<int64_t>(sg::kInt8TileN, round_up(std::max<int64_t>(mean, 1), 32)));
+        if (G == 1 && T > sg::kInt8TileN) {
             double best = 0.0;
-            for (int n = sg::kInt8TileN; n >= 32; n -= 32) {
-                const double cost = double(ceil_div(high * ceil_div(T, n), pairs)) * (n + 24.0);
+            q.tile_n = 0;
+            for (int n = sg::kInt8TileN; n >= 96; n -= 32) {
+                const double cost = double(ceil_div(high * ceil_div(T, n), pairs)) * std::max(n, 128);
                 if (q.tile_n == 0 || cost < best) { best = cost; q.tile_n = n; }
             }
-        } else {
-            q.tile_n = int(std::min<int64_t>(sg::kInt8TileN, std::max<int64_t>(32, round_up(mean, 32))));
         }
-        q.tile_n = int(std::min<int64_t>(q.tile_n, round_up(T, 32)));
-        const int64_t most = high * (T / q.tile_n + std::min(G, T));
-        q.splits = int(std::max<int64_t>(1, std::min(pairs / most, ceil_div(K, sg::kInt8BlockK) / 6)));
+        const int64_t most = high * (T / q.tile_n + std::min(G, T % q.tile_n == 0 && G == 1 ? 0 : T));
+        q.splits = int(std::max<int64_t>(1, std::min(pairs / std::max<int64_t>(1, most), ceil_div(K, sg::kInt8BlockK) / 4)));
     }
     if (q.parts() > 1) {
         q.ld_part = round_up(N, 8);
