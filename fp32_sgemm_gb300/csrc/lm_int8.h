@@ -24,16 +24,18 @@ struct Int8Args {
     const float *scales;             // [G][N]
     int32_t *row_group;              // [T], where parts of the contraction are joined later, or NULL
     // lm_int8_rows.cu
-    const int8_t *x;                 // [T][ldx], ldx a multiple of 16, base 16-byte aligned
+    const void *x;                   // [T][ldx]; integers: ldx a multiple of 16, base 16-byte aligned
     int64_t ldx;
+    int from, x_vec;                 // sgemmDataType_t of x; numbers: rows take 16-byte loads
     const int8_t *w;
     int64_t ldw, stride_w;
     int K, k_slice, w_vec, early;    // early: the kernel before wrote x and its scales and nothing else
     int x_pitch;                     // bytes of a token's f16 row in shared memory
 };
 
-// Tokens of a tile: 8 or 16; warps 8 or 16.
-LmKernel int8_rows_kernel(int tokens, int warps);
+// Tokens of a tile: 8 or 16; warps 8 (ks 1, 4 or 8) or 16 (ks 4, 8 or 16), ks of
+// which share the contraction of 16 rows.
+LmKernel int8_rows_kernel(int tokens, int warps, int ks);
 int64_t int8_rows_smem(int tokens, int warps, int64_t x_pitch, int64_t G);
 
 LmKernel int8_mma_kernel();

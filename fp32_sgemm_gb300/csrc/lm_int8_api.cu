@@ -19,7 +19,7 @@ struct Int8 {
     bool w_copy = false;
     int64_t ldw = 0, stride_w = 0;
     // rows
-    int tokens = 0, warps = 0, slices = 1;
+    int tokens = 0, warps = 0, ks = 0, slices = 1;
     int64_t k_slice = 0, x_pitch = 0, smem = 0;
     // tensor cores
     int tile_n = 0, splits = 1;
@@ -40,6 +40,7 @@ sgemmStatus_t check_x(int from, const void *X, int64_t T, int64_t K, int64_t ldx
 // Few rows a group in the mean: straight from memory, W read once for 8 or 16 of
 // them; otherwise the tensor cores.
 constexpr int64_t kInt8FewRows = 16;
+constexpr int64_t kInt8OwnBytes = 16384;
 
 sgemmStatus_t plan_int8(const sgemmContext *h, int from, int to, int64_t T, int64_t N, int64_t K, int64_t G,
                         const void *X, int64_t ldx, const int8_t *W, int64_t ldw, int64_t strideW, Int8 &q) {
@@ -68,7 +69,9 @@ sgemmStatus_t plan_int8(const sgemmContext *h, int from, int to, int64_t T, int6
     q.rows = mean <= kInt8FewRows;
     q.ws_scales = from == SGEMM_TYPE_S8 ? 0 : align256(T * 4);
     if (q.rows) {
-        q.x_copy = from != SGEMM_TYPE_S8 || !aligned(X, 16) || ldx % 16 != 0;
+        // A row or two that one matrix meets: each CTA quantises them itself.
+        const bool own = from != SGEMM_TYPE_S8 && G == 1 && T * K * type_size(from) <= kInt8OwnBytes;
+        q.x_copy = !own && (from != SGEMM_TYPE_S8 || !aligned(X, 16) || ldx % 16 != 0);
         q.ldx = q.x_copy ? round_up(K, 16) : ldx;
         q.ws_x = q.x_copy ? align256(T * q.ldx) : 0;
         q.tokens = int(std::min<int64_t>(T, mean <= 8 ? 8 : 16));
@@ -85,6 +88,12 @@ sgemmStatus_t plan_int8(const sgemmContext *h, int from, int to, int64_t T, int6
             if (q.smem <= kMaxSmem) break;
         }
         q.slices = int(ceil_div(K, q.k_slice));
+        // Warps that share 16 rows of W: as few as give every slot a tile, and no
+        // more than there are steps.
+        const int64_t slots = int64_t(h->sm_count) * (q.warps == 8 ? 2 : 1) / q.slices;
+        const int64_t tokens = ceil_div(T, mean <= 8 ? 8 : 16) + std::min(G, T) - 1, steps = q.k_slice / 256;
+        for (q.ks = q.warps == 8 ? 1 : 4; q.ks < q.warps; q.ks = q.ks == 1 ? 4 : 2 * q.ks)
+            if (ceil_div(N, 16 * (q.warps / q.ks)) * tokens >= slots || 2 * q.ks > steps) break;
     } else {
         q.x_copy = true;
         q.ldx = round_up(K, 8);
@@ -212,7 +221,7 @@ sgemmStatus_t sgemmInt8(sgemmHandle_t h, sgemmDataType_t typeX, sgemmDataType_t 
     sg::LmKernel k;
     int64_t tiles;
     if (q.rows) {
-        k = sg::int8_rows_kernel(q.tokens, q.warps);
+        k = sg::int8_rows_kernel(q.tokens, q.warps, q.ks);
         a.lm.tile_n = k.bn;
         a.lm.tiles_m = int(ceil_div(N, k.tile_m));
         tiles = int64_t(a.lm.tiles_m) * (ceil_div(T, a.lm.tile_n) + G + 1);
@@ -227,7 +236,7 @@ sgemmStatus_t sgemmInt8(sgemmHandle_t h, sgemmDataType_t typeX, sgemmDataType_t 
     if (q.w_copy && (st = status(sg::int8_copy_launch(B, ldb, G > 1 ? strideB : 0, N, K, G, w_ws, q.ldw, groupEnds,
                                                       stream))) != SGEMM_STATUS_SUCCESS)
         return st;
-    if (q.x_copy && (st = status(sg::int8_quantize_launch(typeX, X, ldx, T, K, x_ws, q.ldx, q.ldx, !q.rows, x_scales_ws, q.rows,
+    if (q.x_copy && (st = status(sg::int8_quantize_launch(typeX, X, ldx, T, K, x_ws, q.ldx, q.ldx, !q.rows, x_scales_ws, true,
                                                           stream))) != SGEMM_STATUS_SUCCESS)
         return st;
 
@@ -244,7 +253,9 @@ sgemmStatus_t sgemmInt8(sgemmHandle_t h, sgemmDataType_t typeX, sgemmDataType_t 
     cfg.blockDim = dim3(unsigned(k.threads));
     cfg.stream = stream;
     if (q.rows) {
-        a.x = static_cast<const int8_t *>(q.x_copy ? x_ws : X);
+        a.x = q.x_copy ? x_ws : X;
+        a.from = q.x_copy ? int(SGEMM_TYPE_S8) : typeX;
+        a.x_vec = a.from == SGEMM_TYPE_S8 ? 1 : vec_ok(X, ldx, 0, type_size(typeX), 16);
         a.ldx = q.ldx;
         a.w = B;
         a.ldw = ldb;

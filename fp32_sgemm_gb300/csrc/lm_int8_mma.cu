@@ -125,8 +125,10 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         prefetch_tensormap(&tmW);
         prefetch_tensormap(&tmX);
     }
+    // The kernel before wrote x and its scales, and let this one begin when all
+    // before it was done: only what reads those two, and what C is written by,
+    // waits for it.  W is on its way and converted meanwhile.
     griddep_launch_dependents();
-    griddep_wait();
     if (warp == 2) {
         if (p.ends != nullptr) {
             lm_group_tables<Tile, kRagN>(p, g_start, g_prefix, lane);
@@ -149,6 +151,7 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         // (Rings of their own: a stage of W is free once it is converted, long
         // before the MMAs have read the x beside it.)
         const bool of_w = warp == 0;
+        if (!of_w) griddep_wait();
         uint64_t *full = of_w ? wfull : ready, *empty = of_w ? wempty : xempty;
         int stage = 0, issued = 0;
         uint32_t phase = 0;
@@ -306,6 +309,7 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         const int quarter = warp & 3, ew = warp - 2 - Tile::CONV_WARPS;
         const int slab0 = (ew >> 2) * SLAB;
         float *stg = staging + ew * Tile::STG;
+        griddep_wait();
         const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
         int gc = 0;
         bool ok = true;

@@ -1,150 +1,96 @@
-// Rows of numbers as 8-bit integers with a scale each:
+// Rows of numbers as 8-bit integers with a scale each (lm_int8_round.cuh has the
+// rounding).
 //
-//   s = max |x| / 127 (rounded to FP32, at least 2^-126 unless all are 0)
-//   q = x / s rounded to the nearest integer, ties to even
-//
-// The quotient's rounding is exact: r = rint(x * (1 / s)) is at most one off, and
-// x - r s, which one fused operation gives without rounding (it is a multiple of
-// half a unit of s and no larger than s), says whether a neighbour is nearer.  A
-// row with an infinity or a NaN has scale NaN and integers 0, so that products
-// with it are NaN.
-//
-// One CTA a row, 8 neighbours a thread and step; two steps stay in registers
-// (a row of 16384), more are read again.
+// One CTA a row, 8 neighbours a thread and step; what a thread has in its first
+// one or four steps stays in registers, more is read again.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "../../include/sgemm_gb300_lm.h"
 #include "lm_int8.h"
+#include "lm_int8_round.cuh"
 #include "lm_launch.cuh"
 #include "lm_ptx.cuh"
 
 namespace sg {
 namespace {
 
-__device__ __forceinline__ float as_float(float x) { return x; }
-__device__ __forceinline__ float as_float(__half x) { return __half2float(x); }
-__device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float as_float(int8_t x) { return (float)x; }
-
-template <class T>
-__device__ __forceinline__ void load8(const T *row, int64_t c, int64_t K, bool vec, float (&v)[8]) {
-    if (vec && c + 8 <= K) {
-        alignas(16) T e[8];
-        if constexpr (sizeof(T) == 1) {
-            *reinterpret_cast<uint2 *>(e) = *reinterpret_cast<const uint2 *>(row + c);
-        } else {
-#pragma unroll
-            for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-                reinterpret_cast<uint4 *>(e)[i] = reinterpret_cast<const uint4 *>(row + c)[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = as_float(e[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c + i < K ? as_float(row[c + i]) : 0.f;
-    }
-}
-
-__device__ __forceinline__ int nearest(float x, float s, float inv) {
-    float r = rintf(x * inv);
-    const float rest = fmaf(-r, s, x);
-    const float twice = 2.f * fabsf(rest);
-    if (twice > s || (twice == s && ((int)r & 1))) r += copysignf(1.f, rest);
-    return (int)fminf(fmaxf(r, -127.f), 127.f);
-}
-
-// (In f16 the rows are always those of a workspace: aligned, whole chunks.)
-template <bool OUT16>
-__device__ __forceinline__ void store8(void *out, int64_t at, const int (&q)[8], int n) {
-    if constexpr (OUT16) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __half2 h = __halves2half2(__int2half_rn(q[2 * i]), __int2half_rn(q[2 * i + 1]));
-            w[i] = *reinterpret_cast<const uint32_t *>(&h);
-        }
-        *reinterpret_cast<uint4 *>(static_cast<__half *>(out) + at) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else if (n < 8) {
-        for (int i = 0; i < n; ++i) static_cast<int8_t *>(out)[at + i] = (int8_t)q[i];
-    } else {
-        uint32_t w[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            w[i] = (q[4 * i] & 0xFF) | (q[4 * i + 1] & 0xFF) << 8 | (q[4 * i + 2] & 0xFF) << 16 |
-                   (uint32_t)q[4 * i + 3] << 24;
-        *reinterpret_cast<uint2 *>(static_cast<int8_t *>(out) + at) = make_uint2(w[0], w[1]);
-    }
-}
-
-constexpr int kHeld = 2;
-
 // T8: X holds integers already.  The kernel lets the next one begin only when it
 // has waited itself (chained): what comes behind may then read everything but
 // this kernel's outputs at once.
-template <class T, bool OUT16>
-__global__ void __launch_bounds__(1024)
-lm_int8_quantize_kernel(const T *x, int64_t ldx, int64_t K, bool vec, void *out, int64_t ldo, int64_t cols,
+template <class T, bool OUT16, int HELD>
+__global__ void __launch_bounds__(HELD == 1 ? 1024 : 256, HELD == 1 ? 1 : 3)
+lm_int8_quantize_kernel(const T *x, int64_t ldx, int64_t rows, int64_t K, bool vec, void *out, int64_t ldo, int64_t cols,
                         bool out_vec, float *scales, bool chained) {
     if (!chained) griddep_launch_dependents();
     griddep_wait();
     if (chained) griddep_launch_dependents();
-    const T *row = x + blockIdx.x * ldx;
-    const int64_t chunks = (cols + 7) / 8, to = blockIdx.x * ldo;
-    float v[kHeld][8];
-    float s = 1.f, inv = 1.f;
-    bool good = true;
-    if constexpr (sizeof(T) == 1) {
+    __shared__ uint32_t part[2][32];
+    const int64_t chunks = (cols + 7) / 8;
+    const int warps = (int)blockDim.x / 32, lane = threadIdx.x & 31;
+    Eight<T> next[HELD];
+    auto load = [&](int64_t r) {
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            const int64_t c = threadIdx.x + i * (int64_t)blockDim.x;
-            if (c < chunks) load8(row, c * 8, K, vec, v[i]);
+        for (int h = 0; h < HELD; ++h) {
+            const int64_t c = threadIdx.x + h * (int64_t)blockDim.x;
+            next[h].load(x + r * ldx + c * 8, K - c * 8, vec);
         }
-    } else {
-        // The largest |x| by its bits: infinities and NaN come out on top.
-        uint32_t most = 0;
-        for (int64_t c = threadIdx.x, i = 0; c < chunks; c += blockDim.x, ++i) {
-            float u[8];
-            load8(row, c * 8, K, vec, u);
+    };
+    // (Rows of one warp each: several in a CTA, blockDim.y of them.)
+    const int64_t first = blockIdx.x * (int64_t)blockDim.y + threadIdx.y, step = gridDim.x * (int64_t)blockDim.y;
+    int turn = 0;
+    if (first < rows) load(first);
+    for (int64_t r = first; r < rows; r += step, turn ^= 1) {
+        const T *row = x + r * ldx;
+        Eight<T> v[HELD];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(u[e]) & 0x7FFFFFFFu);
+        for (int h = 0; h < HELD; ++h) v[h] = next[h];
+        if (r + step < rows) load(r + step);
+        float s = 1.f, inv = 1.f;
+        bool zero = false;
+        if constexpr (sizeof(T) != 1) {
+            uint32_t most = 0;
 #pragma unroll
-            for (int h = 0; h < kHeld; ++h)
-                if (i == h)
+            for (int h = 0; h < HELD; ++h) most = max(most, v[h].most());
+            for (int64_t c = threadIdx.x + HELD * (int64_t)blockDim.x; c < chunks; c += blockDim.x) {
+                Eight<T> u;
+                u.load(row + c * 8, K - c * 8, vec);
+                most = max(most, u.most());
+            }
+            most = __reduce_max_sync(~0u, most);
+            if (warps > 1) {                       // (two tables: a warp may be one row ahead)
+                if (lane == 0) part[turn][threadIdx.x >> 5] = most;
+                __syncthreads();
+                most = __reduce_max_sync(~0u, lane < warps ? part[turn][lane] : 0u);
+            }
+            const RowScale of(most);
+            s = of.s;
+            inv = of.inv;
+            if (threadIdx.x == 0) scales[r] = of.scale;
+            if (!of.finite) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[h][e] = u[e];
+                for (int h = 0; h < HELD; ++h) v[h].clear();
+                zero = true;
+            }
         }
-        __shared__ uint32_t part[32];
-        most = __reduce_max_sync(~0u, most);
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = most;
-        __syncthreads();
-        most = 0;
-        for (int w = 0; w < (int)blockDim.x / 32; ++w) most = max(most, part[w]);
-        good = most < 0x7F800000u;
-        s = most == 0u ? 0.f : fmaxf(__uint_as_float(most) / 127.f, 1.17549435e-38f);
-        if (!good) s = __uint_as_float(0x7FC00000u);
-        inv = s > 0.f ? 1.f / s : 0.f;
-        if (threadIdx.x == 0) scales[blockIdx.x] = s;
-    }
-    for (int64_t c = threadIdx.x, i = 0; c < chunks; c += blockDim.x, ++i) {
-        float u[8];
-        if (i >= kHeld) load8(row, c * 8, K, vec, u);
+        auto put = [&](const Eight<T> &u, int64_t c) {
+            // (Integers already: by themselves.  A row that is not finite: zeros.)
+            const Rounded q = nearest(u.e, s, inv);
+            const int n = (int)min((int64_t)8, cols - c * 8);
+            store8<OUT16>(out, r * ldo + c * 8, q, n, out_vec);
+        };
 #pragma unroll
-        for (int h = 0; h < kHeld; ++h)
-            if (i == h)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) u[e] = v[h][e];
-        int q[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            q[e] = sizeof(T) == 1 ? (int)u[e] : good ? nearest(u[e], s, inv) : 0;
-        const int n = (int)min((int64_t)8, cols - c * 8);
-        if (out_vec || n < 8) {
-            store8<OUT16>(out, to + c * 8, q, n);
-        } else {
-            for (int e = 0; e < 8; ++e) static_cast<int8_t *>(out)[to + c * 8 + e] = (int8_t)q[e];
+        for (int h = 0; h < HELD; ++h) {
+            const int64_t c = threadIdx.x + h * (int64_t)blockDim.x;
+            if (c < chunks) put(v[h], c);
+        }
+        for (int64_t c = threadIdx.x + HELD * (int64_t)blockDim.x; c < chunks; c += blockDim.x) {
+            Eight<T> u;
+            u.load(row + c * 8, zero ? 0 : K - c * 8, vec);
+            put(u, c);
         }
     }
 }
@@ -155,9 +101,22 @@ cudaError_t quantize(const void *x, int64_t ldx, int64_t rows, int64_t K, void *
     const int64_t bytes = sizeof(T) == 1 ? 8 : 16;
     const bool vec = reinterpret_cast<uintptr_t>(x) % bytes == 0 && ldx * (int64_t)sizeof(T) % bytes == 0;
     const bool out_vec = reinterpret_cast<uintptr_t>(out) % 8 == 0 && ldo % 8 == 0;
-    const int threads = (int)std::min<int64_t>(1024, std::max<int64_t>(32, ((cols + 7) / 8 + 31) / 32 * 32));
-    return launch(out16 ? lm_int8_quantize_kernel<T, true> : lm_int8_quantize_kernel<T, false>, rows, threads, s,
-                  static_cast<const T *>(x), ldx, K, vec, out, ldo, cols, out_vec, scales, chained);
+    const int64_t chunks = (cols + 7) / 8;
+    // A thread for every 8 columns of every row while the device holds them all at
+    // once; then fewer, each with the loads of its next row on their way (8192
+    // rows of 4096, bf16: 41 us, 24.5).
+    auto run = [&](auto held, bool all) {
+        constexpr int H = decltype(held)::value;
+        const int threads = (int)std::min<int64_t>(H == 1 ? 1024 : 256, std::max<int64_t>(32, ((chunks + H - 1) / H + 31) / 32 * 32));
+        const int many = threads == 32 && rows > 152 ? 8 : 1;
+        const int64_t blocks = all ? rows : 152 * (many > 1 ? 4 : std::max(1, 768 / threads));
+        return launch(out16 ? lm_int8_quantize_kernel<T, true, H> : lm_int8_quantize_kernel<T, false, H>,
+                      std::min((rows + many - 1) / many, blocks), dim3(unsigned(threads), unsigned(many)), s,
+                      static_cast<const T *>(x), ldx, rows, K, vec, out, ldo, cols, out_vec, scales, chained);
+    };
+    constexpr int HELD = sizeof(T) == 4 ? 2 : 4;
+    if (rows * chunks <= 304 * 1024) return run(std::integral_constant<int, 1>(), true);
+    return chunks <= 32 ? run(std::integral_constant<int, 1>(), false) : run(std::integral_constant<int, HELD>(), false);
 }
 
 // ------------------------------------------------------------------- join

@@ -10,15 +10,17 @@
 // terms exactly; these are added as 32-bit integers, so a result does not
 // depend on how the contraction is cut.
 //
-// A CTA takes 16 rows of W for 8 NB tokens; its warps share the contraction.  A
-// lane loads 16 neighbouring bytes of a row (four lanes 64 of them) and
+// A warp takes 16 rows of W for 8 NB tokens, KS of them share the contraction, and
+// a CTA's other warps the rows that follow.  A lane loads 16 neighbouring bytes of a row (four lanes 64 of them) and
 // multiplies them with the same 16 columns of x, which lie in shared memory as
 // f16 (rows 16 bytes off a multiple of 128: no bank is met twice): the order of
 // k within a product is free as long as both operands agree.  Loads run one
 // step ahead, also from one tile to the next.
 #include <type_traits>
 
+#include "../../include/sgemm_gb300_lm.h"
 #include "lm_int8.h"
+#include "lm_int8_round.cuh"
 #include "lm_mma.cuh"
 
 namespace sg {
@@ -46,7 +48,13 @@ __device__ __forceinline__ void to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
 // 16 bytes at p, n of them in the row (the others 0).
 __device__ __forceinline__ uint4 load16(const int8_t *p, int n, bool vec) {
     if (n <= 0) return make_uint4(0, 0, 0, 0);
-    if (vec && n >= 16) return __ldg(reinterpret_cast<const uint4 *>(p));
+    if (vec && n >= 16) {
+        // (Read once: kept out of L1.)
+        uint4 w;
+        asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "l"(p));
+        return w;
+    }
     uint32_t v[5] = {0, 0, 0, 0, 0};
     const int skip = (int)(reinterpret_cast<uintptr_t>(p) & 3);
     if (n >= 20 && skip != 0) {
@@ -68,25 +76,77 @@ __device__ __forceinline__ uint4 load16(const int8_t *p, int n, bool vec) {
     return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
+// Tokens t0 .. t0 + nt of numbers, quantised as lm_int8_quant.cu does: columns
+// k_begin .. k_end as f16 in xs (to `width` columns, 0 behind k_end).  The warps
+// are dealt to the tokens, a power of two to each.
+template <class T, int WARPS>
+__device__ __forceinline__ void stage_typed(const Int8Args &q, int64_t t0, int nt, int k_begin, int k_end, int width,
+                                            unsigned char *xs, uint32_t *most_of, float *scale_of) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int share = WARPS;                                  // warps of a token
+    while (share > 1 && share * nt > WARPS) share >>= 1;
+    const int side = WARPS / share, part = warp % share, in = part * 32 + lane;
+    for (int r0 = 0; r0 < nt; r0 += side) {
+        const int r = r0 + warp / share;
+        const T *row = static_cast<const T *>(q.x) + (t0 + min(r, nt - 1)) * q.ldx;
+        uint32_t most = 0;
+#pragma unroll 4
+        for (int c = in * 8; c < q.K; c += share * 256) {
+            Eight<T> v;
+            v.load(row + c, q.K - c, q.x_vec);
+            most = max(most, v.most());
+        }
+        most = __reduce_max_sync(~0u, most);
+        if (share > 1) {
+            __syncthreads();
+            if (lane == 0) most_of[warp] = most;
+            __syncthreads();
+            most = 0;
+            for (int u = 0; u < share; ++u) most = max(most, most_of[warp / share * share + u]);
+        }
+        const RowScale s(most);
+        if (r < nt) {
+            if (in == 0) scale_of[r] = s.scale;
+#pragma unroll 4
+            for (int c = in * 8; c < width; c += share * 256) {
+                Eight<T> v;
+                v.load(row + k_begin + c, s.finite ? k_end - k_begin - c : 0, q.x_vec);
+                store8<true>(xs + r * q.x_pitch, c, nearest(v.e, s.s, s.inv), 8, true);
+            }
+        }
+    }
+}
+template <int WARPS>
+__device__ __forceinline__ void stage_numbers(const Int8Args &q, int64_t t0, int nt, int k_begin, int k_end, int width,
+                                              unsigned char *xs, uint32_t *most_of, float *scale_of) {
+    if (q.from == SGEMM_TYPE_F32) stage_typed<float, WARPS>(q, t0, nt, k_begin, k_end, width, xs, most_of, scale_of);
+    else if (q.from == SGEMM_TYPE_F16) stage_typed<__half, WARPS>(q, t0, nt, k_begin, k_end, width, xs, most_of, scale_of);
+    else stage_typed<__nv_bfloat16, WARPS>(q, t0, nt, k_begin, k_end, width, xs, most_of, scale_of);
+}
+
 // Columns of k in one step of a warp: a lane has 16 of every 64 of two rows.
 constexpr int kStep = 256, kLoads = kStep / 64;
 
-template <int NB, int WARPS>
+template <int NB, int WARPS, int KS>
 __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
 lm_int8_rows_kernel(const Int8Args q) {
-    constexpr int TOKENS = NB * 8, THREADS = WARPS * 32;
+    constexpr int TOKENS = NB * 8, THREADS = WARPS * 32, HIGH = 16 * (WARPS / KS);
     const LmArgs &p = q.lm;
     extern __shared__ unsigned char smem_raw[];
-    int *red = reinterpret_cast<int *>(smem_raw);                           // [2][warp][NB * 4][32]
+    uint32_t *most_of = reinterpret_cast<uint32_t *>(smem_raw);             // [16]
+    float *scale_of = reinterpret_cast<float *>(most_of + 16);              // [16]
+    int *red = reinterpret_cast<int *>(scale_of + 16);                           // [2][warp][NB * 4][32]
     int *start = red + 2 * WARPS * NB * 128;
     uint32_t *prefix = reinterpret_cast<uint32_t *>(start + p.G + 2);
-    unsigned char *xs = smem_raw + ((2 * WARPS * NB * 128 + 2 * (p.G + 2)) * 4 + 15) / 16 * 16;
+    unsigned char *xs = smem_raw + ((32 + 2 * WARPS * NB * 128 + 2 * (p.G + 2)) * 4 + 15) / 16 * 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int kw = warp % KS, rw = warp / KS;
     const int g = lane >> 2, c4 = lane & 3;
     const int k_begin = blockIdx.y * q.k_slice, k_end = min(q.K, k_begin + q.k_slice);
-    // This warp's steps of the contraction.
+    // This warp's steps of the contraction: every KS-th, so that a CTA reads
+    // neighbouring pieces of its rows at a time.
     const int steps = (k_end - k_begin + kStep - 1) / kStep;
-    const int s0 = steps * warp / WARPS, per = steps * (warp + 1) / WARPS - s0;
+    const int per = steps > kw ? (steps - 1 - kw) / KS + 1 : 0;
 
     griddep_launch_dependents();
     if (!q.early) griddep_wait();
@@ -116,7 +176,7 @@ lm_int8_rows_kernel(const Int8Args q) {
         const int local = t - (int)prefix[lo], chunk = local / p.tiles_m;
         Tile w;
         w.g = lo;
-        w.n0 = (local - chunk * p.tiles_m) * 16;
+        w.n0 = (local - chunk * p.tiles_m) * HIGH;
         w.t0 = start[lo] + chunk * TOKENS;
         w.nt = min(TOKENS, start[lo + 1] - w.t0);
         return w;
@@ -139,12 +199,12 @@ lm_int8_rows_kernel(const Int8Args q) {
         nt = tile_of(l_tile);
         l_live = nt.g < p.G;                     // (rows behind the last end have no W)
         const int8_t *base = q.w + (int64_t)min(nt.g, p.G - 1) * q.stride_w;
-        pa = base + (int64_t)min(nt.n0 + g, p.M - 1) * q.ldw;
-        pb = base + (int64_t)min(nt.n0 + g + 8, p.M - 1) * q.ldw;
+        pa = base + (int64_t)min(nt.n0 + rw * 16 + g, p.M - 1) * q.ldw;
+        pb = base + (int64_t)min(nt.n0 + rw * 16 + g + 8, p.M - 1) * q.ldw;
     };
     auto load = [&](uint4 (&a)[kLoads], uint4 (&b)[kLoads]) {
         if (l_live) {
-            const int k = k_begin + (s0 + l_step) * kStep + c4 * 16;
+            const int k = k_begin + (kw + l_step * KS) * kStep + c4 * 16;
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
                 a[i] = load16(pa + k + i * 64, k_end - k - i * 64, q.w_vec);
@@ -168,18 +228,23 @@ lm_int8_rows_kernel(const Int8Args q) {
         if (w.g < p.G && (w.g != staged_g || w.t0 != staged_t)) {
             // x of this tile's tokens as f16; columns behind K become 0.
             __syncthreads();
-            const int chunks = steps * (kStep / 16), total = chunks * w.nt;
-            for (int i = threadIdx.x; i < total; i += THREADS) {
-                const int r = i / chunks, c = i - r * chunks;
-                const uint4 v = load16(q.x + (int64_t)(w.t0 + r) * q.ldx + k_begin + c * 16, k_end - k_begin - c * 16, true);
-                uint32_t h[8];
-                to_f16(v.x, h[0], h[1]);
-                to_f16(v.y, h[2], h[3]);
-                to_f16(v.z, h[4], h[5]);
-                to_f16(v.w, h[6], h[7]);
-                uint4 *to = reinterpret_cast<uint4 *>(xs + r * q.x_pitch + c * 32);
-                to[0] = make_uint4(h[0], h[1], h[2], h[3]);
-                to[1] = make_uint4(h[4], h[5], h[6], h[7]);
+            if (q.from != SGEMM_TYPE_S8) {
+                stage_numbers<WARPS>(q, w.t0, w.nt, k_begin, k_end, steps * kStep, xs, most_of, scale_of);
+            } else {
+                const int chunks = steps * (kStep / 16), total = chunks * w.nt;
+                for (int i = threadIdx.x; i < total; i += THREADS) {
+                    const int r = i / chunks, c = i - r * chunks;
+                    const uint4 v = load16(static_cast<const int8_t *>(q.x) + (int64_t)(w.t0 + r) * q.ldx + k_begin + c * 16,
+                                           k_end - k_begin - c * 16, true);
+                    uint32_t h[8];
+                    to_f16(v.x, h[0], h[1]);
+                    to_f16(v.y, h[2], h[3]);
+                    to_f16(v.z, h[4], h[5]);
+                    to_f16(v.w, h[6], h[7]);
+                    uint4 *to = reinterpret_cast<uint4 *>(xs + r * q.x_pitch + c * 32);
+                    to[0] = make_uint4(h[0], h[1], h[2], h[3]);
+                    to[1] = make_uint4(h[4], h[5], h[6], h[7]);
+                }
             }
             __syncthreads();
             staged_g = w.g;
@@ -187,7 +252,7 @@ lm_int8_rows_kernel(const Int8Args q) {
         }
         // (Columns of tokens that are not there take the last one's x; their sums go nowhere.)
 #pragma unroll
-        for (int n = 0; n < NB; ++n) x_lane[n] = xs + min(n * 8 + g, w.nt - 1) * q.x_pitch + (s0 * kStep + c4 * 16) * 2;
+        for (int n = 0; n < NB; ++n) x_lane[n] = xs + min(n * 8 + g, w.nt - 1) * q.x_pitch + (kw * kStep + c4 * 16) * 2;
         int sum[NB][4];
 #pragma unroll
         for (int n = 0; n < NB; ++n)
@@ -225,7 +290,7 @@ lm_int8_rows_kernel(const Int8Args q) {
                     to_f16(b[i].w, hb[6], hb[7]);
 #pragma unroll
                     for (int n = 0; n < NB; ++n) {
-                        const uint4 *x = reinterpret_cast<const uint4 *>(x_lane[n] + (s * kStep + i * 64) * 2);
+                        const uint4 *x = reinterpret_cast<const uint4 *>(x_lane[n] + (s * (KS * kStep) + i * 64) * 2);
                         const uint4 u = x[0], v = x[1];
                         mma16816(acc[0][n], ha[0], hb[0], ha[1], hb[1], u.x, u.y);
                         mma16816(acc[1][n], ha[2], hb[2], ha[3], hb[3], u.z, u.w);
@@ -244,29 +309,33 @@ lm_int8_rows_kernel(const Int8Args q) {
         } else {
             for (int s = 0; s < per; ++s) load(wa, wb);         // (moves on to the next tile)
         }
-        // Join the warps' sums (two buffers: a warp may be one tile ahead).
+        // Join the sums of the KS warps (two buffers: a warp may be one tile ahead).
         int *buf = red + (t & 1) * (WARPS * NB * 128);
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) buf[(warp * NB * 4 + n * 4 + i) * 32 + lane] = sum[n][i];
-        __syncthreads();
-        for (int o = threadIdx.x; o < 16 * w.nt; o += THREADS) {
+        if constexpr (KS == 1) __syncwarp();
+        else __syncthreads();
+        const int own = KS == 1 ? lane : (int)threadIdx.x, all = KS == 1 ? 16 * w.nt : HIGH * w.nt;
+        for (int o = own; o < all; o += KS == 1 ? 32 : THREADS) {
             // Column `col` of the MMA's row r sits in lane (r % 8) * 4 + (col % 8) / 2,
             // register (r / 8) * 2 + col % 2 of block col / 8.
-            const int col = o >> 4, r = o & 15;
+            const int col = KS == 1 ? o >> 4 : o / HIGH, high = KS == 1 ? rw * 16 + (o & 15) : o % HIGH, r = high & 15;
             const int at = ((col >> 3) * 4 + (r >> 3) * 2 + (col & 1)) * 32 + (r & 7) * 4 + ((col & 7) >> 1);
+            const int *of = buf + (high >> 4) * (KS * NB * 128);
             int v = 0;
 #pragma unroll
-            for (int u = 0; u < WARPS; ++u) v += buf[u * NB * 128 + at];
-            const int n = w.n0 + r;
+            for (int u = 0; u < KS; ++u) v += of[u * NB * 128 + at];
+            const int n = w.n0 + high;
             const int64_t row = w.t0 + col;
             if (n < p.M) {
                 if (p.splits > 1) {
                     static_cast<int *>(p.C)[blockIdx.y * p.stride_c + row * p.ldc + n] = v;
                     if (n == 0 && blockIdx.y == 0) q.row_group[row] = w.g < p.G ? w.g : -1;
                 } else {
-                    const float y = w.g < p.G ? (float)v * q.x_scales[row] * q.scales[(int64_t)w.g * p.M + n] : 0.f;
+                    const float xs_of = q.from == SGEMM_TYPE_S8 ? q.x_scales[row] : scale_of[col];
+                    const float y = w.g < p.G ? (float)v * xs_of * q.scales[(int64_t)w.g * p.M + n] : 0.f;
                     if (p.out == kOutF32) static_cast<float *>(p.C)[row * p.ldc + n] = y;
                     else if (p.out == kOutF16) static_cast<__half *>(p.C)[row * p.ldc + n] = __float2half_rn(y);
                     else static_cast<__nv_bfloat16 *>(p.C)[row * p.ldc + n] = __float2bfloat16_rn(y);
@@ -276,24 +345,29 @@ lm_int8_rows_kernel(const Int8Args q) {
     }
 }
 
+template <int NB, int WARPS, int KS>
+const void *rows_kernel() {
+    return reinterpret_cast<const void *>(&lm_int8_rows_kernel<NB, WARPS, KS>);
+}
+template <int NB>
+const void *rows_kernel(int warps, int ks) {
+    if (warps == 16) return ks == 16 ? rows_kernel<NB, 16, 16>() : ks == 8 ? rows_kernel<NB, 16, 8>() : rows_kernel<NB, 16, 4>();
+    return ks == 8 ? rows_kernel<NB, 8, 8>() : ks == 4 ? rows_kernel<NB, 8, 4>() : rows_kernel<NB, 8, 1>();
+}
+
 }  // namespace
 
-LmKernel int8_rows_kernel(int tokens, int warps) {
+LmKernel int8_rows_kernel(int tokens, int warps, int ks) {
     LmKernel k;
-    if (tokens <= 8)
-        k.fn = warps == 8 ? reinterpret_cast<const void *>(&lm_int8_rows_kernel<1, 8>)
-                          : reinterpret_cast<const void *>(&lm_int8_rows_kernel<1, 16>);
-    else
-        k.fn = warps == 8 ? reinterpret_cast<const void *>(&lm_int8_rows_kernel<2, 8>)
-                          : reinterpret_cast<const void *>(&lm_int8_rows_kernel<2, 16>);
+    k.fn = tokens <= 8 ? rows_kernel<1>(warps, ks) : rows_kernel<2>(warps, ks);
     k.threads = warps * 32;
     k.bn = tokens <= 8 ? 8 : 16;
-    k.tile_m = 16;
+    k.tile_m = 16 * (warps / ks);
     return k;
 }
 int64_t int8_rows_smem(int tokens, int warps, int64_t x_pitch, int64_t G) {
     const int64_t nb = tokens <= 8 ? 1 : 2;
-    return ((2 * warps * nb * 128 + 2 * (G + 2)) * 4 + 15) / 16 * 16 + std::min<int64_t>(tokens, nb * 8) * x_pitch;
+    return ((32 + 2 * warps * nb * 128 + 2 * (G + 2)) * 4 + 15) / 16 * 16 + std::min<int64_t>(tokens, nb * 8) * x_pitch;
 }
 
 }  // namespace sg

@@ -11,10 +11,10 @@ namespace sg {
 // A launch that may begin while the kernel before it in the stream ends
 // (griddepcontrol.wait orders its memory accesses).
 template <class... P, class... A>
-cudaError_t launch(void (*fn)(P...), int64_t blocks, int threads, cudaStream_t s, A... args) {
+cudaError_t launch(void (*fn)(P...), int64_t blocks, dim3 threads, cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(std::max<int64_t>(1, blocks)));
-    cfg.blockDim = dim3(threads);
+    cfg.blockDim = threads;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
