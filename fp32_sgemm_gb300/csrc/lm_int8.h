@@ -30,13 +30,15 @@ struct Int8Args {
     const int8_t *w;
     int64_t ldw, stride_w;
     int K, k_slice, w_vec, early;    // early: the kernel before wrote x and its scales and nothing else
-    int x_pitch;                     // bytes of a token's f16 row in shared memory
+    int x_pitch;                     // bytes of a token's x in shared memory
 };
 
-// Tokens of a tile: 8 or 16; warps 8 (ks 1, 4 or 8) or 16 (ks 4, 8 or 16), ks of
-// which share the contraction of 16 rows.
+// Tokens of a tile: 1, 2, 4, 8 or 16; warps 8 (ks 1, 4 or 8) or 16 (ks 4, 8 or
+// 16), ks of which share the contraction of 16 rows.
 LmKernel int8_rows_kernel(int tokens, int warps, int ks);
-int64_t int8_rows_smem(int tokens, int warps, int64_t x_pitch, int64_t G);
+// Bytes of one token's x, and of a CTA with x of `rows` tokens.
+int64_t int8_rows_pitch(int tokens, int64_t k_slice);
+int64_t int8_rows_smem(int tokens, int rows, int warps, int64_t k_slice, int64_t G);
 
 LmKernel int8_mma_kernel();
 constexpr int kInt8TileN = 192;      // tokens of a tile at most

@@ -74,26 +74,41 @@ sgemmStatus_t plan_int8(const sgemmContext *h, int from, int to, int64_t T, int6
         q.x_copy = !own && (from != SGEMM_TYPE_S8 || !aligned(X, 16) || ldx % 16 != 0);
         q.ldx = q.x_copy ? round_up(K, 16) : ldx;
         q.ws_x = q.x_copy ? align256(T * q.ldx) : 0;
-        q.tokens = int(std::min<int64_t>(T, mean <= 8 ? 8 : 16));
+        // (By group the mean decides, the sizes being on the device: tiles of four
+        // tokens where it is about one.)
+        if (G == 1) q.tokens = T == 1 ? 1 : T == 2 ? 2 : T <= 4 ? 4 : T <= 8 ? 8 : 16;
+        else q.tokens = mean <= 1 ? 4 : mean <= 8 ? 8 : 16;
+        const int rows = int(std::min<int64_t>(T, q.tokens));
         // x of a tile's tokens beside half of an SM's shared memory, all of it,
         // or the contraction in parts.
         for (q.slices = 1;; ++q.slices) {
             q.k_slice = round_up(ceil_div(K, q.slices), 256);
-            q.x_pitch = q.k_slice * 2 + 16;
             q.warps = 8;
-            q.smem = sg::int8_rows_smem(q.tokens, 8, q.x_pitch, G);
+            q.smem = sg::int8_rows_smem(q.tokens, rows, 8, q.k_slice, G);
             if (q.smem <= 113 * 1024) break;
             q.warps = 16;
-            q.smem = sg::int8_rows_smem(q.tokens, 16, q.x_pitch, G);
+            q.smem = sg::int8_rows_smem(q.tokens, rows, 16, q.k_slice, G);
             if (q.smem <= kMaxSmem) break;
         }
+        q.x_pitch = sg::int8_rows_pitch(q.tokens, q.k_slice);
         q.slices = int(ceil_div(K, q.k_slice));
-        // Warps that share 16 rows of W: as few as give every slot a tile, and no
-        // more than there are steps.
-        const int64_t slots = int64_t(h->sm_count) * (q.warps == 8 ? 2 : 1) / q.slices;
-        const int64_t tokens = ceil_div(T, mean <= 8 ? 8 : 16) + std::min(G, T) - 1, steps = q.k_slice / 256;
-        for (q.ks = q.warps == 8 ? 1 : 4; q.ks < q.warps; q.ks = q.ks == 1 ? 4 : 2 * q.ks)
-            if (ceil_div(N, 16 * (q.warps / q.ks)) * tokens >= slots || 2 * q.ks > steps) break;
+        // Warps that share 16 rows of W, no more than there are steps: with the least
+        // rounds of tiles times what a tile costs: its rows, and for its beginning and
+        // end about what 24 KB of W take (128 rows over 64 groups of 2048 x 1024: 35 us
+        // with tiles of 128 rows, 41 of 32; one row, 28672 x 8192: 41 of 32, 45 of 128).
+        const int64_t slots = std::max<int64_t>(1, int64_t(h->sm_count) * (q.warps == 8 ? 2 : 1) / q.slices);
+        const int64_t chunks = ceil_div(T, q.tokens) + std::min(G, T) - 1, steps = q.k_slice / 256;
+        int64_t best = 0;
+        const int least = q.warps == 8 ? 1 : 4;
+        for (int ks = q.warps; ks >= least; ks = ks == 4 ? 1 : ks / 2) {
+            if (ks > steps && ks > least) continue;
+            const int64_t high = 16 * (q.warps / ks), rounds = ceil_div(ceil_div(N, high) * chunks, slots);
+            const int64_t cost = rounds * (high + 4 + 24576 / q.k_slice);
+            if (best == 0 || cost < best) {
+                best = cost;
+                q.ks = ks;
+            }
+        }
     } else {
         q.x_copy = true;
         q.ldx = round_up(K, 8);

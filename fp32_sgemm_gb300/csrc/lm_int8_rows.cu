@@ -2,20 +2,25 @@
 //
 //   y[t, n] = sx[t] sw[n] sum_k x[t, k] w[n, k]
 //
-// The weights are read once, straight into registers, and that read bounds the
-// product.  sm_103a has no tensor instruction for 8-bit integers beyond
-// mma.sync at the rate of the integer pipes (151 TOPS measured, 592 TFLOP/s in
-// f16), so they become f16 on the way, exactly: a byte less 128 under the
-// leading bits of 1024, and 1152 less.  FP32 accumulators hold sums of 1024
-// terms exactly; these are added as 32-bit integers, so a result does not
-// depend on how the contraction is cut.
+// The weights are read once, straight into registers, one step ahead (also from
+// one tile to the next), and that read should bound the product; what does bound
+// it is the instructions beside it, so they are few:
+//   * up to four tokens: __dp4a, one instruction for four products, x as bytes;
+//   * more: mma.sync in f16.  (In 8-bit integers it runs at __dp4a's rate: 151 TOPS
+//     measured, 592 TFLOP/s in f16.)  The bytes become f16 on the way, exactly: a
+//     byte plus 128 under the leading bits of 1024, and 1152 less.  FP32
+//     accumulators hold sums of 1024 terms exactly; these are added as 32-bit
+//     integers.
+// Either way the sum is exact, so a result does not depend on how the contraction
+// is cut.
 //
-// A warp takes 16 rows of W for 8 NB tokens, KS of them share the contraction, and
-// a CTA's other warps the rows that follow.  A lane loads 16 neighbouring bytes of a row (four lanes 64 of them) and
-// multiplies them with the same 16 columns of x, which lie in shared memory as
-// f16 (rows 16 bytes off a multiple of 128: no bank is met twice): the order of
-// k within a product is free as long as both operands agree.  Loads run one
-// step ahead, also from one tile to the next.
+// A warp takes 16 rows of W, KS of them share the contraction, and a CTA's other
+// warps the rows that follow.  A lane loads 16 neighbouring bytes of a row (four
+// lanes 64 of them) and multiplies them with the same 16 columns of x, which lie
+// in shared memory (f16 rows 16 bytes off a multiple of 128: no bank is met twice):
+// the order of k within a product is free as long as both operands agree.
+//
+// Measured (one GB300): MEASURED
 #include <type_traits>
 
 #include "../../include/sgemm_gb300_lm.h"
@@ -46,41 +51,39 @@ __device__ __forceinline__ void to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
 }
 
 // 16 bytes at p, n of them in the row (the others 0).
-__device__ __forceinline__ uint4 load16(const int8_t *p, int n, bool vec) {
-    if (n <= 0) return make_uint4(0, 0, 0, 0);
-    if (vec && n >= 16) {
-        // (Read once: kept out of L1.)
-        uint4 w;
-        asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "l"(p));
-        return w;
-    }
+__device__ __noinline__ uint4 load_some(const int8_t *p, int n) {
     uint32_t v[5] = {0, 0, 0, 0, 0};
     const int skip = (int)(reinterpret_cast<uintptr_t>(p) & 3);
-    if (n >= 20 && skip != 0) {
+    if (n >= 20) {
         // The aligned words that hold them (all in the row: n - 16 more follow).
         const uint32_t *from = reinterpret_cast<const uint32_t *>(p + 4 - skip);
-        uint32_t head = 0;
-        for (int e = 0; e < 4 - skip; ++e) head |= (uint32_t)(uint8_t)p[e] << (8 * (skip + e));
-        v[0] = head;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < 4 - skip) v[0] |= (uint32_t)(uint8_t)p[e] << (8 * (skip + e));
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e + 1] = from[e];
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = __funnelshift_r(v[e], v[e + 1], 8 * skip);
-    } else if (n >= 16 && skip == 0) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = reinterpret_cast<const uint32_t *>(p)[e];
     } else {
-        for (int e = 0; e < min(n, 16); ++e) v[e / 4] |= (uint32_t)(uint8_t)p[e] << (8 * (e % 4));
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            if (e < n) v[e / 4] |= (uint32_t)(uint8_t)p[e] << (8 * (e % 4));
     }
     return make_uint4(v[0], v[1], v[2], v[3]);
 }
+// (Read once: kept out of L1.)
+__device__ __forceinline__ uint4 load_whole(const int8_t *p) {
+    uint4 w;
+    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "l"(p));
+    return w;
+}
 
 // Tokens t0 .. t0 + nt of numbers, quantised as lm_int8_quant.cu does: columns
-// k_begin .. k_end as f16 in xs (to `width` columns, 0 behind k_end).  The warps
+// k_begin .. k_end as f16 or bytes in xs (to `width` columns, 0 behind k_end).  The warps
 // are dealt to the tokens, a power of two to each.
-template <class T, int WARPS>
-__device__ __forceinline__ void stage_typed(const Int8Args &q, int64_t t0, int nt, int k_begin, int k_end, int width,
+template <class T, int WARPS, bool F16>
+__device__ __forceinline__ void stage_typed(const Int8Args &q, int64_t t0, int nt, int k_end, int width,
                                             unsigned char *xs, uint32_t *most_of, float *scale_of) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int share = WARPS;                                  // warps of a token
@@ -89,9 +92,15 @@ __device__ __forceinline__ void stage_typed(const Int8Args &q, int64_t t0, int n
     for (int r0 = 0; r0 < nt; r0 += side) {
         const int r = r0 + warp / share;
         const T *row = static_cast<const T *>(q.x) + (t0 + min(r, nt - 1)) * q.ldx;
+        // (The first pieces are kept.)
+        constexpr int HELD = 4;
+        Eight<T> held[HELD];
         uint32_t most = 0;
-#pragma unroll 4
-        for (int c = in * 8; c < q.K; c += share * 256) {
+#pragma unroll
+        for (int h = 0; h < HELD; ++h) held[h].load(row + in * 8 + h * share * 256, q.K - in * 8 - h * share * 256, q.x_vec);
+#pragma unroll
+        for (int h = 0; h < HELD; ++h) most = max(most, held[h].most());
+        for (int c = in * 8 + HELD * share * 256; c < q.K; c += share * 256) {
             Eight<T> v;
             v.load(row + c, q.K - c, q.x_vec);
             most = max(most, v.most());
@@ -107,38 +116,47 @@ __device__ __forceinline__ void stage_typed(const Int8Args &q, int64_t t0, int n
         const RowScale s(most);
         if (r < nt) {
             if (in == 0) scale_of[r] = s.scale;
-#pragma unroll 4
-            for (int c = in * 8; c < width; c += share * 256) {
+            // (k_begin is 0 here: a row that a CTA quantises itself is not cut.)
+#pragma unroll
+            for (int h = 0; h < HELD; ++h) {
+                const int c = in * 8 + h * share * 256;
+                if (!s.finite) held[h].clear();
+                if (c < width) store8<F16>(xs + r * q.x_pitch, c, nearest(held[h].e, s.s, s.inv), 8, true);
+            }
+            for (int c = in * 8 + HELD * share * 256; c < width; c += share * 256) {
                 Eight<T> v;
-                v.load(row + k_begin + c, s.finite ? k_end - k_begin - c : 0, q.x_vec);
-                store8<true>(xs + r * q.x_pitch, c, nearest(v.e, s.s, s.inv), 8, true);
+                v.load(row + c, s.finite ? k_end - c : 0, q.x_vec);
+                store8<F16>(xs + r * q.x_pitch, c, nearest(v.e, s.s, s.inv), 8, true);
             }
         }
     }
 }
-template <int WARPS>
-__device__ __forceinline__ void stage_numbers(const Int8Args &q, int64_t t0, int nt, int k_begin, int k_end, int width,
+template <int WARPS, bool F16>
+__device__ __forceinline__ void stage_numbers(const Int8Args &q, int64_t t0, int nt, int k_end, int width,
                                               unsigned char *xs, uint32_t *most_of, float *scale_of) {
-    if (q.from == SGEMM_TYPE_F32) stage_typed<float, WARPS>(q, t0, nt, k_begin, k_end, width, xs, most_of, scale_of);
-    else if (q.from == SGEMM_TYPE_F16) stage_typed<__half, WARPS>(q, t0, nt, k_begin, k_end, width, xs, most_of, scale_of);
-    else stage_typed<__nv_bfloat16, WARPS>(q, t0, nt, k_begin, k_end, width, xs, most_of, scale_of);
+    if (q.from == SGEMM_TYPE_F32) stage_typed<float, WARPS, F16>(q, t0, nt, k_end, width, xs, most_of, scale_of);
+    else if (q.from == SGEMM_TYPE_F16) stage_typed<__half, WARPS, F16>(q, t0, nt, k_end, width, xs, most_of, scale_of);
+    else stage_typed<__nv_bfloat16, WARPS, F16>(q, t0, nt, k_end, width, xs, most_of, scale_of);
 }
 
 // Columns of k in one step of a warp: a lane has 16 of every 64 of two rows.
 constexpr int kStep = 256, kLoads = kStep / 64;
 
-template <int NB, int WARPS, int KS>
+// TOKENS: 1, 2 or 4 by __dp4a, 8 or 16 by mma.sync.
+template <int TOKENS, int WARPS, int KS>
 __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
-lm_int8_rows_kernel(const Int8Args q) {
-    constexpr int TOKENS = NB * 8, THREADS = WARPS * 32, HIGH = 16 * (WARPS / KS);
+lm_int8_rows_kernel(const __grid_constant__ Int8Args q) {
+    constexpr bool DOT = TOKENS <= 4;
+    constexpr int NB = DOT ? 1 : TOKENS / 8, THREADS = WARPS * 32, HIGH = 16 * (WARPS / KS);
+    constexpr int SUMS = 16 * TOKENS;                                       // of one warp
     const LmArgs &p = q.lm;
     extern __shared__ unsigned char smem_raw[];
     uint32_t *most_of = reinterpret_cast<uint32_t *>(smem_raw);             // [16]
     float *scale_of = reinterpret_cast<float *>(most_of + 16);              // [16]
-    int *red = reinterpret_cast<int *>(scale_of + 16);                           // [2][warp][NB * 4][32]
-    int *start = red + 2 * WARPS * NB * 128;
+    int *red = reinterpret_cast<int *>(scale_of + 16);                      // [2][warp][SUMS]
+    int *start = red + 2 * WARPS * SUMS;
     uint32_t *prefix = reinterpret_cast<uint32_t *>(start + p.G + 2);
-    unsigned char *xs = smem_raw + ((32 + 2 * WARPS * NB * 128 + 2 * (p.G + 2)) * 4 + 15) / 16 * 16;
+    unsigned char *xs = smem_raw + ((32 + 2 * WARPS * SUMS + 2 * (p.G + 2)) * 4 + 15) / 16 * 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int kw = warp % KS, rw = warp / KS;
     const int g = lane >> 2, c4 = lane & 3;
@@ -187,30 +205,38 @@ lm_int8_rows_kernel(const Int8Args q) {
 
     // The loads of one step, and the place of the next one.
     uint4 wa[kLoads], wb[kLoads];
-    Tile nt{};
-    int l_tile = first, l_step = 0;
+    int l_tile = first, l_step = 0, l_k = 0;
     const int8_t *pa = nullptr, *pb = nullptr;
     bool l_live = false;
     auto point = [&]() {
-        if (l_tile >= last) {
-            l_live = false;
-            return;
-        }
-        nt = tile_of(l_tile);
-        l_live = nt.g < p.G;                     // (rows behind the last end have no W)
-        const int8_t *base = q.w + (int64_t)min(nt.g, p.G - 1) * q.stride_w;
+        // (Rows behind the last end, which have no W, are the last tiles.)
+        l_live = false;
+        if (l_tile >= last) return;
+        const Tile nt = tile_of(l_tile);
+        l_live = nt.g < p.G;
+        l_k = k_begin + kw * kStep + c4 * 16;
+        const int8_t *base = q.w + (int64_t)min(nt.g, p.G - 1) * q.stride_w + l_k;
         pa = base + (int64_t)min(nt.n0 + rw * 16 + g, p.M - 1) * q.ldw;
         pb = base + (int64_t)min(nt.n0 + rw * 16 + g + 8, p.M - 1) * q.ldw;
     };
-    auto load = [&](uint4 (&a)[kLoads], uint4 (&b)[kLoads]) {
-        if (l_live) {
-            const int k = k_begin + (kw + l_step * KS) * kStep + c4 * 16;
+    auto load = [&]() {
+        if (!l_live) return;
+        if (q.w_vec && l_k + kStep - 48 <= k_end) {                 // (all lanes alike, or nearly)
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
-                a[i] = load16(pa + k + i * 64, k_end - k - i * 64, q.w_vec);
-                b[i] = load16(pb + k + i * 64, k_end - k - i * 64, q.w_vec);
+                wa[i] = load_whole(pa + i * 64);
+                wb[i] = load_whole(pb + i * 64);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                wa[i] = load_some(pa + i * 64, k_end - l_k - i * 64);
+                wb[i] = load_some(pb + i * 64, k_end - l_k - i * 64);
             }
         }
+        l_k += KS * kStep;
+        pa += KS * kStep;
+        pb += KS * kStep;
         if (++l_step == per) {
             l_step = 0;
             ++l_tile;
@@ -218,115 +244,162 @@ lm_int8_rows_kernel(const Int8Args q) {
         }
     };
     point();
-    if (per > 0 && first < last) load(wa, wb);
+    if (per > 0) load();
     if (q.early) griddep_wait();
 
     int staged_g = -1, staged_t = -1;
-    const unsigned char *x_lane[NB];
     for (int t = first; t < last; ++t) {
         const Tile w = tile_of(t);
         if (w.g < p.G && (w.g != staged_g || w.t0 != staged_t)) {
-            // x of this tile's tokens as f16; columns behind K become 0.
+            // x of this tile's tokens; columns behind K become 0.
             __syncthreads();
             if (q.from != SGEMM_TYPE_S8) {
-                stage_numbers<WARPS>(q, w.t0, w.nt, k_begin, k_end, steps * kStep, xs, most_of, scale_of);
+                stage_numbers<WARPS, !DOT>(q, w.t0, w.nt, k_end, steps * kStep, xs, most_of, scale_of);
             } else {
                 const int chunks = steps * (kStep / 16), total = chunks * w.nt;
                 for (int i = threadIdx.x; i < total; i += THREADS) {
                     const int r = i / chunks, c = i - r * chunks;
-                    const uint4 v = load16(static_cast<const int8_t *>(q.x) + (int64_t)(w.t0 + r) * q.ldx + k_begin + c * 16,
-                                           k_end - k_begin - c * 16, true);
-                    uint32_t h[8];
-                    to_f16(v.x, h[0], h[1]);
-                    to_f16(v.y, h[2], h[3]);
-                    to_f16(v.z, h[4], h[5]);
-                    to_f16(v.w, h[6], h[7]);
-                    uint4 *to = reinterpret_cast<uint4 *>(xs + r * q.x_pitch + c * 32);
-                    to[0] = make_uint4(h[0], h[1], h[2], h[3]);
-                    to[1] = make_uint4(h[4], h[5], h[6], h[7]);
+                    const int8_t *from = static_cast<const int8_t *>(q.x) + (int64_t)(w.t0 + r) * q.ldx + k_begin + c * 16;
+                    const int n = k_end - k_begin - c * 16;
+                    const uint4 v = n >= 16 ? *reinterpret_cast<const uint4 *>(from) : load_some(from, n);
+                    if constexpr (DOT) {
+                        *reinterpret_cast<uint4 *>(xs + r * q.x_pitch + c * 16) = v;
+                    } else {
+                        uint32_t h[8];
+                        to_f16(v.x, h[0], h[1]);
+                        to_f16(v.y, h[2], h[3]);
+                        to_f16(v.z, h[4], h[5]);
+                        to_f16(v.w, h[6], h[7]);
+                        uint4 *to = reinterpret_cast<uint4 *>(xs + r * q.x_pitch + c * 32);
+                        to[0] = make_uint4(h[0], h[1], h[2], h[3]);
+                        to[1] = make_uint4(h[4], h[5], h[6], h[7]);
+                    }
                 }
             }
             __syncthreads();
             staged_g = w.g;
             staged_t = w.t0;
         }
-        // (Columns of tokens that are not there take the last one's x; their sums go nowhere.)
+        // Two buffers: a warp may be one tile ahead.
+        int *own = red + ((t & 1) * WARPS + warp) * SUMS;                   // [token][row]
+        if constexpr (DOT) {
+            // (Tokens that are not there take the last one's x; their sums go nowhere.)
+            const unsigned char *x_lane[TOKENS];
 #pragma unroll
-        for (int n = 0; n < NB; ++n) x_lane[n] = xs + min(n * 8 + g, w.nt - 1) * q.x_pitch + (kw * kStep + c4 * 16) * 2;
-        int sum[NB][4];
+            for (int n = 0; n < TOKENS; ++n) x_lane[n] = xs + min(n, w.nt - 1) * q.x_pitch + kw * kStep + c4 * 16;
+            int sum[2][TOKENS];
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
+            for (int n = 0; n < TOKENS; ++n) sum[0][n] = sum[1][n] = 0;
+            if (w.g < p.G)
+                for (int s = 0; s < per; ++s) {
+                    uint4 a[kLoads], b[kLoads];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sum[n][i] = 0;
-        if (w.g < p.G) {
-            float acc[2][NB][4];
-            for (int s = 0; s < per; ++s) {
-                uint4 a[kLoads], b[kLoads];
-#pragma unroll
-                for (int i = 0; i < kLoads; ++i) {
-                    a[i] = wa[i];
-                    b[i] = wb[i];
-                }
-                load(wa, wb);
-                // Two accumulators in turn, each of at most kInt8Run terms.
-                constexpr int FLUSH = 2 * kInt8Run / kStep;
-                if (s % FLUSH == 0)
-#pragma unroll
-                    for (int z = 0; z < 2; ++z)
-#pragma unroll
-                        for (int n = 0; n < NB; ++n)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) acc[z][n][i] = 0.f;
-#pragma unroll
-                for (int i = 0; i < kLoads; ++i) {
-                    uint32_t ha[8], hb[8];
-                    to_f16(a[i].x, ha[0], ha[1]);
-                    to_f16(a[i].y, ha[2], ha[3]);
-                    to_f16(a[i].z, ha[4], ha[5]);
-                    to_f16(a[i].w, ha[6], ha[7]);
-                    to_f16(b[i].x, hb[0], hb[1]);
-                    to_f16(b[i].y, hb[2], hb[3]);
-                    to_f16(b[i].z, hb[4], hb[5]);
-                    to_f16(b[i].w, hb[6], hb[7]);
-#pragma unroll
-                    for (int n = 0; n < NB; ++n) {
-                        const uint4 *x = reinterpret_cast<const uint4 *>(x_lane[n] + (s * (KS * kStep) + i * 64) * 2);
-                        const uint4 u = x[0], v = x[1];
-                        mma16816(acc[0][n], ha[0], hb[0], ha[1], hb[1], u.x, u.y);
-                        mma16816(acc[1][n], ha[2], hb[2], ha[3], hb[3], u.z, u.w);
-                        mma16816(acc[0][n], ha[4], hb[4], ha[5], hb[5], v.x, v.y);
-                        mma16816(acc[1][n], ha[6], hb[6], ha[7], hb[7], v.z, v.w);
+                    for (int i = 0; i < kLoads; ++i) {
+                        a[i] = wa[i];
+                        b[i] = wb[i];
                     }
+                    load();
+#pragma unroll
+                    for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+                        for (int n = 0; n < TOKENS; ++n) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(x_lane[n] + i * 64);
+                            sum[0][n] = __dp4a((int)a[i].x, (int)x.x, sum[0][n]);
+                            sum[1][n] = __dp4a((int)b[i].x, (int)x.x, sum[1][n]);
+                            sum[0][n] = __dp4a((int)a[i].y, (int)x.y, sum[0][n]);
+                            sum[1][n] = __dp4a((int)b[i].y, (int)x.y, sum[1][n]);
+                            sum[0][n] = __dp4a((int)a[i].z, (int)x.z, sum[0][n]);
+                            sum[1][n] = __dp4a((int)b[i].z, (int)x.z, sum[1][n]);
+                            sum[0][n] = __dp4a((int)a[i].w, (int)x.w, sum[0][n]);
+                            sum[1][n] = __dp4a((int)b[i].w, (int)x.w, sum[1][n]);
+                        }
+#pragma unroll
+                    for (int n = 0; n < TOKENS; ++n) x_lane[n] += KS * kStep;
                 }
-                if (s % FLUSH == FLUSH - 1 || s == per - 1)
 #pragma unroll
-                    for (int z = 0; z < 2; ++z)
+            for (int n = 0; n < TOKENS; ++n)
 #pragma unroll
-                        for (int n = 0; n < NB; ++n)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) sum[n][i] += __float2int_rn(acc[z][n][i]);
-            }
+                for (int h = 0; h < 2; ++h) {
+                    int v = sum[h][n];
+                    v += __shfl_xor_sync(~0u, v, 1);
+                    v += __shfl_xor_sync(~0u, v, 2);
+                    if (c4 == 0) own[n * 16 + h * 8 + g] = v;
+                }
         } else {
-            for (int s = 0; s < per; ++s) load(wa, wb);         // (moves on to the next tile)
+            const unsigned char *x_lane[NB];
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+                x_lane[n] = xs + min(n * 8 + g, w.nt - 1) * q.x_pitch + (kw * kStep + c4 * 16) * 2;
+            int sum[NB][4];
+            float acc[2][NB][4];
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    sum[n][i] = 0;
+                    acc[0][n][i] = acc[1][n][i] = 0.f;
+                }
+            if (w.g < p.G)
+                for (int s = 0; s < per; ++s) {
+                    uint4 a[kLoads], b[kLoads];
+#pragma unroll
+                    for (int i = 0; i < kLoads; ++i) {
+                        a[i] = wa[i];
+                        b[i] = wb[i];
+                    }
+                    load();
+#pragma unroll
+                    for (int i = 0; i < kLoads; ++i) {
+                        uint32_t ha[8], hb[8];
+                        to_f16(a[i].x, ha[0], ha[1]);
+                        to_f16(a[i].y, ha[2], ha[3]);
+                        to_f16(a[i].z, ha[4], ha[5]);
+                        to_f16(a[i].w, ha[6], ha[7]);
+                        to_f16(b[i].x, hb[0], hb[1]);
+                        to_f16(b[i].y, hb[2], hb[3]);
+                        to_f16(b[i].z, hb[4], hb[5]);
+                        to_f16(b[i].w, hb[6], hb[7]);
+#pragma unroll
+                        for (int n = 0; n < NB; ++n) {
+                            const uint4 *x = reinterpret_cast<const uint4 *>(x_lane[n] + i * 128);
+                            const uint4 u = x[0], v = x[1];
+                            mma16816(acc[0][n], ha[0], hb[0], ha[1], hb[1], u.x, u.y);
+                            mma16816(acc[1][n], ha[2], hb[2], ha[3], hb[3], u.z, u.w);
+                            mma16816(acc[0][n], ha[4], hb[4], ha[5], hb[5], v.x, v.y);
+                            mma16816(acc[1][n], ha[6], hb[6], ha[7], hb[7], v.z, v.w);
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < NB; ++n) x_lane[n] += KS * kStep * 2;
+                    // Two accumulators in turn, each of at most kInt8Run terms.
+                    constexpr int FLUSH = 2 * kInt8Run / kStep;
+                    if (s % FLUSH == FLUSH - 1 || s == per - 1)
+#pragma unroll
+                        for (int z = 0; z < 2; ++z)
+#pragma unroll
+                            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    sum[n][i] += __float2int_rn(acc[z][n][i]);
+                                    acc[z][n][i] = 0.f;
+                                }
+                }
+            // Register i of block n: row lane / 4 + 8 (i / 2), token 8 n + 2 (lane % 4) + i % 2.
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) own[(n * 8 + c4 * 2 + (i & 1)) * 16 + g + (i >> 1) * 8] = sum[n][i];
         }
-        // Join the sums of the KS warps (two buffers: a warp may be one tile ahead).
-        int *buf = red + (t & 1) * (WARPS * NB * 128);
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) buf[(warp * NB * 4 + n * 4 + i) * 32 + lane] = sum[n][i];
+        // Join the sums of the KS warps.
         if constexpr (KS == 1) __syncwarp();
         else __syncthreads();
-        const int own = KS == 1 ? lane : (int)threadIdx.x, all = KS == 1 ? 16 * w.nt : HIGH * w.nt;
-        for (int o = own; o < all; o += KS == 1 ? 32 : THREADS) {
-            // Column `col` of the MMA's row r sits in lane (r % 8) * 4 + (col % 8) / 2,
-            // register (r / 8) * 2 + col % 2 of block col / 8.
-            const int col = KS == 1 ? o >> 4 : o / HIGH, high = KS == 1 ? rw * 16 + (o & 15) : o % HIGH, r = high & 15;
-            const int at = ((col >> 3) * 4 + (r >> 3) * 2 + (col & 1)) * 32 + (r & 7) * 4 + ((col & 7) >> 1);
-            const int *of = buf + (high >> 4) * (KS * NB * 128);
+        const int all = KS == 1 ? 16 * w.nt : HIGH * w.nt;
+        for (int o = KS == 1 ? lane : (int)threadIdx.x; o < all; o += KS == 1 ? 32 : THREADS) {
+            const int col = KS == 1 ? o >> 4 : o / HIGH, high = KS == 1 ? rw * 16 + (o & 15) : o % HIGH;
+            const int *of = red + ((t & 1) * WARPS + (high >> 4) * KS) * SUMS + col * 16 + (high & 15);
             int v = 0;
 #pragma unroll
-            for (int u = 0; u < KS; ++u) v += of[u * NB * 128 + at];
+            for (int u = 0; u < KS; ++u) v += of[u * SUMS];
             const int n = w.n0 + high;
             const int64_t row = w.t0 + col;
             if (n < p.M) {
@@ -345,29 +418,34 @@ lm_int8_rows_kernel(const Int8Args q) {
     }
 }
 
-template <int NB, int WARPS, int KS>
+template <int TOKENS, int WARPS, int KS>
 const void *rows_kernel() {
-    return reinterpret_cast<const void *>(&lm_int8_rows_kernel<NB, WARPS, KS>);
+    return reinterpret_cast<const void *>(&lm_int8_rows_kernel<TOKENS, WARPS, KS>);
 }
-template <int NB>
+template <int TOKENS>
 const void *rows_kernel(int warps, int ks) {
-    if (warps == 16) return ks == 16 ? rows_kernel<NB, 16, 16>() : ks == 8 ? rows_kernel<NB, 16, 8>() : rows_kernel<NB, 16, 4>();
-    return ks == 8 ? rows_kernel<NB, 8, 8>() : ks == 4 ? rows_kernel<NB, 8, 4>() : rows_kernel<NB, 8, 1>();
+    if (warps == 16)
+        return ks == 16 ? rows_kernel<TOKENS, 16, 16>() : ks == 8 ? rows_kernel<TOKENS, 16, 8>() : rows_kernel<TOKENS, 16, 4>();
+    return ks == 8 ? rows_kernel<TOKENS, 8, 8>() : ks == 4 ? rows_kernel<TOKENS, 8, 4>() : rows_kernel<TOKENS, 8, 1>();
 }
 
 }  // namespace
 
 LmKernel int8_rows_kernel(int tokens, int warps, int ks) {
     LmKernel k;
-    k.fn = tokens <= 8 ? rows_kernel<1>(warps, ks) : rows_kernel<2>(warps, ks);
+    k.fn = tokens == 1   ? rows_kernel<1>(warps, ks)
+           : tokens == 2 ? rows_kernel<2>(warps, ks)
+           : tokens == 4 ? rows_kernel<4>(warps, ks)
+           : tokens == 8 ? rows_kernel<8>(warps, ks)
+                         : rows_kernel<16>(warps, ks);
     k.threads = warps * 32;
-    k.bn = tokens <= 8 ? 8 : 16;
+    k.bn = tokens;
     k.tile_m = 16 * (warps / ks);
     return k;
 }
-int64_t int8_rows_smem(int tokens, int warps, int64_t x_pitch, int64_t G) {
-    const int64_t nb = tokens <= 8 ? 1 : 2;
-    return ((32 + 2 * warps * nb * 128 + 2 * (G + 2)) * 4 + 15) / 16 * 16 + std::min<int64_t>(tokens, nb * 8) * x_pitch;
+int64_t int8_rows_pitch(int tokens, int64_t k_slice) { return tokens <= 4 ? k_slice : k_slice * 2 + 16; }
+int64_t int8_rows_smem(int tokens, int rows, int warps, int64_t k_slice, int64_t G) {
+    return ((32 + 2 * warps * 16 * tokens + 2 * (G + 2)) * 4 + 15) / 16 * 16 + rows * int8_rows_pitch(tokens, k_slice);
 }
 
 }  // namespace sg
