@@ -14,6 +14,8 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <initializer_list>
+#include <type_traits>
 
 #include "../../include/sgemm_gb300_lm.h"
 #include "lm_expert.h"
@@ -29,8 +31,8 @@ namespace {
 // counts it by expert (a histogram of its own in shared memory), the histograms
 // are added up over warps and, through distributed shared memory, over CTAs, and
 // each warp goes over its run again with the row at which its choices of each
-// expert start.  No atomics: the order is that of the choices.
-constexpr int kSortThreads = 1024, kSortWarps = 32, kSortCluster = 8;
+// expert start, 32 choices at a time: the order is that of the choices.
+constexpr int kSortThreads = 1024, kSortWarps = 32, kSortCluster = 8, kAhead = 8;
 
 __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
     uint32_t v;
@@ -38,8 +40,8 @@ __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
     return v;
 }
 
-// Choice a's expert, G for none.
-__device__ __forceinline__ int bin_of(const int64_t *experts, int64_t a, int n, int G) {
+// Choice a's expert, G for none; -1 from n on.
+__device__ __forceinline__ int bin_of(const int64_t *experts, int64_t a, int64_t n, int G) {
     if (a >= n) return -1;
     const int64_t e = experts[a];
     return e >= 0 && e < G ? (int)e : G;
@@ -54,7 +56,7 @@ lm_expert_sort_kernel(const int64_t *experts, int n, int G, int32_t *slots, int3
     uint32_t *hist = first + bins;               // [warp][bins]
     __shared__ uint32_t sums[kSortWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)cluster_rank(), ctas = (int)gridDim.x;
+    const int rank = (int)cluster_rank(), ctas = (int)gridDim.x, bits = 32 - __clz(G);
     griddep_launch_dependents();
     griddep_wait();
     for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) hist[i] = 0u;
@@ -63,11 +65,20 @@ lm_expert_sort_kernel(const int64_t *experts, int n, int G, int32_t *slots, int3
     const int64_t run = ((n + warps - 1) / warps + 31) / 32 * 32;
     const int64_t a0 = (rank * kSortWarps + warp) * run, a1 = min(a0 + run, (int64_t)n);
     uint32_t *own = hist + warp * bins;
-    for (int64_t a = a0; a < a1; a += 32) {
-        const int b = bin_of(experts, a + lane, n, G);
-        const uint32_t same = __match_any_sync(~0u, b);
-        if (b >= 0 && lane == __ffs(same) - 1) own[b] += __popc(same);
-        __syncwarp();
+    // (Loads of kAhead steps together; the first are kept for the second time.)
+    int kept[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) kept[i] = bin_of(experts, a0 + 32 * i + lane, a1, G);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (kept[i] >= 0) atomicAdd(own + kept[i], 1u);
+    for (int64_t a = a0 + 32 * kAhead; a < a1; a += 32 * kAhead) {
+        int b[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) b[i] = bin_of(experts, a + 32 * i + lane, a1, G);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (b[i] >= 0) atomicAdd(own + b[i], 1u);
     }
     __syncthreads();
     for (int b = threadIdx.x; b < bins; b += kSortThreads) {
@@ -112,17 +123,30 @@ lm_expert_sort_kernel(const int64_t *experts, int n, int G, int32_t *slots, int3
     }
     // (No CTA leaves, or goes on to write, before the others have read.)
     cluster_sync();
-    for (int64_t a = a0; a < a1; a += 32) {
-        const int b = bin_of(experts, a + lane, n, G);
-        const uint32_t same = __match_any_sync(~0u, b);
-        const uint32_t below = same & ((1u << lane) - 1u);
-        if (b >= 0) {
-            const int32_t r = (int32_t)(first[b] + own[b] + __popc(below));
-            slots[a + lane] = b < G ? r : ~r;
+    for (int64_t a = a0; a < a1; a += 32 * kAhead) {
+        int b[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) b[i] = a == a0 ? kept[i] : bin_of(experts, a + 32 * i + lane, a1, G);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (a + 32 * i >= a1) break;
+            // Lanes of the same expert, by the bits of its number (524288 choices of
+            // 256 experts: 80 us with __match_any_sync, 60).
+            uint32_t same = __ballot_sync(~0u, b[i] >= 0);
+            for (int bit = 0; bit < bits; ++bit) {
+                const bool set = (b[i] >> bit) & 1;
+                const uint32_t with = __ballot_sync(~0u, set);
+                same &= set ? with : ~with;
+            }
+            const uint32_t below = same & ((1u << lane) - 1u);
+            if (b[i] >= 0) {
+                const int32_t r = (int32_t)(first[b[i]] + own[b[i]] + __popc(below));
+                slots[a + 32 * i + lane] = b[i] < G ? r : ~r;
+            }
+            __syncwarp();
+            if (b[i] >= 0 && below == 0u) own[b[i]] += __popc(same);
+            __syncwarp();
         }
-        __syncwarp();
-        if (b >= 0 && below == 0u) own[b] += __popc(same);
-        __syncwarp();
     }
 }
 
@@ -141,6 +165,77 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int64_t kMaxBlocks = 152 * 8;
 
 int64_t blocks_for(int64_t tasks) { return std::min((tasks + kWarps - 1) / kWarps, kMaxBlocks); }
+
+// Few choices are not sorted first: each warp counts those that come before its
+// token's in shared memory, and CTA 0 the ends as well: one launch in the place of
+// two.  Measured on the device, us: 16 tokens, two of 64 experts, 1024 bf16, 3.0,
+// sorted first 6.5; 512 of two, 1024, 3.4 / 7.4; 128 of eight, 2048, 6.6 / 9.7; 256 of
+// eight, 2048, 9.8 / 10.0; 512 of eight, 2048, 22.5 / 10.2.  A count is n / 32 steps,
+// and there are n of them for each part of a row that a warp takes.
+constexpr int kFewChoices = 4096;
+bool few_choices(int64_t n, int64_t parts) { return n <= kFewChoices && n * n * parts <= 1 << 23; }
+
+// Row of choice a among n, by one warp.
+__device__ __forceinline__ int32_t place_of(const uint16_t *bins, int n, int a, int G, int lane) {
+    const int b = bins[a];
+    uint32_t before = 0;
+    for (int i = lane; i < n; i += 32) {
+        const int o = bins[i];
+        before += o < b || (o == b && i < a);
+    }
+    const int32_t r = (int32_t)__reduce_add_sync(~0u, before);
+    return b < G ? r : ~r;
+}
+
+template <class P, int U>
+__global__ void __launch_bounds__(kThreads)
+lm_expert_dispatch_few_kernel(const ExpertRows p, const int64_t *experts, int G, int32_t *ends, int64_t pieces,
+                              int64_t parts) {
+    __shared__ uint16_t bins[kFewChoices];
+    __shared__ uint32_t count[kRouteMaxExperts + 1];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31, n = (int)p.T * p.k;
+    for (int i = threadIdx.x; i < n; i += kThreads) bins[i] = (uint16_t)bin_of(experts, i, n, G);
+    if (blockIdx.x == 0)
+        for (int g = threadIdx.x; g <= G; g += kThreads) count[g] = 0u;
+    __syncthreads();
+    if (blockIdx.x == 0) {
+        for (int i = threadIdx.x; i < n; i += kThreads) atomicAdd(count + bins[i], 1u);
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            uint32_t sum = 0;
+            for (int g0 = 0; g0 < G; g0 += 32) {
+                uint32_t c = g0 + lane < G ? count[g0 + lane] : 0u;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const uint32_t o = __shfl_up_sync(~0u, c, d);
+                    if (lane >= d) c += o;
+                }
+                if (g0 + lane < G) ends[g0 + lane] = (int32_t)(sum + c);
+                sum += __shfl_sync(~0u, c, 31);
+            }
+        }
+    }
+    int32_t *slots = const_cast<int32_t *>(p.slots);
+    const int64_t tasks = p.T * parts;
+    for (int64_t i = blockIdx.x * (int64_t)kWarps + (threadIdx.x >> 5); i < tasks; i += gridDim.x * (int64_t)kWarps) {
+        const int64_t t = i / parts, part = i - t * parts, c0 = part * (U * 32) + lane;
+        const P *from = reinterpret_cast<const P *>(static_cast<const char *>(p.x) + t * p.ldx);
+        P v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (c0 + u * 32 < pieces) v[u] = from[c0 + u * 32];
+        for (int j = 0; j < p.k; ++j) {
+            const int32_t slot = place_of(bins, n, (int)t * p.k + j, G, lane);
+            if (part == 0 && lane == 0) slots[t * p.k + j] = slot;
+            P *to = reinterpret_cast<P *>(static_cast<char *>(p.out) + (int64_t)(slot < 0 ? ~slot : slot) * p.ldo);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (c0 + u * 32 < pieces) to[c0 + u * 32] = slot < 0 ? P{} : v[u];
+        }
+    }
+}
 
 // A warp takes U * 32 pieces of one token at a time.
 template <class P, int U>
@@ -231,10 +326,14 @@ lm_expert_combine_kernel(const ExpertRows p, int64_t pieces, int64_t parts) {
     }
 }
 
-// A CTA a token: KC choices at a time, so that dy's pieces meet KC rows.
-constexpr int KC = 8;
-template <class T, class P>
-__global__ void __launch_bounds__(kThreads)
+// A CTA a token: KC choices at a time, so that dy's pieces meet KC rows, and U
+// pieces of each at once.  What counts is how many loads are on their way on an SM,
+// so the registers are held down: 16384 tokens of two choices, 4096 bf16, two
+// choices at a time 107 us, with two pieces and as many registers as it likes 191;
+// 8192 of eight, 2048, 89 and 133, four at a time 116; odd f16 rows, 8192 of four,
+// 1001, eight pieces 49, two 64.
+template <class T, class P, int KC, int U>
+__global__ void __launch_bounds__(kThreads, sizeof(P) == 16 ? 5 : 3)
 lm_expert_combine_grad_kernel(const ExpertRows p, int64_t pieces) {
     griddep_launch_dependents();
     griddep_wait();
@@ -245,40 +344,53 @@ lm_expert_combine_grad_kernel(const ExpertRows p, int64_t pieces) {
     const P *dy = reinterpret_cast<const P *>(static_cast<const char *>(p.x) + t * p.ldx);
     for (int j0 = 0; j0 < p.k; j0 += KC) {
         float dot[KC], w[KC];
-        int32_t slot[KC];
+        bool none[KC];                                      // zeros, whatever dy holds
+        const P *row[KC];                                   // NULL: takes no part in dweights
+        P *to[KC];                                          // NULL: no row
 #pragma unroll
         for (int j = 0; j < KC; ++j) {
             dot[j] = 0.f;
             w[j] = 0.f;
-            slot[j] = INT32_MIN;                            // no row at all
+            row[j] = nullptr;
+            to[j] = nullptr;
+            none[j] = true;
             if (j0 + j < p.k) {
-                slot[j] = p.slots[t * p.k + j0 + j];
-                w[j] = p.weights != nullptr ? p.weights[t * p.k + j0 + j] : 1.f;
+                const int32_t slot = p.slots[t * p.k + j0 + j], at = slot < 0 ? ~slot : slot;
+                none[j] = slot < 0;
+                if (slot >= 0) w[j] = p.weights != nullptr ? p.weights[t * p.k + j0 + j] : 1.f;
+                if (p.dweights != nullptr && row_of(p, slot))
+                    row[j] = reinterpret_cast<const P *>(static_cast<const char *>(p.rows) + slot * p.ldr);
+                if (p.out != nullptr && row_of(p, at))
+                    to[j] = reinterpret_cast<P *>(static_cast<char *>(p.out) + at * p.ldo);
             }
         }
-        for (int64_t c = threadIdx.x; c < pieces; c += blockDim.x) {
-            Pc g, r[KC];
-            g.p = dy[c];
-            if (p.dweights != nullptr) {
+        for (int64_t c0 = threadIdx.x; c0 < pieces; c0 += (int64_t)blockDim.x * U) {
+            Pc g[U], r[KC][U];
 #pragma unroll
-                for (int j = 0; j < KC; ++j)
-                    if (row_of(p, slot[j]))
-                        r[j].p = reinterpret_cast<const P *>(static_cast<const char *>(p.rows) + slot[j] * p.ldr)[c];
+            for (int u = 0; u < U; ++u) {
+                const int64_t c = c0 + u * blockDim.x;
+                if (c < pieces) {
+                    g[u].p = dy[c];
 #pragma unroll
-                for (int j = 0; j < KC; ++j)
-                    if (row_of(p, slot[j]))
-#pragma unroll
-                        for (int e = 0; e < Pc::N; ++e) dot[j] = fmaf(g.get(e), r[j].get(e), dot[j]);
+                    for (int j = 0; j < KC; ++j)
+                        if (row[j] != nullptr) r[j][u].p = row[j][c];
+                }
             }
-            if (p.out != nullptr) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t c = c0 + u * blockDim.x;
+                if (c >= pieces) break;
 #pragma unroll
                 for (int j = 0; j < KC; ++j) {
-                    const int32_t at = slot[j] < 0 ? ~slot[j] : slot[j];
-                    if (!row_of(p, at)) continue;
-                    Pc v;
+                    if (row[j] != nullptr)
 #pragma unroll
-                    for (int e = 0; e < Pc::N; ++e) v.set(e, slot[j] < 0 ? 0.f : w[j] * g.get(e));
-                    reinterpret_cast<P *>(static_cast<char *>(p.out) + at * p.ldo)[c] = v.p;
+                        for (int e = 0; e < Pc::N; ++e) dot[j] = fmaf(g[u].get(e), r[j][u].get(e), dot[j]);
+                    if (to[j] != nullptr) {
+                        Pc v;
+#pragma unroll
+                        for (int e = 0; e < Pc::N; ++e) v.set(e, none[j] ? 0.f : w[j] * g[u].get(e));
+                        to[j][c] = v.p;
+                    }
                 }
             }
         }
@@ -301,16 +413,12 @@ lm_expert_combine_grad_kernel(const ExpertRows p, int64_t pieces) {
     }
 }
 
-template <class P>
-cudaError_t dispatch_by_piece(const ExpertRows &p, cudaStream_t s) {
-    constexpr int U = 4;
-    const int64_t pieces = p.D * p.elem / (int64_t)sizeof(P), parts = (pieces + U * 32 - 1) / (U * 32);
-    return launch(lm_expert_dispatch_kernel<P, U>, blocks_for(p.T * parts), kThreads, s, p, pieces, parts);
-}
+// Pieces that a lane takes at once: narrow ones (rows of odd bases or pitches) many.
+template <class P> constexpr int kPieces = sizeof(P) >= 8 ? 4 : 8;
 
 template <class T, class P>
 cudaError_t combine_by_piece(const ExpertRows &p, cudaStream_t s) {
-    constexpr int U = 2;
+    constexpr int U = kPieces<P> / 2;
     const int64_t pieces = p.D * p.elem / (int64_t)sizeof(P), parts = (pieces + U * 32 - 1) / (U * 32);
     return launch(lm_expert_combine_kernel<T, P, U>, blocks_for(p.T * parts), kThreads, s, p, pieces, parts);
 }
@@ -318,13 +426,16 @@ cudaError_t combine_by_piece(const ExpertRows &p, cudaStream_t s) {
 template <class T, class P>
 cudaError_t grad_by_piece(const ExpertRows &p, cudaStream_t s) {
     const int64_t pieces = p.D * p.elem / (int64_t)sizeof(P);
-    const int threads = (int)std::min<int64_t>(kThreads, std::max<int64_t>(32, (pieces + 31) / 32 * 32));
-    return launch(lm_expert_combine_grad_kernel<T, P>, p.T, threads, s, p, pieces);
+    auto run = [&](auto choices) {
+        constexpr int KC = decltype(choices)::value, U = (sizeof(P) == 16 ? 4 : 16) / KC;
+        const int64_t each = (pieces + U - 1) / U;
+        const int threads = (int)std::min<int64_t>(kThreads, std::max<int64_t>(32, (each + 31) / 32 * 32));
+        return launch(lm_expert_combine_grad_kernel<T, P, KC, U>, p.T, threads, s, p, pieces);
+    };
+    return p.k == 1 ? run(std::integral_constant<int, 1>()) : run(std::integral_constant<int, 2>());
 }
 
-}  // namespace
-
-cudaError_t expert_sort_launch(const int64_t *experts, int n, int G, int32_t *slots, int32_t *ends, cudaStream_t s) {
+cudaError_t sort_launch(const int64_t *experts, int n, int G, int32_t *slots, int32_t *ends, cudaStream_t s) {
     const size_t smem = size_t(G + 1) * (kSortWarps + 2) * 4;
     if (smem > 48 * 1024) {                       // (for any number of experts: another call may ask for more)
         const cudaError_t opted = cudaFuncSetAttribute(lm_expert_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -351,12 +462,29 @@ cudaError_t expert_sort_launch(const int64_t *experts, int n, int G, int32_t *sl
     return cudaLaunchKernelEx(&cfg, lm_expert_sort_kernel, experts, n, G, slots, ends);
 }
 
-cudaError_t expert_dispatch_launch(const ExpertRows &p, cudaStream_t s) {
+template <class P>
+cudaError_t dispatch_by_piece(const ExpertRows &p, const int64_t *experts, int G, int32_t *slots, int32_t *ends,
+                              cudaStream_t s) {
+    constexpr int U = kPieces<P>;
+    const int64_t pieces = p.D * p.elem / (int64_t)sizeof(P), parts = (pieces + U * 32 - 1) / (U * 32);
+    const bool any = p.T * p.k > 0 && p.D > 0;
+    if (any && few_choices(p.T * p.k, parts))
+        return launch(lm_expert_dispatch_few_kernel<P, U>, blocks_for(p.T * parts), kThreads, s, p, experts, G, ends,
+                      pieces, parts);
+    const cudaError_t e = sort_launch(experts, int(p.T * p.k), G, slots, ends, s);
+    if (e != cudaSuccess || !any) return e;
+    return launch(lm_expert_dispatch_kernel<P, U>, blocks_for(p.T * parts), kThreads, s, p, pieces, parts);
+}
+
+}  // namespace
+
+cudaError_t expert_dispatch_launch(const ExpertRows &p, const int64_t *experts, int G, int32_t *slots, int32_t *ends,
+                                   cudaStream_t s) {
     switch (piece_bytes({address(p.x), p.ldx, address(p.out), p.ldo, p.D * p.elem})) {
-        case 16: return dispatch_by_piece<uint4>(p, s);
-        case 8: return dispatch_by_piece<uint2>(p, s);
-        case 4: return dispatch_by_piece<uint32_t>(p, s);
-        default: return dispatch_by_piece<uint16_t>(p, s);
+        case 16: return dispatch_by_piece<uint4>(p, experts, G, slots, ends, s);
+        case 8: return dispatch_by_piece<uint2>(p, experts, G, slots, ends, s);
+        case 4: return dispatch_by_piece<uint32_t>(p, experts, G, slots, ends, s);
+        default: return dispatch_by_piece<uint16_t>(p, experts, G, slots, ends, s);
     }
 }
 

@@ -25,10 +25,7 @@ struct RouteArgs {
 // type: sgemmDataType_t.
 cudaError_t route_launch(int type, bool grad, const RouteArgs &p, cudaStream_t s);
 
-// slots[a] of n choices of G experts, and ends[g].
-cudaError_t expert_sort_launch(const int64_t *experts, int n, int G, int32_t *slots, int32_t *ends, cudaStream_t s);
-
-// Rows of `bytes` bytes each, pitches in bytes.
+// Rows; pitches in bytes.
 struct ExpertRows {
     int64_t T;
     int k;
@@ -43,7 +40,9 @@ struct ExpertRows {
     int64_t ldr;                // bytes
     float *dweights;            // gradient: [T][k] or NULL
 };
-cudaError_t expert_dispatch_launch(const ExpertRows &p, cudaStream_t s);
+// Writes slots (p.slots) and ends[G] as well.
+cudaError_t expert_dispatch_launch(const ExpertRows &p, const int64_t *experts, int G, int32_t *slots, int32_t *ends,
+                                   cudaStream_t s);
 cudaError_t expert_combine_launch(int type, const ExpertRows &p, cudaStream_t s);
 cudaError_t expert_combine_grad_launch(int type, const ExpertRows &p, cudaStream_t s);
 

@@ -87,9 +87,6 @@ sgemmStatus_t sgemmExpertDispatch(sgemmHandle_t h, sgemmDataType_t type, int64_t
     if (!any && G == 0) return SGEMM_STATUS_SUCCESS;
     if (h == nullptr) return SGEMM_STATUS_INVALID_VALUE;
     if ((st = check_device(h)) != SGEMM_STATUS_SUCCESS) return st;
-    if ((st = status(sg::expert_sort_launch(experts, int(T * k), int(G), slots, groupEnds, stream))) !=
-            SGEMM_STATUS_SUCCESS || !any || D == 0)
-        return st;
     sg::ExpertRows p{};
     p.T = T;
     p.k = int(k);
@@ -100,7 +97,7 @@ sgemmStatus_t sgemmExpertDispatch(sgemmHandle_t h, sgemmDataType_t type, int64_t
     p.slots = slots;
     p.out = rows;
     p.ldo = ldr * p.elem;
-    return status(sg::expert_dispatch_launch(p, stream));
+    return status(sg::expert_dispatch_launch(p, experts, int(G), slots, groupEnds, stream));
 }
 
 sgemmStatus_t sgemmExpertCombine(sgemmHandle_t h, sgemmDataType_t type, int64_t T, int64_t D, int64_t k,
