@@ -126,8 +126,8 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         prefetch_tensormap(&tmX);
     }
     // The kernel before wrote x and its scales, and let this one begin when all
-    // before it was done: only what reads those two, and what C is written by,
-    // waits for it.  W is on its way and converted meanwhile.
+    // before it was done: W's first stages are on their way and converted meanwhile.
+    // Every wait that has a limit begins behind it, however long it takes.
     griddep_launch_dependents();
     if (warp == 2) {
         if (p.ends != nullptr) {
@@ -164,6 +164,7 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
             const int nx = w.n0 + (int)rank * (w.nmma >> 1);
             for (int kb = 0; kb < w.nkb; ++kb) {
                 if (p.withhold == kWithholdRefill && issued >= STAGES) { ok = false; break; }
+                if (issued == STAGES) griddep_wait();
                 if (!mbar_wait_bounded<false>(&empty[stage], phase ^ 1u, p.timeout_ns)) {
                     if (lane == 0) record_error(p.err, kSiteProducerEmpty);
                     ok = false;
@@ -204,6 +205,7 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         }
     } else if (warp == 1 && rank == 0) {
         // ---------------- MMAs (one elected lane of a uniform warp) ----------------
+        griddep_wait();
         const uint64_t db0 = smem_desc_k_sw128(smem_u32(smem_x));
         int stage = 0, gc = 0;
         uint32_t phase = 0, block = 0;
@@ -279,6 +281,7 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&wempty[stage]);
                 if (block >= SLOTS) {
+                    if (block == SLOTS) griddep_wait();
                     // The MMAs of the block that had this slot are done.
                     const uint32_t before = block - SLOTS;
                     ok = mbar_wait_bounded<false>(&xempty[before % STAGES], (before / STAGES) & 1u,
@@ -298,7 +301,7 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                 __syncwarp();
                 // (Only the stores to tensor memory have to come before: they are
                 // complete, and fenced.  With release semantics the arrival waits
-                // for more: 8192 rows, 4096 x 14336, 1461 us, without 644.)
+                // for more: 8192 rows, 4096 x 14336, 1461 us, without 644, at that time.)
                 if (lane == 0) mbar_arrive_cluster_relaxed(ready0 + (uint32_t)stage * 8u);
                 ++block;
                 if (++stage == STAGES) { stage = 0; phase ^= 1u; }

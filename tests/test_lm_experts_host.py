@@ -84,3 +84,49 @@ def test_combine(lib):
     assert combine(lib, T=0, rows=None, slots=None, weights=None, Y=None, h=None) == S.SUCCESS
     # Nothing asked for.
     assert combine_grad(lib, drows=None, dw=None, rows=None, h=None) == S.SUCCESS
+
+
+S8 = 3
+
+
+def quantize(lib, ty=BF16, T=4, K=32, X=F, ldx=32, Q=F, ldq=32, scales=F, h=F):
+    return lib.sgemmInt8Quantize(h, ty, T, K, X, ldx, Q, ldq, scales, None)
+
+
+def int8(lib, tx=BF16, tc=BF16, T=4, N=16, K=32, G=1, X=F, ldx=32, xs=None, B=F, ldb=32, sb=16 * 32, scales=F, ends=None,
+         C=F, ldc=16, h=F):
+    return lib.sgemmInt8(h, tx, tc, T, N, K, G, X, ldx, xs, B, ldb, sb, scales, ends, C, ldc, None)
+
+
+def test_quantize(lib):
+    for bad in (dict(ty=S8), dict(T=-1), dict(K=-1), dict(X=None), dict(ldx=31), dict(Q=None), dict(ldq=31),
+                dict(scales=None), dict(h=None)):
+        assert quantize(lib, **bad) == S.INVALID_VALUE, bad
+    assert quantize(lib, X=F + 1) == S.MISALIGNED
+    assert quantize(lib, scales=F + 2) == S.MISALIGNED
+    assert quantize(lib, K=2 ** 31, ldx=2 ** 31, ldq=2 ** 31) == S.NOT_SUPPORTED
+    assert quantize(lib, T=0, X=None, Q=None, scales=None, h=None) == S.SUCCESS
+
+
+def test_int8(lib):
+    for bad in (dict(tx=4), dict(tc=S8), dict(tc=-1), dict(T=-1), dict(N=-1), dict(K=-1), dict(G=-1), dict(X=None),
+                dict(ldx=31), dict(B=None), dict(ldb=31), dict(scales=None), dict(C=None), dict(ldc=15), dict(h=None),
+                dict(xs=F), dict(tx=S8), dict(G=2), dict(G=2, ends=F, sb=511), dict(sb=-1)):
+        assert int8(lib, **bad) == S.INVALID_VALUE, bad
+    for bad in (dict(X=F + 1), dict(scales=F + 2), dict(C=F + 1), dict(ends=F + 2), dict(tx=S8, xs=F + 1)):
+        assert int8(lib, **bad) == S.MISALIGNED, bad
+    for bad in (dict(K=131072, ldx=131072, ldb=131072, sb=16 * 131072), dict(G=1025, ends=F), dict(T=2 ** 31),
+                dict(N=2 ** 31, ldc=2 ** 31)):
+        assert int8(lib, **bad) == S.NOT_SUPPORTED, bad
+    assert int8(lib, T=0, X=None, B=None, scales=None, C=None, h=None) == S.SUCCESS
+    assert int8(lib, N=0, ldc=1, X=None, B=None, scales=None, C=None, h=None) == S.SUCCESS
+
+
+def test_int8_workspace(lib):
+    import ctypes
+    n = ctypes.c_size_t(7)
+    ask = lib.sgemmInt8WorkspaceSize
+    assert ask(F, BF16, BF16, 0, 16, 32, 1, None, 32, None, 32, 512, ctypes.byref(n)) == S.SUCCESS and n.value == 0
+    assert ask(None, BF16, BF16, 4, 16, 32, 1, F, 32, F, 32, 512, ctypes.byref(n)) == S.INVALID_VALUE
+    assert ask(F, BF16, 7, 4, 16, 32, 1, F, 32, F, 32, 512, ctypes.byref(n)) == S.INVALID_VALUE
+    assert ask(F, BF16, BF16, 4, 16, 32, 1, F, 32, F, 32, 512, None) == S.INVALID_VALUE
