@@ -41,8 +41,8 @@ int64_t int8_rows_pitch(int tokens, int64_t k_slice);
 int64_t int8_rows_smem(int tokens, int rows, int warps, int64_t k_slice, int64_t G);
 
 LmKernel int8_mma_kernel();
-constexpr int kInt8TileN = 192;      // tokens of a tile at most
-constexpr int kInt8BlockK = 128;
+constexpr int kInt8TileN = 128;      // tokens of a tile at most
+constexpr int kInt8BlockK = 256;
 
 // out = x_scales * scales * (sum of `splits` int32 planes), rounded to `out_type`;
 // rows of no group (row_group < 0) become zeros.

@@ -127,13 +127,13 @@ sgemmStatus_t plan_int8(const sgemmContext *h, int from, int to, int64_t T, int6
         if (G == 1 && T > sg::kInt8TileN) {
             double best = 0.0;
             q.tile_n = 0;
-            for (int n = sg::kInt8TileN; n >= 96; n -= 32) {
-                const double cost = double(ceil_div(high * ceil_div(T, n), pairs)) * std::max(n, 128);
+            for (int n = sg::kInt8TileN; n >= 64; n -= 32) {
+                const double cost = double(ceil_div(high * ceil_div(T, n), pairs)) * (n + 16);
                 if (q.tile_n == 0 || cost < best) { best = cost; q.tile_n = n; }
             }
         }
         const int64_t most = high * (T / q.tile_n + std::min(G, T % q.tile_n == 0 && G == 1 ? 0 : T));
-        q.splits = int(std::max<int64_t>(1, std::min(pairs / std::max<int64_t>(1, most), ceil_div(K, sg::kInt8BlockK) / 4)));
+        q.splits = int(std::max<int64_t>(1, std::min(pairs / std::max<int64_t>(1, most), ceil_div(K, sg::kInt8BlockK) / 2)));
     }
     if (q.parts() > 1) {
         q.ld_part = round_up(N, 8);

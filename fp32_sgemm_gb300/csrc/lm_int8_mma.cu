@@ -29,11 +29,11 @@ namespace {
 
 struct Int8Tile {
     static constexpr int GRAN = 32, TILE_M = 256, BN = kInt8TileN, BK = kInt8BlockK;
-    static constexpr int STAGES = 5, SLOTS = 2;
-    static constexpr int W_BYTES = 128 * BK, X_CHUNK = BN / 2 * 128, X_BYTES = 2 * X_CHUNK;
-    static constexpr int CONV_WARPS = 4, EPI_WARPS = 8, SLAB = BN / 2;
+    static constexpr int STAGES = 3, SLOTS = 2;
+    static constexpr int W_CHUNK = 128 * 128, W_BYTES = BK / 128 * W_CHUNK, X_CHUNK = BN / 2 * 128, X_BYTES = BK / 64 * X_CHUNK;
+    static constexpr int CONV_WARPS = 8, EPI_WARPS = 8, SLAB = BN / 2;
     static constexpr int THREADS = (3 + CONV_WARPS + EPI_WARPS) * 32;
-    static constexpr int TMEM_COLS = 512, SLOT0 = 2 * BN, SLOT_COLS = 64;
+    static constexpr int TMEM_COLS = 512, SLOT0 = 2 * BN, SLOT_COLS = BK / 2;
     static constexpr int BARS = 4 * STAGES + 5;
     static constexpr int STG = 32 * 17, STAGING = EPI_WARPS * STG * 4;
     static constexpr int RING = STAGES * (W_BYTES + X_BYTES);
@@ -156,7 +156,7 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         int stage = 0, issued = 0;
         uint32_t phase = 0;
         bool ok = true;
-        const uint32_t x_bytes = (uint32_t)(p.tile_n / 2 * 128) * 2;       // of this SM, both halves of the block
+        const uint32_t x_bytes = (uint32_t)(p.tile_n / 2 * 128) * (Tile::BK / 64);      // of this SM
         const uint32_t ready0 = cluster_addr(&ready[0], 0);
         for (int t = slot0; ok && t < num_tiles; t += slots) {
             const LmWork w = lm_work<Tile, kRagN>(p, g_start, g_prefix, t);
@@ -175,12 +175,16 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                 if (elect_one()) {
                     if (of_w) {
                         mbar_arrive_expect_tx(&wfull[stage], Tile::W_BYTES);
-                        tma_load_3d(smem + stage * Tile::W_BYTES, &tmW, &wfull[stage], kc, mw, w.g);
+#pragma unroll
+                        for (int c = 0; c < Tile::BK / 128; ++c)
+                            tma_load_3d(smem + stage * Tile::W_BYTES + c * Tile::W_CHUNK, &tmW, &wfull[stage], kc + c * 128, mw,
+                                        w.g);
                     } else {
                         unsigned char *sx = smem_x + stage * Tile::X_BYTES;
                         if (rank == 0) mbar_arrive_expect_tx(&ready[stage], 2 * x_bytes);
-                        tma_load_3d_pair(sx, &tmX, ready0 + (uint32_t)stage * 8u, kc, nx, 0);
-                        tma_load_3d_pair(sx + Tile::X_CHUNK, &tmX, ready0 + (uint32_t)stage * 8u, kc + 64, nx, 0);
+#pragma unroll
+                        for (int c = 0; c < Tile::BK / 64; ++c)
+                            tma_load_3d_pair(sx + c * Tile::X_CHUNK, &tmX, ready0 + (uint32_t)stage * 8u, kc + c * 64, nx, 0);
                     }
                 }
                 __syncwarp();
@@ -236,7 +240,7 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                     const uint32_t a = tmem_base + Tile::SLOT0 + block % SLOTS * Tile::SLOT_COLS;
                     const uint64_t b = db0 + (uint64_t)(stage * (Tile::X_BYTES >> 4));
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
+                    for (int kk = 0; kk < Tile::BK / 16; ++kk)
                         mma_f16_pair_ts(d_tmem, a + kk * 8, b + (kk >> 2) * (Tile::X_CHUNK >> 4) + (kk & 3) * 2, idesc,
                                         first && kk == 0 ? 0u : 1u);
                     if (p.withhold != kWithholdRelease) mma_commit_pair_mc(&xempty[stage], 0x3);
@@ -253,8 +257,10 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         mbar_wait_bounded(drain, 0u, p.timeout_ns);
     } else if (warp >= 2 && warp < 2 + Tile::CONV_WARPS) {
         // ---------------- W into tensor memory ----------------
-        const int quarter = warp & 3, row = quarter * 32 + lane;
-        const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16) + Tile::SLOT0;
+        // (Four warps reach all lanes of tensor memory; the first four take the first
+        // 128 columns of a block, the others the rest.)
+        const int quarter = warp & 3, row = quarter * 32 + lane, half = (warp - 2) >> 2;
+        const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16) + Tile::SLOT0 + half * 64;
         const uint32_t ready0 = cluster_addr(&ready[0], 0);
         int stage = 0;
         uint32_t phase = 0, block = 0;
@@ -267,19 +273,6 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                     if (lane == 0) record_error(p.err, kSiteConsumerFull);
                     break;
                 }
-                const unsigned char *sw = smem + stage * Tile::W_BYTES + row * 128;
-                uint32_t r[2][32];
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(sw + ((c ^ (row & 7)) << 4));
-                    uint32_t *to = &r[c >> 2][(c & 3) * 8];
-                    to_f16(v.x, to[0], to[1]);
-                    to_f16(v.y, to[2], to[3]);
-                    to_f16(v.z, to[4], to[5]);
-                    to_f16(v.w, to[6], to[7]);
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&wempty[stage]);
                 if (block >= SLOTS) {
                     if (block == SLOTS) griddep_wait();
                     // The MMAs of the block that had this slot are done.
@@ -293,9 +286,22 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                     }
                     tc_fence_after();
                 }
-                const uint32_t to = lane_base + block % SLOTS * Tile::SLOT_COLS;
-                tmem_st_32cols(to, r[0]);
-                tmem_st_32cols(to + 32, r[1]);
+                const unsigned char *sw = smem + stage * Tile::W_BYTES + half * Tile::W_CHUNK + row * 128;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t r[32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(sw + (((h * 4 + c) ^ (row & 7)) << 4));
+                        to_f16(v.x, r[8 * c], r[8 * c + 1]);
+                        to_f16(v.y, r[8 * c + 2], r[8 * c + 3]);
+                        to_f16(v.z, r[8 * c + 4], r[8 * c + 5]);
+                        to_f16(v.w, r[8 * c + 6], r[8 * c + 7]);
+                    }
+                    tmem_st_32cols(lane_base + block % SLOTS * Tile::SLOT_COLS + h * 32, r);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&wempty[stage]);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
