@@ -33,16 +33,15 @@ struct Int8Args {
     int x_pitch;                     // bytes of a token's x in shared memory
 };
 
-// Tokens of a tile: 1, 2, 4, 8 or 16; warps 8 (ks 1, 4 or 8) or 16 (ks 4, 8 or
+// Tokens of a tile: 1, 2, 4 or 8; warps 8 (ks 1, 4 or 8) or 16 (ks 4, 8 or
 // 16), ks of which share the contraction of 16 rows.
 LmKernel int8_rows_kernel(int tokens, int warps, int ks);
 // Bytes of one token's x, and of a CTA with x of `rows` tokens.
 int64_t int8_rows_pitch(int tokens, int64_t k_slice);
 int64_t int8_rows_smem(int tokens, int rows, int warps, int64_t k_slice, int64_t G);
 
-LmKernel int8_mma_kernel();
-constexpr int kInt8TileN = 128;      // tokens of a tile at most
-constexpr int kInt8BlockK = 256;
+// bn: rows of x in a tile at most; gran: columns of K in a block.
+LmKernel int8_mma_kernel(bool wide);
 
 // out = x_scales * scales * (sum of `splits` int32 planes), rounded to `out_type`;
 // rows of no group (row_group < 0) become zeros.

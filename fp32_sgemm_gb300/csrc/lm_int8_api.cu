@@ -22,6 +22,7 @@ struct Int8 {
     int tokens = 0, warps = 0, ks = 0, slices = 1;
     int64_t k_slice = 0, x_pitch = 0, smem = 0;
     // tensor cores
+    bool wide = false;
     int tile_n = 0, splits = 1;
     int64_t ld_part = 0;
     size_t ws_x = 0, ws_scales = 0, ws_w = 0, ws_group = 0, ws_part = 0;
@@ -37,9 +38,13 @@ sgemmStatus_t check_x(int from, const void *X, int64_t T, int64_t K, int64_t ldx
     return T > kMaxDim || ldx > kMaxBytes / T ? SGEMM_STATUS_NOT_SUPPORTED : SGEMM_STATUS_SUCCESS;
 }
 
-// Few rows a group in the mean: straight from memory, W read once for 8 or 16 of
-// them; otherwise the tensor cores.
-constexpr int64_t kInt8FewRows = 16;
+// Few rows a group in the mean: straight from memory, W read once for up to 8 of
+// them; otherwise the tensor cores (8 rows, 28672 x 8192: 46 and 51 us, 12 rows 84 of
+// 16 at a time and 51; 16 groups of 8 rows, 2048 x 1408: 16.8 and 17.9, of 12, 20.0
+// and 18.1).
+constexpr int64_t kInt8FewRows = 8;
+// Bytes of x that every CTA quantises itself instead of a launch of its own (one
+// row, 4096 x 4096: 5.5 us, 7.3).
 constexpr int64_t kInt8OwnBytes = 16384;
 
 sgemmStatus_t plan_int8(const sgemmContext *h, int from, int to, int64_t T, int64_t N, int64_t K, int64_t G,
@@ -69,15 +74,14 @@ sgemmStatus_t plan_int8(const sgemmContext *h, int from, int to, int64_t T, int6
     q.rows = mean <= kInt8FewRows;
     q.ws_scales = from == SGEMM_TYPE_S8 ? 0 : align256(T * 4);
     if (q.rows) {
-        // A row or two that one matrix meets: each CTA quantises them itself.
         const bool own = from != SGEMM_TYPE_S8 && G == 1 && T * K * type_size(from) <= kInt8OwnBytes;
         q.x_copy = !own && (from != SGEMM_TYPE_S8 || !aligned(X, 16) || ldx % 16 != 0);
         q.ldx = q.x_copy ? round_up(K, 16) : ldx;
         q.ws_x = q.x_copy ? align256(T * q.ldx) : 0;
         // (By group the mean decides, the sizes being on the device: tiles of four
         // tokens where it is about one.)
-        if (G == 1) q.tokens = T == 1 ? 1 : T == 2 ? 2 : T <= 4 ? 4 : T <= 8 ? 8 : 16;
-        else q.tokens = mean <= 1 ? 4 : mean <= 8 ? 8 : 16;
+        if (G == 1) q.tokens = T == 1 ? 1 : T == 2 ? 2 : T <= 4 ? 4 : 8;
+        else q.tokens = mean <= 1 ? 4 : 8;
         const int rows = int(std::min<int64_t>(T, q.tokens));
         // x of a tile's tokens beside half of an SM's shared memory, all of it,
         // or the contraction in parts.
@@ -119,21 +123,37 @@ sgemmStatus_t plan_int8(const sgemmContext *h, int from, int to, int64_t T, int6
             q.stride_w = q.ldw * N;
             q.ws_w = align256(q.stride_w * G);
         }
-        // Rows of a tile: as many as a group has in the mean.  A block of W costs
-        // its conversion whatever the rows are, so that few tiles with the
-        // contraction cut between pairs come before more tiles.
+        // Kernel and rows of a tile.  One matrix: what has the least rounds of tiles times
+        // what a tile costs, which is hardly less for fewer rows, as its W is converted
+        // all the same (8192 rows, 4096 x 14336: 48 rounds of 128, 583 us, 32 of 192,
+        // 552; 2048 rows: 12 of 128, 152, 9 of 192, 193; 2048 rows, 4096 x 4096: 4 of 128,
+        // 68, 3 of 160, 62).  Groups: as many as one has in the mean, wide from 512 on
+        // (16 of 2048 rows, 4096 x 2048: 429 us, 441; 64 of 128, 1024 x 2048: 57, 53).
         const int64_t pairs = h->sm_count / 2, high = ceil_div(N, 256);
-        q.tile_n = int(std::min<int64_t>(sg::kInt8TileN, round_up(std::max<int64_t>(mean, 1), 32)));
-        if (G == 1 && T > sg::kInt8TileN) {
-            double best = 0.0;
-            q.tile_n = 0;
-            for (int n = sg::kInt8TileN; n >= 64; n -= 32) {
-                const double cost = double(ceil_div(high * ceil_div(T, n), pairs)) * (n + 16);
-                if (q.tile_n == 0 || cost < best) { best = cost; q.tile_n = n; }
+        const int64_t blocks = ceil_div(K, 256);
+        // (Parts of the contraction, of two blocks at least, where the tiles leave
+        // pairs idle; joining them takes what ten blocks do.)
+        auto parts_of = [&](int64_t tiles) {
+            return std::max<int64_t>(1, std::min(pairs / std::max<int64_t>(1, tiles), blocks / 2));
+        };
+        if (G == 1) {
+            int64_t best = 0;
+            for (int n = 192; n >= 32; n -= 32) {
+                if (n >= T + 32) continue;
+                const int64_t tiles = high * ceil_div(T, n), parts = parts_of(tiles);
+                const int64_t cost = ceil_div(tiles, pairs) * ceil_div(blocks, parts) * (n > 160 ? 196 : n > 128 ? 184 : 138) +
+                                     (parts > 1 ? 1380 : 0);
+                if (best != 0 && cost >= best) continue;
+                best = cost;
+                q.tile_n = n;
             }
+            q.splits = int(parts_of(high * ceil_div(T, q.tile_n)));
+        } else {
+            const int most = sg::int8_mma_kernel(mean >= 512).bn;
+            q.tile_n = int(std::min<int64_t>(most, round_up(std::max<int64_t>(mean, 1), 32)));
+            q.splits = int(parts_of(high * (T / q.tile_n + std::min(G, T))));
         }
-        const int64_t most = high * (T / q.tile_n + std::min(G, T % q.tile_n == 0 && G == 1 ? 0 : T));
-        q.splits = int(std::max<int64_t>(1, std::min(pairs / std::max<int64_t>(1, most), ceil_div(K, sg::kInt8BlockK) / 2)));
+        q.wide = q.tile_n > 128;
     }
     if (q.parts() > 1) {
         q.ld_part = round_up(N, 8);
@@ -241,10 +261,10 @@ sgemmStatus_t sgemmInt8(sgemmHandle_t h, sgemmDataType_t typeX, sgemmDataType_t 
         a.lm.tiles_m = int(ceil_div(N, k.tile_m));
         tiles = int64_t(a.lm.tiles_m) * (ceil_div(T, a.lm.tile_n) + G + 1);
     } else {
-        k = sg::int8_mma_kernel();
+        k = sg::int8_mma_kernel(q.wide);
         a.lm.tile_n = q.tile_n;
         a.lm.tiles_m = int(ceil_div(N, k.tile_m));
-        a.lm.kb = int(ceil_div(K, sg::kInt8BlockK));
+        a.lm.kb = int(ceil_div(K, k.gran));
         tiles = int64_t(a.lm.tiles_m) * (ceil_div(T, a.lm.tile_n) + G + 1) * q.splits;
     }
     if (tiles > kMaxDim) return SGEMM_STATUS_NOT_SUPPORTED;

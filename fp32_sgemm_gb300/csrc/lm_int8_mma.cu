@@ -17,8 +17,8 @@
 // the 512 columns of tensor memory).  An accumulator takes 1024 terms, whose sum
 // FP32 holds exactly; the epilogue's warps add them up as 32-bit integers.
 //
-// Warps: 0 copies W, 14 x, 1 issues the MMAs, 2 to 5 convert, 6 to 13 are the
-// epilogue.
+// Warps: 0 copies W, the last one x, 1 issues the MMAs, four or eight from 2 on
+// convert, then eight are the epilogue.
 #include <type_traits>
 
 #include "lm_int8.h"
@@ -27,11 +27,14 @@
 namespace sg {
 namespace {
 
+// BN: rows of x in a tile at most; BK: columns of K in a block.
+template <int BN_, int BK_, int STAGES_, int CONV_>
 struct Int8Tile {
-    static constexpr int GRAN = 32, TILE_M = 256, BN = kInt8TileN, BK = kInt8BlockK;
-    static constexpr int STAGES = 3, SLOTS = 2;
+    static constexpr int GRAN = 32, TILE_M = 256, BN = BN_, BK = BK_;
+    static constexpr int STAGES = STAGES_, SLOTS = 2;
     static constexpr int W_CHUNK = 128 * 128, W_BYTES = BK / 128 * W_CHUNK, X_CHUNK = BN / 2 * 128, X_BYTES = BK / 64 * X_CHUNK;
-    static constexpr int CONV_WARPS = 8, EPI_WARPS = 8, SLAB = BN / 2;
+    static constexpr int CONV_WARPS = CONV_, EPI_WARPS = 8, SLAB = BN / 2;
+    static constexpr int CONV_COLS = BK / (CONV_WARPS / 4);         // of a converting warp (four reach all lanes)
     static constexpr int THREADS = (3 + CONV_WARPS + EPI_WARPS) * 32;
     static constexpr int TMEM_COLS = 512, SLOT0 = 2 * BN, SLOT_COLS = BK / 2;
     static constexpr int BARS = 4 * STAGES + 5;
@@ -42,6 +45,11 @@ struct Int8Tile {
     static_assert(SLOT0 + SLOTS * SLOT_COLS <= TMEM_COLS && X_CHUNK % 1024 == 0 && W_BYTES % 1024 == 0, "");
     static_assert(FIXED + 8 * (kLmMaxGroups + 2) <= 227 * 1024, "room for the group tables");
 };
+// Few turns of the warps' loops, which bound all but the largest products; and wide
+// tiles, which move less through shared memory and L2.  2048 rows, 4096 x 14336:
+// 157 us, in wide tiles 196; 8192 rows: 598 and 547.
+using Int8Deep = Int8Tile<128, 256, 3, 8>;
+using Int8Wide = Int8Tile<192, 128, 5, 4>;
 
 __device__ __forceinline__ void mma_f16_pair_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                                 uint32_t accumulate) {
@@ -78,11 +86,50 @@ __device__ __forceinline__ void to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
     hi = *reinterpret_cast<const uint32_t *>(&dh);
 }
 
+// Tile t as lm_work gives it (kRagN), without its 64-bit divisions: every warp asks
+// at every tile, and the MMAs' warp is waited for meanwhile.
+template <class Tile>
+__device__ __forceinline__ LmWork int8_work(const LmArgs &p, const int *start, const uint32_t *prefix, int tile) {
+    LmWork w;
+    uint32_t t = (uint32_t)tile;
+    w.s = 0;
+    w.kb0 = 0;
+    w.nkb = p.kb;
+    if (p.splits > 1) {
+        w.s = (int)(t % (uint32_t)p.splits);
+        t /= (uint32_t)p.splits;
+        // (p.kb is at most 1024.)
+        w.kb0 = (int)((uint32_t)(p.kb * w.s) / (uint32_t)p.splits);
+        w.nkb = (int)((uint32_t)(p.kb * (w.s + 1)) / (uint32_t)p.splits) - w.kb0;
+    }
+    int lo = 0, hi = p.G;                   // last g with prefix[g] <= t
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (prefix[mid] <= t) lo = mid;
+        else hi = mid - 1;
+    }
+    w.g = lo;
+    const uint32_t local = t - prefix[lo], rows = (uint32_t)(start[lo + 1] - start[lo]);
+    const uint32_t nt = (rows + (uint32_t)p.tile_n - 1) / (uint32_t)p.tile_n;
+    const uint32_t per = ((rows + nt - 1) / nt + Tile::GRAN - 1) / Tile::GRAN * Tile::GRAN;
+    const uint32_t wide = (uint32_t)p.group_m * nt, band = local / wide, in = local - band * wide;
+    const uint32_t bw = min((uint32_t)p.group_m, (uint32_t)p.tiles_m - band * (uint32_t)p.group_m);
+    const uint32_t tn = in / bw, tm = band * (uint32_t)p.group_m + in - tn * bw;
+    w.m0 = (int)(tm * Tile::TILE_M);
+    w.n0 = start[lo] + (int)(tn * per);
+    w.nvalid = (int)min(per, rows - tn * per);
+    w.nmma = (w.nvalid + Tile::GRAN - 1) / Tile::GRAN * Tile::GRAN;
+    if (lo == p.G) w.nkb = 0;
+    w.krow0 = 0;
+    w.klast = 64;
+    return w;
+}
+
 // tmW: bytes {K, N, G}, boxes of 128 x 128.  tmX: f16 {K, T}, boxes of 64 x tile_n / 2.
-__global__ void __launch_bounds__(Int8Tile::THREADS, 1)
+template <class Tile>
+__global__ void __launch_bounds__(Tile::THREADS, 1)
 lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                    const __grid_constant__ Int8Args q) {
-    using Tile = Int8Tile;
     constexpr int STAGES = Tile::STAGES, SLOTS = Tile::SLOTS, BN = Tile::BN, SLAB = Tile::SLAB;
     const LmArgs &p = q.lm;
     extern __shared__ unsigned char smem_raw[];
@@ -159,7 +206,7 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         const uint32_t x_bytes = (uint32_t)(p.tile_n / 2 * 128) * (Tile::BK / 64);      // of this SM
         const uint32_t ready0 = cluster_addr(&ready[0], 0);
         for (int t = slot0; ok && t < num_tiles; t += slots) {
-            const LmWork w = lm_work<Tile, kRagN>(p, g_start, g_prefix, t);
+            const LmWork w = int8_work<Tile>(p, g_start, g_prefix, t);
             const int mw = w.m0 + (int)rank * 128;
             const int nx = w.n0 + (int)rank * (w.nmma >> 1);
             for (int kb = 0; kb < w.nkb; ++kb) {
@@ -215,7 +262,7 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         uint32_t phase = 0, block = 0;
         bool ok = true;
         for (int t = slot0; ok && t < num_tiles; t += slots) {
-            const LmWork w = lm_work<Tile, kRagN>(p, g_start, g_prefix, t);
+            const LmWork w = int8_work<Tile>(p, g_start, g_prefix, t);
             const uint32_t idesc = idesc_f16(0, false, false, Tile::TILE_M, w.nmma);
             uint32_t d_tmem = 0;
             for (int kb = 0; kb < w.nkb; ++kb) {
@@ -257,16 +304,16 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         mbar_wait_bounded(drain, 0u, p.timeout_ns);
     } else if (warp >= 2 && warp < 2 + Tile::CONV_WARPS) {
         // ---------------- W into tensor memory ----------------
-        // (Four warps reach all lanes of tensor memory; the first four take the first
-        // 128 columns of a block, the others the rest.)
-        const int quarter = warp & 3, row = quarter * 32 + lane, half = (warp - 2) >> 2;
-        const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16) + Tile::SLOT0 + half * 64;
+        // (Four warps reach all lanes of tensor memory; the next four, if there are
+        // any, take the second half of a block's columns.)
+        const int quarter = warp & 3, row = quarter * 32 + lane, col0 = ((warp - 2) >> 2) * Tile::CONV_COLS;
+        const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16) + Tile::SLOT0 + col0 / 2;
         const uint32_t ready0 = cluster_addr(&ready[0], 0);
         int stage = 0;
         uint32_t phase = 0, block = 0;
         bool ok = true;
         for (int t = slot0; ok && t < num_tiles; t += slots) {
-            const LmWork w = lm_work<Tile, kRagN>(p, g_start, g_prefix, t);
+            const LmWork w = int8_work<Tile>(p, g_start, g_prefix, t);
             for (int kb = 0; kb < w.nkb; ++kb) {
                 ok = __all_sync(~0u, mbar_wait_bounded(&wfull[stage], phase, downstream_limit(p.timeout_ns)));
                 if (!ok) {
@@ -286,7 +333,8 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                     }
                     tc_fence_after();
                 }
-                const unsigned char *sw = smem + stage * Tile::W_BYTES + half * Tile::W_CHUNK + row * 128;
+                const unsigned char *sw = smem + stage * Tile::W_BYTES + col0 / 128 * Tile::W_CHUNK + row * 128;
+                static_assert(Tile::CONV_COLS == 128, "one chunk of W for a warp");
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t r[32];
@@ -323,7 +371,7 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         int gc = 0;
         bool ok = true;
         for (int t = slot0; ok && t < num_tiles; t += slots) {
-            const LmWork w = lm_work<Tile, kRagN>(p, g_start, g_prefix, t);
+            const LmWork w = int8_work<Tile>(p, g_start, g_prefix, t);
             const int row0 = w.m0 + (int)rank * 128 + quarter * 32;       // first channel of this warp
             int sum[SLAB];
 #pragma unroll
@@ -390,17 +438,19 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
 
 }  // namespace
 
-LmKernel int8_mma_kernel() {
+template <class Tile>
+LmKernel mma_kernel_info() {
     LmKernel k;
-    k.fn = reinterpret_cast<const void *>(&lm_int8_mma_kernel);
-    k.threads = Int8Tile::THREADS;
-    k.smem = Int8Tile::FIXED;
-    k.tile_m = Int8Tile::TILE_M;
-    k.bn = Int8Tile::BN;
-    k.gran = Int8Tile::GRAN;
+    k.fn = reinterpret_cast<const void *>(&lm_int8_mma_kernel<Tile>);
+    k.threads = Tile::THREADS;
+    k.smem = Tile::FIXED;
+    k.tile_m = Tile::TILE_M;
+    k.bn = Tile::BN;
+    k.gran = Tile::BK;
     k.pair = 1;
     k.box_a = 128;
     return k;
 }
+LmKernel int8_mma_kernel(bool wide) { return wide ? mma_kernel_info<Int8Wide>() : mma_kernel_info<Int8Deep>(); }
 
 }  // namespace sg

@@ -123,25 +123,51 @@ cudaError_t quantize(const void *x, int64_t ldx, int64_t rows, int64_t K, void *
 
 constexpr int kThreads = 256;
 
+// Four columns of one row a thread (the planes' pitch is a multiple of 8), rows dealt
+// to blockIdx.y.
+template <class T>
 __global__ void __launch_bounds__(kThreads)
 lm_int8_join_kernel(const int32_t *part, int64_t ld, int64_t plane, int splits, const int32_t *row_group,
-                    const float *x_scales, const float *scales, int64_t rows, int64_t cols, void *out, int64_t ldo,
-                    int out_type) {
+                    const float *x_scales, const float *scales, int64_t rows, int64_t cols, T *out, int64_t ldo, bool vec) {
     griddep_launch_dependents();
     griddep_wait();
-    const int64_t total = rows * cols;
-    for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < total; i += gridDim.x * (int64_t)kThreads) {
-        const int64_t r = total <= 0xFFFFFFFFll ? (uint32_t)i / (uint32_t)cols : i / cols, c = i - r * cols;
+    const int64_t c = (blockIdx.x * (int64_t)kThreads + threadIdx.x) * 4;
+    if (c >= cols) return;
+    const int n = (int)min((int64_t)4, cols - c);
+    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
         const int g = row_group[r];
-        float y = 0.f;
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
         if (g >= 0) {
-            int32_t sum = 0;
-            for (int z = 0; z < splits; ++z) sum += part[z * plane + r * ld + c];
-            y = (float)sum * x_scales[r] * scales[g * cols + c];
+            int4 sum = make_int4(0, 0, 0, 0);
+#pragma unroll 4
+            for (int z = 0; z < splits; ++z) {
+                const int4 v = *reinterpret_cast<const int4 *>(part + z * plane + r * ld + c);
+                sum.x += v.x;
+                sum.y += v.y;
+                sum.z += v.z;
+                sum.w += v.w;
+            }
+            const float xs = x_scales[r], s[4] = {(float)sum.x, (float)sum.y, (float)sum.z, (float)sum.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < n) y[i] = s[i] * xs * scales[g * cols + c + i];
         }
-        if (out_type == kOutF32) static_cast<float *>(out)[r * ldo + c] = y;
-        else if (out_type == kOutF16) static_cast<__half *>(out)[r * ldo + c] = __float2half_rn(y);
-        else static_cast<__nv_bfloat16 *>(out)[r * ldo + c] = __float2bfloat16_rn(y);
+        T *to = out + r * ldo + c;
+        alignas(16) T v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) v[i] = y[i];
+            else if constexpr (std::is_same_v<T, __half>) v[i] = __float2half_rn(y[i]);
+            else v[i] = __float2bfloat16_rn(y[i]);
+        }
+        if (vec && n == 4) {
+            if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(v);
+            else *reinterpret_cast<uint2 *>(to) = *reinterpret_cast<const uint2 *>(v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < n) to[i] = v[i];
+        }
     }
 }
 
@@ -187,9 +213,25 @@ cudaError_t int8_quantize_launch(int from, const void *x, int64_t ldx, int64_t T
 cudaError_t int8_join_launch(const int32_t *part, int64_t ld_part, int64_t plane, int splits, const int32_t *row_group,
                              const float *x_scales, const float *scales, int64_t rows, int64_t cols, void *out,
                              int64_t ldo, int out_type, cudaStream_t s) {
-    const int64_t blocks = std::min<int64_t>((rows * cols + kThreads - 1) / kThreads, 152 * 16);
-    return launch(lm_int8_join_kernel, blocks, kThreads, s, part, ld_part, plane, splits, row_group, x_scales, scales,
-                  rows, cols, out, ldo, out_type);
+    const int elem = out_type == kOutF32 ? 4 : 2;
+    const bool vec = reinterpret_cast<uintptr_t>(out) % (4 * elem) == 0 && ldo % 4 == 0;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned((cols + 4 * kThreads - 1) / (4 * kThreads)), unsigned(std::min<int64_t>(rows, 65535)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (out_type == kOutF32)
+        return cudaLaunchKernelEx(&cfg, lm_int8_join_kernel<float>, part, ld_part, plane, splits, row_group, x_scales,
+                                  scales, rows, cols, static_cast<float *>(out), ldo, vec);
+    if (out_type == kOutF16)
+        return cudaLaunchKernelEx(&cfg, lm_int8_join_kernel<__half>, part, ld_part, plane, splits, row_group, x_scales,
+                                  scales, rows, cols, static_cast<__half *>(out), ldo, vec);
+    return cudaLaunchKernelEx(&cfg, lm_int8_join_kernel<__nv_bfloat16>, part, ld_part, plane, splits, row_group, x_scales,
+                              scales, rows, cols, static_cast<__nv_bfloat16 *>(out), ldo, vec);
 }
 
 cudaError_t int8_copy_launch(const int8_t *w, int64_t ldw, int64_t stride, int64_t rows, int64_t cols, int64_t batch,

@@ -142,12 +142,12 @@ __device__ __forceinline__ void stage_numbers(const Int8Args &q, int64_t t0, int
 // Columns of k in one step of a warp: a lane has 16 of every 64 of two rows.
 constexpr int kStep = 256, kLoads = kStep / 64;
 
-// TOKENS: 1, 2 or 4 by __dp4a, 8 or 16 by mma.sync.
+// TOKENS: 1, 2 or 4 by __dp4a, 8 by mma.sync.
 template <int TOKENS, int WARPS, int KS>
 __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
 lm_int8_rows_kernel(const __grid_constant__ Int8Args q) {
     constexpr bool DOT = TOKENS <= 4;
-    constexpr int NB = DOT ? 1 : TOKENS / 8, THREADS = WARPS * 32, HIGH = 16 * (WARPS / KS);
+    constexpr int THREADS = WARPS * 32, HIGH = 16 * (WARPS / KS);
     constexpr int SUMS = 16 * TOKENS;                                       // of one warp
     const LmArgs &p = q.lm;
     extern __shared__ unsigned char smem_raw[];
@@ -326,19 +326,14 @@ lm_int8_rows_kernel(const __grid_constant__ Int8Args q) {
                     if (c4 == 0) own[n * 16 + h * 8 + g] = v;
                 }
         } else {
-            const unsigned char *x_lane[NB];
+            const unsigned char *x_lane = xs + min(g, w.nt - 1) * q.x_pitch + (kw * kStep + c4 * 16) * 2;
+            int sum[4];
+            float acc[2][4];
 #pragma unroll
-            for (int n = 0; n < NB; ++n)
-                x_lane[n] = xs + min(n * 8 + g, w.nt - 1) * q.x_pitch + (kw * kStep + c4 * 16) * 2;
-            int sum[NB][4];
-            float acc[2][NB][4];
-#pragma unroll
-            for (int n = 0; n < NB; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    sum[n][i] = 0;
-                    acc[0][n][i] = acc[1][n][i] = 0.f;
-                }
+            for (int i = 0; i < 4; ++i) {
+                sum[i] = 0;
+                acc[0][i] = acc[1][i] = 0.f;
+            }
             if (w.g < p.G)
                 for (int s = 0; s < per; ++s) {
                     uint4 a[kLoads], b[kLoads];
@@ -359,36 +354,28 @@ lm_int8_rows_kernel(const __grid_constant__ Int8Args q) {
                         to_f16(b[i].y, hb[2], hb[3]);
                         to_f16(b[i].z, hb[4], hb[5]);
                         to_f16(b[i].w, hb[6], hb[7]);
-#pragma unroll
-                        for (int n = 0; n < NB; ++n) {
-                            const uint4 *x = reinterpret_cast<const uint4 *>(x_lane[n] + i * 128);
-                            const uint4 u = x[0], v = x[1];
-                            mma16816(acc[0][n], ha[0], hb[0], ha[1], hb[1], u.x, u.y);
-                            mma16816(acc[1][n], ha[2], hb[2], ha[3], hb[3], u.z, u.w);
-                            mma16816(acc[0][n], ha[4], hb[4], ha[5], hb[5], v.x, v.y);
-                            mma16816(acc[1][n], ha[6], hb[6], ha[7], hb[7], v.z, v.w);
-                        }
+                        const uint4 *x = reinterpret_cast<const uint4 *>(x_lane + i * 128);
+                        const uint4 u = x[0], v = x[1];
+                        mma16816(acc[0], ha[0], hb[0], ha[1], hb[1], u.x, u.y);
+                        mma16816(acc[1], ha[2], hb[2], ha[3], hb[3], u.z, u.w);
+                        mma16816(acc[0], ha[4], hb[4], ha[5], hb[5], v.x, v.y);
+                        mma16816(acc[1], ha[6], hb[6], ha[7], hb[7], v.z, v.w);
                     }
-#pragma unroll
-                    for (int n = 0; n < NB; ++n) x_lane[n] += KS * kStep * 2;
+                    x_lane += KS * kStep * 2;
                     // Two accumulators in turn, each of at most kInt8Run terms.
                     constexpr int FLUSH = 2 * kInt8Run / kStep;
                     if (s % FLUSH == FLUSH - 1 || s == per - 1)
 #pragma unroll
                         for (int z = 0; z < 2; ++z)
 #pragma unroll
-                            for (int n = 0; n < NB; ++n)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    sum[n][i] += __float2int_rn(acc[z][n][i]);
-                                    acc[z][n][i] = 0.f;
-                                }
+                            for (int i = 0; i < 4; ++i) {
+                                sum[i] += __float2int_rn(acc[z][i]);
+                                acc[z][i] = 0.f;
+                            }
                 }
-            // Register i of block n: row lane / 4 + 8 (i / 2), token 8 n + 2 (lane % 4) + i % 2.
+            // Register i: row lane / 4 + 8 (i / 2), token 2 (lane % 4) + i % 2.
 #pragma unroll
-            for (int n = 0; n < NB; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) own[(n * 8 + c4 * 2 + (i & 1)) * 16 + g + (i >> 1) * 8] = sum[n][i];
+            for (int i = 0; i < 4; ++i) own[(c4 * 2 + (i & 1)) * 16 + g + (i >> 1) * 8] = sum[i];
         }
         // Join the sums of the KS warps.
         if constexpr (KS == 1) __syncwarp();
@@ -436,8 +423,7 @@ LmKernel int8_rows_kernel(int tokens, int warps, int ks) {
     k.fn = tokens == 1   ? rows_kernel<1>(warps, ks)
            : tokens == 2 ? rows_kernel<2>(warps, ks)
            : tokens == 4 ? rows_kernel<4>(warps, ks)
-           : tokens == 8 ? rows_kernel<8>(warps, ks)
-                         : rows_kernel<16>(warps, ks);
+                         : rows_kernel<8>(warps, ks);
     k.threads = warps * 32;
     k.bn = tokens;
     k.tile_m = 16 * (warps / ks);
