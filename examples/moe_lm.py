@@ -1,12 +1,13 @@
 """A language model's expert layer and vocabulary head on this library, trained
 and then served.
 
-Training: tokens are sorted by the expert a router picked, each expert
-multiplies its rows (grouped_gemm; the counts stay on the device), and the
-loss over the vocabulary is taken without its logits (linear_cross_entropy);
-torch's backward pass goes through both.  Serving: the
-head's matrix is quantised to 4 bits and one token at a time goes through
-w4_gemm.
+Training: a router picks experts (route_topk), the tokens are sorted by expert
+(expert_dispatch), each expert multiplies its rows (grouped_gemm; the counts
+stay on the device), the rows come back with their weights (expert_combine), and
+the loss over the vocabulary is taken without its logits (linear_cross_entropy);
+torch's backward pass goes through all of it.  Serving: the experts' matrices are
+quantised to 8 bits (int8_quantize) and the head's to 4, and one token at a time
+goes through int8_grouped_gemm and w4_gemm.
 
     python examples/moe_lm.py            # on a GB300
 """
@@ -35,21 +36,28 @@ class ExpertModel(torch.nn.Module):
         self.down = weight(experts, dim, hidden)
         self.head = weight(vocab, dim)
 
-    def experts(self, x):
-        scores = torch.softmax(x.float() @ self.router.float().t(), dim=1)
-        gate, expert = scores.max(dim=1)
-        order = torch.argsort(expert, stable=True)
-        # Ends of the experts' rows: computed and used on the device.
-        ends = torch.searchsorted(expert[order], torch.arange(self.up.shape[0], device=x.device),
-                                  right=True).to(torch.int32)
-        rows = x[order]
-        h = torch.nn.functional.silu(sg.grouped_gemm(rows, self.up, ends, trans_w=True))
-        y = sg.grouped_gemm(h, self.down, ends, trans_w=True)
-        y = y * gate[order, None].to(y.dtype)
-        return x + torch.zeros_like(y).index_copy(0, order, y)
+    def experts(self, x, served=None):
+        """One expert for each token; `served` the experts' matrices in 8 bits."""
+        weights, experts = sg.route_topk(x.float() @ self.router.float().t(), 1, normalize=False)
+        rows, slots, ends = sg.expert_dispatch(x, experts, self.up.shape[0])
+        if served is None:
+            h = torch.nn.functional.silu(sg.grouped_gemm(rows, self.up, ends, trans_w=True))
+            y = sg.grouped_gemm(h, self.down, ends, trans_w=True)
+        else:
+            (up, up_scales), (down, down_scales) = served
+            h = torch.nn.functional.silu(sg.int8_grouped_gemm(rows, up, up_scales, ends))
+            y = sg.int8_grouped_gemm(h, down, down_scales, ends)
+        return x + sg.expert_combine(y, slots, weights)
 
-    def hidden(self, tokens):
-        return self.experts(self.embed[tokens])
+    def eight_bits(self):
+        """The experts' matrices in 8 bits, a scale for each output column."""
+        def of(w):
+            q, scales = sg.int8_quantize(w.detach().flatten(0, 1))
+            return q.view(w.shape), scales.view(w.shape[:2])
+        return of(self.up), of(self.down)
+
+    def hidden(self, tokens, served=None):
+        return self.experts(self.embed[tokens], served)
 
     def loss(self, tokens, target):
         losses, _ = sg.linear_cross_entropy(self.hidden(tokens), self.head, target)
@@ -84,12 +92,13 @@ def main(steps=30, vocab=1000, dim=256, hidden=512, experts=8, tokens=512, dtype
                     p -= (20.0 * p.grad.float()).to(dtype)
                     p.grad = None
         losses.append(loss.item())
-    # Serving: a token at a time, the head in 4 bits.
+    # Serving: a token at a time, the experts in 8 bits and the head in 4.
     with torch.no_grad():
         q, scales, zeros = quantise(model.head)
+        served = model.eight_bits()
         right = 0
         for t in range(16, 48):
-            x = model.hidden(text[t:t + 1])
+            x = model.hidden(text[t:t + 1], served)
             right += int(sg.w4_gemm(x, q, scales, zeros).argmax().item() == target[t].item())
     return losses, right / 32
 
@@ -97,4 +106,4 @@ def main(steps=30, vocab=1000, dim=256, hidden=512, experts=8, tokens=512, dtype
 if __name__ == "__main__":
     curve, share = main()
     print("loss: " + " ".join(f"{v:.3f}" for v in curve[::5] + curve[-1:]))
-    print(f"4-bit head predicts {share:.0%} of 32 tokens")
+    print(f"8-bit experts and 4-bit head predict {share:.0%} of 32 tokens")
