@@ -2,7 +2,7 @@
 include/sgemm_gb300_lm.h.
 
 Every function takes float32, float16 or bfloat16 CUDA tensors (the same type
-for all matrices of a call) with any row pitch (stride(-1) == 1), enqueues its
+for all matrices of a call; weights in 4 or 8 bits beside them) with any row pitch (stride(-1) == 1), enqueues its
 work on torch's current stream (or `stream`) and returns new tensors unless
 `out` is given.  A call's workspace comes from torch's allocator and is its
 own, so calls on several streams or from several threads need no handles of
@@ -10,11 +10,13 @@ their own, and calls can be captured with torch.cuda.graph; a `handle` (the
 device's default one otherwise) carries the wait limit and the error word.
 The checks and the calls are in csrc/lm_binding.cpp.
 
-grouped_gemm() and linear_cross_entropy() are differentiable in x and w: where
-gradients are recorded and one of them requires one, the result carries a graph
-whose backward pass makes the gradient calls below, on the stream current there.
-(A result in `out` carries none.)  What has no gradient here, the products with
-4-bit weights and lse by itself, says so when one is asked for.
+grouped_gemm() and linear_cross_entropy() are differentiable in x and w,
+route_topk() in the logits, expert_dispatch() in x and expert_combine() in rows
+and weights: where gradients are recorded and one of them requires one, the result
+carries a graph whose backward pass makes the gradient calls below, on the stream
+current there.  (A result in `out` carries none.)  What has no gradient here, the
+products with 4-bit and 8-bit weights and lse by itself, says so when one is asked
+for.
 """
 
 from __future__ import annotations

