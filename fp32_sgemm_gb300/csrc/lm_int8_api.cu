@@ -298,7 +298,7 @@ sgemmStatus_t sgemmInt8(sgemmHandle_t h, sgemmDataType_t typeX, sgemmDataType_t 
         a.w_vec = aligned(B, 16) && ldb % 16 == 0 && a.stride_w % 16 == 0;
         a.k_slice = int(q.k_slice);
         a.x_pitch = int(q.x_pitch);
-        a.early = q.x_copy;
+        a.early = q.x_copy && a.w_vec;
         const int slots = resident_slots(h, k, int(q.smem));
         if (slots < 1) return SGEMM_STATUS_LAUNCH_FAILED;
         cfg.gridDim = dim3(unsigned(std::max<int64_t>(1, std::min<int64_t>(tiles, slots / q.slices))), unsigned(q.slices));

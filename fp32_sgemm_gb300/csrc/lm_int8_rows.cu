@@ -57,7 +57,8 @@ __device__ __forceinline__ void to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
     hi = *reinterpret_cast<const uint32_t *>(&dh);
 }
 
-// 16 bytes at p, n of them in the row (the others 0).
+// 16 bytes at p, n of them in the row (the others 0).  (The end of a row may be read
+// before the kernel has waited, so past L1; rows that are not aligned are not.)
 __device__ __noinline__ uint4 load_some(const int8_t *p, int n) {
     uint32_t v[5] = {0, 0, 0, 0, 0};
     const int skip = (int)(reinterpret_cast<uintptr_t>(p) & 3);
@@ -74,14 +75,14 @@ __device__ __noinline__ uint4 load_some(const int8_t *p, int n) {
     } else {
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-            if (e < n) v[e / 4] |= (uint32_t)(uint8_t)p[e] << (8 * (e % 4));
+            if (e < n) v[e / 4] |= (uint32_t)__ldcg(reinterpret_cast<const uint8_t *>(p) + e) << (8 * (e % 4));
     }
     return make_uint4(v[0], v[1], v[2], v[3]);
 }
-// (Read once: kept out of L1.)
+// (Read once: kept out of L1, and past what it may hold.)
 __device__ __forceinline__ uint4 load_whole(const int8_t *p) {
     uint4 w;
-    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.relaxed.gpu.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "l"(p));
     return w;
 }
