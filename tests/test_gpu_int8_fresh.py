@@ -1,5 +1,6 @@
-"""Weights, scales and ends that a kernel right before the call has written: the
-products read some of it before x is quantised, and none of it may be old."""
+"""Weights, scales and ends that a kernel right before the call has written (the
+products read some of it before x is quantised, and none of it may be old), and
+groups that are cut or alone."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -62,3 +63,26 @@ def test_ends_written_right_before(sg, T, N, K):
         got.append(sg.int8_grouped_gemm(x, w, ones, ends))
     for i, y in enumerate(got):
         assert torch.equal(y, want[i % 4]), i
+
+
+@pytest.mark.parametrize("sizes,N,K,behind", [([2], 50, 300, 0), ([1], 70, 4096, 2), ([5], 33, 130, 4), ([40], 60, 700, 9),
+                                              ([0], 20, 64, 3), ([3, 0, 2, 1], 40, 70001, 2), ([9, 1, 30], 40, 70001, 5),
+                                              ([0, 60, 0, 0, 0, 0, 0, 0], 129, 513, 1)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_one_group_and_cut_groups(sg, sizes, N, K, behind, dtype):
+    # One group with an end of its own, contractions in parts by group, all rows
+    # in one of many groups.
+    T, G = sum(sizes) + behind, len(sizes)
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x = torch.randn(T, K, generator=g, device="cuda").to(dtype)
+    w = torch.randint(-128, 128, (G, N, K), generator=g, device="cuda", dtype=torch.int8)
+    ws = torch.rand(G, N, generator=g, device="cuda")
+    ends = torch.tensor(sizes, device="cuda").cumsum(0).to(torch.int32)
+    q, s = sg.int8_quantize(x)
+    want, a = torch.zeros(T, N, dtype=dtype, device="cuda"), 0
+    for i, n in enumerate(sizes):
+        total = (q[a:a + n].double() @ w[i].double().t()).to(torch.int64)
+        want[a:a + n] = (total.float() * s[a:a + n, None] * ws[i]).to(dtype)
+        a += n
+    assert torch.equal(sg.int8_grouped_gemm(x, w, ws, ends), want)
+    assert torch.equal(sg.int8_grouped_gemm(q, w, ws, ends, x_scales=s, dtype=dtype), want)
