@@ -31,6 +31,7 @@
 #include <type_traits>
 
 #include "lm_int8.h"
+#include "lm_int8_round.cuh"
 #include "lm_mma.cuh"
 
 namespace sg {
@@ -82,18 +83,6 @@ __device__ __forceinline__ void tmem_st_32cols(uint32_t taddr, const uint32_t (&
         : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Four integers as two pairs of f16: a byte plus 128 under the leading bits of
-// 1024, less 1152.
-__device__ __forceinline__ void to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    w ^= 0x80808080u;
-    const uint32_t magic = 0x64646464u, less = 0x64806480u;
-    const uint32_t l = __byte_perm(w, magic, 0x4140), h = __byte_perm(w, magic, 0x4342);
-    const __half2 dl = __hsub2(*reinterpret_cast<const __half2 *>(&l), *reinterpret_cast<const __half2 *>(&less));
-    const __half2 dh = __hsub2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&less));
-    lo = *reinterpret_cast<const uint32_t *>(&dl);
-    hi = *reinterpret_cast<const uint32_t *>(&dh);
-}
 
 // Tile t as lm_work gives it (kRagN), without its 64-bit divisions: every warp asks
 // at every tile, and the MMAs' warp is waited for meanwhile.

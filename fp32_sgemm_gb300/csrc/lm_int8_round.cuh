@@ -1,4 +1,5 @@
-// Rows of numbers as 8-bit integers with a scale each:
+// Arithmetic of the 8-bit products.  Rows of numbers as 8-bit integers with a scale
+// each:
 //
 //   s = max |x| / 127 (rounded to FP32, at least 2^-126 unless all are 0)
 //   q = x / s rounded to the nearest integer, ties to even
@@ -123,5 +124,17 @@ struct RowScale {
         scale = finite ? s : __uint_as_float(0x7FC00000u);
     }
 };
+
+// Four integers as two pairs of f16: a byte plus 128 under the leading bits of
+// 1024, less 1152 (bytes 0 1 and 2 3; a published conversion: Kim et al., 2022).
+__device__ __forceinline__ void to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    w ^= 0x80808080u;
+    const uint32_t magic = 0x64646464u, less = 0x64806480u;
+    const uint32_t l = __byte_perm(w, magic, 0x4140), h = __byte_perm(w, magic, 0x4342);
+    const __half2 dl = __hsub2(*reinterpret_cast<const __half2 *>(&l), *reinterpret_cast<const __half2 *>(&less));
+    const __half2 dh = __hsub2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&less));
+    lo = *reinterpret_cast<const uint32_t *>(&dl);
+    hi = *reinterpret_cast<const uint32_t *>(&dh);
+}
 
 }  // namespace sg

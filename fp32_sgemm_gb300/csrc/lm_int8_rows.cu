@@ -25,8 +25,9 @@
 // another), four 41.8, eight 46.4; 14336 x 4096, one 13.6, seven (14335) 17.2; 4096 x
 // 4096, one 6.9, eight 10.2; 64 groups of 2048 x 1024, 32 tokens 18.3, 128 tokens
 // 30.3 (4.5 TB/s).  A ring of TMA copies in the place of the registers kept more
-// bytes on their way and took longer (one token, 28672 x 8192: 48 us): the
-// instructions bound it, not the loads.  W that is not 16-byte aligned or of a pitch
+// bytes on their way and took longer (one token, 28672 x 8192: 48 us), as did loads
+// of 512 columns a step (eight tokens: 57 us): the instructions bound it, and the
+// registers, not the loads.  W that is not 16-byte aligned or of a pitch
 // that is no multiple of 16 is put together from words: 4096 x 4095, one token, 15 us.
 #include <type_traits>
 
@@ -44,17 +45,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
                  "{%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Four integers as two pairs of f16: bytes 0 1 and 2 3.
-__device__ __forceinline__ void to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    w ^= 0x80808080u;
-    const uint32_t magic = 0x64646464u, less = 0x64806480u;             // 1024 + u - 1152
-    const uint32_t l = __byte_perm(w, magic, 0x4140), h = __byte_perm(w, magic, 0x4342);
-    const __half2 dl = __hsub2(*reinterpret_cast<const __half2 *>(&l), *reinterpret_cast<const __half2 *>(&less));
-    const __half2 dh = __hsub2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&less));
-    lo = *reinterpret_cast<const uint32_t *>(&dl);
-    hi = *reinterpret_cast<const uint32_t *>(&dh);
 }
 
 // 16 bytes at p, n of them in the row (the others 0).  (The end of a row may be read
