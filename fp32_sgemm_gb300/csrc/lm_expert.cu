@@ -37,6 +37,10 @@ namespace {
 // expert start, 32 choices at a time: the order is that of the choices.
 constexpr int kSortThreads = 1024, kSortWarps = 32, kSortCluster = 8, kAhead = 8;
 
+// Bytes of its shared memory, all of it dynamic: what a launch may have without
+// asking (48 KB) counts static arrays as well.
+constexpr size_t sort_smem(int G) { return (size_t(G + 1) * (kSortWarps + 2) + kSortWarps) * 4; }
+
 __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
     uint32_t v;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
@@ -57,7 +61,7 @@ lm_expert_sort_kernel(const int64_t *experts, int n, int G, int32_t *slots, int3
     uint32_t *total = sm;                        // [bins] this CTA's
     uint32_t *first = total + bins;              // [bins] row of this CTA's first
     uint32_t *hist = first + bins;               // [warp][bins]
-    __shared__ uint32_t sums[kSortWarps];
+    uint32_t *sums = hist + kSortWarps * bins;   // [warp]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank(), ctas = (int)gridDim.x, bits = 32 - __clz(G);
     griddep_launch_dependents();
@@ -446,10 +450,10 @@ cudaError_t grad_by_piece(const ExpertRows &p, cudaStream_t s) {
 }
 
 cudaError_t sort_launch(const int64_t *experts, int n, int G, int32_t *slots, int32_t *ends, cudaStream_t s) {
-    const size_t smem = size_t(G + 1) * (kSortWarps + 2) * 4;
+    const size_t smem = sort_smem(G);
     if (smem > 48 * 1024) {                       // (for any number of experts: another call may ask for more)
         const cudaError_t opted = cudaFuncSetAttribute(lm_expert_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       (kRouteMaxExperts + 1) * (kSortWarps + 2) * 4);
+                                                       int(sort_smem(SGEMM_MAX_GROUPS)));
         if (opted != cudaSuccess) return opted;
     }
     // A warp has at least 64 choices before there is another CTA.
