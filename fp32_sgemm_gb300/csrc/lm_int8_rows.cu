@@ -47,13 +47,28 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 16 bytes at p, n of them in the row (the others 0).  (The end of a row may be read
-// before the kernel has waited, so past L1; rows that are not aligned are not.)
+// W may be read before the kernel has waited, where nothing says that L1 holds no
+// older copy: rows that are aligned go past it (relaxed loads at the device's scope),
+// whole pieces and the bytes of a row's end alike.  (Read once: kept out of L1, too.)
+__device__ __forceinline__ uint4 load_whole(const int8_t *p) {
+    uint4 w;
+    asm volatile("ld.relaxed.gpu.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "l"(p));
+    return w;
+}
+__device__ __forceinline__ uint32_t load_byte(const int8_t *p) {
+    uint32_t b;
+    asm volatile("ld.relaxed.gpu.global.u8 %0, [%1];" : "=r"(b) : "l"(p));
+    return b;
+}
+// 16 bytes at p, n of them in the row (the others 0).
 __device__ __noinline__ uint4 load_some(const int8_t *p, int n) {
-    uint32_t v[5] = {0, 0, 0, 0, 0};
     const int skip = (int)(reinterpret_cast<uintptr_t>(p) & 3);
+    if (n >= 16 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) return load_whole(p);
+    uint32_t v[5] = {0, 0, 0, 0, 0};
     if (n >= 20) {
-        // The aligned words that hold them (all in the row: n - 16 more follow).
+        // (A row that is not aligned: the kernel has waited.)  The aligned words that
+        // hold them, all in the row: n - 16 more follow.
         const uint32_t *from = reinterpret_cast<const uint32_t *>(p + 4 - skip);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -65,16 +80,9 @@ __device__ __noinline__ uint4 load_some(const int8_t *p, int n) {
     } else {
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-            if (e < n) v[e / 4] |= (uint32_t)__ldcg(reinterpret_cast<const uint8_t *>(p) + e) << (8 * (e % 4));
+            if (e < n) v[e / 4] |= load_byte(p + e) << (8 * (e % 4));
     }
     return make_uint4(v[0], v[1], v[2], v[3]);
-}
-// (Read once: kept out of L1, and past what it may hold.)
-__device__ __forceinline__ uint4 load_whole(const int8_t *p) {
-    uint4 w;
-    asm volatile("ld.relaxed.gpu.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "l"(p));
-    return w;
 }
 
 // Tokens t0 .. t0 + nt of numbers, quantised as lm_int8_quant.cu does: columns
