@@ -190,16 +190,21 @@ struct LmWork {
 // by one warp.  Ends that run backwards or past T are pulled into range
 // (every access stays inside the operands) and reported (kSiteGroupEnds).
 // Entry G is a group of its own, the rows behind the last end, which get zeros.
+// (Read past L1: the 8-bit products come here before they have waited, when nothing
+// says that L1 holds no older copy.)
 template <class Tile, int RAG>
 __device__ __forceinline__ void lm_group_tables(const LmArgs &p, int *start, uint32_t *prefix, int lane) {
     int row = 0;
     uint32_t tiles = 0;
     bool bad = false;
-    int following = lane < p.G ? p.ends[lane] : p.T;
+    auto end_of = [&](int g) {
+        return g < p.G ? (int)ld_relaxed_gpu(reinterpret_cast<const uint32_t *>(p.ends + g)) : p.T;
+    };
+    int following = end_of(lane);
     for (int g0 = 0; g0 <= p.G; g0 += 32) {
         const int g = g0 + lane;
         int e = following;
-        following = g + 32 < p.G ? p.ends[g + 32] : p.T;
+        following = end_of(g + 32);
         bad |= e < 0 || e > p.T;
         e = min(max(e, 0), p.T);
         int top = e;
