@@ -141,6 +141,8 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     uint64_t *xempty = wempty + STAGES;         // MMAs -> copies of x, and converting warps
     uint64_t *tfull = xempty + STAGES;          // MMAs -> epilogue, per accumulator
     uint64_t *tempty = tfull + 2;               // epilogue -> MMAs
+    // (The other SM's threads or MMAs signal all but wfull and wempty: waited for at
+    // the cluster's scope.)
     uint64_t *drain = tempty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Tile::BARS);
     volatile uint32_t *progress = tmem_slot + 1;
@@ -210,7 +212,7 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
             for (int kb = 0; kb < w.nkb; ++kb) {
                 if (p.withhold == kWithholdRefill && issued >= STAGES) { ok = false; break; }
                 if (issued == STAGES) griddep_wait();
-                if (!mbar_wait_bounded<false>(&empty[stage], phase ^ 1u, p.timeout_ns)) {
+                if (!mbar_wait_bounded<true>(&empty[stage], phase ^ 1u, p.timeout_ns)) {
                     if (lane == 0) record_error(p.err, kSiteProducerEmpty);
                     ok = false;
                 }
@@ -249,7 +251,7 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                 int s = stage - back;
                 uint32_t ph = phase;
                 if (s < 0) { s += STAGES; ph ^= 1u; }
-                mbar_wait_bounded<false>(of_w || rank == 0 ? &full[s] : &empty[s], ph, p.timeout_ns);
+                mbar_wait_bounded<true>(of_w || rank == 0 ? &full[s] : &empty[s], ph, p.timeout_ns);
             }
         }
     } else if (warp == 1 && rank == 0) {
@@ -268,13 +270,13 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                 const bool last = kb == w.nkb - 1 || kb % Tile::RUN_BLOCKS == Tile::RUN_BLOCKS - 1;
                 if (first) {
                     const int ab = gc & 1;
-                    if (!mbar_wait_bounded<false>(&tempty[ab], ((uint32_t)(gc >> 1) & 1u) ^ 1u, p.timeout_ns)) {
+                    if (!mbar_wait_bounded<true>(&tempty[ab], ((uint32_t)(gc >> 1) & 1u) ^ 1u, p.timeout_ns)) {
                         if (lane == 0) record_error(p.err, kSiteConsumerFull);
                         ok = false;
                     }
                     d_tmem = tmem_base + (uint32_t)(ab * BN);
                 }
-                if (ok && !mbar_wait_bounded<false>(&ready[stage], phase, 3 * downstream_limit(p.timeout_ns))) {
+                if (ok && !mbar_wait_bounded<true>(&ready[stage], phase, 3 * downstream_limit(p.timeout_ns))) {
                     if (lane == 0) record_error(p.err, kSiteConsumerFull);
                     ok = false;
                 }
@@ -322,7 +324,7 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                     if (block == SLOTS) griddep_wait();
                     // The MMAs of the block that had this slot are done.
                     const uint32_t before = block - SLOTS;
-                    ok = mbar_wait_bounded<false>(&xempty[before % STAGES], (before / STAGES) & 1u,
+                    ok = mbar_wait_bounded<true>(&xempty[before % STAGES], (before / STAGES) & 1u,
                                                   2 * downstream_limit(p.timeout_ns));
                     ok = __all_sync(~0u, ok);
                     if (!ok) {
@@ -351,9 +353,13 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                // (Only the stores to tensor memory have to come before: they are
-                // complete, and fenced.  With release semantics the arrival waits
-                // for more: 8192 rows, 4096 x 14336, 1461 us, without 644, at that time.)
+                // What this publishes is in tensor memory alone, and complete.  The
+                // fence above and the one behind the MMAs' wait order it: as the PTX
+                // ISA describes tcgen05.fence, a relaxed signal between the two is
+                // enough (its example has st.relaxed and ld.relaxed), at a scope that
+                // holds both threads, here the cluster.  (A release waits for more:
+                // 8192 rows, 14336 x 4096, 1157 us in the place of 591; 2048 rows, 242
+                // and 160; 64 groups of 128 rows, 2048 x 1024, 67 and 52.)
                 if (lane == 0) mbar_arrive_cluster_relaxed(ready0 + (uint32_t)stage * 8u);
                 ++block;
                 if (++stage == STAGES) { stage = 0; phase ^= 1u; }
@@ -375,7 +381,7 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
 #pragma unroll
             for (int c = 0; c < SLAB; ++c) sum[c] = 0;
             for (int kb = 0; kb < w.nkb; kb += Tile::RUN_BLOCKS) {
-                ok = __all_sync(~0u, lm_wait_working<false>(&tfull[gc & 1], (uint32_t)(gc >> 1) & 1u,
+                ok = __all_sync(~0u, lm_wait_working<true>(&tfull[gc & 1], (uint32_t)(gc >> 1) & 1u,
                                                            downstream_limit(p.timeout_ns), progress));
                 if (!ok) {
                     if (lane == 0) record_error(p.err, kSiteConsumerFull);
