@@ -130,6 +130,8 @@ SIGNATURES = {
     "sgemmExpertCombine": (_st, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp]),
     "sgemmExpertCombineGrad": (_st, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
                                      _i64, _vp, _vp]),
+    "sgemmExpertCombineGradEx": (_st, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                                       _i64, _vp, _vp, _vp]),
 }
 
 _lock = threading.Lock()

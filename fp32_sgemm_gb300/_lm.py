@@ -262,10 +262,11 @@ def expert_dispatch(x, experts, num_experts, *, handle=None, stream=None):
 def expert_combine(rows, slots, weights=None, *, out=None, handle=None, stream=None):
     """y[t] = sum_j weights[t, j] * rows[slots[t, j]]; returns y [T, D].
 
-    rows [T * k, D] and slots [T, k] as expert_dispatch() lays them out (negative
-    slots add nothing), weights [T, k] float32 or None (1).  Summed in float32 in
-    the order of j.  Differentiable in rows and weights; expert_combine_grad() by
-    itself.
+    rows [T * k, D] and slots [T, k] as expert_dispatch() lays them out, weights
+    [T, k] float32 or None (1).  A slot that names no row (a negative one, as of a
+    choice of no expert or one that is dropped, or T * k and more) adds nothing; a
+    row is named at most once.  Summed in float32 in the order of j.  Differentiable
+    in rows and weights; expert_combine_grad() by itself.
     """
     handle = _handle(rows, handle, "rows")
     y = _c.expert_combine(rows, slots, weights, out, handle, stream)
@@ -274,7 +275,9 @@ def expert_combine(rows, slots, weights=None, *, out=None, handle=None, stream=N
 
 def expert_combine_grad(dy, rows, slots, weights=None, *, handle=None, stream=None):
     """Gradients (drows [T * k, D], dweights [T, k] float32) of expert_combine()
-    for the gradient dy [T, D] by y.  Rows behind the last end get zeros."""
+    for the gradient dy [T, D] by y: drows[slots[t, j]] = weights[t, j] * dy[t], zeros
+    for rows that no slot names (none may be named twice), dweights[t, j] = dy[t] .
+    rows[slots[t, j]], 0 for a slot that names no row."""
     return _c.expert_combine_grad(dy, rows, slots, weights, True, True, _handle(rows, handle, "rows"), stream)
 
 

@@ -537,11 +537,12 @@ PyObject *py_expert_combine_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
         at::Tensor drows, dweights;
         if (need_rows) drows = make({o.T * o.k, o.D}, o.st, o.dev);
         if (need_weights) dweights = make({o.T, o.k}, at::kFloat, o.dev);
-        check(sgemmExpertCombineGrad(c.handle, o.ty, o.T, o.D, o.k, md.ptr, md.ld, o.rows.ptr, std::max(o.rows.ld, o.D), o.slots,
-                                     o.weights, need_rows ? drows.mutable_data_ptr() : nullptr,
-                                     std::max<int64_t>(o.D, 1),
-                                     need_weights ? static_cast<float *>(dweights.mutable_data_ptr()) : nullptr, c.stream),
-              "sgemmExpertCombineGrad");
+        if (need_rows) c.workspace(size_t(o.T) * size_t(o.k) * sizeof(int32_t));
+        check(sgemmExpertCombineGradEx(c.handle, o.ty, o.T, o.D, o.k, md.ptr, md.ld, o.rows.ptr,
+                                       std::max(o.rows.ld, o.D), o.slots, o.weights,
+                                       need_rows ? drows.mutable_data_ptr() : nullptr, std::max<int64_t>(o.D, 1),
+                                       need_weights ? static_cast<float *>(dweights.mutable_data_ptr()) : nullptr,
+                                       static_cast<int32_t *>(c.buffer.get()), c.stream), "sgemmExpertCombineGradEx");
         return Py_BuildValue("NN", need_rows ? wrap(drows) : Py_NewRef(Py_None),
                              need_weights ? wrap(dweights) : Py_NewRef(Py_None));
     });

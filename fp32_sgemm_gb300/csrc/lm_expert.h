@@ -39,6 +39,7 @@ struct ExpertRows {
     const void *rows;           // gradient: rows, or NULL if dweights is not wanted
     int64_t ldr;                // bytes
     float *dweights;            // gradient: [T][k] or NULL
+    int32_t *owner;             // gradient: [T k] for the choice that names each row, or NULL
 };
 // Writes slots (p.slots) and ends[G] as well.
 cudaError_t expert_dispatch_launch(const ExpertRows &p, const int64_t *experts, int G, int32_t *slots, int32_t *ends,

@@ -128,10 +128,10 @@ sgemmStatus_t sgemmExpertCombine(sgemmHandle_t h, sgemmDataType_t type, int64_t 
     return status(sg::expert_combine_launch(type, p, stream));
 }
 
-sgemmStatus_t sgemmExpertCombineGrad(sgemmHandle_t h, sgemmDataType_t type, int64_t T, int64_t D, int64_t k,
-                                     const void *dY, int64_t lddy, const void *rows, int64_t ldr, const int32_t *slots,
-                                     const float *weights, void *dRows, int64_t lddr, float *dWeights,
-                                     cudaStream_t stream) {
+sgemmStatus_t sgemmExpertCombineGradEx(sgemmHandle_t h, sgemmDataType_t type, int64_t T, int64_t D, int64_t k,
+                                       const void *dY, int64_t lddy, const void *rows, int64_t ldr,
+                                       const int32_t *slots, const float *weights, void *dRows, int64_t lddr,
+                                       float *dWeights, int32_t *owners, cudaStream_t stream) {
     sgemmStatus_t st = check_rows(type, T, D, k);
     if (st != SGEMM_STATUS_SUCCESS) return st;
     const bool any = T * k > 0, used = any && D > 0;
@@ -140,7 +140,7 @@ sgemmStatus_t sgemmExpertCombineGrad(sgemmHandle_t h, sgemmDataType_t type, int6
         (st = check_matrix(dRows, T * k, D, lddr, type, used && dRows != nullptr)) != SGEMM_STATUS_SUCCESS ||
         (any && (st = check_vector(slots, 4)) != SGEMM_STATUS_SUCCESS))
         return st;
-    if (!aligned(weights, 4) || !aligned(dWeights, 4)) return SGEMM_STATUS_MISALIGNED;
+    if (!aligned(weights, 4) || !aligned(dWeights, 4) || !aligned(owners, 4)) return SGEMM_STATUS_MISALIGNED;
     if (!any || (dWeights == nullptr && (dRows == nullptr || D == 0))) return SGEMM_STATUS_SUCCESS;
     if (h == nullptr) return SGEMM_STATUS_INVALID_VALUE;
     if ((st = check_device(h)) != SGEMM_STATUS_SUCCESS) return st;
@@ -158,7 +158,16 @@ sgemmStatus_t sgemmExpertCombineGrad(sgemmHandle_t h, sgemmDataType_t type, int6
     p.rows = rows;
     p.ldr = ldr * p.elem;
     p.dweights = dWeights;
+    p.owner = owners;
     return status(sg::expert_combine_grad_launch(type, p, stream));
+}
+
+sgemmStatus_t sgemmExpertCombineGrad(sgemmHandle_t h, sgemmDataType_t type, int64_t T, int64_t D, int64_t k,
+                                     const void *dY, int64_t lddy, const void *rows, int64_t ldr, const int32_t *slots,
+                                     const float *weights, void *dRows, int64_t lddr, float *dWeights,
+                                     cudaStream_t stream) {
+    return sgemmExpertCombineGradEx(h, type, T, D, k, dY, lddy, rows, ldr, slots, weights, dRows, lddr, dWeights,
+                                    nullptr, stream);
 }
 
 }  // extern "C"

@@ -318,12 +318,16 @@ sgemmStatus_t sgemmRouteTopKGrad(sgemmHandle_t handle, sgemmDataType_t type, int
  * in the order of j, in FP32, rounded once.  Its gradients, either of which
  * may be NULL:
  *
- *   dRows[slots[t, j], :] = weights[t, j] * dY[t, :]          (row ~slots[t, j]: zeros)
- *   dWeights[t, j] = dY[t, :] . rows[slots[t, j], :]          (0 for a negative slot)
+ *   dRows[slots[t, j], :] = weights[t, j] * dY[t, :]
+ *   dRows[r, :] = 0                                           for a row r that no slot names
+ *   dWeights[t, j] = dY[t, :] . rows[slots[t, j], :]          (0 for a slot that names no row)
  *
- * slots are those of sgemmExpertDispatch(), or any that name each row at most
- * once: rows named by none keep in dRows what was there, of one named twice
- * either gradient is written, and what lies outside the rows is left out.
+ * A negative slot, or one of T * k or more, names no row, and a row is named at
+ * most once (of one named twice either gradient is written).  Which rows no slot
+ * names is noted in `owners`, T * k numbers of scratch.  Without them (NULL, or
+ * sgemmExpertCombineGrad()) the slots have to be those of sgemmExpertDispatch():
+ * row ~slots[t, j] of a negative slot gets zeros, and a row that is named neither
+ * way keeps what was there.
  *
  * INVALID_VALUE, MISALIGNED as for sgemmGrouped().  NOT_SUPPORTED: T * k, D of
  * 2^31 or more, G > SGEMM_MAX_GROUPS.  No workspace.
@@ -340,6 +344,11 @@ sgemmStatus_t sgemmExpertCombineGrad(sgemmHandle_t handle, sgemmDataType_t type,
                                      const void *dY, int64_t lddy, const void *rows, int64_t ldr,
                                      const int32_t *slots, const float *weights, void *dRows, int64_t lddr,
                                      float *dWeights, cudaStream_t stream);
+
+sgemmStatus_t sgemmExpertCombineGradEx(sgemmHandle_t handle, sgemmDataType_t type, int64_t T, int64_t D, int64_t k,
+                                       const void *dY, int64_t lddy, const void *rows, int64_t ldr,
+                                       const int32_t *slots, const float *weights, void *dRows, int64_t lddr,
+                                       float *dWeights, int32_t *owners, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
