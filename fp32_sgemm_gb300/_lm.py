@@ -14,9 +14,9 @@ grouped_gemm() and linear_cross_entropy() are differentiable in x and w,
 route_topk() in the logits, expert_dispatch() in x and expert_combine() in rows
 and weights: where gradients are recorded and one of them requires one, the result
 carries a graph whose backward pass makes the gradient calls below, on the stream
-current there.  (A result in `out` carries none.)  What has no gradient here, the
-products with 4-bit and 8-bit weights and lse by itself, says so when one is asked
-for.
+current there.  (A result in `out` carries none, nor do those of the gradient calls
+themselves.)  What has no gradient here, the products with 4-bit and 8-bit weights,
+int8_quantize() and lse by itself, says so when one is asked for.
 """
 
 from __future__ import annotations
@@ -108,6 +108,18 @@ class _W4Gemm(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         raise NotImplementedError("w4_gemm has no gradient")
+
+
+class _Int8Quantize(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, handle, stream):
+        q, scales = _c.int8_quantize(x, handle, stream)
+        ctx.mark_non_differentiable(q)
+        return q, scales
+
+    @staticmethod
+    def backward(ctx, dq, dscales):
+        raise NotImplementedError("int8_quantize has no gradient")
 
 
 class _Int8Gemm(torch.autograd.Function):
@@ -289,7 +301,9 @@ def int8_quantize(x, *, handle=None, stream=None):
     even).  A row with an infinity or a NaN has scale NaN.  Weights are quantised
     the same way, a row per output channel.
     """
-    return _c.int8_quantize(x, _handle(x, handle), stream)
+    handle = _handle(x, handle)
+    both = _c.int8_quantize(x, handle, stream)
+    return _Int8Quantize.apply(x, handle, stream) if both is None else both
 
 
 def int8_gemm(x, w, scales, *, x_scales=None, dtype=None, out=None, handle=None, stream=None):

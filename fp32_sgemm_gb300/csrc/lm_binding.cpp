@@ -553,6 +553,7 @@ PyObject *py_int8_quantize(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&] {
         expect(n, 3);
         const at::Tensor &x = tensor(a[0], "x");
+        if (recorded(x)) Py_RETURN_NONE;
         const sgemmDataType_t ty = type_of(x, "x");
         const c10::Device dev = device_of(x, "x");
         const Matrix mx = matrix(x, "x", x.scalar_type(), dev);
