@@ -14,9 +14,10 @@ grouped_gemm() and linear_cross_entropy() are differentiable in x and w,
 route_topk() in the logits, expert_dispatch() in x and expert_combine() in rows
 and weights: where gradients are recorded and one of them requires one, the result
 carries a graph whose backward pass makes the gradient calls below, on the stream
-current there.  (A result in `out` carries none, nor do those of the gradient calls
-themselves.)  What has no gradient here, the products with 4-bit and 8-bit weights,
-int8_quantize() and lse by itself, says so when one is asked for.
+current there.  (A result in `out` carries neither graph nor tangent, nor do those of
+the gradient calls themselves.)  What has no gradient here, the products with 4-bit and 8-bit weights,
+int8_quantize() and lse by itself, says so when one is asked for; so do all of them
+of an operand with a tangent (forward mode).
 """
 
 from __future__ import annotations

@@ -8,6 +8,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -250,13 +251,15 @@ bool truth(PyObject *o) {
     return is != 0;
 }
 
-// Whether the call belongs into torch's graph: then it answers None, and
-// _lm.py takes it there (inside, nothing is recorded).
-bool recorded(const at::Tensor &a, const at::Tensor &b) {
-    return (a.requires_grad() || b.requires_grad()) && c10::GradMode::is_enabled();
+// Whether the call belongs into torch's graph, by an operand that requires a gradient
+// or has a tangent (which goes on where nothing is recorded): then it answers None,
+// and _lm.py takes it there (inside, neither counts).
+bool recorded(const at::Tensor &a) {
+    return (a.requires_grad() && c10::GradMode::is_enabled()) ||
+           (c10::AutogradState::get_tls_state().get_fw_grad_mode() && a._fw_grad(0).defined());
 }
 
-bool recorded(const at::Tensor &a) { return a.requires_grad() && c10::GradMode::is_enabled(); }
+bool recorded(const at::Tensor &a, const at::Tensor &b) { return recorded(a) || recorded(b); }
 
 PyObject *wrap(const at::Tensor &t) { return THPVariable_Wrap(t); }
 
