@@ -2,9 +2,9 @@
 include/sgemm_gb300_lm.h.
 
 Every function takes float32, float16 or bfloat16 CUDA tensors (the same type
-for all matrices of a call; weights in 4 or 8 bits beside them) with any row pitch (stride(-1) == 1), enqueues its
-work on torch's current stream (or `stream`) and returns new tensors unless
-`out` is given.  A call's workspace comes from torch's allocator and is its
+for all matrices of a call; weights in 4 or 8 bits beside them) with any row
+pitch (stride(-1) == 1), enqueues its work on torch's current stream (or
+`stream`) and returns new tensors unless `out` is given.  A call's workspace comes from torch's allocator and is its
 own, so calls on several streams or from several threads need no handles of
 their own, and calls can be captured with torch.cuda.graph; a `handle` (the
 device's default one otherwise) carries the wait limit and the error word.
@@ -15,9 +15,9 @@ route_topk() in the logits, expert_dispatch() in x and expert_combine() in rows
 and weights: where gradients are recorded and one of them requires one, the result
 carries a graph whose backward pass makes the gradient calls below, on the stream
 current there.  (A result in `out` carries neither graph nor tangent, nor do those of
-the gradient calls themselves.)  What has no gradient here, the products with 4-bit and 8-bit weights,
-int8_quantize() and lse by itself, says so when one is asked for; so do all of them
-of an operand with a tangent (forward mode).
+the gradient calls themselves.)  What has no gradient here, the products with 4-bit
+and 8-bit weights, int8_quantize() and lse by itself, says so when one is asked for;
+so do all of them of an operand with a tangent (forward mode).
 """
 
 from __future__ import annotations

@@ -136,8 +136,9 @@ sgemmStatus_t sgemmExpertCombineGradEx(sgemmHandle_t h, sgemmDataType_t type, in
     if (st != SGEMM_STATUS_SUCCESS) return st;
     const bool any = T * k > 0, used = any && D > 0;
     if ((st = check_matrix(dY, T, D, lddy, type, used)) != SGEMM_STATUS_SUCCESS ||
-        (st = check_matrix(rows, T * k, D, ldr, type, used && dWeights != nullptr)) != SGEMM_STATUS_SUCCESS ||
-        (st = check_matrix(dRows, T * k, D, lddr, type, used && dRows != nullptr)) != SGEMM_STATUS_SUCCESS ||
+        ((rows != nullptr || dWeights != nullptr) &&
+         (st = check_matrix(rows, T * k, D, ldr, type, used && dWeights != nullptr)) != SGEMM_STATUS_SUCCESS) ||
+        (dRows != nullptr && (st = check_matrix(dRows, T * k, D, lddr, type, used)) != SGEMM_STATUS_SUCCESS) ||
         (any && (st = check_vector(slots, 4)) != SGEMM_STATUS_SUCCESS))
         return st;
     if (!aligned(weights, 4) || !aligned(dWeights, 4) || !aligned(owners, 4)) return SGEMM_STATUS_MISALIGNED;

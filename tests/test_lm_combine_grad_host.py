@@ -28,3 +28,12 @@ def test_refusals(lib):
     assert grad(lib, T=2 ** 30) == S.NOT_SUPPORTED
     assert grad(lib, drows=None, dw=None, rows=None, owners=None, h=None) == S.SUCCESS
     assert grad(lib, T=0, dy=None, rows=None, slots=None, drows=None, dw=None, owners=None, h=None) == S.SUCCESS
+
+
+def test_a_gradient_that_is_not_wanted_needs_no_pitch(lib):
+    assert grad(lib, drows=None, lddr=0, dw=None, rows=None, ldr=0, h=None) == S.SUCCESS
+    assert grad(lib, T=0, drows=None, lddr=0, dw=None, rows=None, ldr=0, h=None) == S.SUCCESS
+    # The one that is wanted has to have its own.
+    for bad in (dict(drows=None, lddr=0, ldr=7), dict(dw=None, rows=None, ldr=0, lddr=7), dict(drows=None, lddr=0, rows=None),
+                dict(rows=None, ldr=0)):
+        assert grad(lib, **bad) == S.INVALID_VALUE, bad
