@@ -10,10 +10,12 @@
 //
 // The gradient of a dispatch is a combine without weights.  All three are bound
 // by memory and go by token, so that what a token has once (x, y, dy) is moved
-// once.  On the device (one GB300): 16384 tokens of two choices, 4096 bf16: dispatch 68
-// us, of which the sort is 7 (402 MB, 5.9 TB/s), combine 67, without weights 62 (6.5
-// TB/s), gradients 107 (6.3 TB/s); 8192 of eight, 2048: 57, 52, 89; 8192 of four, 1001
-// f16, whose rows lie at odd addresses: 24, 23, 50 (3 TB/s); 16 of two, 1024: 3 each.
+// once.  On the device (one GB300): 16384 tokens of two choices, 4096 bf16: dispatch 67
+// us, of which the sort is 7 (402 MB, 6 TB/s), combine 66, without weights 62 (6.5
+// TB/s), gradients 109 (6.2 TB/s); 8192 of eight, 2048: 57, 52, 92; 8192 of four, 1001
+// f16, whose rows lie at odd addresses: 22, 23, 49 (3 TB/s); 16 of two, 1024: 2.5, 2.3,
+// 3.6.  Many choices of narrow rows, 65536 of eight, 512 bf16: 154, 102, 187; there the
+// sort, which has one cluster, takes 60 us ahead of the copy (bytes alone: 90).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -339,7 +341,7 @@ lm_expert_combine_kernel(const ExpertRows p, int64_t pieces, int64_t parts) {
 // so the registers are held down: 16384 tokens of two choices, 4096 bf16, two
 // choices at a time 107 us, with two pieces and as many registers as it likes 191;
 // 8192 of eight, 2048, 89 and 133, four at a time 116; odd f16 rows, 8192 of four,
-// 1001, eight pieces 49, two 64.
+// 1001, eight pieces 49, two 64 (without the rows that no slot names, below).
 template <class T, class P, int KC, int U>
 __global__ void __launch_bounds__(kThreads, sizeof(P) == 16 ? 5 : 3)
 lm_expert_combine_grad_kernel(const ExpertRows p, int64_t pieces) {

@@ -41,7 +41,11 @@ sgemmStatus_t check_x(int from, const void *X, int64_t T, int64_t K, int64_t ldx
 // Few rows a group in the mean: straight from memory, W read once for up to 8 of
 // them; otherwise the tensor cores (8 rows, 28672 x 8192: 46 and 51 us, 12 rows 84 of
 // 16 at a time and 51; 16 groups of 8 rows, 2048 x 1408: 16.8 and 17.9, of 12, 20.0
-// and 18.1).
+// and 18.1).  The sizes of the groups are on the device, so T / G decides, and it was
+// chosen for even ones.  Where a few groups have all rows, W is read and converted
+// again for every 8 of them, and the other kernel would be faster: 512 rows, 64 groups
+// of 1024 x 2048, even 31.3 and 31.7 us, in 16 groups 28 and 13.6, in one 27 and 13.5;
+// 1024 rows, 128 groups, even 53 and 56, in four 46 and 20.5.
 constexpr int64_t kInt8FewRows = 8;
 // Bytes of x that every CTA quantises itself instead of a launch of its own (one
 // row, 4096 x 4096: 5.5 us, 7.3).

@@ -174,7 +174,8 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     }
     // The kernel before wrote x and its scales, and let this one begin when all
     // before it was done: W's first stages are on their way and converted meanwhile.
-    // Every wait that has a limit begins behind it, however long it takes.
+    // Waits that have a limit begin behind it, however long it takes, but those for
+    // W's first stages, which need nothing of it.
     griddep_launch_dependents();
     if (warp == 2) {
         if (p.ends != nullptr) {
