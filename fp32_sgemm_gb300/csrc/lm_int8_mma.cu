@@ -179,7 +179,7 @@ lm_int8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     griddep_launch_dependents();
     if (warp == 2) {
         if (p.ends != nullptr) {
-            lm_group_tables<Tile, kRagN>(p, g_start, g_prefix, lane);
+            lm_group_tables<Tile, kRagN, true>(p, g_start, g_prefix, lane);
         } else if (lane == 0) {
             const uint32_t tiles = (uint32_t)((p.T + p.tile_n - 1) / p.tile_n) * (uint32_t)p.tiles_m;
             g_start[0] = 0; g_start[1] = g_start[2] = p.T;

@@ -176,7 +176,7 @@ lm_int8_rows_kernel(const __grid_constant__ Int8Args q) {
     if (!q.early) griddep_wait();
     if (warp == 0) {
         if (p.ends != nullptr) {
-            lm_group_tables<LmThin, kRagN>(p, start, prefix, lane);
+            lm_group_tables<LmThin, kRagN, true>(p, start, prefix, lane);
         } else if (lane == 0) {
             const uint32_t tiles = (uint32_t)((p.T + p.tile_n - 1) / p.tile_n) * (uint32_t)p.tiles_m;
             start[0] = 0; start[1] = start[2] = p.T;
