@@ -289,7 +289,7 @@ def expert_combine(rows, slots, weights=None, *, out=None, handle=None, stream=N
 def expert_combine_grad(dy, rows, slots, weights=None, *, handle=None, stream=None):
     """Gradients (drows [T * k, D], dweights [T, k] float32) of expert_combine()
     for the gradient dy [T, D] by y: drows[slots[t, j]] = weights[t, j] * dy[t], zeros
-    for rows that no slot names (none may be named twice), dweights[t, j] = dy[t] .
+    for rows that no slot names (of one named twice undefined), dweights[t, j] = dy[t] .
     rows[slots[t, j]], 0 for a slot that names no row."""
     return _c.expert_combine_grad(dy, rows, slots, weights, True, True, _handle(rows, handle, "rows"), stream)
 

@@ -323,7 +323,7 @@ sgemmStatus_t sgemmRouteTopKGrad(sgemmHandle_t handle, sgemmDataType_t type, int
  *   dWeights[t, j] = dY[t, :] . rows[slots[t, j], :]          (0 for a slot that names no row)
  *
  * A negative slot, or one of T * k or more, names no row, and a row is named at
- * most once (of one named twice either gradient is written).  Which rows no slot
+ * most once (of one named twice dRows is undefined).  Which rows no slot
  * names is noted in `owners`, T * k numbers of scratch.  Without them (NULL, or
  * sgemmExpertCombineGrad()) the slots have to be those of sgemmExpertDispatch():
  * row ~slots[t, j] of a negative slot gets zeros, and a row that is named neither
